@@ -35,15 +35,31 @@ PI_MAX_BATCH = 128
 PI_STACK_LAYERS_PER_LAUNCH = 32   # include/pi.h
 PI_ROWS_FP16 = 0
 PI_ROWS_FP8_E4M3 = 1
+PI_DT_F16 = 0
+PI_DT_BF16 = 1
+PI_DT_F32 = 2
+PI_KV_BLOCK = 16
+PI_KV_MAX_PAGE = 256
+PI_MAX_TOP_K = 64
 
 _p = C.c_void_p
 _i32 = C.c_int32
+_i64 = C.c_int64
 
 
 class pi_layer_desc(C.Structure):
     _fields_ = [("d", _i32), ("ffn", _i32), ("rank", _i32), ("act", _i32),
                 ("W_up", _p), ("W_gate", _p), ("b", _p), ("W_down", _p),
                 ("W_p1", _p), ("W_p2", _p), ("c_p", _p), ("row_format", _i32)]
+
+
+class pi_kv_cache(C.Structure):
+    _fields_ = [("n_pages", _i32), ("page_size", _i32), ("heads", _i32), ("head_dim", _i32),
+                ("k_codes", _p), ("k_scales", _p), ("v_codes", _p), ("v_scales", _p), ("status", _p)]
+
+
+class pi_kv_tokens(C.Structure):
+    _fields_ = [("n_seqs", _i32), ("n_tokens", _i32), ("cu", _p), ("page_table", _p), ("table_stride", _i32)]
 
 
 _SIG = {
@@ -69,6 +85,16 @@ _SIG = {
     "pi_layer_set_timing_events": (C.c_int, [_p, _p, _p]),
     "pi_forward_launches": (C.c_int32, [_p, _i32]),
     "pi_layer_set_hot_count": (C.c_int, [_p, _i32]),
+    "pi_kv_write": (C.c_int, [_p, _p, _p, _p, _p, _p, _p, _i32, _p]),
+    "pi_kv_read": (C.c_int, [_p, _p, _p, _p, _p, _i32, _p]),
+    "pi_kv_attention_workspace_bytes": (C.c_size_t, [_p, _i32, _i32, _i32]),
+    "pi_kv_attention": (C.c_int, [_p, _p, _p, _i32, _p, _p, _i32, _i32, C.c_float, _i32, _p, _p, _p, C.c_size_t, _p]),
+    "pi_kv_status": (C.c_int, [_p, _p]),
+    "pi_layer_norm": (C.c_int, [_p, _i64, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, C.c_float, _p, _p, _p, _p, _p]),
+    "pi_layer_norm_backward_workspace_bytes": (C.c_size_t, [_i32, _i32]),
+    "pi_layer_norm_backward": (C.c_int, [_p, _p, _i64, _p, _i32, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p, _p,
+                                         C.c_size_t, _p]),
+    "pi_token_logprobs": (C.c_int, [_p, _i64, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _p, _p, _p]),
     "pi_last_error": (C.c_char_p, []),
     "pi_status_string": (C.c_char_p, [C.c_int]),
 }

@@ -1,0 +1,649 @@
+// Attention of a sequence's newest tokens over its 8-bit key/value cache.
+//
+//   x_j = log2(e) sm_scale q.k_j,  p_j = 2^(x_j - m),  out = sum p_j v_j / sum p_j
+//
+// in one pass over the cache with a running maximum m.  For a single token the
+// work is bound by HBM: each code is used by q_heads / heads rows only.
+//
+// Rows and products.  The query rows of one key/value head (n_s tokens x
+// q_heads / heads) are the M rows of mma.sync m16n8k16 (fp16 operands, binary32
+// sums); E4M3 codes are exact in fp16, so q.k has no rounding but that of the
+// sums.  bf16 rows are scaled by a power of two per row to fit fp16.  Codes go
+// from global memory straight into the lanes' operand registers: the order of
+// the head_dim in a product and of the columns of V is free as long as both
+// operands agree, so each lane takes contiguous bytes of a token's row, and no
+// shared memory or transposition is needed.
+//
+// Scales.  A 16-token step of a warp is one block of the cache: its K scale is
+// one factor of x, its V scale 2^ev is folded into the weights: acc holds
+// sum 2^(x_j + ev_j - R) c_j with R + kBoost the running maximum of x_j + ev_j, so
+// neither very large nor very small scales leave fp16's range, while
+// l = sum 2^(x_j - m) runs on m.  out = acc 2^(R - m) / l.
+//
+// Split.  The tiles (64 keys of one unit = sequence, head, row tile) of all
+// units form one line that is cut evenly over the CTAs, so a batch of very
+// different lengths keeps every SM busy to the end.  A unit cut between CTAs
+// leaves partial sums, which k_attn_combine adds in CTA order.
+#include "pi_kv.cuh"
+#include "pi_ops.cuh"
+
+#include <algorithm>
+
+using namespace pidev;
+
+namespace {
+
+constexpr int kTile = 64;                 // keys of a tile
+constexpr float kBoost = 12.f;             // weights go up to 2^kBoost, so that fp16 is subnormal only below 2^-(14 + kBoost)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  pi_kv_cache c;
+  pi_kv_tokens tok;
+  const int32_t *length;
+  const void *q;
+  int64_t qt, qh;
+  void *out;
+  float *lse;
+  float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
+  float scale;             // sm_scale log2(e)
+  int q_heads, group, max_q, causal, row_tiles, grid;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma16816(float *c, const unsigned *a, unsigned b0, unsigned b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The low / high two codes of a word as an fp16 pair.
+__device__ __forceinline__ unsigned cvt_lo(unsigned w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  return h.x | (unsigned)h.y << 16;
+}
+__device__ __forceinline__ unsigned cvt_hi(unsigned w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  return h.x | (unsigned)h.y << 16;
+}
+__device__ __forceinline__ unsigned pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// Sequence s as the kernels see it: lengths made safe, faults flagged by flag_seq.
+struct Seq {
+  int row0, n, rows, len, first;    // packed row, query tokens used, query rows, keys, position of the first token
+};
+template <int ROWS>
+__device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
+  Seq q;
+  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1];
+  const int n = r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens ? 0 : r1 - r0;
+  const int64_t cap = min((int64_t)p.tok.table_stride * p.c.page_size, (int64_t)1 << 30);
+  const int len = p.length[s];
+  q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group;
+  q.len = len < 0 ? 0 : (int)min((int64_t)len, cap);
+  q.first = (len < 0 ? 0 : len) - n;
+  return q;
+}
+__device__ __forceinline__ void flag_seq(const AttnParams &p, int s) {
+  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1], len = p.length[s];
+  if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens || r1 - r0 > p.max_q) atomicOr(p.c.status, pi::kKvBadRows);
+  if (len < 0 || len > (int64_t)p.tok.table_stride * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
+}
+// Keys that any row of a row tile sees, and the tiles that hold them.
+template <int ROWS>
+__device__ __forceinline__ int unit_keys(const AttnParams &p, const Seq &q, int rt) {
+  if (rt * ROWS >= q.rows) return 0;
+  if (!p.causal) return q.len;
+  const int last = min(q.rows, (rt + 1) * ROWS) - 1;
+  return max(0, min(q.len, q.first + last / p.group + 1));
+}
+template <int ROWS>
+__device__ __forceinline__ int unit_tiles(const AttnParams &p, const Seq &q, int rt) {
+  return (unit_keys<ROWS>(p, q, rt) + kTile - 1) / kTile;
+}
+template <int ROWS>
+__device__ __forceinline__ int64_t seq_tiles(const AttnParams &p, int s) {
+  const Seq q = load_seq<ROWS>(p, s);
+  int64_t t = 0;
+  for (int rt = 0; rt < p.row_tiles && rt * ROWS < q.rows; ++rt) t += unit_tiles<ROWS>(p, q, rt);
+  return t * p.c.heads;
+}
+
+// Exclusive sum over the CTA's 128 threads; *total gets the whole sum.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm[w] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < w) before += sm[i];
+    all += sm[i];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
+__device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
+
+template <int D>
+struct KvRegs {
+  uint4 k[D / 32];        // K: tokens g and 8 + g, D / 4 codes each
+  unsigned v[4][D / 32];  // V: tokens 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q, D / 8 codes each
+  float ks, vs;
+};
+
+// WARPS_M == 1: 16 rows, the four warps take a tile's four blocks.
+// WARPS_M == 4: 64 rows, 16 a warp; every warp goes over all four blocks.
+template <int DT, int D, int WARPS_M>
+__global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
+  using E = Elem<DT>;
+  constexpr int ROWS = 16 * WARPS_M, KS = D / 16, NT = D / 8, CH = D / 4;
+  extern __shared__ float sm[];                    // WARPS_M == 1: [4][16][D] sums, [4][16][3] (m, l, R)
+  __shared__ int64_t scan[4];
+  __shared__ int64_t found[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
+
+  // Where this CTA's share of the line of tiles begins.
+  const int per = (p.tok.n_seqs + 127) / 128;
+  int64_t mine = 0, total;
+  for (int i = 0; i < per; ++i) {
+    const int s = threadIdx.x * per + i;
+    if (s < p.tok.n_seqs) mine += seq_tiles<ROWS>(p, s);
+  }
+  int64_t at = cta_scan(mine, scan, &total);
+  if (total == 0) return;
+  const int shares = (int)min((int64_t)gridDim.x, total);    // every share has a tile, so every part between two of a unit is written
+  if (blockIdx.x >= shares) return;
+  const int64_t begin = cta_begin(blockIdx.x, total, shares), end = cta_begin(blockIdx.x + 1, total, shares);
+  if (at <= begin && begin < at + mine)
+    for (int i = 0; i < per; ++i) {
+      const int s = threadIdx.x * per + i;
+      const int64_t n = seq_tiles<ROWS>(p, s);
+      if (begin < at + n) {
+        found[0] = s, found[1] = at;
+        break;
+      }
+      at += n;
+    }
+  __syncthreads();
+  int s = (int)found[0], h = 0, rt = 0;
+  Seq sq = load_seq<ROWS>(p, s);
+  int64_t u0 = found[1];                           // line position of the current unit
+  {
+    const int64_t per_head = seq_tiles<ROWS>(p, s) / p.c.heads;
+    h = (int)((begin - u0) / per_head);
+    u0 += h * per_head;
+    for (int n; begin >= u0 + (n = unit_tiles<ROWS>(p, sq, rt)); ++rt) u0 += n;
+  }
+
+  for (int64_t pos = begin; pos < end;) {
+    const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
+    const int t0 = (int)(pos - u0), t1 = (int)min((int64_t)tiles, end - u0);
+    // ---- the rows of this unit ----
+    const int base_row = rt * ROWS + (WARPS_M == 1 ? 0 : warp * 16);
+    unsigned a[KS][4];
+    int lim[2];
+    float fac[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = base_row + g + 8 * e;
+      const bool in = r < sq.rows;
+      const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
+      // a padding row masks what every row masks
+      lim[e] = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
+      alignas(16) typename E::T x[CH];
+      const typename E::T *src = static_cast<const typename E::T *>(p.q) + (int64_t)(sq.row0 + i) * p.qt + hq * p.qh + q4 * CH;
+#pragma unroll
+      for (int c = 0; c < CH; c += 8)
+        if (in) {
+          *reinterpret_cast<uint4 *>(&x[c]) = *reinterpret_cast<const uint4 *>(src + c);
+        } else {
+          *reinterpret_cast<uint4 *>(&x[c]) = make_uint4(0, 0, 0, 0);
+        }
+      float up = 1.f;
+      fac[e] = p.scale;
+      if constexpr (DT == PI_DT_BF16) {
+        // the row's largest finite magnitude to [2^13, 2^14): exact, and fp16 then loses only what is 2^-27 of it
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const float v = fabsf(E::to(x[c]));
+          mx = fmaxf(mx, v < INFINITY ? v : 0.f);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = max((int)(__float_as_uint(mx) >> 23), 27) - 127 - 13;    // up = 2^-ex stays normal
+        if (mx > 0.f) up = __uint_as_float((unsigned)(127 - ex) << 23), fac[e] = p.scale * __uint_as_float((unsigned)(127 + ex) << 23);
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        a[k][e] = pack_half2(E::to(x[4 * k]) * up, E::to(x[4 * k + 1]) * up);
+        a[k][2 + e] = pack_half2(E::to(x[4 * k + 2]) * up, E::to(x[4 * k + 3]) * up);
+      }
+    }
+    int min_lim = min(lim[0], lim[1]);             // below it no row of the warp masks anything
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
+
+    float acc[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, R[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+
+    const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
+    const int step = WARPS_M == 1 ? kTile : 16;
+    for (int k0 = t0 * kTile + (WARPS_M == 1 ? warp * 16 : 0); k0 < min(keys, t1 * kTile); k0 += step) {
+      const int pg = k0 / p.c.page_size, page = table[pg];
+      if (page < 0 || page >= p.c.n_pages) {
+        if (lane == 0) atomicOr(p.c.status, pi::kKvBadPage);
+        continue;
+      }
+      const int in_page = k0 - pg * p.c.page_size;
+      const int64_t ph = (int64_t)page * p.c.heads + h;
+      const int64_t sc = ph * (p.c.page_size / PI_KV_BLOCK) + in_page / PI_KV_BLOCK;
+      const uint8_t *kb = p.c.k_codes + (ph * p.c.page_size + in_page) * D;
+      const uint8_t *vb = p.c.v_codes + (ph * p.c.page_size + in_page) * D;
+      const float ks = p.c.k_scales[sc], vs = p.c.v_scales[sc];
+      // ---- x = q.k ----
+      float x[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+        unsigned w[CH / 4];
+#pragma unroll
+        for (int c = 0; c < CH / 8; ++c)
+          *reinterpret_cast<uint2 *>(&w[2 * c]) = *reinterpret_cast<const uint2 *>(kb + (8 * j + g) * D + q4 * CH + 8 * c);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) mma16816(x[j], a[k], cvt_lo(w[k]), cvt_hi(w[k]));
+      }
+      // ---- running maximum ----
+      const bool ragged = k0 + 16 > min_lim;
+      float bm[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1;
+          x[j][e] *= fac[r] * ks;
+          if (ragged && k0 + 8 * j + 2 * q4 + (e & 1) >= lim[r]) x[j][e] = -INFINITY;
+          bm[r] = fmaxf(bm[r], x[j][e]);
+        }
+      const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+      float f[2], sub[2];
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        bm[r] = fmaxf(bm[r], __shfl_xor_sync(0xffffffffu, bm[r], 1));
+        bm[r] = fmaxf(bm[r], __shfl_xor_sync(0xffffffffu, bm[r], 2));
+        const float mn = fmaxf(m[r], bm[r]);
+        sub[r] = mn == -INFINITY ? 0.f : mn;
+        l[r] *= ex2(m[r] - sub[r]);
+        m[r] = mn;
+        const float Rn = fmaxf(R[r], bm[r] + ev - kBoost);
+        if (Rn != R[r]) moved = true;
+        f[r] = Rn == -INFINITY ? 0.f : ex2(fminf(sub[r] + ev - Rn, 100.f));
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float Rn = fmaxf(R[r], bm[r] + ev - kBoost);
+          const float c = Rn == -INFINITY ? 1.f : ex2(R[r] - Rn);
+          R[r] = Rn;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[j][2 * r] *= c, acc[j][2 * r + 1] *= c;
+        }
+      }
+      // ---- weights ----
+      unsigned pa[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ex2(x[j][e] - sub[e >> 1]);
+          l[e >> 1] += w[e];
+          w[e] *= f[e >> 1];
+        }
+        pa[2 * j] = pack_half2(w[0], w[1]);
+        pa[2 * j + 1] = pack_half2(w[2], w[3]);
+      }
+      // ---- acc += p v ----
+      unsigned v[4][D / 32];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tk = 2 * q4 + (r & 1) + 8 * (r >> 1);
+        const uint8_t *row = vb + tk * D + g * (D / 8);
+        if constexpr (D % 64 == 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; c += 2) *reinterpret_cast<uint2 *>(&v[r][c]) = *reinterpret_cast<const uint2 *>(row + 4 * c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) v[r][c] = *reinterpret_cast<const unsigned *>(row + 4 * c);
+        }
+        if (k0 + tk >= sq.len) {                   // past the sequence: whatever the page held before
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) v[r][c] = 0;
+        }
+      }
+      // A NaN among tokens that only some rows see would reach the others as
+      // 0 * NaN: it is taken out here and given to the rows that see it.
+      bool nan = false;
+      if (ragged) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) nan |= __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+        nan = __any_sync(0xffffffffu, nan);
+      }
+      if (nan) {
+        unsigned see[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int k = k0 + 8 * j + 2 * q4;
+          see[2 * j] = pack_half2(k < lim[0], k + 1 < lim[0]);
+          see[2 * j + 1] = pack_half2(k < lim[1], k + 1 < lim[1]);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          unsigned n[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const unsigned is = __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            n[r] = is & 0x38383838u;               // the code of 1
+            v[r][c] &= ~is;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned sel = e == 0 ? 0x5140 : e == 1 ? 0x5140 : 0x7362;
+            const unsigned w0 = __byte_perm(n[0], n[1], sel), w1 = __byte_perm(n[2], n[3], sel);
+            float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(cnt, see, e & 1 ? cvt_hi(w0) : cvt_lo(w0), e & 1 ? cvt_hi(w1) : cvt_lo(w1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (cnt[i] > 0.f) acc[4 * c + e][i] = __uint_as_float(0x7fffffffu);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const unsigned a0 = __byte_perm(v[0][c], v[1][c], 0x5140), a1 = __byte_perm(v[2][c], v[3][c], 0x5140);
+        const unsigned b0 = __byte_perm(v[0][c], v[1][c], 0x7362), b1 = __byte_perm(v[2][c], v[3][c], 0x7362);
+        mma16816(acc[4 * c], pa, cvt_lo(a0), cvt_lo(a1));
+        mma16816(acc[4 * c + 1], pa, cvt_hi(a0), cvt_hi(a1));
+        mma16816(acc[4 * c + 2], pa, cvt_lo(b0), cvt_lo(b1));
+        mma16816(acc[4 * c + 3], pa, cvt_hi(b0), cvt_hi(b1));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+
+    // ---- the unit's result, or this CTA's part of it ----
+    const bool whole = t0 == 0 && t1 == tiles;
+    float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
+    if constexpr (WARPS_M == 1) {
+      float *st = sm + 4 * 16 * D;
+      __syncthreads();                             // the last unit's sums have been read
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        if (q4 == 0) st[(warp * 16 + row) * 3] = m[r], st[(warp * 16 + row) * 3 + 1] = l[r], st[(warp * 16 + row) * 3 + 2] = R[r];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float *o = sm + (warp * 16 + row) * D + (2 * q4 + e) * NT;
+#pragma unroll
+          for (int j = 0; j < NT; j += 4)
+            *reinterpret_cast<float4 *>(o + j) = make_float4(acc[j][2 * r + e], acc[j + 1][2 * r + e], acc[j + 2][2 * r + e], acc[j + 3][2 * r + e]);
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * (D / 4); i += 128) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, st[(w * 16 + row) * 3]);
+        const float ms = M == -INFINITY ? 0.f : M;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float *t = st + (w * 16 + row) * 3;
+          L += t[1] * ex2(t[0] - ms);
+          const float c = t[2] == -INFINITY ? 0.f : ex2(t[2] - ms);
+          const float4 x = *reinterpret_cast<const float4 *>(sm + (w * 16 + row) * D + d);
+          o.x = fmaf(x.x, c, o.x), o.y = fmaf(x.y, c, o.y), o.z = fmaf(x.z, c, o.z), o.w = fmaf(x.w, c, o.w);
+        }
+        if (whole) {
+          const int r = rt * ROWS + row;
+          if (r >= sq.rows) continue;
+          const int64_t orow = (int64_t)(sq.row0 + r / p.group) * p.q_heads + h * p.group + r % p.group;
+          const float inv = L == 0.f ? 0.f : 1.0f / L;
+          Pack<DT, 4> y;
+          y.v[0] = E::from(o.x * inv), y.v[1] = E::from(o.y * inv), y.v[2] = E::from(o.z * inv), y.v[3] = E::from(o.w * inv);
+          *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
+          if (p.lse && d == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
+        } else {
+          *reinterpret_cast<float4 *>(part + row * D + d) = o;
+          if (d == 0) part[ROWS * D + 2 * row] = M, part[ROWS * D + 2 * row + 1] = L;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = warp * 16 + g + 8 * r, gr = rt * ROWS + row;
+        const float ms = m[r] == -INFINITY ? 0.f : m[r];
+        const float c = (R[r] == -INFINITY ? 0.f : ex2(R[r] - ms)) * (whole ? (l[r] == 0.f ? 0.f : 1.0f / l[r]) : 1.f);
+        if (whole && gr >= sq.rows) continue;
+        const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int d = (2 * q4 + e) * NT;
+#pragma unroll
+          for (int j = 0; j < NT; j += 4) {
+            const float4 o = make_float4(acc[j][2 * r + e] * c, acc[j + 1][2 * r + e] * c, acc[j + 2][2 * r + e] * c, acc[j + 3][2 * r + e] * c);
+            if (whole) {
+              Pack<DT, 4> y;
+              y.v[0] = E::from(o.x), y.v[1] = E::from(o.y), y.v[2] = E::from(o.z), y.v[3] = E::from(o.w);
+              *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d + j) = y;
+            } else {
+              *reinterpret_cast<float4 *>(part + row * D + d + j) = o;
+            }
+          }
+        }
+        if (q4 == 0) {
+          if (whole) {
+            if (p.lse) p.lse[orow] = l[r] == 0.f ? -INFINITY : (ms + log2f(l[r])) * kLn2;
+          } else {
+            part[ROWS * D + 2 * row] = m[r], part[ROWS * D + 2 * row + 1] = l[r];
+          }
+        }
+      }
+    }
+
+    // ---- next unit ----
+    pos = u0 + t1;
+    if (pos >= end) break;
+    u0 += tiles;
+    do {                                           // units without keys take no place in the line
+      if (++rt >= p.row_tiles || rt * ROWS >= sq.rows) {
+        rt = 0;
+        if (++h >= p.c.heads) {
+          h = 0;
+          if (++s >= p.tok.n_seqs) return;
+          sq = load_seq<ROWS>(p, s);
+        }
+      }
+    } while (unit_tiles<ROWS>(p, sq, rt) == 0);
+  }
+}
+
+// Units cut between CTAs: their parts added in CTA order.  Units without keys:
+// 0 and -inf.  One CTA per (sequence, head).
+template <int DT, int D, int WARPS_M>
+__global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
+  using E = Elem<DT>;
+  constexpr int ROWS = 16 * WARPS_M;
+  __shared__ int64_t scan[4], start;
+  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
+  const int per = (p.tok.n_seqs + 127) / 128;
+  int64_t mine = 0, total;
+  for (int i = 0; i < per; ++i) {
+    const int t = threadIdx.x * per + i;
+    if (t < p.tok.n_seqs) mine += seq_tiles<ROWS>(p, t);
+  }
+  int64_t at = cta_scan(mine, scan, &total);
+  if (s / per == threadIdx.x) {
+    for (int t = threadIdx.x * per; t < s; ++t) at += seq_tiles<ROWS>(p, t);
+    start = at;
+  }
+  __syncthreads();
+  const int shares = (int)min((int64_t)p.grid, total);
+  const Seq sq = load_seq<ROWS>(p, s);
+  int64_t u0 = start + h * (seq_tiles<ROWS>(p, s) / p.c.heads);
+  for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows; ++rt) {
+    const int tiles = unit_tiles<ROWS>(p, sq, rt);
+    int64_t c0 = 0, c1 = 0;
+    if (tiles) {
+      c0 = cta_owner(u0, total, shares), c1 = cta_owner(u0 + tiles - 1, total, shares);
+      if (c0 == c1) {
+        u0 += tiles;
+        continue;
+      }
+    }
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 128) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4, gr = rt * ROWS + row;
+      if (gr >= sq.rows) break;
+      float M = -INFINITY, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tiles) {
+        for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, p.part[(2 * c + (c == c0)) * ROWS * (D + 2) + ROWS * D + 2 * row]);
+        const float ms = M == -INFINITY ? 0.f : M;
+        for (int64_t c = c0; c <= c1; ++c) {
+          const float *part = p.part + (2 * c + (c == c0)) * ROWS * (D + 2);
+          const float w = ex2(part[ROWS * D + 2 * row] - ms);
+          L += part[ROWS * D + 2 * row + 1] * w;
+          const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
+          o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+        }
+      }
+      const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+      Pack<DT, 4> y;
+      y.v[0] = E::from(o.x * inv), y.v[1] = E::from(o.y * inv), y.v[2] = E::from(o.z * inv), y.v[3] = E::from(o.w * inv);
+      *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
+      if (p.lse && d == 0) p.lse[orow] = L == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+    }
+    u0 += tiles;
+  }
+}
+
+// CTAs of the main kernel.
+int attn_grid() { return 2 * std::max(1, pi::current_sms()); }
+// Rows of a row tile: one warp's 16 while they hold all query rows of a head, else 64.
+int attn_warps_m(int64_t max_rows) { return max_rows <= 16 ? 1 : 4; }
+
+template <int DT, int D, int WARPS_M>
+cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
+  const size_t smem = WARPS_M == 1 ? sizeof(float) * (4 * 16 * D + 4 * 16 * 3) : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  k_attn<DT, D, WARPS_M><<<p.grid, 128, smem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  k_attn_combine<DT, D, WARPS_M><<<(unsigned)p.tok.n_seqs * p.c.heads, 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT, int D>
+cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
+  return attn_warps_m((int64_t)p.max_q * p.group) == 1 ? launch_attn<DT, D, 1>(p, s) : launch_attn<DT, D, 4>(p, s);
+}
+
+template <int DT>
+cudaError_t attn_by_dim(const AttnParams &p, cudaStream_t s) {
+  switch (p.c.head_dim) {
+    case 64: return attn_by_rows<DT, 64>(p, s);
+    case 96: return attn_by_rows<DT, 96>(p, s);
+    case 128: return attn_by_rows<DT, 128>(p, s);
+    default: return attn_by_rows<DT, 256>(p, s);
+  }
+}
+
+}  // namespace
+
+namespace pi {
+
+int current_sms() {
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms[dev];
+}
+
+}  // namespace pi
+
+extern "C" {
+
+size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, int32_t n_tokens, int32_t n_seqs) {
+  pi::clear_error();
+  if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
+  return sizeof(float) * 2 * (size_t)attn_grid() * 64 * (size_t)(c->head_dim + 2);
+}
+
+pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
+                          const void *q, const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
+                          int32_t causal, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  pi::clear_error();
+  pi_status st = pi::check_cache(cache);
+  if (st == PI_OK) st = pi::check_tokens(tokens);
+  if (st != PI_OK) return st;
+  if (dtype != PI_DT_F16 && dtype != PI_DT_BF16) return pi::fail(PI_ERR_INVALID_ARG, "q must be fp16 or bf16");
+  if (q_heads < 1 || q_heads % cache->heads)
+    return pi::fail(PI_ERR_INVALID_ARG, "q_heads=%d is not a multiple of the cache's %d heads", q_heads, cache->heads);
+  if (max_q < 0) return pi::fail(PI_ERR_INVALID_ARG, "max_q=%d is negative", max_q);
+  if (!(fabsf(sm_scale) < INFINITY)) return pi::fail(PI_ERR_INVALID_ARG, "sm_scale must be finite");
+  if (tokens->n_tokens == 0 || tokens->n_seqs == 0 || max_q == 0) return PI_OK;
+  if (!q || !q_stride || !out || !length || !pi::aligned_to(q, 16) || !pi::aligned_to(out, 16))
+    return pi::fail(PI_ERR_INVALID_ARG, "q, q_stride, out and length must be non-NULL, q and out 16-byte aligned");
+  if (q_stride[0] < 0 || q_stride[1] < 0 || q_stride[0] % 8 || q_stride[1] % 8)
+    return pi::fail(PI_ERR_INVALID_ARG, "q's strides must be multiples of 8 elements");
+  if (!pi::aligned_to(length, 4) || !pi::aligned_to(lse, 4))
+    return pi::fail(PI_ERR_INVALID_ARG, "length and lse must be 4-byte aligned");
+  if ((int64_t)tokens->n_seqs * cache->heads >= (int64_t)1 << 31 || (int64_t)max_q * (q_heads / cache->heads) >= 1 << 30)
+    return pi::fail(PI_ERR_UNSUPPORTED, "n_seqs x heads or max_q x q_heads / heads is too large");
+  const size_t need = pi_kv_attention_workspace_bytes(cache, q_heads, tokens->n_tokens, tokens->n_seqs);
+  if (!ws || !pi::aligned_to(ws, 16) || ws_bytes < need)
+    return pi::fail(PI_ERR_INVALID_ARG, "ws must be 16-byte aligned and hold %zu bytes, has %zu", need, ws_bytes);
+  max_q = std::min(max_q, tokens->n_tokens);
+  const int group = q_heads / cache->heads, rows = 16 * attn_warps_m((int64_t)max_q * group);
+  const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<float *>(ws),
+                     sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
+                     (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid()};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
+  return PI_OK;
+}
+
+}  // extern "C"

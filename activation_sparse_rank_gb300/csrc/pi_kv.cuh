@@ -1,0 +1,11 @@
+// Argument checks of the key/value cache's entry points (pi_kv.cu, pi_attn.cu).
+#pragma once
+
+#include "pi_internal.cuh"
+
+namespace pi {
+
+pi_status check_cache(const pi_kv_cache *c);
+pi_status check_tokens(const pi_kv_tokens *t);
+
+}  // namespace pi

@@ -1,0 +1,325 @@
+"""The operators around the FFN block, as Python calls on torch tensors.
+
+``KVCache`` (a paged key/value cache in E4M3 codes: ``write``, ``read``,
+``attention``), ``layer_norm`` with ``layer_norm_backward``, and
+``token_logprobs``.  Argument checks and marshalling only; include/pi.h states
+each operator's formula, limits and treatment of special values.
+
+``stream`` is a torch stream (default: the current one).  Outputs and scratch
+that the caller does not supply are allocated on the stream the call runs on;
+inputs made on another stream have to be ordered before it by the caller, and
+must not be freed before it has passed, as with every torch operator.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+import math
+from typing import NamedTuple, Optional
+
+import torch
+
+from .binding import (PI_DT_BF16, PI_DT_F16, PI_DT_F32, PI_KV_BLOCK, PI_KV_MAX_PAGE, PI_MAX_TOP_K, PiError, _check,
+                      lib, pi_kv_cache, pi_kv_tokens)
+
+__all__ = ["KVCache", "TokenScores", "layer_norm", "layer_norm_backward", "token_logprobs", "PI_KV_BLOCK",
+           "PI_KV_MAX_PAGE", "PI_MAX_TOP_K"]
+
+_DT = {torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16, torch.float32: PI_DT_F32}
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+
+
+def _dt(t: torch.Tensor, name: str) -> int:
+    d = _DT.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, not {t.dtype}")
+    return d
+
+
+def _dev(t: torch.Tensor, device: Optional[torch.device], name: str) -> torch.device:
+    """t is a CUDA tensor, on `device` if given."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    return t.device
+
+
+def _whole(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
+    """t is a contiguous CUDA tensor of this shape and type."""
+    _dev(t, device, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _run_on(device: torch.device, stream):
+    """(context that allocates on the call's device and stream, the stream's handle)."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext(), torch.cuda.current_stream(device).cuda_stream
+    if stream is None:
+        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+class KVCache:
+    """A paged key/value cache in E4M3 codes with one power-of-two scale for
+    each PI_KV_BLOCK tokens of a head.
+
+    Pages are [heads, page_size, head_dim] codes; a sequence's pages are the
+    entries of its row of a page table (int32 [sequences, most pages]).  The
+    four tensors and the table are plain torch tensors of the caller's to keep,
+    copy or hand out: ``k_codes``, ``v_codes`` uint8 [pages, heads, page_size,
+    head_dim] and ``k_scales``, ``v_scales`` float32 [pages, heads,
+    page_size / PI_KV_BLOCK].
+    """
+
+    def __init__(self, n_pages: int, heads: int, head_dim: int, page_size: int = 64, device="cuda"):
+        if page_size < 1 or page_size % PI_KV_BLOCK:
+            raise ValueError(f"page_size must be a multiple of {PI_KV_BLOCK}, not {page_size}")
+        codes = (n_pages, heads, page_size, head_dim)
+        scales = (n_pages, heads, page_size // PI_KV_BLOCK)
+        self._init(torch.zeros(codes, dtype=_u8, device=device), torch.ones(scales, dtype=_f32, device=device),
+                   torch.zeros(codes, dtype=_u8, device=device), torch.ones(scales, dtype=_f32, device=device))
+
+    @classmethod
+    def wrap(cls, k_codes, k_scales, v_codes, v_scales) -> "KVCache":
+        """A cache over tensors that exist already (shapes as above)."""
+        self = cls.__new__(cls)
+        self._init(k_codes, k_scales, v_codes, v_scales)
+        return self
+
+    def _init(self, k_codes, k_scales, v_codes, v_scales):
+        device = _dev(k_codes, None, "k_codes")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page_size, head_dim]")
+        pages, heads, page, dim = k_codes.shape
+        if page % PI_KV_BLOCK:
+            raise ValueError(f"page_size must be a multiple of {PI_KV_BLOCK}, not {page}")
+        for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _whole(t, k_codes.shape, _u8, device, n)
+        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _whole(t, (pages, heads, page // PI_KV_BLOCK), _f32, device, n)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.device, self.n_pages, self.heads, self.page_size, self.head_dim = device, pages, heads, page, dim
+        self._status = torch.zeros(1, dtype=_i32, device=device)
+        self._c = pi_kv_cache(pages, page, heads, dim, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                              v_scales.data_ptr(), self._status.data_ptr())
+        self._ref = C.addressof(self._c)
+        if lib.pi_kv_attention_workspace_bytes(self._ref, heads, 0, 0) == 0:
+            raise PiError(2, "KVCache")
+
+    def _tokens(self, page_table, cu, per_seq, name, n_tokens):
+        dev = self.device
+        _dev(page_table, dev, "page_table")
+        if page_table.dtype != _i32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+            raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
+        n = page_table.shape[0]
+        _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
+        _whole(per_seq, (n,), _i32, dev, name)
+        # a table of one row may carry any stride for it
+        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(),
+                            page_table.stride(0) if n > 1 else page_table.shape[1])
+
+    def _rows(self, t, heads, name):
+        """A [tokens, heads, head_dim] tensor with contiguous heads: its token and head strides."""
+        _dev(t, self.device, name)
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
+            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(t.shape)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}: the elements of a head must be contiguous")
+        return (C.c_int64 * 2)(t.stride(0), t.stride(1))
+
+    def write(self, k, v, page_table, cu_tokens, start, stream=None):
+        """Quantise new tokens into the cache: row cu_tokens[s] + i of k and v
+        [tokens, heads, head_dim] becomes position start[s] + i of sequence s."""
+        ks, vs = self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v")
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must have one shape and type")
+        tok = self._tokens(page_table, cu_tokens, start, "start", k.shape[0])
+        ctx, handle = _run_on(self.device, stream)
+        with ctx:
+            _check(lib.pi_kv_write(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs,
+                                   _dt(k, "k"), handle), "pi_kv_write")
+
+    def read(self, page_table, cu_tokens, start, n_tokens, dtype=torch.float16, k=None, v=None, stream=None):
+        """Positions start[s] .. of each sequence as (k, v) [n_tokens, heads, head_dim] of `dtype`."""
+        if dtype not in _DT:
+            raise TypeError(f"dtype must be float16, bfloat16 or float32, not {dtype}")
+        shape = (n_tokens, self.heads, self.head_dim)
+        tok = self._tokens(page_table, cu_tokens, start, "start", n_tokens)
+        ctx, handle = _run_on(self.device, stream)
+        with ctx:
+            k = torch.empty(shape, dtype=dtype, device=self.device) if k is None else _whole(k, shape, dtype, self.device, "k")
+            v = torch.empty(shape, dtype=dtype, device=self.device) if v is None else _whole(v, shape, dtype, self.device, "v")
+            _check(lib.pi_kv_read(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype],
+                                  handle), "pi_kv_read")
+        return k, v
+
+    def attention_workspace(self, q_heads: int, n_tokens: int, n_seqs: int) -> torch.Tensor:
+        """Scratch for ``attention`` calls of up to this size; calls that overlap need separate ones."""
+        n = lib.pi_kv_attention_workspace_bytes(self._ref, q_heads, n_tokens, n_seqs)
+        if n == 0:
+            raise PiError(1, "pi_kv_attention_workspace_bytes")
+        return torch.empty(n, dtype=_u8, device=self.device)
+
+    def attention(self, q, page_table, cu_tokens, length, max_q=1, sm_scale=None, causal=True, out=None, lse=None,
+                  want_lse=False, ws=None, stream=None):
+        """Attention of each sequence's newest tokens q [tokens, q_heads, head_dim]
+        (float16 or bfloat16) over its cache.  length[s] counts the tokens in the
+        cache, the new ones among them; max_q bounds the new tokens of any
+        sequence.  Returns out, or (out, lse) with want_lse or an lse tensor."""
+        tokens, heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+        qs = self._rows(q, heads, "q")
+        if q.dtype != torch.float16 and q.dtype != torch.bfloat16:
+            raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
+        tok = self._tokens(page_table, cu_tokens, length, "length", tokens)
+        ctx, handle = _run_on(self.device, stream)
+        with ctx:
+            shape = (tokens, heads, self.head_dim)
+            out = torch.empty(shape, dtype=q.dtype, device=self.device) if out is None else _whole(
+                out, shape, q.dtype, self.device, "out")
+            if lse is not None:
+                _whole(lse, (tokens, heads), _f32, self.device, "lse")
+            elif want_lse:
+                lse = torch.empty((tokens, heads), dtype=_f32, device=self.device)
+            if ws is None:
+                ws = self.attention_workspace(heads, tokens, tok.n_seqs)
+            _check(lib.pi_kv_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, q.data_ptr(), qs, heads,
+                                       _DT[q.dtype], 1.0 / math.sqrt(self.head_dim) if sm_scale is None else sm_scale,
+                                       1 if causal else 0, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), handle),
+                   "pi_kv_attention")
+        return out if lse is None else (out, lse)
+
+    def device_status(self, stream=None) -> int:
+        """0 if no call met a bad page, position or token range since the last query, else the status code."""
+        ctx, handle = _run_on(self.device, stream)
+        with ctx:
+            return int(lib.pi_kv_status(self._ref, handle))
+
+
+def _rows2d(x, name):
+    """x as rows of its last dimension: (rows, d, elements between rows)."""
+    d = x.shape[-1] if x.dim() else 0
+    if x.dim() == 2 and (x.stride(1) == 1 or d == 1):
+        return x.shape[0], d, x.stride(0) if x.shape[0] > 1 else d
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return x.numel() // d if d else 0, d, d
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, y=None, sum=None, mean=None, rstd=None,
+               want_stats=False, stream=None):
+    """Layer norm of x over its last dimension; with ``add``, of x + add, which
+    is stored in ``sum`` in x's type (``sum`` may be x).  Returns (y, sum, mean,
+    rstd): sum is None without add, mean and rstd (float32, one a row) are None
+    unless given or asked for with want_stats."""
+    dev = _dev(x, None, "x")
+    dt = _dt(x, "x")
+    rows, d, stride = _rows2d(x, "x")
+    w_dt = 0
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _whole(t, (d,), t.dtype, dev, n)
+            w_dt = _dt(t, n)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one type")
+    if add is not None:
+        _whole(add, x.shape, add.dtype, dev, "add")
+    elif sum is not None:
+        raise ValueError("sum needs add")
+    ctx, handle = _run_on(dev, stream)
+    with ctx:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _whole(y, x.shape, x.dtype, dev, "y")
+        if add is not None:
+            sum = torch.empty(x.shape, dtype=x.dtype, device=dev) if sum is None else _whole(sum, x.shape, x.dtype, dev, "sum")
+        if want_stats:
+            mean = torch.empty(rows, dtype=_f32, device=dev) if mean is None else mean
+            rstd = torch.empty(rows, dtype=_f32, device=dev) if rstd is None else rstd
+        for t, n in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _whole(t, (rows,), _f32, dev, n)
+        _check(lib.pi_layer_norm(x.data_ptr(), stride, _ptr(add), 0 if add is None else _dt(add, "add"), _ptr(weight),
+                                 _ptr(bias), w_dt, rows, d, dt, eps, y.data_ptr(), _ptr(sum), _ptr(mean), _ptr(rstd),
+                                 handle), "pi_layer_norm")
+    return y, sum, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, d_sum=None, dx=None, dweight=None, dbias=None, ws=None,
+                        want_weight_grad=True, stream=None):
+    """Gradient of ``layer_norm``: x is what was normed (``sum`` where something
+    was added), mean and rstd as it returned them, d_sum the gradient that
+    reaches ``sum`` another way.  Returns (dx, dweight, dbias); dx has x's type
+    and may be dy, the other two are float32 (None without want_weight_grad)."""
+    dev = _dev(x, None, "x")
+    dt = _dt(x, "x")
+    rows, d, stride = _rows2d(x, "x")
+    _whole(dy, x.shape, x.dtype, dev, "dy")
+    if d_sum is not None:
+        _whole(d_sum, x.shape, x.dtype, dev, "d_sum")
+    if weight is not None:
+        _whole(weight, (d,), weight.dtype, dev, "weight")
+    _whole(mean, (rows,), _f32, dev, "mean")
+    _whole(rstd, (rows,), _f32, dev, "rstd")
+    ctx, handle = _run_on(dev, stream)
+    with ctx:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else _whole(dx, x.shape, x.dtype, dev, "dx")
+        if want_weight_grad:
+            dweight = torch.empty(d, dtype=_f32, device=dev) if dweight is None else dweight
+            dbias = torch.empty(d, dtype=_f32, device=dev) if dbias is None else dbias
+        for t, n in ((dweight, "dweight"), (dbias, "dbias")):
+            if t is not None:
+                _whole(t, (d,), _f32, dev, n)
+        if ws is None and (dweight is not None or dbias is not None):
+            ws = torch.empty(lib.pi_layer_norm_backward_workspace_bytes(rows, d), dtype=_u8, device=dev)
+        _check(lib.pi_layer_norm_backward(dy.data_ptr(), x.data_ptr(), stride, _ptr(weight),
+                                          0 if weight is None else _dt(weight, "weight"), mean.data_ptr(),
+                                          rstd.data_ptr(), _ptr(d_sum), rows, d, dt, dx.data_ptr(), _ptr(dweight),
+                                          _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), handle),
+               "pi_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+class TokenScores(NamedTuple):
+    """What ``token_logprobs`` returns; float32 [rows], top_* [rows, top_k]."""
+    logprob: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_index: Optional[torch.Tensor]
+    top_logprob: Optional[torch.Tensor]
+
+
+def token_logprobs(logits, targets=None, top_k=0, stream=None) -> TokenScores:
+    """Log-probability of targets (int32 [rows]; below 0: padding, 0), entropy
+    and log of the sum of exponentials of logits [rows, vocab], and its top_k
+    tokens (int32 indices, log-probabilities), equal logits by lower index."""
+    dev = _dev(logits, None, "logits")
+    dt = _dt(logits, "logits")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    if targets is not None:
+        _whole(targets, (rows,), _i32, dev, "targets")
+    ctx, handle = _run_on(dev, stream)
+    with ctx:
+        entropy = torch.empty(rows, dtype=_f32, device=dev)
+        lse = torch.empty(rows, dtype=_f32, device=dev)
+        logprob = None if targets is None else torch.empty(rows, dtype=_f32, device=dev)
+        index = value = None
+        if top_k > 0:
+            index = torch.empty((rows, top_k), dtype=_i32, device=dev)
+            value = torch.empty((rows, top_k), dtype=_f32, device=dev)
+        _check(lib.pi_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
+                                     _ptr(targets), top_k, _ptr(logprob), entropy.data_ptr(), lse.data_ptr(),
+                                     _ptr(index), _ptr(value), handle), "pi_token_logprobs")
+    return TokenScores(logprob, entropy, lse, index, value)

@@ -347,6 +347,158 @@ int32_t pi_forward_launches(const pi_layer *layer, int32_t B);
  * clear the flag), else PI_OK. */
 pi_status pi_device_status(pi_layer *layer, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the FFN block of a decoder layer.  The pages leave the
+ * rest of the layer to the host framework; a decode step that stays on the GPU
+ * runs it as layer norm -> (projection) -> key/value cache -> attention ->
+ * (projection) -> layer norm -> pi_layer_forward, and after the last layer
+ * reads off the log-probabilities of the tokens it chose.
+ *
+ * Tensors may be fp16, bf16 or binary32 (pi_dtype); strides are in elements.
+ * Sums, softmax statistics and norms are binary32; an output is rounded once,
+ * to its own type.  Calls are asynchronous on `stream`, allocate nothing and
+ * use no float atomics: two calls on the same inputs give the same bits.
+ * ------------------------------------------------------------------------- */
+typedef enum { PI_DT_F16 = 0, PI_DT_BF16 = 1, PI_DT_F32 = 2 } pi_dtype;
+
+/* Tokens that share one scale of the cache, per head, keys and values apart. */
+#define PI_KV_BLOCK 16
+/* Exponent of the smallest scale. */
+#define PI_KV_MIN_EXP (-64)
+#define PI_KV_MAX_PAGE 256
+
+/* A paged key/value cache in E4M3 codes, in the caller's device memory.
+ *   k_codes, v_codes    uint8 [n_pages, heads, page_size, head_dim], 16-byte aligned
+ *   k_scales, v_scales  fp32 [n_pages, heads, page_size / PI_KV_BLOCK], 4-byte aligned
+ *   status              uint32 [1], zeroed by the caller; kernels set bits in it
+ *                       (pi_kv_status reads and clears it)
+ * A code c of a block with scale s stands for E4M3(c) * s; s is a power of two.
+ * head_dim 64, 96, 128 or 256; page_size a multiple of PI_KV_BLOCK up to
+ * PI_KV_MAX_PAGE.  A page belongs to one sequence at a time while it is
+ * written; any number of sequences may read it. */
+typedef struct {
+  int32_t n_pages, page_size, heads, head_dim;
+  uint8_t *k_codes;
+  float *k_scales;
+  uint8_t *v_codes;
+  float *v_scales;
+  uint32_t *status;
+} pi_kv_cache;
+
+/* Which tokens a call is about.  Sequence s has rows cu[s] .. cu[s+1]-1 of the
+ * call's packed token arrays.  Its position p lies in page
+ * page_table[s * table_stride + p / page_size].  All device int32; entries of
+ * a table row past the sequence's last page are not read.  A page outside
+ * [0, n_pages), a position past table_stride pages, a negative position or a
+ * cu that is not ascending within [0, n_tokens] is skipped and flagged in the
+ * cache's status; the accesses stay in bounds. */
+typedef struct {
+  int32_t n_seqs, n_tokens;
+  const int32_t *cu;           /* [n_seqs + 1] */
+  const int32_t *page_table;   /* [n_seqs, table_stride] */
+  int32_t table_stride;
+} pi_kv_tokens;
+
+/* Quantise new keys and values into the cache.  Row cu[s] + i of k and v goes
+ * to position start[s] + i of sequence s.
+ *   k, v   [n_tokens, heads, head_dim] of `dtype`, elements of a head contiguous;
+ *          k_stride[0] / k_stride[1] elements between tokens / heads (host int64[2])
+ *   start  device int32 [n_seqs]: tokens the sequence has in the cache already
+ * Per block and head, with amax the largest finite magnitude of the new elements:
+ *   need = the smallest power of two >= 2^PI_KV_MIN_EXP with amax <= 448 need
+ *   s    = need if the call writes the block's first token, else max(old s, need)
+ *   code = E4M3(x / s), nearest even; NaN stays NaN, +-inf becomes +-448
+ * and where s grew, the block's earlier tokens become E4M3(old value / s).
+ * With powers of two x / s is exact, so a code is x rounded once, and growing a
+ * scale changes a stored value only where its code turns subnormal. */
+pi_status pi_kv_write(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
+                      const void *k, const int64_t *k_stride, const void *v, const int64_t *v_stride,
+                      int32_t dtype, void *stream);
+
+/* Read positions start[s] .. start[s] + (cu[s+1] - cu[s]) of each sequence back
+ * as k, v [n_tokens, heads, head_dim] of `dtype`, contiguous, 16-byte aligned
+ * (either may be NULL).  Rows that cannot be read (a bad page or position) and
+ * rows of no sequence are zero; rows of a bad cu range are left as they were. */
+pi_status pi_kv_read(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
+                     void *k, void *v, int32_t dtype, void *stream);
+
+/* Attention of each sequence's newest tokens over its cached keys and values.
+ * Row cu[s] + i of q is the token at position length[s] - n_s + i, with
+ * n_s = cu[s+1] - cu[s], and sees positions 0 .. its own (causal != 0) or
+ * 0 .. length[s]-1 (causal == 0).  Query head h reads key/value head
+ * h / (q_heads / heads).
+ *   out = sum_j softmax_j(sm_scale q.k_j) v_j,  lse = log sum_j exp(sm_scale q.k_j)
+ * A row that sees nothing has out 0 and lse -inf.
+ *   q       [n_tokens, q_heads, head_dim], fp16 or bf16, q_stride as k_stride
+ *           (strides multiples of 8 elements, base 16-byte aligned)
+ *   length  device int32 [n_seqs], tokens of the sequence in the cache, the new
+ *           ones among them
+ *   max_q   host: at least the largest n_s (rows past it are left out and flagged)
+ *   out     [n_tokens, q_heads, head_dim] of q's type, contiguous, 16-byte aligned
+ *   lse     fp32 [n_tokens, q_heads] or NULL
+ *   ws      pi_kv_attention_workspace_bytes(...) bytes, 16-byte aligned scratch
+ * q_heads a multiple of heads.  Rows of no sequence are left as they were. */
+size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *cache, int32_t q_heads, int32_t n_tokens,
+                                       int32_t n_seqs);
+pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length,
+                          int32_t max_q, const void *q, const int64_t *q_stride, int32_t q_heads,
+                          int32_t dtype, float sm_scale, int32_t causal, void *out, float *lse,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/* Synchronize `stream`; PI_ERR_DEVICE_CHECK if a kernel flagged a page, position
+ * or token range of this cache since the last query (and clear the flag). */
+pi_status pi_kv_status(const pi_kv_cache *cache, void *stream);
+
+/* Layer norm over the last dimension, with an optional addition before it:
+ *   t = x, or round(x + add) when add is given (stored in `sum`)
+ *   y = (t - mean(t)) * rstd * weight + bias,  rstd = 1 / sqrt(var(t) + eps)
+ * var is the mean square about the mean.
+ *   x, y, sum      [rows, d] of `dtype`; x_stride elements between rows of x;
+ *                  y and sum contiguous; sum may be x itself (contiguous)
+ *   add            [rows, d] of add_dtype, contiguous, or NULL
+ *   weight, bias   [d] of w_dtype; either may be NULL (1, 0)
+ *   mean, rstd     fp32 [rows], or NULL
+ * 1 <= d <= PI_MAX_D; sum is required with add and refused without it. */
+pi_status pi_layer_norm(const void *x, int64_t x_stride, const void *add, int32_t add_dtype,
+                        const void *weight, const void *bias, int32_t w_dtype, int32_t rows, int32_t d,
+                        int32_t dtype, float eps, void *y, void *sum, float *mean, float *rstd, void *stream);
+
+/* Its gradient.  With h = (x - mean) rstd, g = dy weight:
+ *   dx = rstd (g - mean_j(g) - h mean_j(g h)) (+ d_sum)
+ *   dweight = sum_rows dy h,  dbias = sum_rows dy
+ *   x         what was normed (`sum` where something was added): the gradient
+ *             dx is then the gradient of both addends
+ *   dy, d_sum [rows, d] of `dtype`, contiguous; d_sum (gradient that reaches
+ *             `sum` another way) or NULL
+ *   dx        [rows, d] of `dtype`; may be dy or d_sum itself
+ *   dweight, dbias  fp32 [d], overwritten; either may be NULL
+ *   ws        pi_layer_norm_backward_workspace_bytes(rows, d) bytes, 16-byte aligned
+ * Row sums are added in a fixed order that depends on rows and d alone. */
+size_t pi_layer_norm_backward_workspace_bytes(int32_t rows, int32_t d);
+pi_status pi_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, const void *weight,
+                                 int32_t w_dtype, const float *mean, const float *rstd, const void *d_sum,
+                                 int32_t rows, int32_t d, int32_t dtype, void *dx, float *dweight, float *dbias,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/* Log-probabilities of given tokens, entropy and the most likely tokens, from
+ * logits in one call.  With p = softmax(logits[r, :]):
+ *   lse[r]     = log sum_j exp(logits[r, j])
+ *   logprob[r] = logits[r, target[r]] - lse[r]; 0 where target[r] < 0 (padding);
+ *                NaN where target[r] >= vocab
+ *   entropy[r] = -sum_j p_j log p_j  (a token of probability 0 adds 0)
+ *   top_index, top_logprob [rows, top_k]: the top_k tokens by logit descending,
+ *                equal logits by ascending index
+ *   logits  [rows, vocab] of `dtype`, row_stride elements between rows
+ *   target  device int32 [rows], or NULL (logprob is then refused)
+ * logprob, entropy and lse fp32 [rows], any of them NULL; top_index int32.
+ * 0 <= top_k <= PI_MAX_TOP_K, top_k <= vocab.  A row whose logits hold a NaN or
+ * +inf, or are all -inf, has no distribution: its entropy and log-probabilities
+ * are NaN (lse too, or -inf where all are -inf).  top_index ranks NaN first. */
+#define PI_MAX_TOP_K 64
+pi_status pi_token_logprobs(const void *logits, int64_t row_stride, int32_t dtype, int32_t rows, int32_t vocab,
+                            const int32_t *target, int32_t top_k, float *logprob, float *entropy, float *lse,
+                            int32_t *top_index, float *top_logprob, void *stream);
+
 /* Thread-local text of the last error ("" if none). */
 const char *pi_last_error(void);
 
