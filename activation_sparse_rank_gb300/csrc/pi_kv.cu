@@ -26,7 +26,7 @@ struct KvCopyParams {
   const void *src[2];     // k, v (write)
   void *dst[2];           // k, v (read)
   int64_t st[2], sh[2];   // elements between tokens / heads of src
-  int n_slots;
+  int n_slots, per_warp;  // per_warp: (head, key or value) units of a slot that one warp does
 };
 
 // Where a warp's 16 tokens are: rows row0 .. row0+n-1 of the packed arrays are
@@ -39,10 +39,14 @@ struct KvPlace {
 // n / 16 + 2 blocks, so sequence s owns the slots from cu[s] / 16 + 2 s on and
 // no prefix sum is needed.
 __device__ __forceinline__ bool kv_place(const KvCopyParams &p, int slot, KvPlace *o, bool *readable) {
-  int lo = 0, hi = p.tok.n_seqs - 1;
-  while (lo < hi) {                                   // last s with base(s) <= slot
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)p.tok.cu[mid] / PI_KV_BLOCK + 2 * (int64_t)mid <= slot) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0;                                         // last s with base(s) <= slot: 32 probes a step
+  for (int n = p.tok.n_seqs; n > 1;) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool below = lane * step < n && (int64_t)p.tok.cu[at] / PI_KV_BLOCK + 2 * (int64_t)at <= slot;
+    const int last = max(0, __popc(__ballot_sync(0xffffffffu, below)) - 1);
+    n = min(step, n - last * step);
+    lo += last * step;
   }
   const int s = lo, r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1];
   if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens) return false;      // flagged by kv_check_cu
@@ -84,21 +88,33 @@ __device__ __forceinline__ void kv_check_cu(const KvCopyParams &p) {
       atomicOr(p.c.status, pi::kKvBadRange);
 }
 
-__device__ __forceinline__ uint2 encode8(const float *v, float inv) {
+// 8 values (four pairs) times inv as E4M3 codes.
+__device__ __forceinline__ uint2 encode8(const f2 *v, f2 inv) {
   __nv_fp8x2_storage_t q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    q[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * inv, v[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  for (int e = 0; e < 4; ++e) q[e] = __nv_cvt_float2_to_fp8x2(f2_get(f2_mul(v[e], inv)), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(q[0] | (unsigned)q[1] << 16, q[2] | (unsigned)q[3] << 16);
 }
 
-__device__ __forceinline__ void decode8(float *v, uint2 c) {
+// Largest finite magnitude of 16 bytes of elements: NaN and infinities set no scale.
+template <int DT>
+__device__ __forceinline__ float amax16(const uint4 &w, float a) {
+#pragma unroll
+  for (int j = 0; j < 16 / (int)sizeof(typename Elem<DT>::T) / 2; ++j) {
+    const float2 f = f2_get(f2_from16<DT>(w, j));
+    const float x = fabsf(f.x), y = fabsf(f.y);
+    a = fmaxf(a, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+  }
+  return a;
+}
+
+__device__ __forceinline__ void decode8(f2 *v, uint2 c) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const unsigned w = e < 2 ? c.x : c.y;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(e & 1 ? w >> 16 : w & 0xffff), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
-    v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    v[e] = f2_of(f.x, f.y);
   }
 }
 
@@ -116,76 +132,77 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 template <int DT, int D, bool VEC>
 __global__ void __launch_bounds__(256) k_kv_write(const KvCopyParams p) {
   using E = Elem<DT>;
-  constexpr int VR = D / 8, NV = PI_KV_BLOCK * VR / 32;
+  constexpr int VR = D / 8, NV = PI_KV_BLOCK * VR / 32, WPV = 8 * sizeof(typename E::T) / 16;
   kv_check_cu(p);
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int h = (int)(unit % p.c.heads), kv = (int)(unit / p.c.heads % 2);
-  const int64_t slot = unit / p.c.heads / 2;
+  const int lane = threadIdx.x & 31, parts = (2 * p.c.heads + 8 * p.per_warp - 1) / (8 * p.per_warp);
   KvPlace at;
   bool ok;
-  if (slot >= p.n_slots || !kv_place(p, (int)slot, &at, &ok) || !ok) return;
-  const typename E::T *src = static_cast<const typename E::T *>(p.src[kv]) + (int64_t)at.row0 * p.st[kv] + h * p.sh[kv];
-  alignas(16) typename E::T x[NV][8];
+  if (!kv_place(p, blockIdx.x / parts, &at, &ok) || !ok) return;
+  for (int i_unit = 0, unit = blockIdx.x % parts * 8 * p.per_warp + (threadIdx.x >> 5);
+       i_unit < p.per_warp && unit < 2 * p.c.heads; ++i_unit, unit += 8) {
+    const int kv = unit >= p.c.heads, h = unit - kv * p.c.heads;
+    const typename E::T *src = static_cast<const typename E::T *>(p.src[kv]) + (int64_t)at.row0 * p.st[kv] + h * p.sh[kv];
+    uint4 x[NV][WPV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = lane + 32 * i, r = v / VR - at.off;
-    if (r >= 0 && r < at.n) {
-      const typename E::T *row = src + (int64_t)r * p.st[kv] + v % VR * 8;
-      if constexpr (VEC) {
-        constexpr int W = 16 / sizeof(typename E::T);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int c = 0; c < 8; c += W) *reinterpret_cast<Pack<DT, W> *>(&x[i][c]) = *reinterpret_cast<const Pack<DT, W> *>(row + c);
-      } else {
+      for (int c = 0; c < WPV; ++c) x[i][c] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = row[e];
-      }
-    } else {
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + 32 * i, r = v / VR - at.off;
+      if (r >= 0 && r < at.n) {
+        const typename E::T *row = src + (int64_t)r * p.st[kv] + v % VR * 8;
+        if constexpr (VEC) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = E::from(0.f);
-    }
-  }
-  float a = 0.f;
+          for (int c = 0; c < WPV; ++c) x[i][c] = reinterpret_cast<const uint4 *>(row)[c];
+        } else {
+          alignas(16) typename E::T e8[8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+          for (int e = 0; e < 8; ++e) e8[e] = row[e];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(E::to(x[i][e]));
-      a = fmaxf(a, m < INFINITY ? m : 0.f);          // NaN and infinities set no scale
-    }
-  float s = pow2(scale_exp(warp_max(a)));
-  const int64_t page_head = (int64_t)at.page * p.c.heads + h;
-  float *scale = (kv ? p.c.v_scales : p.c.k_scales) + page_head * (p.c.page_size / PI_KV_BLOCK) + at.blk;
-  uint2 *codes = reinterpret_cast<uint2 *>((kv ? p.c.v_codes : p.c.k_codes) +
-                                           (page_head * p.c.page_size + at.blk * PI_KV_BLOCK) * D);
-  if (at.off > 0) {
-    const float old = *scale;
-    if (old < s) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = lane + 32 * i;
-        if (v / VR < at.off) {
-          float f[8];
-          decode8(f, codes[v]);
-          codes[v] = encode8(f, old / s);
+          for (int c = 0; c < WPV; ++c) x[i][c] = reinterpret_cast<const uint4 *>(e8)[c];
         }
       }
-    } else if (old > s) {
-      s = old;
     }
-  }
-  const float inv = 1.0f / s;
+    float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = lane + 32 * i, r = v / VR - at.off;
-    if (r >= 0 && r < at.n) {
-      float f[8];
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = E::to(x[i][e]);
-      codes[v] = encode8(f, inv);
+      for (int c = 0; c < WPV; ++c) a = amax16<DT>(x[i][c], a);
+    float s = pow2(scale_exp(warp_max(a)));
+    const int64_t page_head = (int64_t)at.page * p.c.heads + h;
+    float *scale = (kv ? p.c.v_scales : p.c.k_scales) + page_head * (p.c.page_size / PI_KV_BLOCK) + at.blk;
+    uint2 *codes = reinterpret_cast<uint2 *>((kv ? p.c.v_codes : p.c.k_codes) +
+                                             (page_head * p.c.page_size + at.blk * PI_KV_BLOCK) * D);
+    if (at.off > 0) {
+      const float old = *scale;
+      if (old < s) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int v = lane + 32 * i;
+          if (v / VR < at.off) {
+            f2 f[4];
+            decode8(f, codes[v]);
+            codes[v] = encode8(f, f2_of(old / s, old / s));
+          }
+        }
+      } else if (old > s) {
+        s = old;
+      }
     }
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + 32 * i, r = v / VR - at.off;
+      if (r >= 0 && r < at.n) {
+        f2 f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = f2_from16<DT>(x[i][WPV == 2 ? e / 2 : 0], WPV == 2 ? e % 2 : e);
+        codes[v] = encode8(f, f2_of(inv, inv));
+      }
+    }
+    if (lane == 0) *scale = s;
   }
-  if (lane == 0) *scale = s;
 }
 
 template <int DT, int D>
@@ -204,52 +221,49 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
       if (p.dst[kv]) static_cast<uint4 *>(p.dst[kv])[at] = make_uint4(0, 0, 0, 0);
   }
   if (p.tok.n_seqs == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int h = (int)(unit % p.c.heads), kv = (int)(unit / p.c.heads % 2);
-  const int64_t slot = unit / p.c.heads / 2;
+  const int lane = threadIdx.x & 31, parts = (2 * p.c.heads + 8 * p.per_warp - 1) / (8 * p.per_warp);
   KvPlace at;
   bool ok;
-  if (slot >= p.n_slots || !p.dst[kv] || !kv_place(p, (int)slot, &at, &ok)) return;
-  const int64_t page_head = (int64_t)at.page * p.c.heads + h;
-  const uint2 *codes = reinterpret_cast<const uint2 *>((kv ? p.c.v_codes : p.c.k_codes) +
-                                                       (page_head * p.c.page_size + at.blk * PI_KV_BLOCK) * D);
-  uint2 c[NV];
-  float s = 0.f;
-  if (ok) {
-    s = ((kv ? p.c.v_scales : p.c.k_scales) + page_head * (p.c.page_size / PI_KV_BLOCK))[at.blk];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] = codes[lane + 32 * i];
-  }
-  typename E::T *dst = static_cast<typename E::T *>(p.dst[kv]);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = lane + 32 * i, r = v / VR - at.off;
-    if (r < 0 || r >= at.n) continue;
-    float f[8];
+  if (!kv_place(p, blockIdx.x / parts, &at, &ok)) return;
+  for (int i_unit = 0, unit = blockIdx.x % parts * 8 * p.per_warp + (threadIdx.x >> 5);
+       i_unit < p.per_warp && unit < 2 * p.c.heads; ++i_unit, unit += 8) {
+    const int kv = unit >= p.c.heads, h = unit - kv * p.c.heads;
+    if (!p.dst[kv]) continue;
+    const int64_t page_head = (int64_t)at.page * p.c.heads + h;
+    const uint2 *codes = reinterpret_cast<const uint2 *>((kv ? p.c.v_codes : p.c.k_codes) +
+                                                         (page_head * p.c.page_size + at.blk * PI_KV_BLOCK) * D);
+    uint2 c[NV];
+    float s = 0.f;
     if (ok) {
-      decode8(f, c[i]);
+      s = ((kv ? p.c.v_scales : p.c.k_scales) + page_head * (p.c.page_size / PI_KV_BLOCK))[at.blk];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= s;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+      for (int i = 0; i < NV; ++i) c[i] = codes[lane + 32 * i];
     }
-    typename E::T *row = dst + ((int64_t)(at.row0 + r) * p.c.heads + h) * D + v % VR * 8;
+    typename E::T *dst = static_cast<typename E::T *>(p.dst[kv]);
 #pragma unroll
-    for (int e = 0; e < 8; e += W) {
-      Pack<DT, W> o;
+    for (int i = 0; i < NV; ++i) {
+      const int v = lane + 32 * i, r = v / VR - at.off;
+      if (r < 0 || r >= at.n) continue;
+      f2 f[4] = {0, 0, 0, 0};
+      if (ok) {
+        decode8(f, c[i]);
 #pragma unroll
-      for (int k = 0; k < W; ++k) o.v[k] = E::from(f[e + k]);
-      *reinterpret_cast<Pack<DT, W> *>(row + e) = o;
+        for (int e = 0; e < 4; ++e) f[e] = f2_mul(f[e], f2_of(s, s));
+      }
+      uint4 *row = reinterpret_cast<uint4 *>(dst + ((int64_t)(at.row0 + r) * p.c.heads + h) * D + v % VR * 8);
+      row[0] = f2_to16<DT>(f);
+      if constexpr (DT == PI_DT_F32) row[1] = f2_to16<DT>(f + 2);
     }
   }
 }
 
 template <int DT, int D>
-cudaError_t launch_copy(const KvCopyParams &p, bool write, bool vec, cudaStream_t s) {
-  const int64_t units = std::max<int64_t>(1, (int64_t)p.n_slots * 2 * p.c.heads);
-  const unsigned grid = (unsigned)((units + 7) / 8);
+cudaError_t launch_copy(KvCopyParams p, bool write, bool vec, cudaStream_t s) {
+  const int units = 2 * p.c.heads;
+  // finding a block's place takes three loads one after another: with enough
+  // blocks to fill the GPU a warp uses it for several heads
+  p.per_warp = std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)p.n_slots * units / (64 * std::max(1, pi::current_sms()))));
+  const unsigned grid = (unsigned)((int64_t)std::max(1, p.n_slots) * ((units + 8 * p.per_warp - 1) / (8 * p.per_warp)));
   if (write && vec)
     k_kv_write<DT, D, true><<<grid, 256, 0, s>>>(p);
   else if (write)
@@ -317,8 +331,8 @@ pi_status check_copy(const pi_kv_cache *c, const pi_kv_tokens *t, const int32_t 
   if (!pi::dtype_ok(dtype)) return pi::fail(PI_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   if (t->n_seqs && (!start || !pi::aligned_to(start, 4)))
     return pi::fail(PI_ERR_INVALID_ARG, "start must be non-NULL and 4-byte aligned");
-  *p = KvCopyParams{*c, *t, start, {}, {}, {}, {}, t->n_tokens / PI_KV_BLOCK + 2 * t->n_seqs};
-  if ((int64_t)p->n_slots * 2 * c->heads / 8 >= (int64_t)1 << 31)
+  *p = KvCopyParams{*c, *t, start, {}, {}, {}, {}, t->n_tokens / PI_KV_BLOCK + 2 * t->n_seqs, 1};
+  if ((int64_t)(p->n_slots + 1) * (2 * c->heads / 8 + 1) >= (int64_t)1 << 31)
     return pi::fail(PI_ERR_UNSUPPORTED, "n_tokens=%d with heads=%d is too large for one call", t->n_tokens, c->heads);
   return PI_OK;
 }

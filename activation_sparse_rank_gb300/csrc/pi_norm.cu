@@ -15,35 +15,111 @@ using namespace pidev;
 
 namespace {
 
-// N consecutive elements of a tensor whose type is a run-time value, as
-// binary32.  For N > 1 the address is a multiple of 4 elements and the base
-// 16-byte aligned.
-template <int N>
-__device__ __forceinline__ void load_n(float *o, const void *p, int dt, size_t i) {
-  if constexpr (N == 1) {
-    o[0] = load_any(p, dt, i);
-  } else if (dt == PI_DT_F32) {
+// Which columns a thread has: NP pairs.  VEC: NV packs of 16 bytes (V
+// elements), pack t + i NT; pair j is half of pack j / (V / 2).  Otherwise
+// pair j is the two columns t + 2 j NT and t + (2 j + 1) NT.
+template <int X, bool VEC, int NT, int NV>
+struct Cols {
+  static constexpr int V = 16 / sizeof(typename Elem<X>::T), PP = V / 2, NP = VEC ? NV * PP : NV;
+};
+
+// Pairs of a row of another tensor (a weight, an added row) at this thread's
+// columns, of a type known at run time; `one` where absent or past the row.
+template <int V>
+__device__ __forceinline__ void load_pack(f2 *o, const void *p, int dt, int k) {
+  if (dt == PI_DT_F32) {
 #pragma unroll
-    for (int c = 0; c < N; c += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + c);
-      o[c] = f.x, o[c + 1] = f.y, o[c + 2] = f.z, o[c + 3] = f.w;
+    for (int c = 0; c < V / 4; ++c) {
+      const uint4 w = static_cast<const uint4 *>(p)[k * (V / 4) + c];
+      o[2 * c] = f2_from16<PI_DT_F32>(w, 0), o[2 * c + 1] = f2_from16<PI_DT_F32>(w, 1);
     }
-  } else if (dt == PI_DT_F16) {
+  } else {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if constexpr (V == 8) {
+      w = static_cast<const uint4 *>(p)[k];
+    } else {
+      const uint2 h = static_cast<const uint2 *>(p)[k];
+      w.x = h.x, w.y = h.y;
+    }
 #pragma unroll
-    for (int c = 0; c < N; c += 4) {
-      const Pack<PI_DT_F16, 4> f = *reinterpret_cast<const Pack<PI_DT_F16, 4> *>(static_cast<const __half *>(p) + i + c);
+    for (int j = 0; j < V / 2; ++j) o[j] = dt == PI_DT_F16 ? f2_from16<PI_DT_F16>(w, j) : f2_from16<PI_DT_BF16>(w, j);
+  }
+}
+template <int X, bool VEC, int NT, int NV>
+__device__ __forceinline__ void load_cols(f2 *o, const void *p, int dt, int t, int d, float one) {
+  using C = Cols<X, VEC, NT, NV>;
+  const f2 fill = f2_of(one, one);
+  if constexpr (VEC) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[c + e] = __half2float(f.v[e]);
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < C::PP; ++j) o[i * C::PP + j] = fill;
+      if (p && t + i * NT < d / C::V) load_pack<C::V>(o + i * C::PP, p, dt, t + i * NT);
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < N; c += 4) {
-      const Pack<PI_DT_BF16, 4> f =
-          *reinterpret_cast<const Pack<PI_DT_BF16, 4> *>(static_cast<const __nv_bfloat16 *>(p) + i + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[c + e] = __bfloat162float(f.v[e]);
+    for (int j = 0; j < C::NP; ++j) {
+      const int c0 = t + 2 * j * NT, c1 = c0 + NT;
+      o[j] = f2_of(p && c0 < d ? load_any(p, dt, c0) : one, p && c1 < d ? load_any(p, dt, c1) : one);
     }
   }
+}
+// Pairs of a row of X, 0 past its end; and their store.
+template <int X, int NT, int NP>
+__device__ __forceinline__ void load_scalar(f2 *o, const typename Elem<X>::T *row, int t, int d) {
+  typename Elem<X>::T raw[2 * NP];
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j) raw[j] = Elem<X>::from(0.f);
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j)
+    if (t + j * NT < d) raw[j] = row[t + j * NT];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) o[j] = f2_of(Elem<X>::to(raw[2 * j]), Elem<X>::to(raw[2 * j + 1]));
+}
+template <int X, bool VEC, int NT, int NV>
+__device__ __forceinline__ void store_cols(typename Elem<X>::T *row, const f2 *v, int t, int d) {
+  using C = Cols<X, VEC, NT, NV>;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (t + i * NT < d / C::V) reinterpret_cast<uint4 *>(row)[t + i * NT] = f2_to16<X>(v + i * C::PP);
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::NP; ++j) {
+      const float2 f = f2_get(v[j]);
+      const int c0 = t + 2 * j * NT, c1 = c0 + NT;
+      if (c0 < d) row[c0] = Elem<X>::from(f.x);
+      if (c1 < d) row[c1] = Elem<X>::from(f.y);
+    }
+  }
+}
+// 1 where pair j's halves are columns of the row, 0 past its end (scalar
+// columns; a pack is all in or all out).
+template <int NT>
+__device__ __forceinline__ f2 in_row(int j, int t, int d) {
+  return f2_of(t + 2 * j * NT < d ? 1.f : 0.f, t + (2 * j + 1) * NT < d ? 1.f : 0.f);
+}
+
+// A thread's 16-byte pieces of the rows that its group works on next, in
+// shared memory: it copies them there itself (cp.async) and is the only one to
+// read them, so a stage needs no barrier and no wait but its own.  The copies
+// in flight take no registers, and a row's load is hidden behind the rows
+// before it.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most n of the newest groups are in flight (n < 4).
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 struct NormParams {
@@ -53,72 +129,152 @@ struct NormParams {
   int64_t x_stride;
   int rows, d, add_dt, w_dt;
   float eps;
+  int stages, stage_bytes;   // ring of one CTA
 };
 
-// One row for each group of NT threads (NT == 32: four rows a CTA, no CTA
-// barrier); thread t of the group holds the NV packs t, t + NT, ... of V elements.
-template <int X, int V, int NT, int NV>
+// Group of NT threads (NT == 32: four a CTA, no CTA barrier) per row.
+// VEC: rows come through the ring, one after another to each group; otherwise
+// (odd widths, unaligned rows) plain loads, a group for each row.
+// WREG: weight and bias have x's type (or are absent) and stay in registers.
+template <int X, bool VEC, int NT, int NV, bool WREG>
 __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p) {
-  using P = Pack<X, V>;
   using E = Elem<X>;
-  constexpr int GROUPS = NT < 128 ? 128 / NT : 1;
-  __shared__ float red[2][32];
+  using T = typename E::T;
+  using C = Cols<X, VEC, NT, NV>;
+  constexpr int V = C::V, PP = C::PP, NP = C::NP;
+  constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float red[2][2][32];
   const int t = threadIdx.x % NT;
-  const int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT;
-  if (row >= p.rows) return;
   const int nv = p.d / V;
-  const typename E::T *x = static_cast<const typename E::T *>(p.x) + row * p.x_stride;
-  P raw[NV];
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT;
+
+  const int add_bytes = !VEC || !p.add ? 0 : V * (p.add_dt == PI_DT_F32 ? 4 : 2);   // per pack: 8, 16 or 32
+  auto x_slot = [&](int stage, int i) { return ring + (size_t)stage * p.stage_bytes + (i * CT + threadIdx.x) * 16; };
+  auto a_slot = [&](int stage, int i, int half) {
+    return ring + (size_t)stage * p.stage_bytes + NV * CT * 16 + ((i * (add_bytes > 16 ? 2 : 1) + half) * CT + threadIdx.x) * 16;
+  };
+  auto fetch = [&](int64_t row, int stage) {
+    if constexpr (VEC) {
+      if (row < p.rows) {
+        const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
+        const char *a = static_cast<const char *>(p.add) + (size_t)row * nv * add_bytes;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (t + i * NT < nv) raw[i] = reinterpret_cast<const P *>(x)[t + i * NT];
-  float v[NV][V];
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = t + i * NT < nv;
-    if (in && p.add) {
-      float a[V];
-      const size_t at = (size_t)row * p.d + (size_t)(t + i * NT) * V;
-      load_n<V>(a, p.add, p.add_dt, at);
-#pragma unroll
-      for (int e = 0; e < V; ++e) raw[i].v[e] = E::from(E::to(raw[i].v[e]) + a[e]);
-      *reinterpret_cast<P *>(static_cast<typename E::T *>(p.sum) + at) = raw[i];
+        for (int i = 0; i < NV; ++i) {
+          const int k = t + i * NT;
+          if (k >= nv) continue;
+          copy_async<16>(x_slot(stage, i), x + (size_t)k * V);
+          if (add_bytes == 8) copy_async<8>(a_slot(stage, i, 0), a + (size_t)k * 8);
+          if (add_bytes >= 16) copy_async<16>(a_slot(stage, i, 0), a + (size_t)k * add_bytes);
+          if (add_bytes == 32) copy_async<16>(a_slot(stage, i, 1), a + (size_t)k * 32 + 16);
+        }
+      }
+      copy_commit();
     }
+  };
+  for (int s = 0; s < p.stages - 1; ++s) fetch(row0 + s * step, s);
+
+  uint4 rw[WREG ? NV : 1], rb[WREG ? NV : 1];
+  if constexpr (WREG) {
+    f2 one[PP];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      v[i][e] = in ? E::to(raw[i].v[e]) : 0.f;
-      s += v[i][e];
+    for (int j = 0; j < PP; ++j) one[j] = f2_of(1.f, 1.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = t + i * NT;
+      rw[i] = f2_to16<X>(one), rb[i] = make_uint4(0, 0, 0, 0);
+      if (k < nv && p.w) rw[i] = static_cast<const uint4 *>(p.w)[k];
+      if (k < nv && p.b) rb[i] = static_cast<const uint4 *>(p.b)[k];
     }
   }
-  const float mean = cta_sum<NT>(s, red[0]) / (float)p.d;
-  float q = 0.f;
+
+  int turn = 0, at = 0, next = p.stages - 1;
+  for (int64_t row = row0; row < p.rows; row += step, turn ^= 1) {
+    f2 v[NP];
+    if constexpr (VEC) {
+      fetch(row + (p.stages - 1) * step, next);
+      copy_wait(p.stages - 1);
+      next = next + 1 == p.stages ? 0 : next + 1;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (t + i * NT < nv) w = *reinterpret_cast<const uint4 *>(x_slot(at, i));
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      v[i][e] -= mean;
-      if (t + i * NT < nv) q = fmaf(v[i][e], v[i][e], q);
+        for (int j = 0; j < PP; ++j) v[i * PP + j] = f2_from16<X>(w, j);
+      }
+    } else {
+      load_scalar<X, NT, NP>(v, static_cast<const T *>(p.x) + row * p.x_stride, t, p.d);
     }
-  const float rstd = 1.0f / sqrtf(cta_sum<NT>(q, red[1]) / (float)p.d + p.eps);
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
-  typename E::T *y = static_cast<typename E::T *>(p.y) + (size_t)row * p.d;
+    if (p.add) {
+      T *sum = static_cast<T *>(p.sum) + (size_t)row * p.d;
+      if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = t + i * NT;
-    if (k >= nv) continue;
-    float w[V], b[V];
+        for (int i = 0; i < NV; ++i) {
+          if (t + i * NT >= nv) continue;
+          f2 a[PP];
+          if (p.add_dt == PI_DT_F32) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) w[e] = 1.f, b[e] = 0.f;
-    if (p.w) load_n<V>(w, p.w, p.w_dt, (size_t)k * V);
-    if (p.b) load_n<V>(b, p.b, p.w_dt, (size_t)k * V);
-    P o;
+            for (int c = 0; c < V / 4; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(a_slot(at, i, c));
+              a[2 * c] = f2_from16<PI_DT_F32>(w, 0), a[2 * c + 1] = f2_from16<PI_DT_F32>(w, 1);
+            }
+          } else {
+            load_pack<V>(a, a_slot(at, i, 0), p.add_dt, 0);
+          }
 #pragma unroll
-    for (int e = 0; e < V; ++e) o.v[e] = E::from(fmaf(v[i][e] * rstd, w[e], b[e]));
-    reinterpret_cast<P *>(y)[k] = o;
+          for (int j = 0; j < PP; ++j) a[j] = f2_add(v[i * PP + j], a[j]);
+          const uint4 w = f2_to16<X>(a);
+          reinterpret_cast<uint4 *>(sum)[t + i * NT] = w;
+#pragma unroll
+          for (int j = 0; j < PP; ++j) v[i * PP + j] = f2_from16<X>(w, j);
+        }
+      } else {
+        f2 a[NP];
+        load_cols<X, false, NT, NV>(a, static_cast<const char *>(p.add) + (size_t)row * p.d * (p.add_dt == PI_DT_F32 ? 4 : 2),
+                                    p.add_dt, t, p.d, 0.f);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const float2 f = f2_get(f2_add(v[j], a[j]));
+          v[j] = f2_of(E::to(E::from(f.x)), E::to(E::from(f.y)));
+        }
+        store_cols<X, false, NT, NV>(sum, v, t, p.d);
+      }
+    }
+    at = at + 1 == p.stages ? 0 : at + 1;
+    f2 s = 0, q = 0;                                 // 0: two zeros
+#pragma unroll
+    for (int j = 0; j < NP; ++j) s = f2_add(s, v[j]);
+    const float mean = cta_sum<NT>(f2_sum(s), red[turn][0]) / (float)p.d;
+    const f2 minus = f2_of(-mean, -mean);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      v[j] = f2_add(v[j], minus);
+      if constexpr (VEC) {
+        if (t + j / PP * NT < nv) q = f2_fma(v[j], v[j], q);
+      } else {
+        q = f2_fma(f2_mul(v[j], in_row<NT>(j, t, p.d)), v[j], q);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(cta_sum<NT>(f2_sum(q), red[turn][1]) / (float)p.d + p.eps);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    const f2 scale = f2_of(rstd, rstd);
+    T *y = static_cast<T *>(p.y) + (size_t)row * p.d;
+    if constexpr (WREG) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        v[j] = f2_fma(f2_mul(v[j], scale), f2_from16<X>(rw[j / PP], j % PP), f2_from16<X>(rb[j / PP], j % PP));
+    } else {
+      f2 w[NP], b[NP];
+      load_cols<X, VEC, NT, NV>(w, p.w, p.w_dt, t, p.d, 1.f);
+      load_cols<X, VEC, NT, NV>(b, p.b, p.w_dt, t, p.d, 0.f);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) v[j] = f2_fma(f2_mul(v[j], scale), w[j], b[j]);
+    }
+    store_cols<X, VEC, NT, NV>(y, v, t, p.d);
   }
 }
 
@@ -126,119 +282,149 @@ struct NormGradParams {
   const void *dy, *x, *w, *dsum;
   const float *mean, *rstd;
   void *dx;
-  float *part;          // [groups, 2, d]: dweight, dbias over the rows of one CTA
+  float *part;          // [CTAs, 2, d]: dweight, dbias over the rows of one CTA
   int64_t x_stride;
   int rows, d, w_dt;
+  int stages, stage_bytes;
 };
 
 // Each group of NT threads takes the rows g, g + groups, ...; a thread keeps
 // its columns over all of them, so dweight and dbias add up in its registers.
-template <int X, int V, int NT, int NV>
+// HOLD: h and g of a row stay in registers between the passes; without it
+// (the widest rows, whose threads have 64 registers) they are formed again.
+template <int X, bool VEC, int NT, int NV>
 __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGradParams p) {
-  using P = Pack<X, V>;
   using E = Elem<X>;
-  constexpr int GROUPS = NT < 128 ? 128 / NT : 1;
+  using T = typename E::T;
+  using C = Cols<X, VEC, NT, NV>;
+  constexpr int V = C::V, PP = C::PP, NP = C::NP;
+  constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS;
+  constexpr bool HOLD = NT <= 512;
+  extern __shared__ __align__(16) char ring[];       // stages, then (GROUPS > 1) [2, d] sums
   __shared__ float red[2][2][32];
-  extern __shared__ float acc[];                     // GROUPS > 1: [2, d]
   const int t = threadIdx.x % NT, g = threadIdx.x / NT;
   const int nv = p.d / V;
   const float inv = 1.0f / (float)p.d;
-  float dw[NV][V], db[NV][V];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[i][e] = 0.f, db[i][e] = 0.f;
+  const int64_t step = (int64_t)gridDim.x * GROUPS, row0 = (int64_t)blockIdx.x * GROUPS + g;
+  const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *ds = static_cast<const T *>(p.dsum);
 
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * GROUPS + g; row < p.rows; row += (int64_t)gridDim.x * GROUPS, turn ^= 1) {
-    const typename E::T *x = static_cast<const typename E::T *>(p.x) + row * p.x_stride;
-    const typename E::T *dy = static_cast<const typename E::T *>(p.dy) + row * p.d;
-    const typename E::T *ds = static_cast<const typename E::T *>(p.dsum) + row * p.d;
-    P rx[NV], ry[NV], rs[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = t + i * NT;
-      if (k < nv) {
-        rx[i] = reinterpret_cast<const P *>(x)[k];
-        ry[i] = reinterpret_cast<const P *>(dy)[k];
-        if (p.dsum) rs[i] = reinterpret_cast<const P *>(ds)[k];
-      }
-    }
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = t + i * NT;
-      if (k >= nv) continue;
-      float w[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = 1.f;
-      if (p.w) load_n<V>(w, p.w, p.w_dt, (size_t)k * V);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float h = (E::to(rx[i].v[e]) - mean) * rstd, y = E::to(ry[i].v[e]);
-        dw[i][e] = fmaf(y, h, dw[i][e]);
-        db[i][e] += y;
-        s1 = fmaf(y, w[e], s1);
-        s2 = fmaf(y * w[e], h, s2);
-      }
-    }
-    if constexpr (NT == 32) {
-      s1 = warp_sum(s1), s2 = warp_sum(s2);
-    } else {
-      s1 = warp_sum(s1), s2 = warp_sum(s2);
-      if ((threadIdx.x & 31) == 0) red[turn][0][threadIdx.x >> 5] = s1, red[turn][1][threadIdx.x >> 5] = s2;
-      __syncthreads();
-      const int l = threadIdx.x & 31;
-      s1 = warp_sum(l < NT / 32 ? red[turn][0][l] : 0.f);
-      s2 = warp_sum(l < NT / 32 ? red[turn][1][l] : 0.f);
-    }
-    s1 *= inv, s2 *= inv;
-    typename E::T *dx = static_cast<typename E::T *>(p.dx) + row * p.d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = t + i * NT;
-      if (k >= nv) continue;
-      float w[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = 1.f;
-      if (p.w) load_n<V>(w, p.w, p.w_dt, (size_t)k * V);
-      P o;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float h = (E::to(rx[i].v[e]) - mean) * rstd;
-        float r = rstd * (E::to(ry[i].v[e]) * w[e] - s1 - h * s2);
-        if (p.dsum) r += E::to(rs[i].v[e]);
-        o.v[e] = E::from(r);
-      }
-      reinterpret_cast<P *>(dx)[k] = o;
-    }
-  }
-  if (!p.part) return;
-  float *part = p.part + (size_t)blockIdx.x * 2 * p.d;
-  if constexpr (GROUPS == 1) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = t + i * NT;
-      if (k >= nv) continue;
-#pragma unroll
-      for (int e = 0; e < V; ++e) part[k * V + e] = dw[i][e], part[p.d + k * V + e] = db[i][e];
-    }
-  } else {                                           // the CTA's groups one after another
-    for (int turn_g = 0; turn_g < GROUPS; ++turn_g) {
-      if (g == turn_g) {
+  auto slot = [&](int stage, int which, int i) {
+    return reinterpret_cast<uint4 *>(ring + (size_t)stage * p.stage_bytes + ((which * NV + i) * CT + threadIdx.x) * 16);
+  };
+  auto fetch = [&](int64_t row, int stage) {
+    if constexpr (VEC) {
+      if (row < p.rows) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int k = t + i * NT;
           if (k >= nv) continue;
+          copy_async<16>(slot(stage, 0, i), x + row * p.x_stride + (size_t)k * V);
+          copy_async<16>(slot(stage, 1, i), dy + (size_t)row * p.d + (size_t)k * V);
+          if (ds) copy_async<16>(slot(stage, 2, i), ds + (size_t)row * p.d + (size_t)k * V);
+        }
+      }
+      copy_commit();
+    }
+  };
+  for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
+
+  f2 dw[NP], db[NP], w[HOLD ? NP : 1];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            float &a = acc[k * V + e], &b = acc[p.d + k * V + e];
-            a = (turn_g ? a : 0.f) + dw[i][e];
-            b = (turn_g ? b : 0.f) + db[i][e];
+  for (int j = 0; j < NP; ++j) dw[j] = 0, db[j] = 0;
+  if constexpr (HOLD) load_cols<X, VEC, NT, NV>(w, p.w, p.w_dt, t, p.d, 1.f);
+
+  int turn = 0, at = 0;
+  for (int64_t row = row0; row < p.rows; row += step, turn ^= 1) {
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    const f2 minus = f2_of(-mean, -mean), scale = f2_of(rstd, rstd);
+    if constexpr (VEC) copy_wait(p.stages - 1);
+    // pass 1: h and g (0 past the row's end, where dy is read as 0), the column sums and the row's two sums
+    f2 h[NP], gg[NP], s1 = 0, s2 = 0;
+    auto form = [&](f2 *ho, f2 *go, bool sums) {
+      f2 xs[VEC ? 1 : NP], ys[VEC ? 1 : NP];
+      f2 wl[HOLD ? 1 : NP];
+      if constexpr (!HOLD) load_cols<X, VEC, NT, NV>(wl, p.w, p.w_dt, t, p.d, 1.f);
+      if constexpr (!VEC) {
+        load_scalar<X, NT, NP>(xs, x + row * p.x_stride, t, p.d);
+        load_scalar<X, NT, NP>(ys, dy + (size_t)row * p.d, t, p.d);
+      }
+#pragma unroll
+      for (int i = 0; i < NP / (VEC ? PP : 1); ++i) {
+        uint4 rx = make_uint4(0, 0, 0, 0), ry = make_uint4(0, 0, 0, 0);
+        if constexpr (VEC)
+          if (t + i * NT < nv) rx = *slot(at, 0, i), ry = *slot(at, 1, i);
+#pragma unroll
+        for (int c = 0; c < (VEC ? PP : 1); ++c) {
+          const int j = i * (VEC ? PP : 1) + c;
+          const f2 xv = VEC ? f2_from16<X>(rx, c) : xs[VEC ? 0 : j], yv = VEC ? f2_from16<X>(ry, c) : ys[VEC ? 0 : j];
+          ho[j] = f2_mul(f2_add(xv, minus), scale);
+          go[j] = f2_mul(yv, HOLD ? w[HOLD ? j : 0] : wl[HOLD ? 0 : j]);
+          if (sums) {
+            dw[j] = f2_fma(yv, ho[j], dw[j]);
+            db[j] = f2_add(db[j], yv);
+            s1 = f2_add(s1, go[j]);
+            s2 = f2_fma(go[j], ho[j], s2);
           }
         }
       }
+    };
+    form(h, gg, true);
+    float a = warp_sum(f2_sum(s1)), b = warp_sum(f2_sum(s2));
+    if constexpr (NT > 32) {
+      if ((threadIdx.x & 31) == 0) red[turn][0][threadIdx.x >> 5] = a, red[turn][1][threadIdx.x >> 5] = b;
+      __syncthreads();
+      const int l = threadIdx.x & 31;
+      a = warp_sum(l < NT / 32 ? red[turn][0][l] : 0.f);
+      b = warp_sum(l < NT / 32 ? red[turn][1][l] : 0.f);
+    }
+    const f2 m1 = f2_of(-a * inv, -a * inv), m2 = f2_of(-b * inv, -b * inv);
+    if constexpr (!HOLD) form(h, gg, false);
+    // pass 2: rstd (g - mean(g) - h mean(g h)) + d_sum
+#pragma unroll
+    for (int j = 0; j < NP; ++j) h[j] = f2_add(f2_fma(h[j], m2, gg[j]), m1);
+    if (ds) {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          uint4 rs = make_uint4(0, 0, 0, 0);
+          if (t + i * NT < nv) rs = *slot(at, 2, i);
+#pragma unroll
+          for (int c = 0; c < PP; ++c) h[i * PP + c] = f2_fma(h[i * PP + c], scale, f2_from16<X>(rs, c));
+        }
+      } else {
+        load_scalar<X, NT, NP>(gg, ds + (size_t)row * p.d, t, p.d);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) h[j] = f2_fma(h[j], scale, gg[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) h[j] = f2_mul(h[j], scale);
+    }
+    store_cols<X, VEC, NT, NV>(static_cast<T *>(p.dx) + (size_t)row * p.d, h, t, p.d);
+    fetch(row + p.stages * step, at);                // after the stage's last read
+    at = at + 1 == p.stages ? 0 : at + 1;
+  }
+  if (!p.part) return;
+  float *part = p.part + (size_t)blockIdx.x * 2 * p.d;
+  auto each = [&](auto put) {                        // put(column, dweight, dbias)
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c0 = VEC ? (t + j / PP * NT) * V + j % PP * 2 : t + 2 * j * NT, c1 = VEC ? c0 + 1 : c0 + NT;
+      const float2 fw = f2_get(dw[j]), fb = f2_get(db[j]);
+      if (c0 < p.d) put(c0, fw.x, fb.x);
+      if (c1 < p.d) put(c1, fw.y, fb.y);
+    }
+  };
+  if constexpr (GROUPS == 1) {
+    each([&](int c, float fw, float fb) { part[c] = fw, part[p.d + c] = fb; });
+  } else {                                           // the CTA's groups one after another
+    float *acc = reinterpret_cast<float *>(ring + (size_t)p.stages * p.stage_bytes);
+    for (int k = 0; k < GROUPS; ++k) {
+      if (g == k)
+        each([&](int c, float fw, float fb) {
+          acc[c] = (k ? acc[c] : 0.f) + fw;
+          acc[p.d + c] = (k ? acc[p.d + c] : 0.f) + fb;
+        });
       __syncthreads();
     }
     for (int j = threadIdx.x; j < 2 * p.d; j += blockDim.x) part[j] = acc[j];
@@ -267,56 +453,101 @@ __global__ void __launch_bounds__(256) k_norm_colsum(const float *__restrict__ p
   }
 }
 
-template <int X, int V, int NT, int NV>
-cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
-  constexpr int GROUPS = NT < 128 ? 128 / NT : 1;
-  k_norm<X, V, NT, NV><<<(p.rows + GROUPS - 1) / GROUPS, NT < 128 ? 128 : NT, 0, s>>>(p);
+// Stages of a ring: up to four, in what a CTA may have of an SM's 224 KB.
+int ring_stages(int stage_bytes, int ctas_per_sm) { return std::max(1, std::min(4, 224 * 1024 / ctas_per_sm / stage_bytes)); }
+
+template <typename Kern>
+cudaError_t allow_smem(Kern *k, size_t bytes) {
+  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int X, bool VEC, int NT, int NV, bool WREG>
+cudaError_t launch_norm(NormParams p, cudaStream_t s) {
+  constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS, V = Cols<X, VEC, NT, NV>::V;
+  const int per_sm = std::max(1, 1024 / CT);
+  unsigned grid = (unsigned)((p.rows + GROUPS - 1) / GROUPS);
+  p.stages = 1, p.stage_bytes = 0;
+  size_t smem = 0;
+  if (VEC) {
+    grid = std::min(grid, (unsigned)(per_sm * std::max(1, pi::current_sms())));
+    const int per_pack = 16 * (1 + (!p.add ? 0 : V * pi::dtype_size(p.add_dt) > 16 ? 2 : 1));
+    p.stage_bytes = NV * CT * per_pack;
+    p.stages = std::min(ring_stages(p.stage_bytes, per_sm), (p.rows - 1) / (int)(grid * GROUPS) + 1);
+    smem = (size_t)p.stages * p.stage_bytes;
+    const cudaError_t e = allow_smem(k_norm<X, VEC, NT, NV, WREG>, smem);
+    if (e != cudaSuccess) return e;
+  }
+  k_norm<X, VEC, NT, NV, WREG><<<grid, CT, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-// Smallest group that holds a row: C elements a thread.
-template <int X, int V, int C>
+template <int X, bool VEC, int NT, int NV>
+cudaError_t norm_by_weight(const NormParams &p, cudaStream_t s) {
+  if constexpr (VEC)
+    if (p.w_dt == X || (!p.w && !p.b)) return launch_norm<X, VEC, NT, NV, true>(p, s);
+  return launch_norm<X, VEC, NT, NV, false>(p, s);
+}
+
+// Smallest group that holds a row.
+template <int X, bool VEC, int NV>
 cudaError_t norm_by_width(const NormParams &p, cudaStream_t s) {
-  if (p.d <= 32 * C) return launch_norm<X, V, 32, C / V>(p, s);
-  if (p.d <= 128 * C) return launch_norm<X, V, 128, C / V>(p, s);
-  if (p.d <= 256 * C) return launch_norm<X, V, 256, C / V>(p, s);
-  if (p.d <= 512 * C) return launch_norm<X, V, 512, C / V>(p, s);
-  return launch_norm<X, V, 1024, C / V>(p, s);
+  constexpr int C = 2 * Cols<X, VEC, 32, NV>::NP;    // columns of a thread
+  if (p.d <= 32 * C) return norm_by_weight<X, VEC, 32, NV>(p, s);
+  if (p.d <= 128 * C) return norm_by_weight<X, VEC, 128, NV>(p, s);
+  if (p.d <= 256 * C) return norm_by_weight<X, VEC, 256, NV>(p, s);
+  if constexpr (512 * C < PI_MAX_D)
+    if (p.d > 512 * C) return norm_by_weight<X, VEC, 1024, NV>(p, s);
+  return norm_by_weight<X, VEC, 512, NV>(p, s);
 }
 
 template <int X>
 cudaError_t norm_by_type(const NormParams &p, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(typename Elem<X>::T);
-  return vec ? norm_by_width<X, V, 16>(p, s) : norm_by_width<X, 1, 16>(p, s);
+  if (!vec) return norm_by_width<X, false, 8>(p, s);
+  // few rows: latency counts, one pack a thread; many: four, so that more bytes are on their way
+  return p.rows <= 2 * pi::current_sms() && p.d <= 1024 * V ? norm_by_width<X, true, 1>(p, s) : norm_by_width<X, true, 4>(p, s);
 }
 
+// Columns of the gradient kernel up to which four warps of a CTA take a row each.
+constexpr int kGradWarpD = 256;
 // CTAs of the gradient kernel: a function of rows and d alone, because the
 // order in which dweight's rows are added follows from it.
 constexpr int kGradCtas = 304;
 int grad_ctas(int rows, int d) {
-  const int groups = d <= 512 ? 4 : 1;
+  const int groups = d <= kGradWarpD ? 4 : 1;
   return std::max(1, std::min((rows + groups - 1) / groups, kGradCtas));
 }
 
-template <int X, int V, int NT, int NV>
-cudaError_t launch_grad(const NormGradParams &p, cudaStream_t s) {
-  k_norm_grad<X, V, NT, NV><<<grad_ctas(p.rows, p.d), NT < 128 ? 128 : NT, NT < 128 ? 2 * p.d * sizeof(float) : 0, s>>>(p);
+template <int X, bool VEC, int NT, int COLS>
+cudaError_t launch_grad(NormGradParams p, cudaStream_t s) {
+  constexpr int CT = NT < 128 ? 128 : NT, NV = VEC ? COLS * (int)sizeof(typename Elem<X>::T) / 16 : COLS / 2;
+  const int grid = grad_ctas(p.rows, p.d);
+  p.stages = 0, p.stage_bytes = 0;
+  if (VEC) {
+    p.stage_bytes = (p.dsum ? 3 : 2) * NV * CT * 16;
+    p.stages = ring_stages(p.stage_bytes, NT <= 512 ? 2 : 1);
+  }
+  const size_t smem = (size_t)p.stages * p.stage_bytes + (NT < 128 ? 2 * p.d * sizeof(float) : 0);
+  const cudaError_t e = allow_smem(k_norm_grad<X, VEC, NT, NV>, smem);
+  if (e != cudaSuccess) return e;
+  k_norm_grad<X, VEC, NT, NV><<<grid, CT, smem, s>>>(p);
   return cudaGetLastError();
 }
 
-template <int X, int V, int C>
+template <int X, bool VEC>
 cudaError_t grad_by_width(const NormGradParams &p, cudaStream_t s) {
-  if (p.d <= 32 * C) return launch_grad<X, V, 32, C / V>(p, s);
-  if (p.d <= 128 * C) return launch_grad<X, V, 128, C / V>(p, s);
-  if (p.d <= 256 * C) return launch_grad<X, V, 256, C / V>(p, s);
-  if (p.d <= 512 * C) return launch_grad<X, V, 512, C / V>(p, s);
-  return launch_grad<X, V, 1024, C / V>(p, s);
+  // columns of a thread: 16 at most, two accumulators each
+  if (p.d <= kGradWarpD) return launch_grad<X, VEC, 32, 8>(p, s);
+  if (p.d <= 128 * 8) return launch_grad<X, VEC, 128, 8>(p, s);
+  if (p.d <= 128 * 16) return launch_grad<X, VEC, 128, 16>(p, s);
+  if (p.d <= 256 * 16) return launch_grad<X, VEC, 256, 16>(p, s);
+  if (p.d <= 512 * 16) return launch_grad<X, VEC, 512, 16>(p, s);
+  return launch_grad<X, VEC, 1024, 16>(p, s);
 }
 
 template <int X>
 cudaError_t grad_by_type(const NormGradParams &p, bool vec, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(typename Elem<X>::T);
-  return vec ? grad_by_width<X, V, 16>(p, s) : grad_by_width<X, 1, 16>(p, s);
+  return vec ? grad_by_width<X, true>(p, s) : grad_by_width<X, false>(p, s);
 }
 
 pi_status check_shape(int rows, int d, int dtype, int64_t x_stride) {

@@ -55,6 +55,78 @@ __device__ __forceinline__ float load_any(const void *p, int dt, size_t i) {
   return static_cast<const float *>(p)[i];
 }
 
+// Two binary32 values in one 64-bit register pair: sm_100 and later add,
+// multiply and fuse both in one instruction, each half rounded as the scalar
+// operation rounds.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(f2 a) {
+  const float2 r = f2_get(a);
+  return r.x + r.y;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// A 32-bit word of two 16-bit elements, and back (each rounded to nearest even).
+template <int DT>
+__device__ __forceinline__ f2 f2_widen(unsigned w) {
+  if constexpr (DT == PI_DT_F16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return f2_of(f.x, f.y);
+  } else {
+    return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+}
+template <int DT>
+__device__ __forceinline__ unsigned f2_narrow(f2 a) {
+  const float2 f = f2_get(a);
+  if constexpr (DT == PI_DT_F16) {
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const unsigned *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const unsigned *>(&h);
+  }
+}
+// Pair j of the 16 bytes w (8 or 4 elements), and its opposite.
+template <int DT>
+__device__ __forceinline__ f2 f2_from16(const uint4 &w, int j) {
+  if constexpr (DT == PI_DT_F32)
+    return j ? f2_of(__uint_as_float(w.z), __uint_as_float(w.w)) : f2_of(__uint_as_float(w.x), __uint_as_float(w.y));
+  else
+    return f2_widen<DT>(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w);
+}
+template <int DT>
+__device__ __forceinline__ uint4 f2_to16(const f2 *v) {
+  if constexpr (DT == PI_DT_F32) {
+    const float2 a = f2_get(v[0]), b = f2_get(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  } else {
+    return make_uint4(f2_narrow<DT>(v[0]), f2_narrow<DT>(v[1]), f2_narrow<DT>(v[2]), f2_narrow<DT>(v[3]));
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

@@ -12,7 +12,6 @@ must not be freed before it has passed, as with every torch operator.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import math
 from typing import NamedTuple, Optional
@@ -26,6 +25,7 @@ __all__ = ["KVCache", "TokenScores", "layer_norm", "layer_norm_backward", "token
            "PI_KV_MAX_PAGE", "PI_MAX_TOP_K"]
 
 _DT = {torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16, torch.float32: PI_DT_F32}
+_Stride2 = C.c_int64 * 2
 _f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
 
 
@@ -57,19 +57,39 @@ def _whole(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
+def _fits(t, shape, dtype, device) -> bool:
+    """Whether _whole would pass (the short way through)."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _run_on(device: torch.device, stream):
-    """(context that allocates on the call's device and stream, the stream's handle)."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(), torch.cuda.current_stream(device).cuda_stream
+# Calls of a decode step are short: the usual case (the current device and
+# stream) asks for the stream's handle alone, without a stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(device: torch.device, stream, fn, *args):
+    """fn(stream handle, *args) with `device` current and allocations on the call's stream."""
     if stream is None:
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+        if torch.cuda.current_device() == device.index:
+            return fn(_raw_stream(device.index), *args)
+        with torch.cuda.device(device):
+            return fn(_raw_stream(device.index), *args)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    with torch.cuda.stream(stream):
+        return fn(stream.cuda_stream, *args)
+
+
+def _ws(ws: torch.Tensor, device) -> int:
+    _dev(ws, device, "ws")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel() * ws.element_size()
 
 
 class KVCache:
@@ -116,54 +136,59 @@ class KVCache:
         self._c = pi_kv_cache(pages, page, heads, dim, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                               v_scales.data_ptr(), self._status.data_ptr())
         self._ref = C.addressof(self._c)
+        self._scale = 1.0 / math.sqrt(dim)
         if lib.pi_kv_attention_workspace_bytes(self._ref, heads, 0, 0) == 0:
             raise PiError(2, "KVCache")
 
     def _tokens(self, page_table, cu, per_seq, name, n_tokens):
         dev = self.device
         _dev(page_table, dev, "page_table")
-        if page_table.dtype != _i32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        if page_table.dtype is not _i32 or page_table.dim() != 2 or page_table.stride(1) != 1:
             raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
-        n = page_table.shape[0]
-        _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
-        _whole(per_seq, (n,), _i32, dev, name)
+        n, pages = page_table.shape
+        if not _fits(cu, (n + 1,), _i32, dev):
+            _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
+        if not _fits(per_seq, (n,), _i32, dev):
+            _whole(per_seq, (n,), _i32, dev, name)
         # a table of one row may carry any stride for it
-        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(),
-                            page_table.stride(0) if n > 1 else page_table.shape[1])
+        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(), page_table.stride(0) if n > 1 else pages)
 
     def _rows(self, t, heads, name):
         """A [tokens, heads, head_dim] tensor with contiguous heads: its token and head strides."""
         _dev(t, self.device, name)
         if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
             raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(t.shape)}")
-        if t.stride(2) != 1:
+        st, sh, sd = t.stride()
+        if sd != 1:
             raise ValueError(f"{name}: the elements of a head must be contiguous")
-        return (C.c_int64 * 2)(t.stride(0), t.stride(1))
+        return _Stride2(st, sh)
 
     def write(self, k, v, page_table, cu_tokens, start, stream=None):
         """Quantise new tokens into the cache: row cu_tokens[s] + i of k and v
         [tokens, heads, head_dim] becomes position start[s] + i of sequence s."""
         ks, vs = self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v")
-        if v.shape != k.shape or v.dtype != k.dtype:
+        if v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must have one shape and type")
         tok = self._tokens(page_table, cu_tokens, start, "start", k.shape[0])
-        ctx, handle = _run_on(self.device, stream)
-        with ctx:
-            _check(lib.pi_kv_write(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs,
-                                   _dt(k, "k"), handle), "pi_kv_write")
+        _on(self.device, stream, self._write, tok, start, k, ks, v, vs, _dt(k, "k"))
+
+    def _write(self, handle, tok, start, k, ks, v, vs, dt):
+        _check(lib.pi_kv_write(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, dt,
+                               handle), "pi_kv_write")
 
     def read(self, page_table, cu_tokens, start, n_tokens, dtype=torch.float16, k=None, v=None, stream=None):
         """Positions start[s] .. of each sequence as (k, v) [n_tokens, heads, head_dim] of `dtype`."""
         if dtype not in _DT:
             raise TypeError(f"dtype must be float16, bfloat16 or float32, not {dtype}")
-        shape = (n_tokens, self.heads, self.head_dim)
         tok = self._tokens(page_table, cu_tokens, start, "start", n_tokens)
-        ctx, handle = _run_on(self.device, stream)
-        with ctx:
-            k = torch.empty(shape, dtype=dtype, device=self.device) if k is None else _whole(k, shape, dtype, self.device, "k")
-            v = torch.empty(shape, dtype=dtype, device=self.device) if v is None else _whole(v, shape, dtype, self.device, "v")
-            _check(lib.pi_kv_read(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype],
-                                  handle), "pi_kv_read")
+        return _on(self.device, stream, self._read, tok, start, dtype, k, v)
+
+    def _read(self, handle, tok, start, dtype, k, v):
+        shape = (tok.n_tokens, self.heads, self.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=self.device) if k is None else _whole(k, shape, dtype, self.device, "k")
+        v = torch.empty(shape, dtype=dtype, device=self.device) if v is None else _whole(v, shape, dtype, self.device, "v")
+        _check(lib.pi_kv_read(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype],
+                              handle), "pi_kv_read")
         return k, v
 
     def attention_workspace(self, q_heads: int, n_tokens: int, n_seqs: int) -> torch.Tensor:
@@ -179,33 +204,34 @@ class KVCache:
         (float16 or bfloat16) over its cache.  length[s] counts the tokens in the
         cache, the new ones among them; max_q bounds the new tokens of any
         sequence.  Returns out, or (out, lse) with want_lse or an lse tensor."""
-        tokens, heads = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+        heads = q.shape[1] if q.dim() == 3 else 0
         qs = self._rows(q, heads, "q")
-        if q.dtype != torch.float16 and q.dtype != torch.bfloat16:
+        if q.dtype is not torch.float16 and q.dtype is not torch.bfloat16:
             raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
-        tok = self._tokens(page_table, cu_tokens, length, "length", tokens)
-        ctx, handle = _run_on(self.device, stream)
-        with ctx:
-            shape = (tokens, heads, self.head_dim)
-            out = torch.empty(shape, dtype=q.dtype, device=self.device) if out is None else _whole(
-                out, shape, q.dtype, self.device, "out")
-            if lse is not None:
-                _whole(lse, (tokens, heads), _f32, self.device, "lse")
-            elif want_lse:
-                lse = torch.empty((tokens, heads), dtype=_f32, device=self.device)
-            if ws is None:
-                ws = self.attention_workspace(heads, tokens, tok.n_seqs)
-            _check(lib.pi_kv_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, q.data_ptr(), qs, heads,
-                                       _DT[q.dtype], 1.0 / math.sqrt(self.head_dim) if sm_scale is None else sm_scale,
-                                       1 if causal else 0, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), handle),
-                   "pi_kv_attention")
+        tok = self._tokens(page_table, cu_tokens, length, "length", q.shape[0])
+        scale = self._scale if sm_scale is None else sm_scale
+        return _on(self.device, stream, self._attention, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
+
+    def _attention(self, handle, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws):
+        dev, shape = self.device, q.shape
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        elif not _fits(out, shape, q.dtype, dev):
+            _whole(out, shape, q.dtype, dev, "out")
+        if lse is not None:
+            _whole(lse, shape[:2], _f32, dev, "lse")
+        elif want_lse:
+            lse = torch.empty(shape[:2], dtype=_f32, device=dev)
+        if ws is None:
+            ws = self.attention_workspace(shape[1], tok.n_tokens, tok.n_seqs)
+        _check(lib.pi_kv_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, q.data_ptr(), qs, shape[1],
+                                   _DT[q.dtype], scale, 1 if causal else 0, out.data_ptr(), _ptr(lse), ws.data_ptr(),
+                                   _ws(ws, dev), handle), "pi_kv_attention")
         return out if lse is None else (out, lse)
 
     def device_status(self, stream=None) -> int:
         """0 if no call met a bad page, position or token range since the last query, else the status code."""
-        ctx, handle = _run_on(self.device, stream)
-        with ctx:
-            return int(lib.pi_kv_status(self._ref, handle))
+        return _on(self.device, stream, lambda handle: int(lib.pi_kv_status(self._ref, handle)))
 
 
 def _rows2d(x, name):
@@ -228,30 +254,47 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, y=None, sum=None, 
     dt = _dt(x, "x")
     rows, d, stride = _rows2d(x, "x")
     w_dt = 0
-    for t, n in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _whole(t, (d,), t.dtype, dev, n)
-            w_dt = _dt(t, n)
+    if weight is not None:
+        w_dt = _dt(weight, "weight")
+        if not _fits(weight, (d,), weight.dtype, dev):
+            _whole(weight, (d,), weight.dtype, dev, "weight")
+    if bias is not None:
+        w_dt = _dt(bias, "bias")
+        if not _fits(bias, (d,), bias.dtype, dev):
+            _whole(bias, (d,), bias.dtype, dev, "bias")
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must have one type")
     if add is not None:
-        _whole(add, x.shape, add.dtype, dev, "add")
+        if not _fits(add, x.shape, add.dtype, dev):
+            _whole(add, x.shape, add.dtype, dev, "add")
     elif sum is not None:
         raise ValueError("sum needs add")
-    ctx, handle = _run_on(dev, stream)
-    with ctx:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _whole(y, x.shape, x.dtype, dev, "y")
-        if add is not None:
-            sum = torch.empty(x.shape, dtype=x.dtype, device=dev) if sum is None else _whole(sum, x.shape, x.dtype, dev, "sum")
-        if want_stats:
-            mean = torch.empty(rows, dtype=_f32, device=dev) if mean is None else mean
-            rstd = torch.empty(rows, dtype=_f32, device=dev) if rstd is None else rstd
-        for t, n in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None:
-                _whole(t, (rows,), _f32, dev, n)
-        _check(lib.pi_layer_norm(x.data_ptr(), stride, _ptr(add), 0 if add is None else _dt(add, "add"), _ptr(weight),
-                                 _ptr(bias), w_dt, rows, d, dt, eps, y.data_ptr(), _ptr(sum), _ptr(mean), _ptr(rstd),
-                                 handle), "pi_layer_norm")
+    return _on(dev, stream, _norm, x, rows, d, stride, dt, weight, bias, w_dt, eps, add, y, sum, mean, rstd, want_stats)
+
+
+def _norm(handle, x, rows, d, stride, dt, weight, bias, w_dt, eps, add, y, sum, mean, rstd, want_stats):
+    dev, shape = x.device, x.shape
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif not _fits(y, shape, x.dtype, dev):
+        _whole(y, shape, x.dtype, dev, "y")
+    if add is None:
+        pass
+    elif sum is None:
+        sum = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif not _fits(sum, shape, x.dtype, dev):
+        _whole(sum, shape, x.dtype, dev, "sum")
+    if mean is not None:
+        _whole(mean, (rows,), _f32, dev, "mean")
+    elif want_stats:
+        mean = torch.empty(rows, dtype=_f32, device=dev)
+    if rstd is not None:
+        _whole(rstd, (rows,), _f32, dev, "rstd")
+    elif want_stats:
+        rstd = torch.empty(rows, dtype=_f32, device=dev)
+    _check(lib.pi_layer_norm(x.data_ptr(), stride, _ptr(add), 0 if add is None else _dt(add, "add"), _ptr(weight),
+                             _ptr(bias), w_dt, rows, d, dt, eps, y.data_ptr(), _ptr(sum), _ptr(mean), _ptr(rstd),
+                             handle), "pi_layer_norm")
     return y, sum, mean, rstd
 
 
@@ -264,29 +307,34 @@ def layer_norm_backward(dy, x, weight, mean, rstd, d_sum=None, dx=None, dweight=
     dev = _dev(x, None, "x")
     dt = _dt(x, "x")
     rows, d, stride = _rows2d(x, "x")
-    _whole(dy, x.shape, x.dtype, dev, "dy")
+    for t, shape, dtype, name in ((dy, x.shape, x.dtype, "dy"), (mean, (rows,), _f32, "mean"), (rstd, (rows,), _f32, "rstd")):
+        if not _fits(t, shape, dtype, dev):
+            _whole(t, shape, dtype, dev, name)
     if d_sum is not None:
         _whole(d_sum, x.shape, x.dtype, dev, "d_sum")
     if weight is not None:
         _whole(weight, (d,), weight.dtype, dev, "weight")
-    _whole(mean, (rows,), _f32, dev, "mean")
-    _whole(rstd, (rows,), _f32, dev, "rstd")
-    ctx, handle = _run_on(dev, stream)
-    with ctx:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else _whole(dx, x.shape, x.dtype, dev, "dx")
-        if want_weight_grad:
-            dweight = torch.empty(d, dtype=_f32, device=dev) if dweight is None else dweight
-            dbias = torch.empty(d, dtype=_f32, device=dev) if dbias is None else dbias
-        for t, n in ((dweight, "dweight"), (dbias, "dbias")):
-            if t is not None:
-                _whole(t, (d,), _f32, dev, n)
-        if ws is None and (dweight is not None or dbias is not None):
-            ws = torch.empty(lib.pi_layer_norm_backward_workspace_bytes(rows, d), dtype=_u8, device=dev)
-        _check(lib.pi_layer_norm_backward(dy.data_ptr(), x.data_ptr(), stride, _ptr(weight),
-                                          0 if weight is None else _dt(weight, "weight"), mean.data_ptr(),
-                                          rstd.data_ptr(), _ptr(d_sum), rows, d, dt, dx.data_ptr(), _ptr(dweight),
-                                          _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), handle),
-               "pi_layer_norm_backward")
+    return _on(dev, stream, _norm_backward, dy, x, rows, d, stride, dt, weight, mean, rstd, d_sum, dx, dweight, dbias, ws,
+               want_weight_grad)
+
+
+def _norm_backward(handle, dy, x, rows, d, stride, dt, weight, mean, rstd, d_sum, dx, dweight, dbias, ws, want):
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else _whole(dx, x.shape, x.dtype, dev, "dx")
+    if dweight is not None:
+        _whole(dweight, (d,), _f32, dev, "dweight")
+    elif want:
+        dweight = torch.empty(d, dtype=_f32, device=dev)
+    if dbias is not None:
+        _whole(dbias, (d,), _f32, dev, "dbias")
+    elif want:
+        dbias = torch.empty(d, dtype=_f32, device=dev)
+    if ws is None and (dweight is not None or dbias is not None):
+        ws = torch.empty(lib.pi_layer_norm_backward_workspace_bytes(rows, d), dtype=_u8, device=dev)
+    _check(lib.pi_layer_norm_backward(dy.data_ptr(), x.data_ptr(), stride, _ptr(weight),
+                                      0 if weight is None else _dt(weight, "weight"), mean.data_ptr(), rstd.data_ptr(),
+                                      _ptr(d_sum), rows, d, dt, dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(ws),
+                                      0 if ws is None else _ws(ws, dev), handle), "pi_layer_norm_backward")
     return dx, dweight, dbias
 
 
@@ -308,18 +356,21 @@ def token_logprobs(logits, targets=None, top_k=0, stream=None) -> TokenScores:
     if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
         raise ValueError("logits must be [rows, vocab] with contiguous rows")
     rows, vocab = logits.shape
-    if targets is not None:
+    if targets is not None and not _fits(targets, (rows,), _i32, dev):
         _whole(targets, (rows,), _i32, dev, "targets")
-    ctx, handle = _run_on(dev, stream)
-    with ctx:
-        entropy = torch.empty(rows, dtype=_f32, device=dev)
-        lse = torch.empty(rows, dtype=_f32, device=dev)
-        logprob = None if targets is None else torch.empty(rows, dtype=_f32, device=dev)
-        index = value = None
-        if top_k > 0:
-            index = torch.empty((rows, top_k), dtype=_i32, device=dev)
-            value = torch.empty((rows, top_k), dtype=_f32, device=dev)
-        _check(lib.pi_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
-                                     _ptr(targets), top_k, _ptr(logprob), entropy.data_ptr(), lse.data_ptr(),
-                                     _ptr(index), _ptr(value), handle), "pi_token_logprobs")
+    return _on(dev, stream, _score, logits, rows, vocab, dt, targets, top_k)
+
+
+def _score(handle, logits, rows, vocab, dt, targets, top_k):
+    dev = logits.device
+    entropy = torch.empty(rows, dtype=_f32, device=dev)
+    lse = torch.empty(rows, dtype=_f32, device=dev)
+    logprob = None if targets is None else torch.empty(rows, dtype=_f32, device=dev)
+    index = value = None
+    if top_k > 0:
+        index = torch.empty((rows, top_k), dtype=_i32, device=dev)
+        value = torch.empty((rows, top_k), dtype=_f32, device=dev)
+    _check(lib.pi_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
+                                 _ptr(targets), top_k, _ptr(logprob), entropy.data_ptr(), lse.data_ptr(), _ptr(index),
+                                 _ptr(value), handle), "pi_token_logprobs")
     return TokenScores(logprob, entropy, lse, index, value)
