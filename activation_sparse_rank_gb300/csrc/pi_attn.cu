@@ -143,20 +143,96 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *tot
 __device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
 __device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(char *dst, const void *src) {
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+
+// A block (16 tokens) in the ring: for each lane (g = lane / 4, q = lane % 4)
+//   K rows g and 8 + g, the codes that are its share of the k-steps,
+//   V rows 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q, the codes that are its columns,
+//   the block's two scales,
+// each piece as [32 lanes][piece].  A warp's copy of one piece covers whole
+// contiguous stretches of rows.
 template <int D>
-struct KvRegs {
-  uint4 k[D / 32];        // K: tokens g and 8 + g, D / 4 codes each
-  unsigned v[4][D / 32];  // V: tokens 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q, D / 8 codes each
-  float ks, vs;
+struct Frag {
+  static constexpr int KP = D / 64, V16 = D / 128;                 // 16-byte pieces of a row
+  static constexpr bool REST = D % 64 != 0;                        // 96: 8 more bytes of K, 4 of V
+  static constexpr int K_ROW = 512 * KP + (REST ? 256 : 0);
+  static constexpr int V_ROW = V16 ? 512 * V16 : 256 + (REST ? 128 : 0);
+  static constexpr int V_AT = 2 * K_ROW, S_AT = V_AT + 4 * V_ROW, BYTES = S_AT + 256;
+  static_assert(S_AT == 32 * D);
+  // dims of k-step k (two k indices, and the two 8 further): 4 from here on
+  static __device__ __forceinline__ int kdim(int k, int q) {
+    return REST && k >= 4 * KP ? 64 * KP + q * 8 + (k - 4 * KP) * 4 : k / 4 * 64 + q * 16 + k % 4 * 4;
+  }
+  // dim of column c of n-tile j; 4 tiles in a row are 4 dims in a row
+  static __device__ __forceinline__ int vdim(int j, int c) {
+    if constexpr (V16) return j / 16 * 128 + c * 16 + j % 16;
+    return j < 8 ? c * 8 + j : 64 + c * 4 + j - 8;
+  }
+  static __device__ __forceinline__ void copy(char *dst, const uint8_t *kb, const uint8_t *vb, const float *ks,
+                                              const float *vs, int lane) {
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t *row = kb + (8 * j + g) * D;
+#pragma unroll
+      for (int i = 0; i < KP; ++i) copy_async<16>(dst + j * K_ROW + 512 * i + lane * 16, row + 64 * i + q * 16);
+      if constexpr (REST) copy_async<8>(dst + j * K_ROW + 512 * KP + lane * 8, row + 64 * KP + q * 8);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t *row = vb + (2 * q + (r & 1) + 8 * (r >> 1)) * D;
+      char *d = dst + V_AT + r * V_ROW;
+      if constexpr (V16) {
+#pragma unroll
+        for (int i = 0; i < V16; ++i) copy_async<16>(d + 512 * i + lane * 16, row + 128 * i + g * 16);
+      } else {
+        copy_async<8>(d + lane * 8, row + g * 8);
+        if constexpr (REST) copy_async<4>(d + 256 + lane * 4, row + 64 + g * 4);
+      }
+    }
+    copy_async<4>(dst + S_AT + lane * 4, ks);
+    copy_async<4>(dst + S_AT + 128 + lane * 4, vs);
+  }
+  static __device__ __forceinline__ void load_k(unsigned *w, const char *src, int j, int lane) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = *reinterpret_cast<const uint4 *>(src + j * K_ROW + 512 * i + lane * 16);
+    if constexpr (REST) *reinterpret_cast<uint2 *>(w + 4 * KP) = *reinterpret_cast<const uint2 *>(src + j * K_ROW + 512 * KP + lane * 8);
+  }
+  static __device__ __forceinline__ void load_v(unsigned *w, const char *src, int r, int lane) {
+    const char *d = src + V_AT + r * V_ROW;
+    if constexpr (V16) {
+#pragma unroll
+      for (int i = 0; i < V16; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = *reinterpret_cast<const uint4 *>(d + 512 * i + lane * 16);
+    } else {
+      *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(d + lane * 8);
+      if constexpr (REST) w[2] = *reinterpret_cast<const unsigned *>(d + 256 + lane * 4);
+    }
+  }
 };
+
+// Ring stages of a CTA (a stage: a tile's four blocks), two CTAs an SM.
+template <int D>
+constexpr int attn_stages() {
+  const int n = 108 * 1024 / (4 * Frag<D>::BYTES);
+  return n < 8 ? n : 8;
+}
 
 // WARPS_M == 1: 16 rows, the four warps take a tile's four blocks.
 // WARPS_M == 4: 64 rows, 16 a warp; every warp goes over all four blocks.
 template <int DT, int D, int WARPS_M>
 __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
   using E = Elem<DT>;
-  constexpr int ROWS = 16 * WARPS_M, KS = D / 16, NT = D / 8, CH = D / 4;
-  extern __shared__ float sm[];                    // WARPS_M == 1: [4][16][D] sums, [4][16][3] (m, l, R)
+  constexpr int ROWS = 16 * WARPS_M, KS = D / 16, NT = D / 8, STAGES = attn_stages<D>();
+  using F = Frag<D>;
+  extern __shared__ __align__(16) char ring[];     // stages; then, WARPS_M == 1, a unit's [4][16][D] sums, [4][16][3] (m, l, R)
+  float *sm = reinterpret_cast<float *>(ring);
   __shared__ int64_t scan[4];
   __shared__ int64_t found[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
@@ -210,25 +286,26 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
       // a padding row masks what every row masks
       lim[e] = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
-      alignas(16) typename E::T x[CH];
-      const typename E::T *src = static_cast<const typename E::T *>(p.q) + (int64_t)(sq.row0 + i) * p.qt + hq * p.qh + q4 * CH;
+      f2 x[KS][2];                                 // this lane's four dims of each k-step
+      const typename E::T *src = static_cast<const typename E::T *>(p.q) + (int64_t)(sq.row0 + i) * p.qt + hq * p.qh;
 #pragma unroll
-      for (int c = 0; c < CH; c += 8)
-        if (in) {
-          *reinterpret_cast<uint4 *>(&x[c]) = *reinterpret_cast<const uint4 *>(src + c);
-        } else {
-          *reinterpret_cast<uint4 *>(&x[c]) = make_uint4(0, 0, 0, 0);
-        }
+      for (int k = 0; k < KS; ++k) {
+        uint2 w = make_uint2(0, 0);
+        if (in) w = *reinterpret_cast<const uint2 *>(src + F::kdim(k, q4));
+        x[k][0] = f2_widen<DT>(w.x), x[k][1] = f2_widen<DT>(w.y);
+      }
       float up = 1.f;
       fac[e] = p.scale;
       if constexpr (DT == PI_DT_BF16) {
         // the row's largest finite magnitude to [2^13, 2^14): exact, and fp16 then loses only what is 2^-27 of it
         float mx = 0.f;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const float v = fabsf(E::to(x[c]));
-          mx = fmaxf(mx, v < INFINITY ? v : 0.f);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float2 f = f2_get(x[k][c]);
+            mx = fmaxf(mx, fmaxf(fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f));
+          }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int ex = max((int)(__float_as_uint(mx) >> 23), 27) - 127 - 13;    // up = 2^-ex stays normal
@@ -236,8 +313,8 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       }
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        a[k][e] = pack_half2(E::to(x[4 * k]) * up, E::to(x[4 * k + 1]) * up);
-        a[k][2 + e] = pack_half2(E::to(x[4 * k + 2]) * up, E::to(x[4 * k + 3]) * up);
+        a[k][e] = f2_narrow<PI_DT_F16>(f2_mul(x[k][0], f2_of(up, up)));
+        a[k][2 + e] = f2_narrow<PI_DT_F16>(f2_mul(x[k][1], f2_of(up, up)));
       }
     }
     int min_lim = min(lim[0], lim[1]);             // below it no row of the warp masks anything
@@ -248,29 +325,59 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
+    // ---- the ring: tile t's block `warp` is this warp's to copy ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
-    const int step = WARPS_M == 1 ? kTile : 16;
-    for (int k0 = t0 * kTile + (WARPS_M == 1 ? warp * 16 : 0); k0 < min(keys, t1 * kTile); k0 += step) {
-      const int pg = k0 / p.c.page_size, page = table[pg];
-      if (page < 0 || page >= p.c.n_pages) {
-        if (lane == 0) atomicOr(p.c.status, pi::kKvBadPage);
-        continue;
+    auto page_of = [&](int t) {
+      const int k0 = t * kTile + warp * 16;
+      return t < t1 && k0 < keys ? table[k0 / p.c.page_size] : 0;
+    };
+    auto fetch = [&](int t, int page, int stage) {
+      const int k0 = t * kTile + warp * 16;
+      if (t < t1 && k0 < keys) {
+        char *dst = ring + (stage * 4 + warp) * F::BYTES;
+        if (page < 0 || page >= p.c.n_pages) {     // a negative scale: no block here
+          if (lane == 0) atomicOr(p.c.status, pi::kKvBadPage);
+          *reinterpret_cast<float *>(dst + F::S_AT + lane * 4) = -1.f;
+        } else {
+          const int in_page = k0 % p.c.page_size;
+          const int64_t ph = (int64_t)page * p.c.heads + h;
+          const int64_t sc = ph * (p.c.page_size / PI_KV_BLOCK) + in_page / PI_KV_BLOCK;
+          const int64_t at = (ph * p.c.page_size + in_page) * D;
+          F::copy(dst, p.c.k_codes + at, p.c.v_codes + at, p.c.k_scales + sc, p.c.v_scales + sc, lane);
+        }
       }
-      const int in_page = k0 - pg * p.c.page_size;
-      const int64_t ph = (int64_t)page * p.c.heads + h;
-      const int64_t sc = ph * (p.c.page_size / PI_KV_BLOCK) + in_page / PI_KV_BLOCK;
-      const uint8_t *kb = p.c.k_codes + (ph * p.c.page_size + in_page) * D;
-      const uint8_t *vb = p.c.v_codes + (ph * p.c.page_size + in_page) * D;
-      const float ks = p.c.k_scales[sc], vs = p.c.v_scales[sc];
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (WARPS_M == 1) __syncthreads();   // the last unit's sums, in the same memory, have been read
+    int pages[STAGES];
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) pages[i] = page_of(t0 + i);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(t0 + i, pages[i], i);
+    int page = pages[STAGES - 1], stage = 0;
+
+    for (int t = t0; t < t1; ++t) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      if constexpr (WARPS_M > 1) __syncthreads();  // every warp's block is there, and the stage before is free
+      fetch(t + STAGES - 1, page, stage == 0 ? STAGES - 1 : stage - 1);
+      page = page_of(t + STAGES);
+      const char *tile = ring + stage * 4 * F::BYTES;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+#pragma unroll 1
+    for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
+      const int k0 = t * kTile + blk * 16;
+      const char *src = tile + blk * F::BYTES;
+      if (k0 >= keys) break;
+      const float ks = *reinterpret_cast<const float *>(src + F::S_AT + lane * 4);
+      const float vs = *reinterpret_cast<const float *>(src + F::S_AT + 128 + lane * 4);
+      if (ks < 0.f) continue;
       // ---- x = q.k ----
       float x[2][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-        unsigned w[CH / 4];
-#pragma unroll
-        for (int c = 0; c < CH / 8; ++c)
-          *reinterpret_cast<uint2 *>(&w[2 * c]) = *reinterpret_cast<const uint2 *>(kb + (8 * j + g) * D + q4 * CH + 8 * c);
+        unsigned w[KS];
+        F::load_k(w, src, j, lane);
 #pragma unroll
         for (int k = 0; k < KS; ++k) mma16816(x[j], a[k], cvt_lo(w[k]), cvt_hi(w[k]));
       }
@@ -330,14 +437,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int tk = 2 * q4 + (r & 1) + 8 * (r >> 1);
-        const uint8_t *row = vb + tk * D + g * (D / 8);
-        if constexpr (D % 64 == 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; c += 2) *reinterpret_cast<uint2 *>(&v[r][c]) = *reinterpret_cast<const uint2 *>(row + 4 * c);
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) v[r][c] = *reinterpret_cast<const unsigned *>(row + 4 * c);
-        }
+        F::load_v(v[r], src, r, lane);
         if (k0 + tk >= sq.len) {                   // past the sequence: whatever the page held before
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) v[r][c] = 0;
@@ -392,6 +492,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         mma16816(acc[4 * c + 3], pa, cvt_hi(b0), cvt_hi(b1));
       }
     }
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -403,17 +504,18 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
     float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
     if constexpr (WARPS_M == 1) {
       float *st = sm + 4 * 16 * D;
-      __syncthreads();                             // the last unit's sums have been read
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();                             // every warp is done with the ring
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = g + 8 * r;
         if (q4 == 0) st[(warp * 16 + row) * 3] = m[r], st[(warp * 16 + row) * 3 + 1] = l[r], st[(warp * 16 + row) * 3 + 2] = R[r];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float *o = sm + (warp * 16 + row) * D + (2 * q4 + e) * NT;
+          float *o = sm + (warp * 16 + row) * D;
 #pragma unroll
           for (int j = 0; j < NT; j += 4)
-            *reinterpret_cast<float4 *>(o + j) = make_float4(acc[j][2 * r + e], acc[j + 1][2 * r + e], acc[j + 2][2 * r + e], acc[j + 3][2 * r + e]);
+            *reinterpret_cast<float4 *>(o + F::vdim(j, 2 * q4 + e)) = make_float4(acc[j][2 * r + e], acc[j + 1][2 * r + e], acc[j + 2][2 * r + e], acc[j + 3][2 * r + e]);
         }
       }
       __syncthreads();
@@ -447,6 +549,8 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         }
       }
     } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = warp * 16 + g + 8 * r, gr = rt * ROWS + row;
@@ -456,16 +560,16 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int d = (2 * q4 + e) * NT;
 #pragma unroll
           for (int j = 0; j < NT; j += 4) {
+            const int d = F::vdim(j, 2 * q4 + e);
             const float4 o = make_float4(acc[j][2 * r + e] * c, acc[j + 1][2 * r + e] * c, acc[j + 2][2 * r + e] * c, acc[j + 3][2 * r + e] * c);
             if (whole) {
               Pack<DT, 4> y;
               y.v[0] = E::from(o.x), y.v[1] = E::from(o.y), y.v[2] = E::from(o.z), y.v[3] = E::from(o.w);
-              *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d + j) = y;
+              *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
             } else {
-              *reinterpret_cast<float4 *>(part + row * D + d + j) = o;
+              *reinterpret_cast<float4 *>(part + row * D + d) = o;
             }
           }
         }
@@ -563,13 +667,12 @@ int attn_warps_m(int64_t max_rows) { return max_rows <= 16 ? 1 : 4; }
 
 template <int DT, int D, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
-  const size_t smem = WARPS_M == 1 ? sizeof(float) * (4 * 16 * D + 4 * 16 * 3) : 0;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  constexpr int kRing = attn_stages<D>() * 4 * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * 16 * (D + 3) * 4 : 0;
+  constexpr int smem = kRing > kSums ? kRing : kSums;
+  cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   k_attn<DT, D, WARPS_M><<<p.grid, 128, smem, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   k_attn_combine<DT, D, WARPS_M><<<(unsigned)p.tok.n_seqs * p.c.heads, 128, 0, s>>>(p);
   return cudaGetLastError();
