@@ -64,14 +64,9 @@ __device__ __forceinline__ void mma16816(float *c, const unsigned *a, unsigned b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The low / high two codes of a word as an fp16 pair.
-__device__ __forceinline__ unsigned cvt_lo(unsigned w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  return h.x | (unsigned)h.y << 16;
-}
-__device__ __forceinline__ unsigned cvt_hi(unsigned w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  return h.x | (unsigned)h.y << 16;
+// Four codes as two fp16 pairs: one instruction each.
+__device__ __forceinline__ void widen4(unsigned w, unsigned &lo, unsigned &hi) {
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
 __device__ __forceinline__ unsigned pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -236,6 +231,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
   __shared__ int64_t scan[4];
   __shared__ int64_t found[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  griddep_launch();                                // every CTA of this grid is resident: the next one may take what is left
   for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
 
   // Where this CTA's share of the line of tiles begins.
@@ -327,40 +323,41 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
 
     // ---- the ring: tile t's block `warp` is this warp's to copy ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
-    auto page_of = [&](int t) {
-      const int k0 = t * kTile + warp * 16;
-      return t < t1 && k0 < keys ? table[k0 / p.c.page_size] : 0;
-    };
-    auto fetch = [&](int t, int page, int stage) {
-      const int k0 = t * kTile + warp * 16;
-      if (t < t1 && k0 < keys) {
+    // where the next copy is: its first key, its page's place in the table, its offset in the page
+    int ck = t0 * kTile + warp * 16, cp = ck / p.c.page_size, co = ck - cp * p.c.page_size;
+    const int copies = min(keys, t1 * kTile);
+    const int64_t page_codes = (int64_t)p.c.heads * p.c.page_size * D, page_scales = (int64_t)p.c.heads * (p.c.page_size / PI_KV_BLOCK);
+    const uint8_t *k_head = p.c.k_codes + (int64_t)h * p.c.page_size * D, *v_head = p.c.v_codes + (int64_t)h * p.c.page_size * D;
+    const float *ks_head = p.c.k_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK), *vs_head = p.c.v_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK);
+    auto fetch = [&](int stage, int page) {        // page: table[cp], read ahead of time
+      if (ck < copies) {
         char *dst = ring + (stage * 4 + warp) * F::BYTES;
         if (page < 0 || page >= p.c.n_pages) {     // a negative scale: no block here
           if (lane == 0) atomicOr(p.c.status, pi::kKvBadPage);
           *reinterpret_cast<float *>(dst + F::S_AT + lane * 4) = -1.f;
         } else {
-          const int in_page = k0 % p.c.page_size;
-          const int64_t ph = (int64_t)page * p.c.heads + h;
-          const int64_t sc = ph * (p.c.page_size / PI_KV_BLOCK) + in_page / PI_KV_BLOCK;
-          const int64_t at = (ph * p.c.page_size + in_page) * D;
-          F::copy(dst, p.c.k_codes + at, p.c.v_codes + at, p.c.k_scales + sc, p.c.v_scales + sc, lane);
+          const int64_t at = page * page_codes + co * D, sc = page * page_scales + co / PI_KV_BLOCK;
+          F::copy(dst, k_head + at, v_head + at, ks_head + sc, vs_head + sc, lane);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      ck += kTile, co += kTile;
+      while (co >= p.c.page_size) co -= p.c.page_size, ++cp;
     };
     if constexpr (WARPS_M == 1) __syncthreads();   // the last unit's sums, in the same memory, have been read
-    int pages[STAGES];
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) pages[i] = page_of(t0 + i);
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fetch(t0 + i, pages[i], i);
-    int page = pages[STAGES - 1], stage = 0;
+    int page = ck < copies ? table[cp] : 0;
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) {
+      fetch(i, page);
+      page = ck < copies ? table[cp] : 0;
+    }
+    int stage = 0;
 
     for (int t = t0; t < t1; ++t) {
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       if constexpr (WARPS_M > 1) __syncthreads();  // every warp's block is there, and the stage before is free
-      fetch(t + STAGES - 1, page, stage == 0 ? STAGES - 1 : stage - 1);
-      page = page_of(t + STAGES);
+      fetch(stage == 0 ? STAGES - 1 : stage - 1, page);
+      page = ck < copies ? table[cp] : 0;
       const char *tile = ring + stage * 4 * F::BYTES;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
 #pragma unroll 1
@@ -379,7 +376,11 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         unsigned w[KS];
         F::load_k(w, src, j, lane);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) mma16816(x[j], a[k], cvt_lo(w[k]), cvt_hi(w[k]));
+        for (int k = 0; k < KS; ++k) {
+          unsigned b0, b1;
+          widen4(w[k], b0, b1);
+          mma16816(x[j], a[k], b0, b1);
+        }
       }
       // ---- running maximum ----
       const bool ragged = k0 + 16 > min_lim;
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       for (int r = 0; r < 4; ++r) {
         const int tk = 2 * q4 + (r & 1) + 8 * (r >> 1);
         F::load_v(v[r], src, r, lane);
-        if (k0 + tk >= sq.len) {                   // past the sequence: whatever the page held before
+        if (ragged && k0 + tk >= sq.len) {         // past the sequence: whatever the page held before
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) v[r][c] = 0;
         }
@@ -470,12 +471,15 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
             n[r] = is & 0x38383838u;               // the code of 1
             v[r][c] &= ~is;
           }
+          unsigned b0[4], b1[4];
+          widen4(__byte_perm(n[0], n[1], 0x5140), b0[0], b0[1]);
+          widen4(__byte_perm(n[0], n[1], 0x7362), b0[2], b0[3]);
+          widen4(__byte_perm(n[2], n[3], 0x5140), b1[0], b1[1]);
+          widen4(__byte_perm(n[2], n[3], 0x7362), b1[2], b1[3]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const unsigned sel = e == 0 ? 0x5140 : e == 1 ? 0x5140 : 0x7362;
-            const unsigned w0 = __byte_perm(n[0], n[1], sel), w1 = __byte_perm(n[2], n[3], sel);
             float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(cnt, see, e & 1 ? cvt_hi(w0) : cvt_lo(w0), e & 1 ? cvt_hi(w1) : cvt_lo(w1));
+            mma16816(cnt, see, b0[e], b1[e]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (cnt[i] > 0.f) acc[4 * c + e][i] = __uint_as_float(0x7fffffffu);
@@ -483,13 +487,14 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         }
       }
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const unsigned a0 = __byte_perm(v[0][c], v[1][c], 0x5140), a1 = __byte_perm(v[2][c], v[3][c], 0x5140);
-        const unsigned b0 = __byte_perm(v[0][c], v[1][c], 0x7362), b1 = __byte_perm(v[2][c], v[3][c], 0x7362);
-        mma16816(acc[4 * c], pa, cvt_lo(a0), cvt_lo(a1));
-        mma16816(acc[4 * c + 1], pa, cvt_hi(a0), cvt_hi(a1));
-        mma16816(acc[4 * c + 2], pa, cvt_lo(b0), cvt_lo(b1));
-        mma16816(acc[4 * c + 3], pa, cvt_hi(b0), cvt_hi(b1));
+      for (int c = 0; c < D / 32; ++c) {           // dims 4 c .. 4 c + 3 of the lane, two tokens side by side
+        unsigned b0[4], b1[4];
+        widen4(__byte_perm(v[0][c], v[1][c], 0x5140), b0[0], b0[1]);
+        widen4(__byte_perm(v[0][c], v[1][c], 0x7362), b0[2], b0[3]);
+        widen4(__byte_perm(v[2][c], v[3][c], 0x5140), b1[0], b1[1]);
+        widen4(__byte_perm(v[2][c], v[3][c], 0x7362), b1[2], b1[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mma16816(acc[4 * c + e], pa, b0[e], b1[e]);
       }
     }
     }
@@ -601,13 +606,14 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
 }
 
 // Units cut between CTAs: their parts added in CTA order.  Units without keys:
-// 0 and -inf.  One CTA per (sequence, head).
+// 0 and -inf.  blockIdx.x: (sequence, head); a warp per row.
 template <int DT, int D, int WARPS_M>
 __global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
   using E = Elem<DT>;
-  constexpr int ROWS = 16 * WARPS_M;
+  constexpr int ROWS = 16 * WARPS_M, LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
+  constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
   __shared__ int64_t scan[4], start;
-  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
+  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads, lane = threadIdx.x & 31;
   const int per = (p.tok.n_seqs + 127) / 128;
   int64_t mine = 0, total;
   for (int i = 0; i < per; ++i) {
@@ -620,43 +626,67 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
     start = at;
   }
   __syncthreads();
+  griddep_wait();
   const int shares = (int)min((int64_t)p.grid, total);
   const Seq sq = load_seq<ROWS>(p, s);
   int64_t u0 = start + h * (seq_tiles<ROWS>(p, s) / p.c.heads);
   for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows; ++rt) {
     const int tiles = unit_tiles<ROWS>(p, sq, rt);
-    int64_t c0 = 0, c1 = 0;
+    int64_t c0 = 0, c1 = -1;
     if (tiles) {
       c0 = cta_owner(u0, total, shares), c1 = cta_owner(u0 + tiles - 1, total, shares);
-      if (c0 == c1) {
-        u0 += tiles;
-        continue;
-      }
+      u0 += tiles;
+      if (c0 == c1) continue;
     }
-    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 128) {
-      const int row = i / (D / 4), d = i % (D / 4) * 4, gr = rt * ROWS + row;
+    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
+      const int gr = rt * ROWS + row;
       if (gr >= sq.rows) break;
       float M = -INFINITY, L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (tiles) {
-        for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, p.part[(2 * c + (c == c0)) * ROWS * (D + 2) + ROWS * D + 2 * row]);
-        const float ms = M == -INFINITY ? 0.f : M;
-        for (int64_t c = c0; c <= c1; ++c) {
-          const float *part = p.part + (2 * c + (c == c0)) * ROWS * (D + 2);
-          const float w = ex2(part[ROWS * D + 2 * row] - ms);
-          L += part[ROWS * D + 2 * row + 1] * w;
-          const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
-          o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+      auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
+      for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
+      M = warp_max(M);
+      const float ms = M == -INFINITY ? 0.f : M;
+      float4 o[VECS];
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
+        const int n = (int)min((int64_t)32, c1 - cb + 1);
+        float w = 0.f;
+        if (lane < n) {
+          const float *ml = part(cb + lane) + ROWS * D + 2 * row;
+          w = ex2(ml[0] - ms);
+          L += ml[1] * w;
         }
+#pragma unroll 8
+        for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
+          const float *src = part(cb + min(i, n - 1)) + row * D;
+#pragma unroll
+          for (int k = 0; k < VECS; ++k) {
+            const int d = (lane % LANES + k * 32) * 4;
+            if (d >= D) continue;
+            const float4 x = *reinterpret_cast<const float4 *>(src + d);
+            if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
+          }
+        }
+      }
+      L = warp_sum(L);
+      if constexpr (LANES == 16) {
+        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
+        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
       }
       const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
       const float inv = L == 0.f ? 0.f : 1.0f / L;
-      Pack<DT, 4> y;
-      y.v[0] = E::from(o.x * inv), y.v[1] = E::from(o.y * inv), y.v[2] = E::from(o.z * inv), y.v[3] = E::from(o.w * inv);
-      *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
-      if (p.lse && d == 0) p.lse[orow] = L == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+#pragma unroll
+      for (int k = 0; k < VECS; ++k) {
+        const int d = (lane % LANES + k * 32) * 4;
+        if (d >= D || lane >= LANES) continue;
+        Pack<DT, 4> y;
+        y.v[0] = E::from(o[k].x * inv), y.v[1] = E::from(o[k].y * inv), y.v[2] = E::from(o[k].z * inv), y.v[3] = E::from(o[k].w * inv);
+        *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
+      }
+      if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
     }
-    u0 += tiles;
   }
 }
 
@@ -674,8 +704,8 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   k_attn<DT, D, WARPS_M><<<p.grid, 128, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_attn_combine<DT, D, WARPS_M><<<(unsigned)p.tok.n_seqs * p.c.heads, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  // its prefix sums overlap the main kernel's end
+  return pi::launch_pdl(k_attn_combine<DT, D, WARPS_M>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 4), dim3(128), 0, s, p);
 }
 
 template <int DT, int D>
