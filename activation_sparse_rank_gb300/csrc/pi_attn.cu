@@ -6,13 +6,14 @@
 // work is bound by HBM: each code is used by q_heads / heads rows only.
 //
 // Rows and products.  The query rows of one key/value head (n_s tokens x
-// q_heads / heads) are the M rows of mma.sync m16n8k16 (fp16 operands, binary32
+// q_heads / heads) are columns of mma.sync m16n8k16 (fp16 operands, binary32
 // sums); E4M3 codes are exact in fp16, so q.k has no rounding but that of the
-// sums.  bf16 rows are scaled by a power of two per row to fit fp16.  Codes go
-// from global memory straight into the lanes' operand registers: the order of
-// the head_dim in a product and of the columns of V is free as long as both
-// operands agree, so each lane takes contiguous bytes of a token's row, and no
-// shared memory or transposition is needed.
+// sums.  bf16 rows are scaled by a power of two per row to fit fp16.  The order of
+// the head_dim in a product and of the rows of V^T is free as long as both
+// operands agree, so a lane's operands are contiguous bytes of a token's row: it
+// copies them itself into its own places of a shared-memory ring (cp.async,
+// several steps ahead, no registers held) and reads them back without bank
+// conflicts, transposition or, with one warp's rows, any barrier.
 //
 // Scales.  A 16-token step of a warp is one block of the cache: its K scale is
 // one factor of x, its V scale 2^ev is folded into the weights: acc holds
@@ -212,21 +213,30 @@ struct Frag {
   }
 };
 
-// Ring stages of a CTA (a stage: a tile's four blocks), two CTAs an SM.
-template <int D>
+// CTAs of 128 threads that an SM holds, by the registers of the variant (80 for
+// 8 rows of 64, 128 for 8 of 128, 254 for 16 of 128); the grid is one wave of them.
+constexpr int attn_ctas(int D, int nb) { return nb == 1 ? (D == 64 ? 5 : D <= 128 ? 4 : 2) : D == 64 ? 4 : D == 96 ? 3 : 2; }
+// Ring stages of a CTA (a stage: a tile's four blocks) in its share of 224 KB.
+template <int D, int NB>
 constexpr int attn_stages() {
-  const int n = 108 * 1024 / (4 * Frag<D>::BYTES);
+  const int n = 224 * 1024 / attn_ctas(D, NB) / (4 * Frag<D>::BYTES);
   return n < 8 ? n : 8;
 }
 
-// WARPS_M == 1: 16 rows, the four warps take a tile's four blocks.
-// WARPS_M == 4: 64 rows, 16 a warp; every warp goes over all four blocks.
-template <int DT, int D, int WARPS_M>
+// NB: eights of query rows of a warp.  WARPS_M == 1: 8 NB rows, the four warps
+// take a tile's four blocks.  WARPS_M == 4: 32 NB rows, 8 NB a warp; every warp
+// goes over all four blocks.
+//
+// Both products have the codes as the 16-row operand and the query rows as the
+// 8 columns: S^T = K Q^T and O^T = V^T P^T.  Eight rows (or fewer) then cost
+// half the products and registers of a 16-row tile of queries; P^T comes from
+// S^T's registers by one 8 x 8 transposition (movmatrix) of each half.
+template <int DT, int D, int NB, int WARPS_M>
 __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
   using E = Elem<DT>;
-  constexpr int ROWS = 16 * WARPS_M, KS = D / 16, NT = D / 8, STAGES = attn_stages<D>();
+  constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
   using F = Frag<D>;
-  extern __shared__ __align__(16) char ring[];     // stages; then, WARPS_M == 1, a unit's [4][16][D] sums, [4][16][3] (m, l, R)
+  extern __shared__ __align__(16) char ring[];     // stages; then, WARPS_M == 1, a unit's [4][ROWS][D] sums, [4][ROWS][3] (m, l, R)
   float *sm = reinterpret_cast<float *>(ring);
   __shared__ int64_t scan[4];
   __shared__ int64_t found[2];
@@ -270,56 +280,6 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
   for (int64_t pos = begin; pos < end;) {
     const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
     const int t0 = (int)(pos - u0), t1 = (int)min((int64_t)tiles, end - u0);
-    // ---- the rows of this unit ----
-    const int base_row = rt * ROWS + (WARPS_M == 1 ? 0 : warp * 16);
-    unsigned a[KS][4];
-    int lim[2];
-    float fac[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = base_row + g + 8 * e;
-      const bool in = r < sq.rows;
-      const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
-      // a padding row masks what every row masks
-      lim[e] = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
-      f2 x[KS][2];                                 // this lane's four dims of each k-step
-      const typename E::T *src = static_cast<const typename E::T *>(p.q) + (int64_t)(sq.row0 + i) * p.qt + hq * p.qh;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint2 w = make_uint2(0, 0);
-        if (in) w = *reinterpret_cast<const uint2 *>(src + F::kdim(k, q4));
-        x[k][0] = f2_widen<DT>(w.x), x[k][1] = f2_widen<DT>(w.y);
-      }
-      float up = 1.f;
-      fac[e] = p.scale;
-      if constexpr (DT == PI_DT_BF16) {
-        // the row's largest finite magnitude to [2^13, 2^14): exact, and fp16 then loses only what is 2^-27 of it
-        float mx = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float2 f = f2_get(x[k][c]);
-            mx = fmaxf(mx, fmaxf(fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f));
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = max((int)(__float_as_uint(mx) >> 23), 27) - 127 - 13;    // up = 2^-ex stays normal
-        if (mx > 0.f) up = __uint_as_float((unsigned)(127 - ex) << 23), fac[e] = p.scale * __uint_as_float((unsigned)(127 + ex) << 23);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        a[k][e] = f2_narrow<PI_DT_F16>(f2_mul(x[k][0], f2_of(up, up)));
-        a[k][2 + e] = f2_narrow<PI_DT_F16>(f2_mul(x[k][1], f2_of(up, up)));
-      }
-    }
-    int min_lim = min(lim[0], lim[1]);             // below it no row of the warp masks anything
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
-
-    float acc[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, R[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
     // ---- the ring: tile t's block `warp` is this warp's to copy ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
@@ -344,7 +304,6 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       ck += kTile, co += kTile;
       while (co >= p.c.page_size) co -= p.c.page_size, ++cp;
     };
-    if constexpr (WARPS_M == 1) __syncthreads();   // the last unit's sums, in the same memory, have been read
     int page = ck < copies ? table[cp] : 0;
 #pragma unroll 1
     for (int i = 0; i < STAGES - 1; ++i) {
@@ -352,6 +311,68 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       page = ck < copies ? table[cp] : 0;
     }
     int stage = 0;
+
+    // ---- the rows of this unit: Q^T in registers, row nb * 8 + g of the warp to this lane ----
+    const int base_row = rt * ROWS + (WARPS_M == 1 ? 0 : warp * WROWS);
+    unsigned bq[NB][KS][2];
+    int lim[NB][2];                                // of the lane's columns: rows nb * 8 + 2 q4 + e
+    float fac[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = base_row + nb * 8 + g;
+      const bool in = r < sq.rows;
+      const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
+      const typename E::T *src = static_cast<const typename E::T *>(p.q) + (int64_t)(sq.row0 + i) * p.qt + hq * p.qh;
+      f2 x[KS][2];                                 // this lane's four dims of each k-step
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint2 w = make_uint2(0, 0);
+        if (in) w = *reinterpret_cast<const uint2 *>(src + F::kdim(k, q4));
+        x[k][0] = f2_widen<DT>(w.x), x[k][1] = f2_widen<DT>(w.y);
+      }
+      float up = 1.f, down = p.scale;
+      if constexpr (DT == PI_DT_BF16) {
+        // the row's largest finite magnitude to [2^13, 2^14): exact, and fp16 then loses only what is 2^-27 of it
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float2 f = f2_get(x[k][c]);
+            mx = fmaxf(mx, fmaxf(fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f));
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = max((int)(__float_as_uint(mx) >> 23), 27) - 127 - 13;    // up = 2^-ex stays normal
+        if (mx > 0.f) up = __uint_as_float((unsigned)(127 - ex) << 23), down = p.scale * __uint_as_float((unsigned)(127 + ex) << 23);
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        bq[nb][k][0] = f2_narrow<PI_DT_F16>(f2_mul(x[k][0], f2_of(up, up)));
+        bq[nb][k][1] = f2_narrow<PI_DT_F16>(f2_mul(x[k][1], f2_of(up, up)));
+      }
+      // a padding row masks what every row masks
+      const int sees = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        lim[nb][e] = __shfl_sync(0xffffffffu, sees, (2 * q4 + e) * 4);
+        fac[nb][e] = __shfl_sync(0xffffffffu, down, (2 * q4 + e) * 4);
+      }
+    }
+    int min_lim = lim[0][0];                       // below it no row of the warp masks anything
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) min_lim = min(min_lim, min(lim[nb][0], lim[nb][1]));
+    min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
+    min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
+
+    float acc[NB][MT][4], m[NB][2], l[NB][2], R[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nb][e] = R[nb][e] = -INFINITY, l[nb][e] = 0.f;
+    }
 
     for (int t = t0; t < t1; ++t) {
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -361,182 +382,182 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
       const char *tile = ring + stage * 4 * F::BYTES;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
 #pragma unroll 1
-    for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
-      const int k0 = t * kTile + blk * 16;
-      const char *src = tile + blk * F::BYTES;
-      if (k0 >= keys) break;
-      const float ks = *reinterpret_cast<const float *>(src + F::S_AT + lane * 4);
-      const float vs = *reinterpret_cast<const float *>(src + F::S_AT + 128 + lane * 4);
-      if (ks < 0.f) continue;
-      // ---- x = q.k ----
-      float x[2][4];
+      for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
+        const int k0 = t * kTile + blk * 16;
+        const char *src = tile + blk * F::BYTES;
+        if (k0 >= keys) break;
+        const float ks = *reinterpret_cast<const float *>(src + F::S_AT + lane * 4);
+        const float vs = *reinterpret_cast<const float *>(src + F::S_AT + 128 + lane * 4);
+        if (ks < 0.f) continue;
+        // ---- x = q.k: tokens g and 8 + g, rows 2 q4 and 2 q4 + 1 of each eight ----
+        float x[NB][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-        unsigned w[KS];
-        F::load_k(w, src, j, lane);
+        for (int nb = 0; nb < NB; ++nb) x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.f;
+        {
+          unsigned w0[KS], w1[KS];
+          F::load_k(w0, src, 0, lane);
+          F::load_k(w1, src, 1, lane);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          unsigned b0, b1;
-          widen4(w[k], b0, b1);
-          mma16816(x[j], a[k], b0, b1);
-        }
-      }
-      // ---- running maximum ----
-      const bool ragged = k0 + 16 > min_lim;
-      float bm[2] = {-INFINITY, -INFINITY};
+          for (int k = 0; k < KS; ++k) {
+            unsigned a[4];
+            widen4(w0[k], a[0], a[2]);
+            widen4(w1[k], a[1], a[3]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e >> 1;
-          x[j][e] *= fac[r] * ks;
-          if (ragged && k0 + 8 * j + 2 * q4 + (e & 1) >= lim[r]) x[j][e] = -INFINITY;
-          bm[r] = fmaxf(bm[r], x[j][e]);
-        }
-      const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
-      float f[2], sub[2];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        bm[r] = fmaxf(bm[r], __shfl_xor_sync(0xffffffffu, bm[r], 1));
-        bm[r] = fmaxf(bm[r], __shfl_xor_sync(0xffffffffu, bm[r], 2));
-        const float mn = fmaxf(m[r], bm[r]);
-        sub[r] = mn == -INFINITY ? 0.f : mn;
-        l[r] *= ex2(m[r] - sub[r]);
-        m[r] = mn;
-        const float Rn = fmaxf(R[r], bm[r] + ev - kBoost);
-        if (Rn != R[r]) moved = true;
-        f[r] = Rn == -INFINITY ? 0.f : ex2(fminf(sub[r] + ev - Rn, 100.f));
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float Rn = fmaxf(R[r], bm[r] + ev - kBoost);
-          const float c = Rn == -INFINITY ? 1.f : ex2(R[r] - Rn);
-          R[r] = Rn;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) acc[j][2 * r] *= c, acc[j][2 * r + 1] *= c;
-        }
-      }
-      // ---- weights ----
-      unsigned pa[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(x[j][e] - sub[e >> 1]);
-          l[e >> 1] += w[e];
-          w[e] *= f[e >> 1];
-        }
-        pa[2 * j] = pack_half2(w[0], w[1]);
-        pa[2 * j + 1] = pack_half2(w[2], w[3]);
-      }
-      // ---- acc += p v ----
-      unsigned v[4][D / 32];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tk = 2 * q4 + (r & 1) + 8 * (r >> 1);
-        F::load_v(v[r], src, r, lane);
-        if (ragged && k0 + tk >= sq.len) {         // past the sequence: whatever the page held before
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) v[r][c] = 0;
-        }
-      }
-      // A NaN among tokens that only some rows see would reach the others as
-      // 0 * NaN: it is taken out here and given to the rows that see it.
-      bool nan = false;
-      if (ragged) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) nan |= __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-        nan = __any_sync(0xffffffffu, nan);
-      }
-      if (nan) {
-        unsigned see[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int k = k0 + 8 * j + 2 * q4;
-          see[2 * j] = pack_half2(k < lim[0], k + 1 < lim[0]);
-          see[2 * j + 1] = pack_half2(k < lim[1], k + 1 < lim[1]);
-        }
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          unsigned n[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const unsigned is = __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            n[r] = is & 0x38383838u;               // the code of 1
-            v[r][c] &= ~is;
+            for (int nb = 0; nb < NB; ++nb) mma16816(x[nb], a, bq[nb][k][0], bq[nb][k][1]);
           }
-          unsigned b0[4], b1[4];
-          widen4(__byte_perm(n[0], n[1], 0x5140), b0[0], b0[1]);
-          widen4(__byte_perm(n[0], n[1], 0x7362), b0[2], b0[3]);
-          widen4(__byte_perm(n[2], n[3], 0x5140), b1[0], b1[1]);
-          widen4(__byte_perm(n[2], n[3], 0x7362), b1[2], b1[3]);
+        }
+        // ---- running maximum, taken up only where a score passes it ----
+        const bool ragged = k0 + 16 > min_lim;
+        const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+        bool over = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(cnt, see, b0[e], b1[e]);
+            x[nb][e] *= fac[nb][e & 1] * ks;
+            if (ragged && k0 + g + 8 * (e >> 1) >= lim[nb][e & 1]) x[nb][e] = -INFINITY;
+            over |= x[nb][e] > fminf(m[nb][e & 1], R[nb][e & 1] - ev + kBoost);
+          }
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (cnt[i] > 0.f) acc[4 * c + e][i] = __uint_as_float(0x7fffffffu);
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float bm = fmaxf(x[nb][e], x[nb][2 + e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+              const float mn = fmaxf(m[nb][e], bm), Rn = fmaxf(R[nb][e], bm + ev - kBoost);
+              if (mn != -INFINITY) l[nb][e] *= ex2(m[nb][e] - mn);
+              const float c = Rn == -INFINITY ? 1.f : ex2(R[nb][e] - Rn);
+              m[nb][e] = mn, R[nb][e] = Rn;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) acc[nb][i][e] *= c, acc[nb][i][2 + e] *= c;
+            }
+        }
+        // ---- weights, transposed into the second product's operand ----
+        unsigned pb[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float sub = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+            const float f = R[nb][e] == -INFINITY ? 0.f : ex2(fminf(sub + ev - R[nb][e], 100.f));
+            const float u = ex2(x[nb][e] - sub), v = ex2(x[nb][2 + e] - sub);
+            l[nb][e] += u + v;
+            w[e] = u * f, w[2 + e] = v * f;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[nb][j]) : "r"(pack_half2(w[2 * j], w[2 * j + 1])));
+        }
+        // ---- acc += v p ----
+        unsigned v[4][D / 32];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) F::load_v(v[r], src, r, lane);
+        if (ragged) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (k0 + 2 * q4 + (r & 1) + 8 * (r >> 1) >= sq.len) {    // past the sequence: whatever the page held before
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) v[r][c] = 0;
+            }
+          // A NaN among tokens that only some rows see would reach the others as
+          // 0 * NaN: it is taken out here and given to the rows that see it.
+          bool nan = false;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) nan |= __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+          if (__any_sync(0xffffffffu, nan)) {
+            unsigned see[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
+                             : "=r"(see[nb][j])
+                             : "r"(pack_half2(k0 + 8 * j + g < lim[nb][0], k0 + 8 * j + g < lim[nb][1])));
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              unsigned n[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const unsigned is = __vcmpeq4(v[r][c] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                n[r] = is & 0x38383838u;           // the code of 1
+                v[r][c] &= ~is;
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                unsigned a[4];
+                widen4(__byte_perm(n[0], n[1], i ? 0x7362 : 0x5140), a[0], a[1]);
+                widen4(__byte_perm(n[2], n[3], i ? 0x7362 : 0x5140), a[2], a[3]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(cnt, a, see[nb][0], see[nb][1]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if (cnt[k] > 0.f) acc[nb][2 * c + i][k] = __uint_as_float(0x7fffffffu);
+                }
+              }
+            }
           }
         }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)           // dims 4 c .. 4 c + 3 of the lane, two tokens side by side
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            unsigned a[4];
+            widen4(__byte_perm(v[0][c], v[1][c], i ? 0x7362 : 0x5140), a[0], a[1]);
+            widen4(__byte_perm(v[2][c], v[3][c], i ? 0x7362 : 0x5140), a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][2 * c + i], a, pb[nb][0], pb[nb][1]);
+          }
       }
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {           // dims 4 c .. 4 c + 3 of the lane, two tokens side by side
-        unsigned b0[4], b1[4];
-        widen4(__byte_perm(v[0][c], v[1][c], 0x5140), b0[0], b0[1]);
-        widen4(__byte_perm(v[0][c], v[1][c], 0x7362), b0[2], b0[3]);
-        widen4(__byte_perm(v[2][c], v[3][c], 0x5140), b1[0], b1[1]);
-        widen4(__byte_perm(v[2][c], v[3][c], 0x7362), b1[2], b1[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mma16816(acc[4 * c + e], pa, b0[e], b1[e]);
-      }
-    }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
 
     // ---- the unit's result, or this CTA's part of it ----
+    // Lane (g, q4) has, of rows 2 q4 + e of each eight, the dims vdim(j, g), j = 2 i + (k >> 1) of acc[i][k], k & 1 == e.
     const bool whole = t0 == 0 && t1 == tiles;
     float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                               // every warp is done with the ring
     if constexpr (WARPS_M == 1) {
-      float *st = sm + 4 * 16 * D;
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();                             // every warp is done with the ring
+      float *st = sm + 4 * ROWS * D;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        if (q4 == 0) st[(warp * 16 + row) * 3] = m[r], st[(warp * 16 + row) * 3 + 1] = l[r], st[(warp * 16 + row) * 3 + 2] = R[r];
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float *o = sm + (warp * 16 + row) * D;
+          const int row = nb * 8 + 2 * q4 + e;
+          float *o = st + (warp * ROWS + row) * 3;
+          if (g == 0) o[0] = m[nb][e], o[1] = l[nb][e], o[2] = R[nb][e];
+          o = sm + (warp * ROWS + row) * D;
 #pragma unroll
-          for (int j = 0; j < NT; j += 4)
-            *reinterpret_cast<float4 *>(o + F::vdim(j, 2 * q4 + e)) = make_float4(acc[j][2 * r + e], acc[j + 1][2 * r + e], acc[j + 2][2 * r + e], acc[j + 3][2 * r + e]);
+          for (int i = 0; i < MT; i += 2)
+            *reinterpret_cast<float4 *>(o + F::vdim(2 * i, g)) =
+                make_float4(acc[nb][i][e], acc[nb][i][2 + e], acc[nb][i + 1][e], acc[nb][i + 1][2 + e]);
         }
-      }
       __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (D / 4); i += 128) {
+      for (int i = threadIdx.x; i < ROWS * (D / 4); i += 128) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, st[(w * 16 + row) * 3]);
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, st[(w * ROWS + row) * 3]);
         const float ms = M == -INFINITY ? 0.f : M;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float *t = st + (w * 16 + row) * 3;
+          const float *t = st + (w * ROWS + row) * 3;
           L += t[1] * ex2(t[0] - ms);
           const float c = t[2] == -INFINITY ? 0.f : ex2(t[2] - ms);
-          const float4 x = *reinterpret_cast<const float4 *>(sm + (w * 16 + row) * D + d);
+          const float4 x = *reinterpret_cast<const float4 *>(sm + (w * ROWS + row) * D + d);
           o.x = fmaf(x.x, c, o.x), o.y = fmaf(x.y, c, o.y), o.z = fmaf(x.z, c, o.z), o.w = fmaf(x.w, c, o.w);
         }
         if (whole) {
@@ -553,22 +574,21 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
           if (d == 0) part[ROWS * D + 2 * row] = M, part[ROWS * D + 2 * row + 1] = L;
         }
       }
+      __syncthreads();                             // the sums have been read: the ring is free again
     } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = warp * 16 + g + 8 * r, gr = rt * ROWS + row;
-        const float ms = m[r] == -INFINITY ? 0.f : m[r];
-        const float c = (R[r] == -INFINITY ? 0.f : ex2(R[r] - ms)) * (whole ? (l[r] == 0.f ? 0.f : 1.0f / l[r]) : 1.f);
-        if (whole && gr >= sq.rows) continue;
-        const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const int row = warp * WROWS + nb * 8 + 2 * q4 + e, gr = rt * ROWS + row;
+          if (whole && gr >= sq.rows) continue;
+          const float L = l[nb][e], ms = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+          const float c = (R[nb][e] == -INFINITY ? 0.f : ex2(R[nb][e] - ms)) * (whole ? (L == 0.f ? 0.f : 1.0f / L) : 1.f);
+          const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
 #pragma unroll
-          for (int j = 0; j < NT; j += 4) {
-            const int d = F::vdim(j, 2 * q4 + e);
-            const float4 o = make_float4(acc[j][2 * r + e] * c, acc[j + 1][2 * r + e] * c, acc[j + 2][2 * r + e] * c, acc[j + 3][2 * r + e] * c);
+          for (int i = 0; i < MT; i += 2) {
+            const int d = F::vdim(2 * i, g);
+            const float4 o = make_float4(acc[nb][i][e] * c, acc[nb][i][2 + e] * c, acc[nb][i + 1][e] * c, acc[nb][i + 1][2 + e] * c);
             if (whole) {
               Pack<DT, 4> y;
               y.v[0] = E::from(o.x), y.v[1] = E::from(o.y), y.v[2] = E::from(o.z), y.v[3] = E::from(o.w);
@@ -577,15 +597,14 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
               *reinterpret_cast<float4 *>(part + row * D + d) = o;
             }
           }
-        }
-        if (q4 == 0) {
-          if (whole) {
-            if (p.lse) p.lse[orow] = l[r] == 0.f ? -INFINITY : (ms + log2f(l[r])) * kLn2;
-          } else {
-            part[ROWS * D + 2 * row] = m[r], part[ROWS * D + 2 * row + 1] = l[r];
+          if (g == 0) {
+            if (whole) {
+              if (p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
+            } else {
+              part[ROWS * D + 2 * row] = m[nb][e], part[ROWS * D + 2 * row + 1] = L;
+            }
           }
         }
-      }
     }
 
     // ---- next unit ----
@@ -607,10 +626,10 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
 
 // Units cut between CTAs: their parts added in CTA order.  Units without keys:
 // 0 and -inf.  blockIdx.x: (sequence, head); a warp per row.
-template <int DT, int D, int WARPS_M>
+template <int DT, int D, int ROWS>
 __global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
   using E = Elem<DT>;
-  constexpr int ROWS = 16 * WARPS_M, LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
+  constexpr int LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
   constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
   __shared__ int64_t scan[4], start;
   const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads, lane = threadIdx.x & 31;
@@ -690,27 +709,43 @@ __global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
   }
 }
 
-// CTAs of the main kernel.
-int attn_grid() { return 2 * std::max(1, pi::current_sms()); }
-// Rows of a row tile: one warp's 16 while they hold all query rows of a head, else 64.
-int attn_warps_m(int64_t max_rows) { return max_rows <= 16 ? 1 : 4; }
+struct AttnShape {
+  int nb, warps_m;
+};
+// Rows of a row tile: the fewest eights that hold all query rows of a head
+// while a warp's registers can (16 rows, 8 of 256 dims); above, four warps of
+// that share a tile of keys.
+AttnShape attn_shape(int D, int64_t max_rows) {
+  const int nb_max = D <= 128 ? 2 : 1;
+  const int nb = max_rows <= 8 ? 1 : nb_max;
+  return AttnShape{nb, max_rows <= 8 * nb ? 1 : 4};
+}
 
-template <int DT, int D, int WARPS_M>
+int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current_sms()); }
+
+template <int DT, int D, int NB, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
-  constexpr int kRing = attn_stages<D>() * 4 * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * 16 * (D + 3) * 4 : 0;
+  constexpr int ROWS = 8 * NB * WARPS_M;
+  constexpr int kRing = attn_stages<D, NB>() * 4 * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * ROWS * (D + 3) * 4 : 0;
   constexpr int smem = kRing > kSums ? kRing : kSums;
-  cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, NB, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_attn<DT, D, WARPS_M><<<p.grid, 128, smem, s>>>(p);
+  k_attn<DT, D, NB, WARPS_M><<<p.grid, 128, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, WARPS_M>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS < 16 ? ROWS / 4 : 4), dim3(128), 0, s, p);
 }
 
 template <int DT, int D>
 cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
-  return attn_warps_m((int64_t)p.max_q * p.group) == 1 ? launch_attn<DT, D, 1>(p, s) : launch_attn<DT, D, 4>(p, s);
+  const AttnShape k = attn_shape(D, (int64_t)p.max_q * p.group);
+  if constexpr (D <= 128) {
+    if (k.nb == 1) return launch_attn<DT, D, 1, 1>(p, s);
+    return k.warps_m == 1 ? launch_attn<DT, D, 2, 1>(p, s) : launch_attn<DT, D, 2, 4>(p, s);
+  } else {
+    return k.warps_m == 1 ? launch_attn<DT, D, 1, 1>(p, s) : launch_attn<DT, D, 1, 4>(p, s);
+  }
 }
 
 template <int DT>
@@ -742,7 +777,9 @@ extern "C" {
 size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, int32_t n_tokens, int32_t n_seqs) {
   pi::clear_error();
   if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
-  return sizeof(float) * 2 * (size_t)attn_grid() * 64 * (size_t)(c->head_dim + 2);
+  const int D = c->head_dim;
+  const size_t rows = D <= 128 ? std::max((size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 64) : (size_t)attn_grid(D, 1) * 32;
+  return sizeof(float) * 2 * rows * (size_t)(D + 2);
 }
 
 pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
@@ -770,10 +807,12 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
   if (!ws || !pi::aligned_to(ws, 16) || ws_bytes < need)
     return pi::fail(PI_ERR_INVALID_ARG, "ws must be 16-byte aligned and hold %zu bytes, has %zu", need, ws_bytes);
   max_q = std::min(max_q, tokens->n_tokens);
-  const int group = q_heads / cache->heads, rows = 16 * attn_warps_m((int64_t)max_q * group);
+  const int group = q_heads / cache->heads;
+  const AttnShape shape = attn_shape(cache->head_dim, (int64_t)max_q * group);
+  const int rows = 8 * shape.nb * shape.warps_m;
   const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<float *>(ws),
                      sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
-                     (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid()};
+                     (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
   return PI_OK;
