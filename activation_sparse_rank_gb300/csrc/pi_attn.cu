@@ -11,9 +11,9 @@
 // sums.  bf16 rows are scaled by a power of two per row to fit fp16.  The order of
 // the head_dim in a product and of the rows of V^T is free as long as both
 // operands agree, so a lane's operands are contiguous bytes of a token's row: it
-// copies them itself into its own places of a shared-memory ring (cp.async,
-// several steps ahead, no registers held) and reads them back without bank
-// conflicts, transposition or, with one warp's rows, any barrier.
+// reads them from the tile that a tensor-map copy left in a shared-memory ring,
+// several steps ahead, without bank conflicts or transposition.  Each warp copies
+// its own blocks: with one warp's rows there is no barrier between warps.
 //
 // Scales.  A 16-token step of a warp is one block of the cache: its K scale is
 // one factor of x, its V scale 2^ev is folded into the weights: acc holds
@@ -27,6 +27,7 @@
 // leaves partial sums, which k_attn_combine adds in CTA order.
 #include "pi_kv.cuh"
 #include "pi_ops.cuh"
+#include "pi_ptx.cuh"
 
 #include <algorithm>
 
@@ -139,76 +140,58 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *tot
 __device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
 __device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(char *dst, const void *src) {
-  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
-}
+struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 16 tokens and up to 128 bytes
+  CUtensorMap k, v;
+};
 
-// A block (16 tokens) in the ring: for each lane (g = lane / 4, q = lane % 4)
-//   K rows g and 8 + g, the codes that are its share of the k-steps,
-//   V rows 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q, the codes that are its columns,
-//   the block's two scales,
-// each piece as [32 lanes][piece].  A warp's copy of one piece covers whole
-// contiguous stretches of rows.
+// A block (16 tokens) in shared memory, K then V, as the tile copies leave it:
+// boxes of min(D, 128) bytes by 16 rows, 16-byte chunks swizzled so that the
+// loads below meet no bank twice (D = 96 is not swizzled).  Lane (g = lane / 4,
+// q = lane % 4) takes of K rows g and 8 + g its share of the k-steps, of V rows
+// 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q its dims.
 template <int D>
 struct Frag {
-  static constexpr int KP = D / 64, V16 = D / 128;                 // 16-byte pieces of a row
-  static constexpr bool REST = D % 64 != 0;                        // 96: 8 more bytes of K, 4 of V
-  static constexpr int K_ROW = 512 * KP + (REST ? 256 : 0);
-  static constexpr int V_ROW = V16 ? 512 * V16 : 256 + (REST ? 128 : 0);
-  static constexpr int V_AT = 2 * K_ROW, S_AT = V_AT + 4 * V_ROW, BYTES = S_AT + 256;
-  static_assert(S_AT == 32 * D);
+  static constexpr int HALF = 16 * D, BYTES = 2 * HALF;
+  static constexpr int BOX = D < 128 ? D : 128, BOXES = D / BOX;
   // dims of k-step k (two k indices, and the two 8 further): 4 from here on
   static __device__ __forceinline__ int kdim(int k, int q) {
-    return REST && k >= 4 * KP ? 64 * KP + q * 8 + (k - 4 * KP) * 4 : k / 4 * 64 + q * 16 + k % 4 * 4;
+    if constexpr (D == 96) return k >= 4 ? 64 + q * 8 + (k - 4) * 4 : q * 16 + k * 4;
+    return k / (BOX / 16) * BOX + q * (BOX / 4) + k % (BOX / 16) * 4;
   }
   // dim of column c of n-tile j; 4 tiles in a row are 4 dims in a row
   static __device__ __forceinline__ int vdim(int j, int c) {
-    if constexpr (V16) return j / 16 * 128 + c * 16 + j % 16;
+    if constexpr (D >= 128) return j / 16 * 128 + c * 16 + j % 16;
     return j < 8 ? c * 8 + j : 64 + c * 4 + j - 8;
   }
-  static __device__ __forceinline__ void copy(char *dst, const uint8_t *kb, const uint8_t *vb, const float *ks,
-                                              const float *vs, int lane) {
-    const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint8_t *row = kb + (8 * j + g) * D;
-#pragma unroll
-      for (int i = 0; i < KP; ++i) copy_async<16>(dst + j * K_ROW + 512 * i + lane * 16, row + 64 * i + q * 16);
-      if constexpr (REST) copy_async<8>(dst + j * K_ROW + 512 * KP + lane * 8, row + 64 * KP + q * 8);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint8_t *row = vb + (2 * q + (r & 1) + 8 * (r >> 1)) * D;
-      char *d = dst + V_AT + r * V_ROW;
-      if constexpr (V16) {
-#pragma unroll
-        for (int i = 0; i < V16; ++i) copy_async<16>(d + 512 * i + lane * 16, row + 128 * i + g * 16);
-      } else {
-        copy_async<8>(d + lane * 8, row + g * 8);
-        if constexpr (REST) copy_async<4>(d + 256 + lane * 4, row + 64 + g * 4);
-      }
-    }
-    copy_async<4>(dst + S_AT + lane * 4, ks);
-    copy_async<4>(dst + S_AT + 128 + lane * 4, vs);
-  }
-  static __device__ __forceinline__ void load_k(unsigned *w, const char *src, int j, int lane) {
-#pragma unroll
-    for (int i = 0; i < KP; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = *reinterpret_cast<const uint4 *>(src + j * K_ROW + 512 * i + lane * 16);
-    if constexpr (REST) *reinterpret_cast<uint2 *>(w + 4 * KP) = *reinterpret_cast<const uint2 *>(src + j * K_ROW + 512 * KP + lane * 8);
-  }
-  static __device__ __forceinline__ void load_v(unsigned *w, const char *src, int r, int lane) {
-    const char *d = src + V_AT + r * V_ROW;
-    if constexpr (V16) {
-#pragma unroll
-      for (int i = 0; i < V16; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = *reinterpret_cast<const uint4 *>(d + 512 * i + lane * 16);
+  static __device__ __forceinline__ uint4 ld16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
+  static __device__ __forceinline__ uint2 ld8(const char *p) { return *reinterpret_cast<const uint2 *>(p); }
+  // words of row 8 j + g: k-step k's codes are word k
+  static __device__ __forceinline__ void load_k(unsigned *w, const char *src, int j, int g, int q) {
+    if constexpr (D == 64) {
+      *reinterpret_cast<uint4 *>(w) = ld16(src + (8 * j + g) * 64 + ((q ^ (g >> 1 & 3)) << 4));
+    } else if constexpr (D == 96) {
+      const char *row = src + (8 * j + g) * 96;
+      *reinterpret_cast<uint4 *>(w) = ld16(row + q * 16);
+      *reinterpret_cast<uint2 *>(w + 4) = ld8(row + 64 + q * 8);
     } else {
-      *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(d + lane * 8);
-      if constexpr (REST) w[2] = *reinterpret_cast<const unsigned *>(d + 256 + lane * 4);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i / 2 * 2048 + (8 * j + g) * 128 + (((2 * q + i % 2) ^ g) << 4));
+    }
+  }
+  // words of row 2 q + (r & 1) + 8 (r >> 1): byte j is dim vdim(j, g)
+  static __device__ __forceinline__ void load_v(unsigned *w, const char *src, int r, int g, int q) {
+    const int row = 2 * q + (r & 1), h = r >> 1;
+    src += HALF;
+    if constexpr (D == 64) {
+      *reinterpret_cast<uint2 *>(w) = ld8(src + (8 * h + row) * 64 + (((g >> 1) ^ q) << 4) + (g & 1) * 8);
+    } else if constexpr (D == 96) {
+      *reinterpret_cast<uint2 *>(w) = ld8(src + (8 * h + row) * 96 + g * 8);
+      w[2] = *reinterpret_cast<const unsigned *>(src + (8 * h + row) * 96 + 64 + g * 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i)
+        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i * 2048 + (8 * h + row) * 128 + ((g ^ row) << 4));
     }
   }
 };
@@ -219,7 +202,7 @@ constexpr int attn_ctas(int D, int nb) { return nb == 1 ? (D == 64 ? 5 : D <= 12
 // Ring stages of a CTA (a stage: a tile's four blocks) in its share of 224 KB.
 template <int D, int NB>
 constexpr int attn_stages() {
-  const int n = 224 * 1024 / attn_ctas(D, NB) / (4 * Frag<D>::BYTES);
+  const int n = (224 / attn_ctas(D, NB) - 2) * 1024 / (4 * Frag<D>::BYTES);   // 2 KB: alignment, barriers
   return n < 8 ? n : 8;
 }
 
@@ -232,16 +215,26 @@ constexpr int attn_stages() {
 // half the products and registers of a 16-row tile of queries; P^T comes from
 // S^T's registers by one 8 x 8 transposition (movmatrix) of each half.
 template <int DT, int D, int NB, int WARPS_M>
-__global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
+__global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using E = Elem<DT>;
   constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
   using F = Frag<D>;
-  extern __shared__ __align__(16) char ring[];     // stages; then, WARPS_M == 1, a unit's [4][ROWS][D] sums, [4][ROWS][3] (m, l, R)
+  extern __shared__ char smem_raw[];
+  // stages; then, WARPS_M == 1, a unit's [4][ROWS][D] sums, [4][ROWS][3] (m, l, R)
+  char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *sm = reinterpret_cast<float *>(ring);
   __shared__ int64_t scan[4];
   __shared__ int64_t found[2];
+  __shared__ __align__(8) unsigned long long full[STAGES * 4];   // a block's copies have landed
+  __shared__ float2 scales[STAGES * 4];                          // its K and V scale; K below 0: no block
+  __shared__ int failed;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
   griddep_launch();                                // every CTA of this grid is resident: the next one may take what is left
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES * 4; ++i) bar_init(smem_addr(&full[i]), 3);
+    bar_init_fence();
+    failed = 0;
+  }
   for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
 
   // Where this CTA's share of the line of tiles begins.
@@ -277,6 +270,8 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
     for (int n; begin >= u0 + (n = unit_tiles<ROWS>(p, sq, rt)); ++rt) u0 += n;
   }
 
+  uint32_t parity = 0;                             // of each slot's barrier
+  bool dead = false;                               // a wait ran out: nothing more is copied or computed
   for (int64_t pos = begin; pos < end;) {
     const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
     const int t0 = (int)(pos - u0), t1 = (int)min((int64_t)tiles, end - u0);
@@ -286,21 +281,34 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
     // where the next copy is: its first key, its page's place in the table, its offset in the page
     int ck = t0 * kTile + warp * 16, cp = ck / p.c.page_size, co = ck - cp * p.c.page_size;
     const int copies = min(keys, t1 * kTile);
-    const int64_t page_codes = (int64_t)p.c.heads * p.c.page_size * D, page_scales = (int64_t)p.c.heads * (p.c.page_size / PI_KV_BLOCK);
-    const uint8_t *k_head = p.c.k_codes + (int64_t)h * p.c.page_size * D, *v_head = p.c.v_codes + (int64_t)h * p.c.page_size * D;
     const float *ks_head = p.c.k_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK), *vs_head = p.c.v_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK);
+    // lanes 0 and 1: a block's barrier counts lane 0's arrival and both lanes' scale copies
     auto fetch = [&](int stage, int page) {        // page: table[cp], read ahead of time
-      if (ck < copies) {
-        char *dst = ring + (stage * 4 + warp) * F::BYTES;
-        if (page < 0 || page >= p.c.n_pages) {     // a negative scale: no block here
-          if (lane == 0) atomicOr(p.c.status, pi::kKvBadPage);
-          *reinterpret_cast<float *>(dst + F::S_AT + lane * 4) = -1.f;
+      if (ck < copies && lane < 2 && !dead) {
+        const int slot = stage * 4 + warp;
+        const uint32_t bar = smem_addr(&full[slot]);
+        float *sc = lane ? &scales[slot].y : &scales[slot].x;
+        if (page < 0 || page >= p.c.n_pages) {
+          *sc = -1.f;
+          if (lane == 0) {
+            atomicOr(p.c.status, pi::kKvBadPage);
+            bar_arrive(bar);
+          }
         } else {
-          const int64_t at = page * page_codes + co * D, sc = page * page_scales + co / PI_KV_BLOCK;
-          F::copy(dst, k_head + at, v_head + at, ks_head + sc, vs_head + sc, lane);
+          if (lane == 0) {
+            const uint32_t dst = smem_addr(ring + slot * F::BYTES);
+            bar_expect(bar, F::BYTES);
+#pragma unroll
+            for (int i = 0; i < F::BOXES; ++i) {
+              tile_copy(dst + i * 2048, &maps.k, i * 128, co, page * p.c.heads + h, bar);
+              tile_copy(dst + F::HALF + i * 2048, &maps.v, i * 128, co, page * p.c.heads + h, bar);
+            }
+          }
+          const float *src = (lane ? vs_head : ks_head) + (int64_t)page * p.c.heads * (p.c.page_size / PI_KV_BLOCK) + co / PI_KV_BLOCK;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(sc)), "l"(src) : "memory");
         }
+        bar_arrive_copies(bar);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
       ck += kTile, co += kTile;
       while (co >= p.c.page_size) co -= p.c.page_size, ++cp;
     };
@@ -375,19 +383,25 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
     }
 
     for (int t = t0; t < t1; ++t) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-      if constexpr (WARPS_M > 1) __syncthreads();  // every warp's block is there, and the stage before is free
+      // the stage before has been read: by this warp, or by all that share it
+      if constexpr (WARPS_M > 1) __syncthreads(); else __syncwarp();
       fetch(stage == 0 ? STAGES - 1 : stage - 1, page);
       page = ck < copies ? table[cp] : 0;
-      const char *tile = ring + stage * 4 * F::BYTES;
+      const int slot0 = stage * 4;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
 #pragma unroll 1
       for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
         const int k0 = t * kTile + blk * 16;
-        const char *src = tile + blk * F::BYTES;
+        const int slot = slot0 + blk;
+        const char *src = ring + slot * F::BYTES;
         if (k0 >= keys) break;
-        const float ks = *reinterpret_cast<const float *>(src + F::S_AT + lane * 4);
-        const float vs = *reinterpret_cast<const float *>(src + F::S_AT + 128 + lane * 4);
+        if (dead) continue;
+        if (!bar_wait(smem_addr(&full[slot]), parity >> slot & 1)) {
+          dead = true;
+          continue;
+        }
+        parity ^= 1u << slot;
+        const float ks = scales[slot].x, vs = scales[slot].y;
         if (ks < 0.f) continue;
         // ---- x = q.k: tokens g and 8 + g, rows 2 q4 and 2 q4 + 1 of each eight ----
         float x[NB][4];
@@ -395,8 +409,8 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         for (int nb = 0; nb < NB; ++nb) x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.f;
         {
           unsigned w0[KS], w1[KS];
-          F::load_k(w0, src, 0, lane);
-          F::load_k(w1, src, 1, lane);
+          F::load_k(w0, src, 0, g, q4);
+          F::load_k(w1, src, 1, g, q4);
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             unsigned a[4];
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
         // ---- acc += v p ----
         unsigned v[4][D / 32];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) F::load_v(v[r], src, r, lane);
+        for (int r = 0; r < 4; ++r) F::load_v(v[r], src, r, g, q4);
         if (ragged) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -527,8 +541,14 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
     // Lane (g, q4) has, of rows 2 q4 + e of each eight, the dims vdim(j, g), j = 2 i + (k >> 1) of acc[i][k], k & 1 == e.
     const bool whole = t0 == 0 && t1 == tiles;
     float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (dead) {                                    // copies may still be on their way: give them time, then leave
+      for (int i = 0; i < STAGES * 4; ++i)
+        if (WARPS_M > 1 || i % 4 == warp) bar_wait(smem_addr(&full[i]), parity >> i & 1);
+      if (lane == 0) atomicOr(p.c.status, pi::kKvTimeout);
+      failed = 1;
+    }
     __syncthreads();                               // every warp is done with the ring
+    if (failed) return;
     if constexpr (WARPS_M == 1) {
       float *st = sm + 4 * ROWS * D;
 #pragma unroll
@@ -574,6 +594,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p) {
           if (d == 0) part[ROWS * D + 2 * row] = M, part[ROWS * D + 2 * row + 1] = L;
         }
       }
+      fence_async_smem();
       __syncthreads();                             // the sums have been read: the ring is free again
     } else {
 #pragma unroll
@@ -721,16 +742,50 @@ AttnShape attn_shape(int D, int64_t max_rows) {
   return AttnShape{nb, max_rows <= 8 * nb ? 1 : 4};
 }
 
+// The driver's tensor-map encoder, looked up through the runtime so that the
+// library does not link libcuda.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Codes as [n_pages heads][page_size][D]: a page of a head is one z, so every
+// coordinate stays small in a cache of any size.
+template <int D>
+bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
+  const EncodeFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * c.page_size};
+  const cuuint32_t box[3] = {(cuuint32_t)Frag<D>::BOX, 16, 1}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : D == 96 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current_sms()); }
 
 template <int DT, int D, int NB, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   constexpr int ROWS = 8 * NB * WARPS_M;
   constexpr int kRing = attn_stages<D, NB>() * 4 * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * ROWS * (D + 3) * 4 : 0;
-  constexpr int smem = kRing > kSums ? kRing : kSums;
+  constexpr int smem = (kRing > kSums ? kRing : kSums) + 1024;
+  static_assert(attn_stages<D, NB>() >= 2 && attn_stages<D, NB>() <= 8);
+  AttnMaps maps;
+  if (!encode_codes<D>(&maps.k, p.c, p.c.k_codes) || !encode_codes<D>(&maps.v, p.c, p.c.v_codes)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, NB, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_attn<DT, D, NB, WARPS_M><<<p.grid, 128, smem, s>>>(p);
+  k_attn<DT, D, NB, WARPS_M><<<p.grid, 128, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
@@ -801,8 +856,9 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
     return pi::fail(PI_ERR_INVALID_ARG, "q's strides must be multiples of 8 elements");
   if (!pi::aligned_to(length, 4) || !pi::aligned_to(lse, 4))
     return pi::fail(PI_ERR_INVALID_ARG, "length and lse must be 4-byte aligned");
-  if ((int64_t)tokens->n_seqs * cache->heads >= (int64_t)1 << 31 || (int64_t)max_q * (q_heads / cache->heads) >= 1 << 30)
-    return pi::fail(PI_ERR_UNSUPPORTED, "n_seqs x heads or max_q x q_heads / heads is too large");
+  if ((int64_t)cache->n_pages * cache->heads >= (int64_t)1 << 31 ||
+      (int64_t)tokens->n_seqs * cache->heads >= (int64_t)1 << 31 || (int64_t)max_q * (q_heads / cache->heads) >= 1 << 30)
+    return pi::fail(PI_ERR_UNSUPPORTED, "n_pages x heads, n_seqs x heads or max_q x q_heads / heads is too large");
   const size_t need = pi_kv_attention_workspace_bytes(cache, q_heads, tokens->n_tokens, tokens->n_seqs);
   if (!ws || !pi::aligned_to(ws, 16) || ws_bytes < need)
     return pi::fail(PI_ERR_INVALID_ARG, "ws must be 16-byte aligned and hold %zu bytes, has %zu", need, ws_bytes);
