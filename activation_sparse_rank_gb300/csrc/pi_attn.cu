@@ -12,8 +12,7 @@
 // the head_dim in a product and of the rows of V^T is free as long as both
 // operands agree, so a lane's operands are contiguous bytes of a token's row: it
 // reads them from the tile that a tensor-map copy left in a shared-memory ring,
-// several steps ahead, without bank conflicts or transposition.  Each warp copies
-// its own blocks: with one warp's rows there is no barrier between warps.
+// several tiles ahead, without transposition.
 //
 // Scales.  A 16-token step of a warp is one block of the cache: its K scale is
 // one factor of x, its V scale 2^ev is folded into the weights: acc holds
@@ -36,7 +35,11 @@ using namespace pidev;
 namespace {
 
 constexpr int kTile = 64;                 // keys of a tile
-constexpr float kBoost = 12.f;             // weights go up to 2^kBoost, so that fp16 is subnormal only below 2^-(14 + kBoost)
+// The second product's weights 2^(x + ev - R) reach 2^(kBoost + kSlack), inside
+// fp16, and are subnormal only below 2^-(14 + kBoost) of the largest.  kSlack:
+// m and R follow a score only where it passes them by that much; the sums do
+// not depend on m and R, and most steps then leave the accumulators alone.
+constexpr float kBoost = 6.f, kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -140,19 +143,19 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *tot
 __device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
 __device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
 
-struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 16 tokens and up to 128 bytes
+struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 or 16 tokens and up to 128 bytes
   CUtensorMap k, v;
 };
 
-// A block (16 tokens) in shared memory, K then V, as the tile copies leave it:
-// boxes of min(D, 128) bytes by 16 rows, 16-byte chunks swizzled so that the
-// loads below meet no bank twice (D = 96 is not swizzled).  Lane (g = lane / 4,
-// q = lane % 4) takes of K rows g and 8 + g its share of the k-steps, of V rows
-// 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q its dims.
+// A tile (64 tokens) in shared memory, K then V, as the tile copies leave it:
+// boxes of min(D, 128) bytes by 64 rows, 16-byte chunks swizzled so that the
+// loads below meet no bank twice (D = 96 is not swizzled; D = 64 meets two).
+// Of a block (16 rows) lane (g = lane / 4, q = lane % 4) takes of K rows g and
+// 8 + g its share of the k-steps, of V rows 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q its dims.
 template <int D>
 struct Frag {
-  static constexpr int HALF = 16 * D, BYTES = 2 * HALF;
   static constexpr int BOX = D < 128 ? D : 128, BOXES = D / BOX;
+  static constexpr int BOX_BYTES = kTile * BOX, V_AT = kTile * D, BYTES = 2 * V_AT;
   // dims of k-step k (two k indices, and the two 8 further): 4 from here on
   static __device__ __forceinline__ int kdim(int k, int q) {
     if constexpr (D == 96) return k >= 4 ? 64 + q * 8 + (k - 4) * 4 : q * 16 + k * 4;
@@ -165,7 +168,7 @@ struct Frag {
   }
   static __device__ __forceinline__ uint4 ld16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
   static __device__ __forceinline__ uint2 ld8(const char *p) { return *reinterpret_cast<const uint2 *>(p); }
-  // words of row 8 j + g: k-step k's codes are word k
+  // words of row 8 j + g of the block at src: k-step k's codes are word k
   static __device__ __forceinline__ void load_k(unsigned *w, const char *src, int j, int g, int q) {
     if constexpr (D == 64) {
       *reinterpret_cast<uint4 *>(w) = ld16(src + (8 * j + g) * 64 + ((q ^ (g >> 1 & 3)) << 4));
@@ -176,13 +179,13 @@ struct Frag {
     } else {
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
-        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i / 2 * 2048 + (8 * j + g) * 128 + (((2 * q + i % 2) ^ g) << 4));
+        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i / 2 * BOX_BYTES + (8 * j + g) * 128 + (((2 * q + i % 2) ^ g) << 4));
     }
   }
   // words of row 2 q + (r & 1) + 8 (r >> 1): byte j is dim vdim(j, g)
   static __device__ __forceinline__ void load_v(unsigned *w, const char *src, int r, int g, int q) {
     const int row = 2 * q + (r & 1), h = r >> 1;
-    src += HALF;
+    src += V_AT;
     if constexpr (D == 64) {
       *reinterpret_cast<uint2 *>(w) = ld8(src + (8 * h + row) * 64 + (((g >> 1) ^ q) << 4) + (g & 1) * 8);
     } else if constexpr (D == 96) {
@@ -191,7 +194,7 @@ struct Frag {
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i)
-        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i * 2048 + (8 * h + row) * 128 + ((g ^ row) << 4));
+        *reinterpret_cast<uint4 *>(w + 4 * i) = ld16(src + i * BOX_BYTES + (8 * h + row) * 128 + ((g ^ row) << 4));
     }
   }
 };
@@ -202,7 +205,7 @@ constexpr int attn_ctas(int D, int nb) { return nb == 1 ? (D == 64 ? 5 : D <= 12
 // Ring stages of a CTA (a stage: a tile's four blocks) in its share of 224 KB.
 template <int D, int NB>
 constexpr int attn_stages() {
-  const int n = (224 / attn_ctas(D, NB) - 2) * 1024 / (4 * Frag<D>::BYTES);   // 2 KB: alignment, barriers
+  const int n = (224 / attn_ctas(D, NB) - 2) * 1024 / Frag<D>::BYTES;   // 2 KB: alignment, barriers
   return n < 8 ? n : 8;
 }
 
@@ -215,7 +218,7 @@ constexpr int attn_stages() {
 // half the products and registers of a 16-row tile of queries; P^T comes from
 // S^T's registers by one 8 x 8 transposition (movmatrix) of each half.
 template <int DT, int D, int NB, int WARPS_M>
-__global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+__global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using E = Elem<DT>;
   constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
   using F = Frag<D>;
@@ -225,13 +228,16 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
   float *sm = reinterpret_cast<float *>(ring);
   __shared__ int64_t scan[4];
   __shared__ int64_t found[2];
-  __shared__ __align__(8) unsigned long long full[STAGES * 4];   // a block's copies have landed
-  __shared__ float2 scales[STAGES * 4];                          // its K and V scale; K below 0: no block
+  __shared__ __align__(8) unsigned long long full[STAGES], empty[STAGES];   // a tile's copies have landed; all warps have read it
+  __shared__ float scales[STAGES][2][4];           // K and V scale of its blocks; K below 0: no block
   __shared__ int failed;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
   griddep_launch();                                // every CTA of this grid is resident: the next one may take what is left
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES * 4; ++i) bar_init(smem_addr(&full[i]), 3);
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(smem_addr(&full[i]), 33);           // the bytes' arrival, and each lane's scale copies
+      bar_init(smem_addr(&empty[i]), 4);
+    }
     bar_init_fence();
     failed = 0;
   }
@@ -270,53 +276,83 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
     for (int n; begin >= u0 + (n = unit_tiles<ROWS>(p, sq, rt)); ++rt) u0 += n;
   }
 
-  uint32_t parity = 0;                             // of each slot's barrier
+  uint32_t full_ph = 0, empty_ph = 0, used = 0, pend = 0;    // a bit a stage: phases to wait for, filled ever, filled and not waited for
   bool dead = false;                               // a wait ran out: nothing more is copied or computed
+  const bool by16 = p.c.page_size % kTile != 0;    // a tile may lie in several pages: blocks are copied one by one
   for (int64_t pos = begin; pos < end;) {
     const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
     const int t0 = (int)(pos - u0), t1 = (int)min((int64_t)tiles, end - u0);
 
-    // ---- the ring: tile t's block `warp` is this warp's to copy ----
+    // ---- the ring: the warps take turns to fill a stage; lane l looks after block l % 4 of the tile ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
-    // where the next copy is: its first key, its page's place in the table, its offset in the page
-    int ck = t0 * kTile + warp * 16, cp = ck / p.c.page_size, co = ck - cp * p.c.page_size;
-    const int copies = min(keys, t1 * kTile);
-    const float *ks_head = p.c.k_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK), *vs_head = p.c.v_scales + (int64_t)h * (p.c.page_size / PI_KV_BLOCK);
-    // lanes 0 and 1: a block's barrier counts lane 0's arrival and both lanes' scale copies
-    auto fetch = [&](int stage, int page) {        // page: table[cp], read ahead of time
-      if (ck < copies && lane < 2 && !dead) {
-        const int slot = stage * 4 + warp;
-        const uint32_t bar = smem_addr(&full[slot]);
-        float *sc = lane ? &scales[slot].y : &scales[slot].x;
-        if (page < 0 || page >= p.c.n_pages) {
-          *sc = -1.f;
-          if (lane == 0) {
-            atomicOr(p.c.status, pi::kKvBadPage);
-            bar_arrive(bar);
+    const int copies = min(keys, t1 * kTile), blocks = p.c.page_size / PI_KV_BLOCK;
+    const float *sc_head = ((lane & 4) ? p.c.v_scales : p.c.k_scales) + (int64_t)h * blocks;
+    // of the next tile: its first key, the page's place in the table and the offset in it of this lane's block
+    int ck = t0 * kTile, cp = (ck + (lane & 3) * 16) / p.c.page_size, co = ck + (lane & 3) * 16 - cp * p.c.page_size;
+    auto next_page = [&] { return ck + (lane & 3) * 16 < copies ? table[cp] : -1; };
+    auto fetch = [&](int st, int page, bool mine) {
+      if (ck < copies) {
+        if (used >> st & 1) {
+          if (mine && !dead && !bar_wait(smem_addr(&empty[st]), empty_ph >> st & 1)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+          empty_ph ^= 1u << st;
+        }
+        used |= 1u << st;
+        if (mine && !dead) {
+          const bool in = ck + (lane & 3) * 16 < copies, ok = in && page >= 0 && page < p.c.n_pages;
+          if (in && !ok && lane < 4) atomicOr(p.c.status, pi::kKvBadPage);
+          const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(ring + st * F::BYTES);
+          if (lane < 8) {
+            float *sc = &scales[st][lane >> 2][lane & 3];
+            if (ok)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(sc)),
+                           "l"(sc_head + (int64_t)page * p.c.heads * blocks + co / PI_KV_BLOCK) : "memory");
+            else
+              *sc = -1.f;
           }
-        } else {
-          if (lane == 0) {
-            const uint32_t dst = smem_addr(ring + slot * F::BYTES);
-            bar_expect(bar, F::BYTES);
+          const unsigned good = __ballot_sync(0xffffffffu, ok) & 15u;
+          if (!by16) {
+            const int z = __shfl_sync(0xffffffffu, page, 0) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, 0);
+            if (elect_one()) {
+              if (good & 1) {
+                bar_expect(bar, F::BYTES);
 #pragma unroll
-            for (int i = 0; i < F::BOXES; ++i) {
-              tile_copy(dst + i * 2048, &maps.k, i * 128, co, page * p.c.heads + h, bar);
-              tile_copy(dst + F::HALF + i * 2048, &maps.v, i * 128, co, page * p.c.heads + h, bar);
+                for (int i = 0; i < F::BOXES; ++i) {
+                  tile_copy(dst + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
+                  tile_copy(dst + F::V_AT + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
+                }
+              } else {
+                bar_arrive(bar);
+              }
+            }
+          } else {
+            if (elect_one()) bar_expect(bar, __popc(good) * (F::BYTES / 4));
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              const int z = __shfl_sync(0xffffffffu, page, b) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, b);
+              if ((good >> b & 1) && elect_one()) {
+#pragma unroll
+                for (int i = 0; i < F::BOXES; ++i) {
+                  tile_copy(dst + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
+                  tile_copy(dst + F::V_AT + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
+                }
+              }
+              __syncwarp();
             }
           }
-          const float *src = (lane ? vs_head : ks_head) + (int64_t)page * p.c.heads * (p.c.page_size / PI_KV_BLOCK) + co / PI_KV_BLOCK;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(sc)), "l"(src) : "memory");
+          __syncwarp();
+          if (lane < 8 && ok) bar_arrive_copies(bar); else bar_arrive(bar);
         }
-        bar_arrive_copies(bar);
+        pend |= 1u << st;
       }
       ck += kTile, co += kTile;
       while (co >= p.c.page_size) co -= p.c.page_size, ++cp;
     };
-    int page = ck < copies ? table[cp] : 0;
+    int page = next_page();
 #pragma unroll 1
     for (int i = 0; i < STAGES - 1; ++i) {
-      fetch(i, page);
-      page = ck < copies ? table[cp] : 0;
+      fetch(i, page, warp == 0);
+      page = next_page();
     }
     int stage = 0;
 
@@ -383,25 +419,18 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
     }
 
     for (int t = t0; t < t1; ++t) {
-      // the stage before has been read: by this warp, or by all that share it
-      if constexpr (WARPS_M > 1) __syncthreads(); else __syncwarp();
-      fetch(stage == 0 ? STAGES - 1 : stage - 1, page);
-      page = ck < copies ? table[cp] : 0;
-      const int slot0 = stage * 4;
+      const int st = stage;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
+      if (!dead && !bar_wait(smem_addr(&full[st]), full_ph >> st & 1)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      if (!dead) full_ph ^= 1u << st, pend &= ~(1u << st);
+      const char *tile = ring + st * F::BYTES;
 #pragma unroll 1
       for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
         const int k0 = t * kTile + blk * 16;
-        const int slot = slot0 + blk;
-        const char *src = ring + slot * F::BYTES;
-        if (k0 >= keys) break;
-        if (dead) continue;
-        if (!bar_wait(smem_addr(&full[slot]), parity >> slot & 1)) {
-          dead = true;
-          continue;
-        }
-        parity ^= 1u << slot;
-        const float ks = scales[slot].x, vs = scales[slot].y;
+        const char *src = tile + blk * 16 * F::BOX;
+        if (k0 >= keys || dead) break;
+        const float ks = scales[st][0][blk], vs = scales[st][1][blk];
         if (ks < 0.f) continue;
         // ---- x = q.k: tokens g and 8 + g, rows 2 q4 and 2 q4 + 1 of each eight ----
         float x[NB][4];
@@ -420,7 +449,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
             for (int nb = 0; nb < NB; ++nb) mma16816(x[nb], a, bq[nb][k][0], bq[nb][k][1]);
           }
         }
-        // ---- running maximum, taken up only where a score passes it ----
+        // ---- running maximum, taken up only where a score passes it by kSlack ----
         const bool ragged = k0 + 16 > min_lim;
         const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
         bool over = false;
@@ -430,7 +459,7 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
           for (int e = 0; e < 4; ++e) {
             x[nb][e] *= fac[nb][e & 1] * ks;
             if (ragged && k0 + g + 8 * (e >> 1) >= lim[nb][e & 1]) x[nb][e] = -INFINITY;
-            over |= x[nb][e] > fminf(m[nb][e & 1], R[nb][e & 1] - ev + kBoost);
+            over |= x[nb][e] > fminf(m[nb][e & 1], R[nb][e & 1] - ev + kBoost) + kSlack;
           }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -529,6 +558,11 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
             for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][2 * c + i], a, pb[nb][0], pb[nb][1]);
           }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&empty[st]));
+      // one stage is kept behind: the tile before this one has been read, or nearly, by every warp
+      fetch(st == 0 ? STAGES - 1 : st - 1, page, (t & 3) == warp);
+      page = next_page();
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -542,8 +576,8 @@ __global__ void __launch_bounds__(128) k_attn(const AttnParams p, const __grid_c
     const bool whole = t0 == 0 && t1 == tiles;
     float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
     if (dead) {                                    // copies may still be on their way: give them time, then leave
-      for (int i = 0; i < STAGES * 4; ++i)
-        if (WARPS_M > 1 || i % 4 == warp) bar_wait(smem_addr(&full[i]), parity >> i & 1);
+      for (int i = 0; i < STAGES; ++i)
+        if (pend >> i & 1) bar_wait(smem_addr(&full[i]), full_ph >> i & 1);
       if (lane == 0) atomicOr(p.c.status, pi::kKvTimeout);
       failed = 1;
     }
@@ -767,7 +801,7 @@ bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.heads};
   const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * c.page_size};
-  const cuuint32_t box[3] = {(cuuint32_t)Frag<D>::BOX, 16, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)Frag<D>::BOX, c.page_size % kTile ? 16u : (cuuint32_t)kTile, 1}, es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : D == 96 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -778,7 +812,7 @@ int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current
 template <int DT, int D, int NB, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   constexpr int ROWS = 8 * NB * WARPS_M;
-  constexpr int kRing = attn_stages<D, NB>() * 4 * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * ROWS * (D + 3) * 4 : 0;
+  constexpr int kRing = attn_stages<D, NB>() * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * ROWS * (D + 3) * 4 : 0;
   constexpr int smem = (kRing > kSums ? kRing : kSums) + 1024;
   static_assert(attn_stages<D, NB>() >= 2 && attn_stages<D, NB>() <= 8);
   AttnMaps maps;

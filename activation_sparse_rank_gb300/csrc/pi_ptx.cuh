@@ -45,6 +45,12 @@ __device__ __forceinline__ void tile_copy(uint32_t dst, const CUtensorMap *map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 // Orders this thread's shared-memory accesses before tile copies that it (or
 // a thread it synchronises with) issues afterwards.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
