@@ -1,11 +1,17 @@
 // Log-probabilities of given tokens, entropy and the most likely tokens.
 //
-//   m = max_j x_j,  Z = sum_j 2^(log2(e) (x_j - m)),  S = sum_j z_j 2^(z_j),  z_j = log2(e) (x_j - m)
+//   m = max_j x_j,  z_j = log2(e) (x_j - m),  Z = sum_j 2^z_j,  S = sum_j z_j 2^z_j
 //   lse = m + ln Z,  logprob = x_t - lse,  entropy = ln 2 (log2 Z - S / Z)
 //
-// The logits are read once, with a running maximum; Z and S move to a new
-// maximum as Z' = c Z, S' = c (S + (m - m') log2(e) Z), c = 2^(log2(e)(m - m')).
-// Bound by HBM for many rows; by latency for the few of a decode step.
+// Sums relative to one maximum move to another as Z' = c Z, S' = c (S + d Z)
+// with d = log2(e) (m - m'), c = 2^d.  Bound by HBM for many rows; by latency
+// for the few of a decode step.
+//
+// A row is read once and kept in registers (up to 128 bytes a thread; a cluster
+// of CTAs a row where one is too small or rows are few).  Each thread's maximum
+// gives its sums their reference and, together, the alternatives a bound: the
+// k-th largest of any selection of elements is at most the k-th largest of all.
+// Elements at or above that bound are few; they are ranked by counting.
 #include "pi_ops.cuh"
 
 #include <algorithm>
@@ -33,12 +39,19 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 struct Stats {
   float m, Z, S;
 };
 // Sums a relative to their own maxima, put together.
 __device__ __forceinline__ Stats join(Stats a, Stats b) {
-  const float m = fmaxf(a.m, b.m), ms = m == -INFINITY ? 0.f : m;
+  const float m = max_nan(a.m, b.m), ms = m == -INFINITY ? 0.f : m;
   const float da = (a.m - ms) * kLog2e, db = (b.m - ms) * kLog2e;
   const float ca = ex2(da), cb = ex2(db);
   // a part whose factor is 0 adds nothing (its difference may be -inf)
@@ -54,29 +67,304 @@ __device__ __forceinline__ unsigned long long order_key(float x, int j) {
   return (unsigned long long)b << 32 | (0xffffffffu - (unsigned)j);
 }
 
-template <int DT, int V>
-__global__ void __launch_bounds__(512) k_score(const ScoreParams p) {
+__device__ __forceinline__ float logit_of(unsigned long long key) {
+  const unsigned b = (unsigned)(key >> 32);
+  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+}
+// What the threads of a CTA's warps agree on for one row's outputs.
+__device__ __forceinline__ void write_stats(const ScoreParams &p, int row, const Stats &st, float lse, float x_target) {
+  if (p.lse) p.lse[row] = lse;
+  const bool none = !(fabsf(st.m) < INFINITY);       // NaN, +inf, or nothing but -inf
+  if (p.entropy) p.entropy[row] = none ? __uint_as_float(0x7fffffffu) : kLn2 * (log2f(st.Z) - st.S / st.Z);
+  if (p.logprob) {
+    const int t = p.target[row];
+    p.logprob[row] = t < 0 ? 0.f : t >= p.vocab || none ? __uint_as_float(0x7fffffffu) : x_target - lse;
+  }
+}
+__device__ __forceinline__ float lse_of(const Stats &st) {
+  return fabsf(st.m) < INFINITY ? st.m + log2f(st.Z) * kLn2 : st.m == -INFINITY ? st.m : __uint_as_float(0x7fffffffu);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Store into the same shared variable of the cluster's CTA 0.
+template <typename T>
+__device__ __forceinline__ void store_leader(T *p, unsigned long long v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+constexpr int kRegVecs = 8;          // 16-byte pieces of a row a thread holds
+constexpr int kList = 512;           // candidates ranked by counting
+constexpr int kMaxCluster = 8;
+
+// keys[0, n) (distinct): the k largest in order, to put(rank, key).
+template <typename F>
+__device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int k, F put) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const unsigned long long mine = keys[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += keys[j] > mine;
+    if (rank < k) put(rank, mine);
+  }
+}
+
+// One row for a cluster of CTAs; CTA r has the row's 16-byte pieces
+// [r share, (r + 1) share), thread t of it pieces t, t + NT, ....  Pieces start at
+// the last 16-byte boundary at or before the row: its first and last one may
+// hold elements of other rows, which are not read.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p, int share) {
   using E = Elem<DT>;
-  using P = Pack<DT, V>;
+  using T = typename E::T;
+  constexpr int V = 16 / sizeof(T), PP = V / 2, NW = NT / 32;
+  __shared__ Stats red[NW];
+  __shared__ unsigned tops[NW * 32];
+  __shared__ unsigned long long list[kList];
+  __shared__ unsigned long long in_keys[kMaxCluster][PI_MAX_TOP_K];
+  __shared__ unsigned long long in_mz[kMaxCluster], in_s[kMaxCluster];
+  __shared__ unsigned long long best_w[NW];
+  __shared__ int count, tau_s;
+  uint32_t rank, size;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  if (size > 1) cluster_arrive();                    // waited for before the leader's memory is written
+  const int row = blockIdx.x / size, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T *x = static_cast<const T *>(p.x) + row * p.stride;
+  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));      // elements of the first piece before the row
+  const uint4 *base = reinterpret_cast<const uint4 *>(x - off);
+  const int pieces = (int)(((int64_t)p.vocab + off + V - 1) / V);
+  const int first = rank * share, last = min(pieces, first + share);
+
+  uint4 raw[kRegVecs];
+  const unsigned low = DT == PI_DT_F32 ? 0xff800000u : DT == PI_DT_F16 ? 0xfc00fc00u : 0xff80ff80u;    // -inf
+#pragma unroll
+  for (int i = 0; i < kRegVecs; ++i) raw[i] = make_uint4(low, low, low, low);
+#pragma unroll
+  for (int i = 0; i < kRegVecs; ++i) {
+    const int c = first + i * NT + threadIdx.x;
+    if (c < last && c > 0 && c < pieces - 1) raw[i] = ld_stream(base + c);
+  }
+  auto edge = [&](int c) {                           // a piece that may be partly outside the row
+    alignas(16) T e[V];
+    *reinterpret_cast<uint4 *>(e) = make_uint4(low, low, low, low);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int j = c * V + k - off;
+      if (j >= 0 && j < p.vocab) e[k] = x[j];
+    }
+    return *reinterpret_cast<const uint4 *>(e);
+  };
+  if (threadIdx.x == 0 && rank == 0) raw[0] = edge(0);
+  if (pieces > 1 && pieces - 1 >= first && pieces - 1 < last && (pieces - 1 - first) % NT == threadIdx.x) {
+    const uint4 w = edge(pieces - 1);
+#pragma unroll
+    for (int i = 0; i < kRegVecs; ++i)
+      if ((pieces - 1 - first) / NT == i) raw[i] = w;
+  }
+
+  // The passes over raw[] widen it each on their own: kept from one to the next
+  // the widened values would take twice the registers.
+  auto forget = [&] {
+#pragma unroll
+    for (int i = 0; i < kRegVecs; ++i) asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
+  };
+  // ---- this thread's maximum and sums ----
+  float mt = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kRegVecs; ++i)
+    if (i == 0 || first + i * NT < last) {           // uniform: pieces of no thread
+      const unsigned w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      if constexpr (DT == PI_DT_F16) {
+        __half2 a = __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[0]), *reinterpret_cast<const __half2 *>(&w[1]));
+        a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[2]), *reinterpret_cast<const __half2 *>(&w[3])));
+        mt = max_nan(mt, max_nan(__low2float(a), __high2float(a)));
+      } else if constexpr (DT == PI_DT_BF16) {
+        __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]), *reinterpret_cast<const __nv_bfloat162 *>(&w[1]));
+        a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[2]), *reinterpret_cast<const __nv_bfloat162 *>(&w[3])));
+        mt = max_nan(mt, max_nan(__low2float(a), __high2float(a)));
+      } else {
+        mt = max_nan(mt, max_nan(max_nan(__uint_as_float(w[0]), __uint_as_float(w[1])), max_nan(__uint_as_float(w[2]), __uint_as_float(w[3]))));
+      }
+    }
+  Stats st{mt, 0.f, 0.f};
+  if (mt > -INFINITY) {                              // else nothing, or a NaN that m carries on
+    const f2 minus = f2_of(-mt, -mt), l2e = f2_of(kLog2e, kLog2e);
+    f2 Z = 0, S = 0;
+#pragma unroll
+    for (int i = 0; i < kRegVecs; ++i)
+      if (i == 0 || first + i * NT < last) {
+#pragma unroll
+        for (int j = 0; j < PP; ++j) {
+          float2 z = f2_get(f2_mul(f2_add(f2_from16<DT>(raw[i], j), minus), l2e));
+          z.x = fmaxf(z.x, -200.f), z.y = fmaxf(z.y, -200.f);     // 2^-200 is 0 here, and 0 (-200) is 0
+          const f2 zz = f2_of(z.x, z.y), w = f2_of(ex2(z.x), ex2(z.y));
+          Z = f2_add(Z, w);
+          S = f2_fma(w, zz, S);
+        }
+      }
+    st.Z = f2_sum(Z), st.S = f2_sum(S);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    st = join(st, Stats{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.Z, o),
+                        __shfl_xor_sync(0xffffffffu, st.S, o)});
+  if (lane == 0) red[warp] = st;
+
+  // ---- alternatives: the largest thread maxima of each warp bound the k-th element from below ----
+  const int K = p.top_k, M = min(32, max(4, (2 * K + NW - 1) / NW));
+  if (K) {
+    unsigned key = (unsigned)(order_key(mt, 0) >> 32), cur = first + (int)threadIdx.x < last ? key : 0u, kept = 0;
+    for (int r = 0; r < M; ++r) {
+      const unsigned mx = __reduce_max_sync(0xffffffffu, cur);
+      if (lane == r) kept = mx;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
+    }
+    if (lane < M) tops[warp * M + lane] = kept;
+    if (threadIdx.x == 0) count = 0, tau_s = 0;
+  }
+  __syncthreads();
+  st = red[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) st = join(st, red[w]);
+  int mine = 0;                                      // entries of this CTA's sorted list (in list[] for the leader's own use)
+  if (K) {
+    for (int i = threadIdx.x; i < NW * M; i += NT) {
+      const unsigned t = tops[i];
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < NW * M; ++j) above += tops[j] > t || (tops[j] == t && j < i);
+      if (above == K - 1) tau_s = (int)t;            // at least K elements are at or above it
+    }
+    __syncthreads();
+    const unsigned tau = (unsigned)tau_s;            // 0: fewer than K maxima, every element counts
+    const float floor = tau ? logit_of((unsigned long long)tau << 32) : -INFINITY;
+    auto push = [&](float f, int at) {               // NaN passes too
+      if (at < 0 || at >= p.vocab) return;
+      const int n = atomicAdd(&count, 1);
+      if (n < kList) list[n] = order_key(f, at);
+    };
+    forget();
+    if ((unsigned)(order_key(mt, 0) >> 32) >= tau) {
+#pragma unroll
+      for (int i = 0; i < kRegVecs; ++i) {
+        const int c = first + i * NT + threadIdx.x;
+        if (c >= last) continue;
+#pragma unroll
+        for (int j = 0; j < PP; ++j) {
+          const float2 f = f2_get(f2_from16<DT>(raw[i], j));
+          const int at = c * V + 2 * j - off;
+          if (!(f.x < floor)) push(f.x, at);
+          if (!(f.y < floor)) push(f.y, at + 1);
+        }
+      }
+    }
+    __syncthreads();
+    mine = min(K, count);
+    if (size > 1) cluster_wait();
+    auto put = [&](int r, unsigned long long key) { store_leader(&in_keys[rank][r], key); };
+    if (count <= kList) {
+      rank_keys(list, count, K, put);
+    } else {                                         // equal logits in great number: one after another
+      unsigned long long prev = ~0ull;
+      for (int r = 0; r < K; ++r) {
+        unsigned long long best = 0;
+        forget();
+#pragma unroll
+        for (int i = 0; i < kRegVecs; ++i) {
+          const int c = first + i * NT + threadIdx.x;
+          if (c >= last) continue;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float2 f = f2_get(f2_from16<DT>(raw[i], j / 2));
+            const int at = c * V + j - off;
+            const unsigned long long key = order_key(j & 1 ? f.y : f.x, at);
+            if (at >= 0 && at < p.vocab && key < prev && key > best) best = key;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (lane == 0) best_w[warp] = best;
+        __syncthreads();
+        prev = best_w[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) prev = max(prev, best_w[w]);
+        if (threadIdx.x == 0) put(r, prev);
+        __syncthreads();
+      }
+    }
+    for (int r = mine + threadIdx.x; r < K; r += NT) put(r, 0);
+  } else if (size > 1) {
+    cluster_wait();
+  }
+  if (threadIdx.x == 0) {
+    store_leader(&in_mz[rank], (unsigned long long)__float_as_uint(st.m) << 32 | __float_as_uint(st.Z));
+    store_leader(&in_s[rank], __float_as_uint(st.S));
+  }
+  if (size > 1) {
+    cluster_arrive();
+    if (rank) return;                                // its memory is nobody's to read
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+
+  // ---- the leader: the row's statistics and alternatives ----
+  st = Stats{-INFINITY, 0.f, 0.f};
+  for (uint32_t r = 0; r < size; ++r)
+    st = join(st, Stats{__uint_as_float((unsigned)(in_mz[r] >> 32)), __uint_as_float((unsigned)in_mz[r]), __uint_as_float((unsigned)in_s[r])});
+  const float lse = lse_of(st);
+  if (threadIdx.x == 0) {
+    const int t = p.logprob ? p.target[row] : -1;
+    write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(x[t]) : 0.f);
+  }
+  if (K) {
+    auto out = [&](int r, unsigned long long key) {
+      p.top_index[(int64_t)row * K + r] = (int)(0xffffffffu - (unsigned)key);
+      p.top_logprob[(int64_t)row * K + r] = st.m == -INFINITY ? __uint_as_float(0x7fffffffu) : logit_of(key) - lse;
+    };
+    if (size == 1) {
+      for (int r = threadIdx.x; r < K; r += NT) out(r, in_keys[0][r]);
+    } else {
+      // every CTA's list is sorted: a key's rank is its own place and how many of each other list are above it
+      for (int i = threadIdx.x; i < (int)size * K; i += NT) {
+        const int c = i / K, r = i % K;
+        const unsigned long long key = in_keys[c][r];
+        if (!key) continue;
+        int above = r;
+        for (int o = 0; o < (int)size; ++o) {
+          if (o == c) continue;
+          int lo = 0, hi = min(K, K - above);        // past K the key is out
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (in_keys[o][mid] > key) lo = mid + 1; else hi = mid;
+          }
+          above += lo;
+          if (above >= K) break;
+        }
+        if (above < K) out(above, key);
+      }
+    }
+  }
+}
+
+// Rows wider than a cluster's registers: one CTA a row, the row read once for
+// the sums and once for each alternative.
+template <int DT>
+__global__ void __launch_bounds__(512) k_score_wide(const ScoreParams p) {
+  using E = Elem<DT>;
   __shared__ Stats red[16];
   __shared__ unsigned long long kred[16];
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const typename E::T *x = static_cast<const typename E::T *>(p.x) + row * p.stride;
-  const int nv = p.vocab / V;
   Stats st{-INFINITY, 0.f, 0.f};
-  for (int i = threadIdx.x; i < nv; i += 512) {
-    const P raw = reinterpret_cast<const P *>(x)[i];
-    float f[V], m = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = E::to(raw.v[e]), m = fmaxf(m, f[e]);
-    if (m > st.m) st = join(st, Stats{m, 0.f, 0.f});
-    const float ms = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float z = (f[e] - ms) * kLog2e, w = ex2(z);
-      st.Z += w;
-      if (w > 0.f) st.S = fmaf(w, z, st.S);
-    }
+  for (int j = threadIdx.x; j < p.vocab; j += 512) {
+    const float f = E::to(x[j]);
+    if (!(f <= st.m)) st = join(st, Stats{f, 0.f, 0.f});       // NaN too
+    const float z = fmaxf((f - (st.m == -INFINITY ? 0.f : st.m)) * kLog2e, -200.f), w = ex2(z);
+    st.Z += w, st.S = fmaf(w, z, st.S);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
@@ -87,47 +375,69 @@ __global__ void __launch_bounds__(512) k_score(const ScoreParams p) {
   st = red[0];
 #pragma unroll
   for (int w = 1; w < 16; ++w) st = join(st, red[w]);
-  const float lse = st.m + log2f(st.Z) * kLn2;
+  const float lse = lse_of(st);
   if (threadIdx.x == 0) {
-    if (p.lse) p.lse[row] = lse;
-    if (p.entropy) p.entropy[row] = kLn2 * (log2f(st.Z) - st.S / st.Z);
-    if (p.logprob) {
-      const int t = p.target[row];
-      p.logprob[row] = t < 0 ? 0.f : t >= p.vocab ? __uint_as_float(0x7fffffffu) : E::to(x[t]) - lse;
-    }
+    const int t = p.logprob ? p.target[row] : -1;
+    write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(x[t]) : 0.f);
   }
-  unsigned long long last = ~0ull;
+  unsigned long long prev = ~0ull;
   for (int k = 0; k < p.top_k; ++k) {
     unsigned long long best = 0;
     for (int j = threadIdx.x; j < p.vocab; j += 512) {
       const unsigned long long key = order_key(E::to(x[j]), j);
-      if (key < last && key > best) best = key;
+      if (key < prev && key > best) best = key;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) kred[warp] = best;
     __syncthreads();
-    best = kred[0];
+    prev = kred[0];
 #pragma unroll
-    for (int w = 1; w < 16; ++w) best = max(best, kred[w]);
-    last = best;
+    for (int w = 1; w < 16; ++w) prev = max(prev, kred[w]);
     if (threadIdx.x == 0) {
-      const int j = (int)(0xffffffffu - (unsigned)best);
-      p.top_index[(int64_t)row * p.top_k + k] = j;
-      p.top_logprob[(int64_t)row * p.top_k + k] = E::to(x[j]) - lse;
+      p.top_index[(int64_t)row * p.top_k + k] = (int)(0xffffffffu - (unsigned)prev);
+      p.top_logprob[(int64_t)row * p.top_k + k] = st.m == -INFINITY ? __uint_as_float(0x7fffffffu) : logit_of(prev) - lse;
     }
     __syncthreads();
   }
 }
 
+template <int DT, int NT>
+cudaError_t launch_row(const ScoreParams &p, int pieces, int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.rows * cluster);
+  cfg.blockDim = dim3(NT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_score_row<DT, NT>, p, (pieces + cluster - 1) / cluster);
+}
+
 template <int DT>
-cudaError_t score_by_type(const ScoreParams &p, bool vec, cudaStream_t s) {
+cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(typename Elem<DT>::T);
-  if (vec)
-    k_score<DT, V><<<p.rows, 512, 0, s>>>(p);
-  else
-    k_score<DT, 1><<<p.rows, 512, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t pieces64 = ((int64_t)p.vocab + V - 1 + V - 1) / V;     // at the worst alignment
+  if (pieces64 > (int64_t)1024 * kRegVecs * kMaxCluster) {
+    k_score_wide<DT><<<p.rows, 512, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const int pieces = (int)pieces64;
+  auto fit = [&](int threads) {                      // CTAs of a cluster that hold a row
+    int c = 1;
+    while (c < kMaxCluster && (int64_t)threads * kRegVecs * c < pieces) c *= 2;
+    return c;
+  };
+  if (pieces <= 64 * kRegVecs) return launch_row<DT, 64>(p, pieces, 1, s);
+  // 256 threads a CTA, so that several are at different stages on an SM; more
+  // where a row needs them.  Few rows: as many CTAs as can share one.
+  int cluster = fit(256);
+  while (cluster < kMaxCluster && (int64_t)p.rows * cluster * 2 <= pi::current_sms() && pieces > 256 * cluster) cluster *= 2;
+  if (pieces <= 256 * kRegVecs * cluster) return launch_row<DT, 256>(p, pieces, cluster, s);
+  if (pieces <= 512 * kRegVecs * kMaxCluster) return launch_row<DT, 512>(p, pieces, kMaxCluster, s);
+  return launch_row<DT, 1024>(p, pieces, kMaxCluster, s);
 }
 
 }  // namespace
@@ -150,12 +460,10 @@ extern "C" pi_status pi_token_logprobs(const void *logits, int64_t row_stride, i
   if (!pi::aligned_to(target, 4) || !pi::aligned_to(logprob, 4) || !pi::aligned_to(entropy, 4) ||
       !pi::aligned_to(lse, 4) || !pi::aligned_to(top_index, 4) || !pi::aligned_to(top_logprob, 4))
     return pi::fail(PI_ERR_INVALID_ARG, "target and the outputs must be 4-byte aligned");
-  const int V = 16 / pi::dtype_size(dtype);
-  const bool vec = pi::aligned_to(logits, 16) && vocab % V == 0 && (rows == 1 || row_stride % V == 0);
   const ScoreParams p{logits, row_stride, rows, vocab, top_k, target, logprob, entropy, lse, top_index, top_logprob};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  PI_TRY_CUDA(dtype == PI_DT_F16    ? score_by_type<PI_DT_F16>(p, vec, s)
-              : dtype == PI_DT_BF16 ? score_by_type<PI_DT_BF16>(p, vec, s)
-                                    : score_by_type<PI_DT_F32>(p, vec, s));
+  PI_TRY_CUDA(dtype == PI_DT_F16    ? score_by_type<PI_DT_F16>(p, s)
+              : dtype == PI_DT_BF16 ? score_by_type<PI_DT_BF16>(p, s)
+                                    : score_by_type<PI_DT_F32>(p, s));
   return PI_OK;
 }
