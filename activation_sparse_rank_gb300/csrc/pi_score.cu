@@ -59,6 +59,16 @@ __device__ __forceinline__ Stats join(Stats a, Stats b) {
   return Stats{m, fmaf(ca, a.Z, cb * b.Z), sa + sb};
 }
 
+// The sums of a warp's 32 lanes, in every lane.
+__device__ __forceinline__ Stats warp_join(Stats a) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float d = (a.m - (m == -INFINITY ? 0.f : m)) * kLog2e, c = ex2(d);
+  const float S = c == 0.f ? 0.f : c * fmaf(d, a.Z, a.S);
+  return Stats{m, warp_sum(c * a.Z), warp_sum(S)};
+}
+
 // Order of the alternatives: larger logit first (NaN above all, -0 as 0), then smaller index.
 __device__ __forceinline__ unsigned long long order_key(float x, int j) {
   unsigned b = __float_as_uint(x == 0.f ? 0.f : x);
@@ -95,9 +105,45 @@ __device__ __forceinline__ void store_leader(T *p, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-constexpr int kRegVecs = 8;          // 16-byte pieces of a row a thread holds
-constexpr int kList = 512;           // candidates ranked by counting
+constexpr int kRegVecs = 16;         // 16-byte pieces of a row a thread holds
+constexpr int kSlots = 64;           // threads whose pieces are looked through for alternatives
+constexpr int kList = 256;           // alternatives ranked by counting
 constexpr int kMaxCluster = 8;
+
+// Largest element of a piece, NaN above all.
+template <int DT>
+__device__ __forceinline__ float piece_max(const uint4 &r) {
+  const unsigned w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (DT == PI_DT_F16) {
+    __half2 a = __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[0]), *reinterpret_cast<const __half2 *>(&w[1]));
+    a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[2]), *reinterpret_cast<const __half2 *>(&w[3])));
+    return max_nan(__low2float(a), __high2float(a));
+  } else if constexpr (DT == PI_DT_BF16) {
+    __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]), *reinterpret_cast<const __nv_bfloat162 *>(&w[1]));
+    a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[2]), *reinterpret_cast<const __nv_bfloat162 *>(&w[3])));
+    return max_nan(__low2float(a), __high2float(a));
+  } else {
+    return max_nan(max_nan(__uint_as_float(w[0]), __uint_as_float(w[1])), max_nan(__uint_as_float(w[2]), __uint_as_float(w[3])));
+  }
+}
+// The piece with nothing below `least` (a finite number, or the rounding of one up to the type's lowest).
+template <int DT>
+__device__ __forceinline__ uint4 clamp_piece(uint4 r, float least) {
+  unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == PI_DT_F16) {
+      const __half2 h = __hmax2(*reinterpret_cast<const __half2 *>(&w[k]), __half2half2(__float2half_rd(fmaxf(least, -65504.f))));
+      w[k] = *reinterpret_cast<const unsigned *>(&h);
+    } else if constexpr (DT == PI_DT_BF16) {
+      const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]), __bfloat162bfloat162(__float2bfloat16_rd(least)));
+      w[k] = *reinterpret_cast<const unsigned *>(&h);
+    } else {
+      w[k] = __float_as_uint(fmaxf(__uint_as_float(w[k]), least));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // keys[0, n) (distinct): the k largest in order, to put(rank, key).
 template <typename F>
@@ -111,22 +157,38 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
   }
 }
 
+template <int I>
+struct Int {
+  static constexpr int v = I;
+};
+// f(Int<0>) .. f(Int<N - 1>), written out: the row's registers are never indexed at run time.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    each<N, I + 1>(f);
+  }
+}
+
 // One row for a cluster of CTAs; CTA r has the row's 16-byte pieces
 // [r share, (r + 1) share), thread t of it pieces t, t + NT, ....  Pieces start at
 // the last 16-byte boundary at or before the row: its first and last one may
 // hold elements of other rows, which are not read.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p, int share) {
+__global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p, int share) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int V = 16 / sizeof(T), PP = V / 2, NW = NT / 32;
   __shared__ Stats red[NW];
   __shared__ unsigned tops[NW * 32];
   __shared__ unsigned long long list[kList];
+  __shared__ uint4 slots[kSlots][kRegVecs];
+  __shared__ int owner[kSlots];
   __shared__ unsigned long long in_keys[kMaxCluster][PI_MAX_TOP_K];
   __shared__ unsigned long long in_mz[kMaxCluster], in_s[kMaxCluster];
   __shared__ unsigned long long best_w[NW];
-  __shared__ int count, tau_s;
+  __shared__ int count, n_slots;
+  __shared__ unsigned tau_s;
   uint32_t rank, size;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
@@ -160,57 +222,39 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p
   if (threadIdx.x == 0 && rank == 0) raw[0] = edge(0);
   if (pieces > 1 && pieces - 1 >= first && pieces - 1 < last && (pieces - 1 - first) % NT == threadIdx.x) {
     const uint4 w = edge(pieces - 1);
-#pragma unroll
-    for (int i = 0; i < kRegVecs; ++i)
-      if ((pieces - 1 - first) / NT == i) raw[i] = w;
+    const int at = (pieces - 1 - first) / NT;
+    each<kRegVecs>([&](auto i) {
+      if (at == i.v) raw[i.v] = w;
+    });
   }
 
-  // The passes over raw[] widen it each on their own: kept from one to the next
-  // the widened values would take twice the registers.
-  auto forget = [&] {
-#pragma unroll
-    for (int i = 0; i < kRegVecs; ++i) asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
-  };
   // ---- this thread's maximum and sums ----
   float mt = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kRegVecs; ++i)
-    if (i == 0 || first + i * NT < last) {           // uniform: pieces of no thread
-      const unsigned w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      if constexpr (DT == PI_DT_F16) {
-        __half2 a = __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[0]), *reinterpret_cast<const __half2 *>(&w[1]));
-        a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[2]), *reinterpret_cast<const __half2 *>(&w[3])));
-        mt = max_nan(mt, max_nan(__low2float(a), __high2float(a)));
-      } else if constexpr (DT == PI_DT_BF16) {
-        __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]), *reinterpret_cast<const __nv_bfloat162 *>(&w[1]));
-        a = __hmax2_nan(a, __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[2]), *reinterpret_cast<const __nv_bfloat162 *>(&w[3])));
-        mt = max_nan(mt, max_nan(__low2float(a), __high2float(a)));
-      } else {
-        mt = max_nan(mt, max_nan(max_nan(__uint_as_float(w[0]), __uint_as_float(w[1])), max_nan(__uint_as_float(w[2]), __uint_as_float(w[3]))));
-      }
-    }
+  each<kRegVecs>([&](auto i) {
+    if (i.v == 0 || first + i.v * NT < last) mt = max_nan(mt, piece_max<DT>(raw[i.v]));    // uniform: pieces of no thread
+  });
   Stats st{mt, 0.f, 0.f};
   if (mt > -INFINITY) {                              // else nothing, or a NaN that m carries on
     const f2 minus = f2_of(-mt, -mt), l2e = f2_of(kLog2e, kLog2e);
+    // what is further below the maximum has weight 0 either way, and this way no 0 (-inf)
+    const float least = mt - 140.f;
     f2 Z = 0, S = 0;
-#pragma unroll
-    for (int i = 0; i < kRegVecs; ++i)
-      if (i == 0 || first + i * NT < last) {
+    each<kRegVecs>([&](auto i) {
+      if (i.v == 0 || first + i.v * NT < last) {
+        const uint4 r = clamp_piece<DT>(raw[i.v], least);
 #pragma unroll
         for (int j = 0; j < PP; ++j) {
-          float2 z = f2_get(f2_mul(f2_add(f2_from16<DT>(raw[i], j), minus), l2e));
-          z.x = fmaxf(z.x, -200.f), z.y = fmaxf(z.y, -200.f);     // 2^-200 is 0 here, and 0 (-200) is 0
-          const f2 zz = f2_of(z.x, z.y), w = f2_of(ex2(z.x), ex2(z.y));
+          const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
+          const float2 z = f2_get(zz);
+          const f2 w = f2_of(ex2(z.x), ex2(z.y));
           Z = f2_add(Z, w);
           S = f2_fma(w, zz, S);
         }
       }
+    });
     st.Z = f2_sum(Z), st.S = f2_sum(S);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    st = join(st, Stats{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.Z, o),
-                        __shfl_xor_sync(0xffffffffu, st.S, o)});
+  st = warp_join(st);
   if (lane == 0) red[warp] = st;
 
   // ---- alternatives: the largest thread maxima of each warp bound the k-th element from below ----
@@ -223,66 +267,68 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p
       if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
     }
     if (lane < M) tops[warp * M + lane] = kept;
-    if (threadIdx.x == 0) count = 0, tau_s = 0;
+    if (threadIdx.x == 0) count = 0, n_slots = 0, tau_s = 0xffffffffu;
   }
   __syncthreads();
-  st = red[0];
-#pragma unroll
-  for (int w = 1; w < NW; ++w) st = join(st, red[w]);
-  int mine = 0;                                      // entries of this CTA's sorted list (in list[] for the leader's own use)
+  if (warp == NW - 1) st = warp_join(lane < NW ? red[lane] : Stats{-INFINITY, 0.f, 0.f});     // of the CTA
+  int mine = 0;                                      // entries of this CTA's list
   if (K) {
     for (int i = threadIdx.x; i < NW * M; i += NT) {
       const unsigned t = tops[i];
       int above = 0;
-#pragma unroll 4
-      for (int j = 0; j < NW * M; ++j) above += tops[j] > t || (tops[j] == t && j < i);
-      if (above == K - 1) tau_s = (int)t;            // at least K elements are at or above it
+#pragma unroll 8
+      for (int j = 0; j < NW * M; ++j) above += tops[j] > t;
+      // at least K maxima are at or above the K-th; equal ones may skip the place itself
+      if (above < K) atomicMin(&tau_s, t);
     }
     __syncthreads();
-    const unsigned tau = (unsigned)tau_s;            // 0: fewer than K maxima, every element counts
+    const unsigned tau = NW * M < K ? 0u : tau_s;    // 0: fewer than K maxima, every element counts
     const float floor = tau ? logit_of((unsigned long long)tau << 32) : -INFINITY;
-    auto push = [&](float f, int at) {               // NaN passes too
-      if (at < 0 || at >= p.vocab) return;
-      const int n = atomicAdd(&count, 1);
-      if (n < kList) list[n] = order_key(f, at);
-    };
-    forget();
-    if ((unsigned)(order_key(mt, 0) >> 32) >= tau) {
-#pragma unroll
-      for (int i = 0; i < kRegVecs; ++i) {
-        const int c = first + i * NT + threadIdx.x;
+    // few threads have a candidate: their pieces go to shared memory and all threads look through them
+    if (first + (int)threadIdx.x < last && !(mt < floor)) {
+      const int n = atomicAdd(&n_slots, 1);
+      if (n < kSlots) {
+        owner[n] = threadIdx.x;
+        each<kRegVecs>([&](auto i) {
+          if (first + i.v * NT < last) slots[n][i.v] = raw[i.v];
+        });
+      }
+    }
+    __syncthreads();
+    const bool few = n_slots <= kSlots;
+    if (few) {
+      for (int i = threadIdx.x; i < n_slots * kRegVecs; i += NT) {
+        const int n = i / kRegVecs, c = first + i % kRegVecs * NT + owner[n];
         if (c >= last) continue;
+        const uint4 r = slots[n][i % kRegVecs];
+        if (piece_max<DT>(r) < floor) continue;
 #pragma unroll
-        for (int j = 0; j < PP; ++j) {
-          const float2 f = f2_get(f2_from16<DT>(raw[i], j));
-          const int at = c * V + 2 * j - off;
-          if (!(f.x < floor)) push(f.x, at);
-          if (!(f.y < floor)) push(f.y, at + 1);
+        for (int k = 0; k < V; ++k) {
+          const float2 f = f2_get(f2_from16<DT>(r, k / 2));
+          const float v = k & 1 ? f.y : f.x;
+          const int at = c * V + k - off;
+          if (v < floor || at < 0 || at >= p.vocab) continue;
+          const int m = atomicAdd(&count, 1);
+          if (m < kList) list[m] = order_key(v, at);
         }
       }
     }
     __syncthreads();
-    mine = min(K, count);
     if (size > 1) cluster_wait();
     auto put = [&](int r, unsigned long long key) { store_leader(&in_keys[rank][r], key); };
-    if (count <= kList) {
+    mine = K;
+    if (few && count <= kList) {
+      mine = min(K, count);
       rank_keys(list, count, K, put);
     } else {                                         // equal logits in great number: one after another
       unsigned long long prev = ~0ull;
       for (int r = 0; r < K; ++r) {
         unsigned long long best = 0;
-        forget();
-#pragma unroll
-        for (int i = 0; i < kRegVecs; ++i) {
-          const int c = first + i * NT + threadIdx.x;
-          if (c >= last) continue;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float2 f = f2_get(f2_from16<DT>(raw[i], j / 2));
-            const int at = c * V + j - off;
-            const unsigned long long key = order_key(j & 1 ? f.y : f.x, at);
-            if (at >= 0 && at < p.vocab && key < prev && key > best) best = key;
-          }
+        // read again (from L2): kept in registers to the end, the row would have to be unrolled here too
+        for (int64_t j = (int64_t)first * V - off + threadIdx.x; j < (int64_t)last * V - off; j += NT) {
+          if (j < 0 || j >= p.vocab) continue;
+          const unsigned long long key = order_key(E::to(x[j]), (int)j);
+          if (key < prev && key > best) best = key;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -299,7 +345,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p
   } else if (size > 1) {
     cluster_wait();
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == NT - 1) {
     store_leader(&in_mz[rank], (unsigned long long)__float_as_uint(st.m) << 32 | __float_as_uint(st.Z));
     store_leader(&in_s[rank], __float_as_uint(st.S));
   }
@@ -313,8 +359,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_score_row(const ScoreParams p
 
   // ---- the leader: the row's statistics and alternatives ----
   st = Stats{-INFINITY, 0.f, 0.f};
-  for (uint32_t r = 0; r < size; ++r)
-    st = join(st, Stats{__uint_as_float((unsigned)(in_mz[r] >> 32)), __uint_as_float((unsigned)in_mz[r]), __uint_as_float((unsigned)in_s[r])});
+  if (lane < (int)size)
+    st = Stats{__uint_as_float((unsigned)(in_mz[lane] >> 32)), __uint_as_float((unsigned)in_mz[lane]), __uint_as_float((unsigned)in_s[lane])};
+  st = warp_join(st);
   const float lse = lse_of(st);
   if (threadIdx.x == 0) {
     const int t = p.logprob ? p.target[row] : -1;
@@ -366,15 +413,10 @@ __global__ void __launch_bounds__(512) k_score_wide(const ScoreParams p) {
     const float z = fmaxf((f - (st.m == -INFINITY ? 0.f : st.m)) * kLog2e, -200.f), w = ex2(z);
     st.Z += w, st.S = fmaf(w, z, st.S);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    st = join(st, Stats{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.Z, o),
-                        __shfl_xor_sync(0xffffffffu, st.S, o)});
+  st = warp_join(st);
   if (lane == 0) red[warp] = st;
   __syncthreads();
-  st = red[0];
-#pragma unroll
-  for (int w = 1; w < 16; ++w) st = join(st, red[w]);
+  st = warp_join(lane < 16 ? red[lane] : Stats{-INFINITY, 0.f, 0.f});
   const float lse = lse_of(st);
   if (threadIdx.x == 0) {
     const int t = p.logprob ? p.target[row] : -1;
@@ -419,8 +461,10 @@ cudaError_t launch_row(const ScoreParams &p, int pieces, int cluster, cudaStream
 template <int DT>
 cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(typename Elem<DT>::T);
-  const int64_t pieces64 = ((int64_t)p.vocab + V - 1 + V - 1) / V;     // at the worst alignment
-  if (pieces64 > (int64_t)1024 * kRegVecs * kMaxCluster) {
+  // elements of a row's first piece before the row: the same for all, or the worst
+  const int e = 16 / V, off = p.rows == 1 || p.stride % V == 0 ? (int)((reinterpret_cast<uintptr_t>(p.x) & 15) / e) : V - 1;
+  const int64_t pieces64 = ((int64_t)p.vocab + off + V - 1) / V;
+  if (pieces64 > (int64_t)512 * kRegVecs * kMaxCluster) {
     k_score_wide<DT><<<p.rows, 512, 0, s>>>(p);
     return cudaGetLastError();
   }
@@ -436,8 +480,7 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   int cluster = fit(256);
   while (cluster < kMaxCluster && (int64_t)p.rows * cluster * 2 <= pi::current_sms() && pieces > 256 * cluster) cluster *= 2;
   if (pieces <= 256 * kRegVecs * cluster) return launch_row<DT, 256>(p, pieces, cluster, s);
-  if (pieces <= 512 * kRegVecs * kMaxCluster) return launch_row<DT, 512>(p, pieces, kMaxCluster, s);
-  return launch_row<DT, 1024>(p, pieces, kMaxCluster, s);
+  return launch_row<DT, 512>(p, pieces, kMaxCluster, s);
 }
 
 }  // namespace
