@@ -397,6 +397,251 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
   }
 }
 
+// Elements not below `floor` (a NaN is not) of the pieces that the lanes of
+// `mask` hold, into the list: the warp takes one piece after another, a lane an
+// element.  A call, because it is rare and would be unrolled over pieces.
+// at: index of the lane's piece's first element.
+template <int DT>
+__device__ __noinline__ void push_pieces(uint4 r, unsigned mask, int at, int vocab, float floor, unsigned long long *list,
+                                         int cap, int *count) {
+  constexpr int V = 16 / sizeof(typename Elem<DT>::T);
+  const int lane = threadIdx.x & 31, k = lane % V;
+  while (mask) {
+    const int src = __ffs(mask) - 1;
+    mask &= mask - 1;
+    const uint4 w = make_uint4(__shfl_sync(0xffffffffu, r.x, src), __shfl_sync(0xffffffffu, r.y, src),
+                               __shfl_sync(0xffffffffu, r.z, src), __shfl_sync(0xffffffffu, r.w, src));
+    const int j = __shfl_sync(0xffffffffu, at, src) + k;
+    const float2 f = f2_get(f2_from16<DT>(w, k / 2));
+    const float v = k & 1 ? f.y : f.x;
+    if (lane < V && !(v < floor) && j >= 0 && j < vocab) {
+      const int n = atomicAdd(count, 1);
+      if (n < cap) list[n] = order_key(v, j);
+    }
+    __syncwarp();
+  }
+}
+
+// Many rows: a persistent CTA takes whole rows, one after another, in batches of
+// kBatch pieces a thread that come through a ring in shared memory: a thread
+// copies its own pieces there (cp.async) and is the only one to read them, so a
+// batch needs no barrier, and what is on its way takes no registers.  Copies run
+// two batches ahead, into the next row too, so a row's reductions cost no
+// bandwidth.  The bound for alternatives is taken from the thread maxima after
+// batches 1, 2, 4, 8, ....
+constexpr int kBatch = 8, kStages = 3, kStreamThreads = 256;
+constexpr int kStreamSmem = kStages * kBatch * kStreamThreads * 16;
+template <int DT>
+__global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreParams p) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int NT = kStreamThreads, NW = NT / 32, V = 16 / sizeof(T), PP = V / 2, RB = kBatch, CAP = 4 * kList;
+  extern __shared__ __align__(16) uint4 ring[];      // [stage][piece][thread]
+  __shared__ Stats red[NW];
+  __shared__ unsigned tops[NW * 32];
+  __shared__ unsigned long long list[CAP], best[kList], best_w[NW];
+  __shared__ int count, n_best;
+  __shared__ unsigned tau_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.top_k;
+  const int M = min(32, max(4, (2 * K + NW - 1) / NW));
+  constexpr unsigned low = DT == PI_DT_F32 ? 0xff800000u : DT == PI_DT_F16 ? 0xfc00fc00u : 0xff80ff80u;    // -inf
+
+  struct Row {
+    const T *x;
+    int off, pieces;                                 // elements of the first piece before the row; pieces
+  };
+  auto row_at = [&](int r) {
+    Row w;
+    w.x = static_cast<const T *>(p.x) + r * p.stride;
+    w.off = (int)((reinterpret_cast<uintptr_t>(w.x) & 15) / sizeof(T));
+    w.pieces = (int)(((int64_t)p.vocab + w.off + V - 1) / V);
+    return w;
+  };
+  // the next batch to copy
+  int crow = blockIdx.x, cb = 0, cstage = 0;
+  Row cw = row_at(min(crow, p.rows - 1));
+  auto copy = [&] {
+    if (crow < p.rows) {
+      uint4 *dst = ring + cstage * RB * NT + threadIdx.x;
+      const uint4 *src = reinterpret_cast<const uint4 *>(cw.x - cw.off);
+      const int c0 = cb * RB * NT + threadIdx.x;
+      if (cb > 0 && (cb + 1) * RB * NT < cw.pieces) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst + i * NT)),
+                       "l"(src + c0 + i * NT) : "memory");
+      } else {                                       // the first and the last piece may hold elements of other rows
+#pragma unroll 1
+        for (int i = 0; i < RB; ++i) {
+          const int c = c0 + i * NT;
+          if (c > 0 && c < cw.pieces - 1) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst + i * NT)),
+                         "l"(src + c) : "memory");
+          } else {
+            uint4 r = make_uint4(low, low, low, low);
+            if (c < cw.pieces) {
+              alignas(16) T e[V];
+              *reinterpret_cast<uint4 *>(e) = r;
+#pragma unroll
+              for (int k = 0; k < V; ++k) {
+                const int j = c * V + k - cw.off;
+                if (j >= 0 && j < p.vocab) e[k] = cw.x[j];
+              }
+              r = *reinterpret_cast<const uint4 *>(e);
+            }
+            dst[i * NT] = r;
+          }
+        }
+      }
+      if ((cb + 1) * RB * NT >= cw.pieces) {
+        cb = 0, crow += gridDim.x;
+        if (crow < p.rows) cw = row_at(crow);
+      } else {
+        ++cb;
+      }
+    }
+    cstage = cstage + 1 == kStages ? 0 : cstage + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) copy();
+  if (threadIdx.x == 0) count = 0;
+
+  int stage = 0;
+#pragma unroll 1
+  for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const Row w = row_at(row);
+    Stats st{-INFINITY, 0.f, 0.f};
+    float floor = -INFINITY;
+#pragma unroll 1
+    for (int b = 0; b * RB * NT < w.pieces; ++b) {
+      copy();                                        // into the stage that the last batch left
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const uint4 *raw = ring + stage * RB * NT + threadIdx.x;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const int n = min(RB, (w.pieces - b * RB * NT + NT - 1) / NT);   // pieces of this batch that any thread has
+      float bm = -INFINITY;
+      if (n == RB) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) bm = max_nan(bm, piece_max<DT>(raw[i * NT]));
+      } else {
+        for (int i = 0; i < n; ++i) bm = max_nan(bm, piece_max<DT>(raw[i * NT]));
+      }
+      const float m = max_nan(st.m, bm);
+      if (K) {
+        if ((b & (b + 1)) == 0) {
+          unsigned cur = (int)threadIdx.x < w.pieces ? (unsigned)(order_key(m, 0) >> 32) : 0u, kept = 0;
+#pragma unroll 1
+          for (int r = 0; r < M; ++r) {
+            const unsigned mx = __reduce_max_sync(0xffffffffu, cur);
+            if (lane == r) kept = mx;
+            if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
+          }
+          if (lane < M) tops[warp * M + lane] = kept;
+          if (threadIdx.x == 0) tau_s = 0xffffffffu;
+          __syncthreads();
+          for (int i = threadIdx.x; i < NW * M; i += NT) {
+            const unsigned t = tops[i];
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < NW * M; ++j) above += tops[j] > t;
+            if (above < K) atomicMin(&tau_s, t);
+          }
+          __syncthreads();
+          floor = tau_s ? logit_of((unsigned long long)tau_s << 32) : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, !(bm < floor))) {
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            const uint4 r = raw[i * NT];
+            const int c = (b * RB + i) * NT + threadIdx.x;
+            const unsigned hit = __ballot_sync(0xffffffffu, c < w.pieces && !(piece_max<DT>(r) < floor));
+            if (hit) push_pieces<DT>(r, hit, c * V - w.off, p.vocab, floor, list, CAP, &count);
+          }
+        }
+      }
+      if (m > -INFINITY) {
+        const float d = (st.m - m) * kLog2e, c = ex2(d);
+        f2 Z = f2_of(c * st.Z, 0.f), S = f2_of(c == 0.f ? 0.f : c * fmaf(d, st.Z, st.S), 0.f);
+        const f2 minus = f2_of(-m, -m), l2e = f2_of(kLog2e, kLog2e);
+        const float least = m - 140.f;               // as in k_score_row
+        auto add = [&](int i) {
+          const uint4 r = clamp_piece<DT>(raw[i * NT], least);
+#pragma unroll
+          for (int j = 0; j < PP; ++j) {
+            const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
+            const float2 z = f2_get(zz);
+            const f2 e = f2_of(ex2(z.x), ex2(z.y));
+            Z = f2_add(Z, e);
+            S = f2_fma(e, zz, S);
+          }
+        };
+        if (n == RB) {
+#pragma unroll
+          for (int i = 0; i < RB; ++i) add(i);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) add(i);
+        }
+        st.Z = f2_sum(Z), st.S = f2_sum(S);
+      }
+      st.m = m;
+      __syncwarp();
+    }
+
+    // ---- the row's results ----
+    st = warp_join(st);
+    if (lane == 0) red[warp] = st;
+    if (threadIdx.x == 0) n_best = 0;
+    __syncthreads();
+    st = warp_join(lane < NW ? red[lane] : Stats{-INFINITY, 0.f, 0.f});
+    const float lse = lse_of(st);
+    if (threadIdx.x == 0) {
+      const int t = p.logprob ? p.target[row] : -1;
+      write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(w.x[t]) : 0.f);
+    }
+    if (K) {
+      auto out = [&](int k, unsigned long long key) {
+        p.top_index[(int64_t)row * K + k] = (int)(0xffffffffu - (unsigned)key);
+        p.top_logprob[(int64_t)row * K + k] = st.m == -INFINITY ? __uint_as_float(0x7fffffffu) : logit_of(key) - lse;
+      };
+      const int n = count;
+      const unsigned tau = floor == -INFINITY ? 0u : (unsigned)(order_key(floor, 0) >> 32);
+      if (n <= CAP)
+        for (int i = threadIdx.x; i < n; i += NT)
+          if ((unsigned)(list[i] >> 32) >= tau) {    // the last bound drops most of what earlier ones let in
+            const int k = atomicAdd(&n_best, 1);
+            if (k < kList) best[k] = list[i];
+          }
+      __syncthreads();
+      if (n <= CAP && n_best <= kList) {
+        rank_keys(best, n_best, K, out);
+      } else {                                       // equal logits in great number: one after another, read again
+        unsigned long long prev = ~0ull;
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+          unsigned long long top = 0;
+          for (int j = threadIdx.x; j < p.vocab; j += NT) {
+            const unsigned long long key = order_key(E::to(w.x[j]), j);
+            if (key < prev && key > top) top = key;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0) best_w[warp] = top;
+          __syncthreads();
+          prev = best_w[0];
+#pragma unroll
+          for (int i = 1; i < NW; ++i) prev = max(prev, best_w[i]);
+          if (threadIdx.x == 0) out(k, prev);
+          __syncthreads();
+        }
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) count = 0;                 // before the next row's first bound, whose barriers order it
+  }
+}
+
 // Rows wider than a cluster's registers: one CTA a row, the row read once for
 // the sums and once for each alternative.
 template <int DT>
@@ -475,6 +720,12 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
     return c;
   };
   if (pieces <= 64 * kRegVecs) return launch_row<DT, 64>(p, pieces, 1, s);
+  if (p.rows >= 2 * pi::current_sms()) {
+    const cudaError_t e = cudaFuncSetAttribute(k_score_stream<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    if (e != cudaSuccess) return e;
+    k_score_stream<DT><<<2 * pi::current_sms(), kStreamThreads, kStreamSmem, s>>>(p);
+    return cudaGetLastError();
+  }
   // 256 threads a CTA, so that several are at different stages on an SM; more
   // where a row needs them.  Few rows: as many CTAs as can share one.
   int cluster = fit(256);

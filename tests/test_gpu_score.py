@@ -49,6 +49,23 @@ def test_values(pi, dtype, rows, vocab, k):
     check(pi, x, rng.integers(0, vocab, rows), k)
 
 
+@pytest.mark.parametrize("dtype,vocab,k", [("float16", 17003, 20), ("bfloat16", 40000, 64), ("float32", 9001, 5), ("bfloat16", 33001, 0)])
+def test_many_rows(pi, dtype, vocab, k):
+    """More rows than the GPU has places for, with ties, masks and special rows among them."""
+    x = logits(307, vocab, dtype, seed=k)
+    x[3] = 2.0
+    x[4] = -torch.inf
+    x[5, 1000:] = -torch.inf
+    x[7] = torch.round(x[7])
+    x[9, vocab - 1] = torch.nan
+    x[11, 0] = torch.inf
+    x[13] = torch.linspace(-90, 90, vocab).to(x.dtype)
+    x[15] = torch.linspace(90, -90, vocab).to(x.dtype)
+    x[17, :-1] = -torch.inf
+    rng = np.random.default_rng(1)
+    check(pi, x, rng.integers(0, vocab, 307), k)
+
+
 @pytest.mark.parametrize("vocab", [40, 1003, 40000, 131072])
 def test_ties(pi, vocab):
     """Equal logits: everywhere, in coarse steps, at the border of the top k, zeros of both signs."""
