@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
     for (int i = 0; i < NV; ++i) {
       const int v = lane + 32 * i, r = v / VR - at.off;
       if (r < 0 || r >= at.n) continue;
-      f2 f[4] = {0, 0, 0, 0};
+      f2 f[4] = {};
       if (ok) {
         decode8(f, c[i]);
 #pragma unroll

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
       }
     }
     at = at + 1 == p.stages ? 0 : at + 1;
-    f2 s = 0, q = 0;                                 // 0: two zeros
+    f2 s = f2_of(0.f, 0.f), q = s;
 #pragma unroll
     for (int j = 0; j < NP; ++j) s = f2_add(s, v[j]);
     const float mean = cta_sum<NT>(f2_sum(s), red[turn][0]) / (float)p.d;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGra
 
   f2 dw[NP], db[NP], w[HOLD ? NP : 1];
 #pragma unroll
-  for (int j = 0; j < NP; ++j) dw[j] = 0, db[j] = 0;
+  for (int j = 0; j < NP; ++j) dw[j] = db[j] = f2_of(0.f, 0.f);
   if constexpr (HOLD) load_cols<X, VEC, NT, NV>(w, p.w, p.w_dt, t, p.d, 1.f);
 
   int turn = 0, at = 0;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGra
     const f2 minus = f2_of(-mean, -mean), scale = f2_of(rstd, rstd);
     if constexpr (VEC) copy_wait(p.stages - 1);
     // pass 1: h and g (0 past the row's end, where dy is read as 0), the column sums and the row's two sums
-    f2 h[NP], gg[NP], s1 = 0, s2 = 0;
+    f2 h[NP], gg[NP], s1 = f2_of(0.f, 0.f), s2 = s1;
     auto form = [&](f2 *ho, f2 *go, bool sums) {
       f2 xs[VEC ? 1 : NP], ys[VEC ? 1 : NP];
       f2 wl[HOLD ? 1 : NP];

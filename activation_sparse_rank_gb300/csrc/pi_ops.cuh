@@ -55,39 +55,16 @@ __device__ __forceinline__ float load_any(const void *p, int dt, size_t i) {
   return static_cast<const float *>(p)[i];
 }
 
-// Two binary32 values in one 64-bit register pair: sm_100 and later add,
+// Two binary32 values in one register pair: sm_100 and later add,
 // multiply and fuse both in one instruction, each half rounded as the scalar
 // operation rounds.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 f2_of(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_get(f2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ float f2_sum(f2 a) {
-  const float2 r = f2_get(a);
-  return r.x + r.y;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+using f2 = float2;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ float2 f2_get(f2 a) { return a; }
+__device__ __forceinline__ float f2_sum(f2 a) { return a.x + a.y; }
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c); }
 // A 32-bit word of two 16-bit elements, and back (each rounded to nearest even).
 template <int DT>
 __device__ __forceinline__ f2 f2_widen(unsigned w) {

@@ -107,7 +107,7 @@ __device__ __forceinline__ void store_leader(T *p, unsigned long long v) {
 
 constexpr int kRegVecs = 16;         // 16-byte pieces of a row a thread holds
 constexpr int kSlots = 64;           // threads whose pieces are looked through for alternatives
-constexpr int kList = 256;           // alternatives ranked by counting
+constexpr int kList = 512;           // alternatives ranked by counting
 constexpr int kMaxCluster = 8;
 
 // Largest element of a piece, NaN above all.
@@ -157,6 +157,162 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
   }
 }
 
+// A row as 16-byte pieces: they start at the last 16-byte boundary at or before
+// it, and its first and last one may hold elements of other rows.
+template <int DT>
+struct Row {
+  using T = typename Elem<DT>::T;
+  static constexpr int V = 16 / sizeof(T);
+  const T *x;
+  int off, pieces, vocab;                            // elements of the first piece before the row; pieces; elements
+  __device__ __forceinline__ Row(const ScoreParams &p, int r) {
+    x = static_cast<const T *>(p.x) + r * p.stride;
+    off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    vocab = p.vocab;
+    pieces = (int)(((int64_t)vocab + off + V - 1) / V);
+  }
+  __device__ __forceinline__ const uint4 *base() const { return reinterpret_cast<const uint4 *>(x - off); }
+  __device__ __forceinline__ bool inner(int c) const { return c > 0 && c < pieces - 1; }
+  // Piece c with -inf for what is not the row's (not read).
+  __device__ __forceinline__ uint4 edge(int c) const {
+    constexpr unsigned low = DT == PI_DT_F32 ? 0xff800000u : DT == PI_DT_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    alignas(16) T e[V];
+    *reinterpret_cast<uint4 *>(e) = make_uint4(low, low, low, low);
+    if (c < pieces) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int j = c * V + k - off;
+        if (j >= 0 && j < vocab) e[k] = x[j];
+      }
+    }
+    return *reinterpret_cast<const uint4 *>(e);
+  }
+};
+
+template <int NW>
+struct TopShared {
+  unsigned tops[NW * 32];
+  unsigned long long list[kList], best[NW];
+  int owner[kSlots], counts[NW];
+  int n_list, n_owners;
+  unsigned tau;
+};
+
+// The k largest keys of pieces [first, last) of a row, in order, to put(rank,
+// key); returns how many there are.  mt: the largest element of this thread's
+// pieces first + t, first + t + NT, ....  The whole CTA calls it.
+//
+// The k-th largest of any of the elements is at most the k-th largest of all: the
+// thread maxima give a bound, and few threads have anything at or above it.
+// Their pieces are read again, from L2, by all threads.
+template <int DT, int NT, typename F>
+__device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, float mt, int K, TopShared<NT / 32> &sh, F put) {
+  using E = Elem<DT>;
+  constexpr int NW = NT / 32, V = Row<DT>::V;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, M = min(32, max(4, (2 * K + NW - 1) / NW));
+  const int begin = max(0, first * V - w.off), end = min(w.vocab, last * V - w.off);      // elements
+  const unsigned key = first + (int)threadIdx.x < last ? (unsigned)(order_key(mt, 0) >> 32) : 0u;
+  unsigned cur = key, kept = 0;                      // 0: no element
+#pragma unroll 1
+  for (int r = 0; r < M; ++r) {                      // the M largest of each warp
+    const unsigned mx = __reduce_max_sync(0xffffffffu, cur);
+    if (lane == r) kept = mx;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
+  }
+  if (lane < M) sh.tops[warp * M + lane] = kept;
+  if (threadIdx.x == 0) sh.tau = NW * M < K ? 0u : 0xffffffffu, sh.n_list = sh.n_owners = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < NW * M; i += NT) {
+    const unsigned t = sh.tops[i];
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < NW * M; ++j) above += sh.tops[j] > t;
+    if (above < K) atomicMin(&sh.tau, t);
+  }
+  __syncthreads();
+  const unsigned tau = sh.tau;
+  // elements whose key is `low` or more, of the threads whose maximum is, into the list; false if they are too many
+  auto collect = [&](unsigned low) {
+    if (key && key >= low) {
+      const int n = atomicAdd(&sh.n_owners, 1);
+      if (n < kSlots) sh.owner[n] = threadIdx.x;
+    }
+    __syncthreads();
+    const int each = (last - first + NT - 1) / NT, n = sh.n_owners;
+    if (n <= kSlots) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < n * each; i += NT) {
+        const int c = first + i % each * NT + sh.owner[i / each];
+        if (c >= last) continue;
+        const uint4 r = w.inner(c) ? ld_stream(w.base() + c) : w.edge(c);
+        if ((unsigned)(order_key(piece_max<DT>(r), 0) >> 32) < low) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float2 f = f2_get(f2_from16<DT>(r, k / 2));
+          const int at = c * V + k - w.off;
+          const unsigned long long e = order_key(k & 1 ? f.y : f.x, at);
+          if ((unsigned)(e >> 32) < low || at < 0 || at >= w.vocab) continue;
+          const int m = atomicAdd(&sh.n_list, 1);
+          if (m < kList) sh.list[m] = e;
+        }
+      }
+    }
+    __syncthreads();
+    return n <= kSlots && sh.n_list <= kList;
+  };
+  if (collect(tau)) {
+    rank_keys(sh.list, sh.n_list, K, put);
+    return min(K, sh.n_list);
+  }
+  // Many equal to the bound (masked rows): those above it, of fewer than K threads, then the equal ones by index.
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n_list = sh.n_owners = 0;
+  __syncthreads();
+  if (tau != 0xffffffffu ? collect(tau + 1) : true) {
+    int found = min(K, sh.n_list);
+    rank_keys(sh.list, sh.n_list, K, put);
+#pragma unroll 1
+    for (int j0 = begin; j0 < end && found < K; j0 += NT) {
+      const int j = j0 + threadIdx.x;
+      const unsigned long long e = j < end ? order_key(E::to(w.x[j]), j) : 0;
+      const bool hit = j < end && (unsigned)(e >> 32) == tau;
+      const unsigned mask = __ballot_sync(0xffffffffu, hit);
+      if (lane == 0) sh.counts[warp] = __popc(mask);
+      __syncthreads();
+      int at = found + __popc(mask & ((1u << lane) - 1)), all = found;
+      for (int i = 0; i < NW; ++i) {
+        if (i < warp) at += sh.counts[i];
+        all += sh.counts[i];
+      }
+      if (hit && at < K) put(at, e);
+      found = min(K, all);
+      __syncthreads();
+    }
+    return found;
+  }
+  // Many above it in few threads: one after another.
+  unsigned long long prev = ~0ull;
+  int found = 0;
+#pragma unroll 1
+  for (; found < min(K, end - begin); ++found) {
+    unsigned long long best = 0;
+    for (int j = begin + threadIdx.x; j < end; j += NT) {
+      const unsigned long long e = order_key(E::to(w.x[j]), j);
+      if (e < prev && e > best) best = e;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) sh.best[warp] = best;
+    __syncthreads();
+    prev = sh.best[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) prev = max(prev, sh.best[i]);
+    if (threadIdx.x == 0) put(found, prev);
+    __syncthreads();
+  }
+  return found;
+}
+
 template <int I>
 struct Int {
   static constexpr int v = I;
@@ -170,35 +326,24 @@ __device__ __forceinline__ void each(F f) {
   }
 }
 
-// One row for a cluster of CTAs; CTA r has the row's 16-byte pieces
-// [r share, (r + 1) share), thread t of it pieces t, t + NT, ....  Pieces start at
-// the last 16-byte boundary at or before the row: its first and last one may
-// hold elements of other rows, which are not read.
+// One row for a cluster of CTAs; CTA r has the row's pieces [r share, (r + 1)
+// share), thread t of it pieces t, t + NT, ..., which it keeps in registers from
+// the maximum to the sums.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p, int share) {
   using E = Elem<DT>;
-  using T = typename E::T;
-  constexpr int V = 16 / sizeof(T), PP = V / 2, NW = NT / 32;
+  constexpr int V = Row<DT>::V, PP = V / 2, NW = NT / 32;
   __shared__ Stats red[NW];
-  __shared__ unsigned tops[NW * 32];
-  __shared__ unsigned long long list[kList];
-  __shared__ uint4 slots[kSlots][kRegVecs];
-  __shared__ int owner[kSlots];
+  __shared__ TopShared<NW> sh;
   __shared__ unsigned long long in_keys[kMaxCluster][PI_MAX_TOP_K];
   __shared__ unsigned long long in_mz[kMaxCluster], in_s[kMaxCluster];
-  __shared__ unsigned long long best_w[NW];
-  __shared__ int count, n_slots;
-  __shared__ unsigned tau_s;
   uint32_t rank, size;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   if (size > 1) cluster_arrive();                    // waited for before the leader's memory is written
-  const int row = blockIdx.x / size, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T *x = static_cast<const T *>(p.x) + row * p.stride;
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));      // elements of the first piece before the row
-  const uint4 *base = reinterpret_cast<const uint4 *>(x - off);
-  const int pieces = (int)(((int64_t)p.vocab + off + V - 1) / V);
-  const int first = rank * share, last = min(pieces, first + share);
+  const int row = blockIdx.x / size, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.top_k;
+  const Row<DT> w(p, row);
+  const int first = rank * share, last = min(w.pieces, first + share);
 
   uint4 raw[kRegVecs];
   const unsigned low = DT == PI_DT_F32 ? 0xff800000u : DT == PI_DT_F16 ? 0xfc00fc00u : 0xff80ff80u;    // -inf
@@ -207,24 +352,14 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
 #pragma unroll
   for (int i = 0; i < kRegVecs; ++i) {
     const int c = first + i * NT + threadIdx.x;
-    if (c < last && c > 0 && c < pieces - 1) raw[i] = ld_stream(base + c);
+    if (c < last && w.inner(c)) raw[i] = ld_stream(w.base() + c);
   }
-  auto edge = [&](int c) {                           // a piece that may be partly outside the row
-    alignas(16) T e[V];
-    *reinterpret_cast<uint4 *>(e) = make_uint4(low, low, low, low);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int j = c * V + k - off;
-      if (j >= 0 && j < p.vocab) e[k] = x[j];
-    }
-    return *reinterpret_cast<const uint4 *>(e);
-  };
-  if (threadIdx.x == 0 && rank == 0) raw[0] = edge(0);
-  if (pieces > 1 && pieces - 1 >= first && pieces - 1 < last && (pieces - 1 - first) % NT == threadIdx.x) {
-    const uint4 w = edge(pieces - 1);
-    const int at = (pieces - 1 - first) / NT;
+  if (threadIdx.x == 0 && rank == 0) raw[0] = w.edge(0);
+  if (w.pieces > 1 && w.pieces - 1 >= first && w.pieces - 1 < last && (w.pieces - 1 - first) % NT == threadIdx.x) {
+    const uint4 r = w.edge(w.pieces - 1);
+    const int at = (w.pieces - 1 - first) / NT;
     each<kRegVecs>([&](auto i) {
-      if (at == i.v) raw[i.v] = w;
+      if (at == i.v) raw[i.v] = r;
     });
   }
 
@@ -238,7 +373,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
     const f2 minus = f2_of(-mt, -mt), l2e = f2_of(kLog2e, kLog2e);
     // what is further below the maximum has weight 0 either way, and this way no 0 (-inf)
     const float least = mt - 140.f;
-    f2 Z = 0, S = 0;
+    f2 Z = f2_of(0.f, 0.f), S = Z;
     each<kRegVecs>([&](auto i) {
       if (i.v == 0 || first + i.v * NT < last) {
         const uint4 r = clamp_piece<DT>(raw[i.v], least);
@@ -246,104 +381,24 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
         for (int j = 0; j < PP; ++j) {
           const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
           const float2 z = f2_get(zz);
-          const f2 w = f2_of(ex2(z.x), ex2(z.y));
-          Z = f2_add(Z, w);
-          S = f2_fma(w, zz, S);
+          const f2 e = f2_of(ex2(z.x), ex2(z.y));
+          Z = f2_add(Z, e);
+          S = f2_fma(e, zz, S);
         }
       }
     });
     st.Z = f2_sum(Z), st.S = f2_sum(S);
   }
+  __syncwarp();
   st = warp_join(st);
   if (lane == 0) red[warp] = st;
-
-  // ---- alternatives: the largest thread maxima of each warp bound the k-th element from below ----
-  const int K = p.top_k, M = min(32, max(4, (2 * K + NW - 1) / NW));
-  if (K) {
-    unsigned key = (unsigned)(order_key(mt, 0) >> 32), cur = first + (int)threadIdx.x < last ? key : 0u, kept = 0;
-    for (int r = 0; r < M; ++r) {
-      const unsigned mx = __reduce_max_sync(0xffffffffu, cur);
-      if (lane == r) kept = mx;
-      if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
-    }
-    if (lane < M) tops[warp * M + lane] = kept;
-    if (threadIdx.x == 0) count = 0, n_slots = 0, tau_s = 0xffffffffu;
-  }
   __syncthreads();
   if (warp == NW - 1) st = warp_join(lane < NW ? red[lane] : Stats{-INFINITY, 0.f, 0.f});     // of the CTA
-  int mine = 0;                                      // entries of this CTA's list
+  if (size > 1) cluster_wait();
   if (K) {
-    for (int i = threadIdx.x; i < NW * M; i += NT) {
-      const unsigned t = tops[i];
-      int above = 0;
-#pragma unroll 8
-      for (int j = 0; j < NW * M; ++j) above += tops[j] > t;
-      // at least K maxima are at or above the K-th; equal ones may skip the place itself
-      if (above < K) atomicMin(&tau_s, t);
-    }
-    __syncthreads();
-    const unsigned tau = NW * M < K ? 0u : tau_s;    // 0: fewer than K maxima, every element counts
-    const float floor = tau ? logit_of((unsigned long long)tau << 32) : -INFINITY;
-    // few threads have a candidate: their pieces go to shared memory and all threads look through them
-    if (first + (int)threadIdx.x < last && !(mt < floor)) {
-      const int n = atomicAdd(&n_slots, 1);
-      if (n < kSlots) {
-        owner[n] = threadIdx.x;
-        each<kRegVecs>([&](auto i) {
-          if (first + i.v * NT < last) slots[n][i.v] = raw[i.v];
-        });
-      }
-    }
-    __syncthreads();
-    const bool few = n_slots <= kSlots;
-    if (few) {
-      for (int i = threadIdx.x; i < n_slots * kRegVecs; i += NT) {
-        const int n = i / kRegVecs, c = first + i % kRegVecs * NT + owner[n];
-        if (c >= last) continue;
-        const uint4 r = slots[n][i % kRegVecs];
-        if (piece_max<DT>(r) < floor) continue;
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float2 f = f2_get(f2_from16<DT>(r, k / 2));
-          const float v = k & 1 ? f.y : f.x;
-          const int at = c * V + k - off;
-          if (v < floor || at < 0 || at >= p.vocab) continue;
-          const int m = atomicAdd(&count, 1);
-          if (m < kList) list[m] = order_key(v, at);
-        }
-      }
-    }
-    __syncthreads();
-    if (size > 1) cluster_wait();
     auto put = [&](int r, unsigned long long key) { store_leader(&in_keys[rank][r], key); };
-    mine = K;
-    if (few && count <= kList) {
-      mine = min(K, count);
-      rank_keys(list, count, K, put);
-    } else {                                         // equal logits in great number: one after another
-      unsigned long long prev = ~0ull;
-      for (int r = 0; r < K; ++r) {
-        unsigned long long best = 0;
-        // read again (from L2): kept in registers to the end, the row would have to be unrolled here too
-        for (int64_t j = (int64_t)first * V - off + threadIdx.x; j < (int64_t)last * V - off; j += NT) {
-          if (j < 0 || j >= p.vocab) continue;
-          const unsigned long long key = order_key(E::to(x[j]), (int)j);
-          if (key < prev && key > best) best = key;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane == 0) best_w[warp] = best;
-        __syncthreads();
-        prev = best_w[0];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) prev = max(prev, best_w[w]);
-        if (threadIdx.x == 0) put(r, prev);
-        __syncthreads();
-      }
-    }
-    for (int r = mine + threadIdx.x; r < K; r += NT) put(r, 0);
-  } else if (size > 1) {
-    cluster_wait();
+    const int n = cta_top<DT, NT>(w, first, last, mt, K, sh, put);
+    for (int r = n + threadIdx.x; r < K; r += NT) put(r, 0);
   }
   if (threadIdx.x == NT - 1) {
     store_leader(&in_mz[rank], (unsigned long long)__float_as_uint(st.m) << 32 | __float_as_uint(st.Z));
@@ -365,7 +420,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
   const float lse = lse_of(st);
   if (threadIdx.x == 0) {
     const int t = p.logprob ? p.target[row] : -1;
-    write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(x[t]) : 0.f);
+    write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(w.x[t]) : 0.f);
   }
   if (K) {
     auto out = [&](int r, unsigned long long key) {
@@ -397,105 +452,46 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
   }
 }
 
-// Elements not below `floor` (a NaN is not) of the pieces that the lanes of
-// `mask` hold, into the list: the warp takes one piece after another, a lane an
-// element.  A call, because it is rare and would be unrolled over pieces.
-// at: index of the lane's piece's first element.
-template <int DT>
-__device__ __noinline__ void push_pieces(uint4 r, unsigned mask, int at, int vocab, float floor, unsigned long long *list,
-                                         int cap, int *count) {
-  constexpr int V = 16 / sizeof(typename Elem<DT>::T);
-  const int lane = threadIdx.x & 31, k = lane % V;
-  while (mask) {
-    const int src = __ffs(mask) - 1;
-    mask &= mask - 1;
-    const uint4 w = make_uint4(__shfl_sync(0xffffffffu, r.x, src), __shfl_sync(0xffffffffu, r.y, src),
-                               __shfl_sync(0xffffffffu, r.z, src), __shfl_sync(0xffffffffu, r.w, src));
-    const int j = __shfl_sync(0xffffffffu, at, src) + k;
-    const float2 f = f2_get(f2_from16<DT>(w, k / 2));
-    const float v = k & 1 ? f.y : f.x;
-    if (lane < V && !(v < floor) && j >= 0 && j < vocab) {
-      const int n = atomicAdd(count, 1);
-      if (n < cap) list[n] = order_key(v, j);
-    }
-    __syncwarp();
-  }
-}
-
 // Many rows: a persistent CTA takes whole rows, one after another, in batches of
 // kBatch pieces a thread that come through a ring in shared memory: a thread
 // copies its own pieces there (cp.async) and is the only one to read them, so a
 // batch needs no barrier, and what is on its way takes no registers.  Copies run
-// two batches ahead, into the next row too, so a row's reductions cost no
-// bandwidth.  The bound for alternatives is taken from the thread maxima after
-// batches 1, 2, 4, 8, ....
-constexpr int kBatch = 8, kStages = 3, kStreamThreads = 256;
+// two batches ahead, into the next row too, so what is done at a row's end costs
+// little bandwidth.
+constexpr int kBatch = 4, kStages = 3, kStreamThreads = 256, kStreamCtas = 4;
 constexpr int kStreamSmem = kStages * kBatch * kStreamThreads * 16;
 template <int DT>
-__global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreParams p) {
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) k_score_stream(const ScoreParams p) {
   using E = Elem<DT>;
-  using T = typename E::T;
-  constexpr int NT = kStreamThreads, NW = NT / 32, V = 16 / sizeof(T), PP = V / 2, RB = kBatch, CAP = 4 * kList;
+  constexpr int NT = kStreamThreads, NW = NT / 32, PP = Row<DT>::V / 2, RB = kBatch;
   extern __shared__ __align__(16) uint4 ring[];      // [stage][piece][thread]
   __shared__ Stats red[NW];
-  __shared__ unsigned tops[NW * 32];
-  __shared__ unsigned long long list[CAP], best[kList], best_w[NW];
-  __shared__ int count, n_best;
-  __shared__ unsigned tau_s;
+  __shared__ TopShared<NW> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.top_k;
-  const int M = min(32, max(4, (2 * K + NW - 1) / NW));
-  constexpr unsigned low = DT == PI_DT_F32 ? 0xff800000u : DT == PI_DT_F16 ? 0xfc00fc00u : 0xff80ff80u;    // -inf
 
-  struct Row {
-    const T *x;
-    int off, pieces;                                 // elements of the first piece before the row; pieces
-  };
-  auto row_at = [&](int r) {
-    Row w;
-    w.x = static_cast<const T *>(p.x) + r * p.stride;
-    w.off = (int)((reinterpret_cast<uintptr_t>(w.x) & 15) / sizeof(T));
-    w.pieces = (int)(((int64_t)p.vocab + w.off + V - 1) / V);
-    return w;
-  };
   // the next batch to copy
   int crow = blockIdx.x, cb = 0, cstage = 0;
-  Row cw = row_at(min(crow, p.rows - 1));
+  Row<DT> cw(p, min(crow, p.rows - 1));
   auto copy = [&] {
     if (crow < p.rows) {
       uint4 *dst = ring + cstage * RB * NT + threadIdx.x;
-      const uint4 *src = reinterpret_cast<const uint4 *>(cw.x - cw.off);
       const int c0 = cb * RB * NT + threadIdx.x;
-      if (cb > 0 && (cb + 1) * RB * NT < cw.pieces) {
+      const bool inner = cb > 0 && (cb + 1) * RB * NT < cw.pieces;
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
+      for (int i = 0; i < RB; ++i) {
+        const int c = c0 + i * NT;
+        if (inner || cw.inner(c))
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst + i * NT)),
-                       "l"(src + c0 + i * NT) : "memory");
-      } else {                                       // the first and the last piece may hold elements of other rows
+                       "l"(cw.base() + c) : "memory");
+      }
+      if (!inner) {
 #pragma unroll 1
-        for (int i = 0; i < RB; ++i) {
-          const int c = c0 + i * NT;
-          if (c > 0 && c < cw.pieces - 1) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst + i * NT)),
-                         "l"(src + c) : "memory");
-          } else {
-            uint4 r = make_uint4(low, low, low, low);
-            if (c < cw.pieces) {
-              alignas(16) T e[V];
-              *reinterpret_cast<uint4 *>(e) = r;
-#pragma unroll
-              for (int k = 0; k < V; ++k) {
-                const int j = c * V + k - cw.off;
-                if (j >= 0 && j < p.vocab) e[k] = cw.x[j];
-              }
-              r = *reinterpret_cast<const uint4 *>(e);
-            }
-            dst[i * NT] = r;
-          }
-        }
+        for (int i = 0; i < RB; ++i)
+          if (!cw.inner(c0 + i * NT)) dst[i * NT] = cw.edge(c0 + i * NT);
       }
       if ((cb + 1) * RB * NT >= cw.pieces) {
         cb = 0, crow += gridDim.x;
-        if (crow < p.rows) cw = row_at(crow);
+        if (crow < p.rows) cw = Row<DT>(p, crow);
       } else {
         ++cb;
       }
@@ -505,14 +501,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreP
   };
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) copy();
-  if (threadIdx.x == 0) count = 0;
 
   int stage = 0;
 #pragma unroll 1
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const Row w = row_at(row);
+    const Row<DT> w(p, row);
     Stats st{-INFINITY, 0.f, 0.f};
-    float floor = -INFINITY;
 #pragma unroll 1
     for (int b = 0; b * RB * NT < w.pieces; ++b) {
       copy();                                        // into the stage that the last batch left
@@ -520,69 +514,28 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreP
       const uint4 *raw = ring + stage * RB * NT + threadIdx.x;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       const int n = min(RB, (w.pieces - b * RB * NT + NT - 1) / NT);   // pieces of this batch that any thread has
-      float bm = -INFINITY;
-      if (n == RB) {
+      float m = st.m;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) bm = max_nan(bm, piece_max<DT>(raw[i * NT]));
-      } else {
-        for (int i = 0; i < n; ++i) bm = max_nan(bm, piece_max<DT>(raw[i * NT]));
-      }
-      const float m = max_nan(st.m, bm);
-      if (K) {
-        if ((b & (b + 1)) == 0) {
-          unsigned cur = (int)threadIdx.x < w.pieces ? (unsigned)(order_key(m, 0) >> 32) : 0u, kept = 0;
-#pragma unroll 1
-          for (int r = 0; r < M; ++r) {
-            const unsigned mx = __reduce_max_sync(0xffffffffu, cur);
-            if (lane == r) kept = mx;
-            if (lane == __ffs(__ballot_sync(0xffffffffu, cur == mx)) - 1) cur = 0;
-          }
-          if (lane < M) tops[warp * M + lane] = kept;
-          if (threadIdx.x == 0) tau_s = 0xffffffffu;
-          __syncthreads();
-          for (int i = threadIdx.x; i < NW * M; i += NT) {
-            const unsigned t = tops[i];
-            int above = 0;
-#pragma unroll 8
-            for (int j = 0; j < NW * M; ++j) above += tops[j] > t;
-            if (above < K) atomicMin(&tau_s, t);
-          }
-          __syncthreads();
-          floor = tau_s ? logit_of((unsigned long long)tau_s << 32) : -INFINITY;
-        }
-        if (__any_sync(0xffffffffu, !(bm < floor))) {
-#pragma unroll 1
-          for (int i = 0; i < n; ++i) {
-            const uint4 r = raw[i * NT];
-            const int c = (b * RB + i) * NT + threadIdx.x;
-            const unsigned hit = __ballot_sync(0xffffffffu, c < w.pieces && !(piece_max<DT>(r) < floor));
-            if (hit) push_pieces<DT>(r, hit, c * V - w.off, p.vocab, floor, list, CAP, &count);
-          }
-        }
-      }
+      for (int i = 0; i < RB; ++i)
+        if (i < n) m = max_nan(m, piece_max<DT>(raw[i * NT]));
       if (m > -INFINITY) {
         const float d = (st.m - m) * kLog2e, c = ex2(d);
         f2 Z = f2_of(c * st.Z, 0.f), S = f2_of(c == 0.f ? 0.f : c * fmaf(d, st.Z, st.S), 0.f);
         const f2 minus = f2_of(-m, -m), l2e = f2_of(kLog2e, kLog2e);
         const float least = m - 140.f;               // as in k_score_row
-        auto add = [&](int i) {
-          const uint4 r = clamp_piece<DT>(raw[i * NT], least);
 #pragma unroll
-          for (int j = 0; j < PP; ++j) {
-            const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
-            const float2 z = f2_get(zz);
-            const f2 e = f2_of(ex2(z.x), ex2(z.y));
-            Z = f2_add(Z, e);
-            S = f2_fma(e, zz, S);
+        for (int i = 0; i < RB; ++i)
+          if (i < n) {
+            const uint4 r = clamp_piece<DT>(raw[i * NT], least);
+#pragma unroll
+            for (int j = 0; j < PP; ++j) {
+              const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
+              const float2 z = f2_get(zz);
+              const f2 e = f2_of(ex2(z.x), ex2(z.y));
+              Z = f2_add(Z, e);
+              S = f2_fma(e, zz, S);
+            }
           }
-        };
-        if (n == RB) {
-#pragma unroll
-          for (int i = 0; i < RB; ++i) add(i);
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < n; ++i) add(i);
-        }
         st.Z = f2_sum(Z), st.S = f2_sum(S);
       }
       st.m = m;
@@ -590,9 +543,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreP
     }
 
     // ---- the row's results ----
+    const float mt = st.m;
     st = warp_join(st);
     if (lane == 0) red[warp] = st;
-    if (threadIdx.x == 0) n_best = 0;
     __syncthreads();
     st = warp_join(lane < NW ? red[lane] : Stats{-INFINITY, 0.f, 0.f});
     const float lse = lse_of(st);
@@ -600,45 +553,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_score_stream(const ScoreP
       const int t = p.logprob ? p.target[row] : -1;
       write_stats(p, row, st, lse, t >= 0 && t < p.vocab ? E::to(w.x[t]) : 0.f);
     }
-    if (K) {
-      auto out = [&](int k, unsigned long long key) {
+    if (K)
+      cta_top<DT, NT>(w, 0, w.pieces, mt, K, sh, [&](int k, unsigned long long key) {
         p.top_index[(int64_t)row * K + k] = (int)(0xffffffffu - (unsigned)key);
         p.top_logprob[(int64_t)row * K + k] = st.m == -INFINITY ? __uint_as_float(0x7fffffffu) : logit_of(key) - lse;
-      };
-      const int n = count;
-      const unsigned tau = floor == -INFINITY ? 0u : (unsigned)(order_key(floor, 0) >> 32);
-      if (n <= CAP)
-        for (int i = threadIdx.x; i < n; i += NT)
-          if ((unsigned)(list[i] >> 32) >= tau) {    // the last bound drops most of what earlier ones let in
-            const int k = atomicAdd(&n_best, 1);
-            if (k < kList) best[k] = list[i];
-          }
-      __syncthreads();
-      if (n <= CAP && n_best <= kList) {
-        rank_keys(best, n_best, K, out);
-      } else {                                       // equal logits in great number: one after another, read again
-        unsigned long long prev = ~0ull;
-#pragma unroll 1
-        for (int k = 0; k < K; ++k) {
-          unsigned long long top = 0;
-          for (int j = threadIdx.x; j < p.vocab; j += NT) {
-            const unsigned long long key = order_key(E::to(w.x[j]), j);
-            if (key < prev && key > top) top = key;
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) best_w[warp] = top;
-          __syncthreads();
-          prev = best_w[0];
-#pragma unroll
-          for (int i = 1; i < NW; ++i) prev = max(prev, best_w[i]);
-          if (threadIdx.x == 0) out(k, prev);
-          __syncthreads();
-        }
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) count = 0;                 // before the next row's first bound, whose barriers order it
+      });
+    __syncthreads();                                 // red and sh are free for the next row
   }
 }
 
@@ -723,7 +643,7 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   if (p.rows >= 2 * pi::current_sms()) {
     const cudaError_t e = cudaFuncSetAttribute(k_score_stream<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
     if (e != cudaSuccess) return e;
-    k_score_stream<DT><<<2 * pi::current_sms(), kStreamThreads, kStreamSmem, s>>>(p);
+    k_score_stream<DT><<<kStreamCtas * pi::current_sms(), kStreamThreads, kStreamSmem, s>>>(p);
     return cudaGetLastError();
   }
   // 256 threads a CTA, so that several are at different stages on an SM; more
