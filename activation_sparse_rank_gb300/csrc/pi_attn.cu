@@ -817,7 +817,8 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   static_assert(attn_stages<D, NB>() >= 2 && attn_stages<D, NB>() <= 8);
   AttnMaps maps;
   if (!encode_codes<D>(&maps.k, p.c, p.c.k_codes) || !encode_codes<D>(&maps.v, p.c, p.c.v_codes)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_attn<DT, D, NB, WARPS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = pi::allow_smem(k_attn<DT, D, NB, WARPS_M>, smem, smem, done);
   if (e != cudaSuccess) return e;
   k_attn<DT, D, NB, WARPS_M><<<p.grid, 128, smem, s>>>(p, maps);
   e = cudaGetLastError();

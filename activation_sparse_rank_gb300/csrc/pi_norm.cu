@@ -454,12 +454,8 @@ __global__ void __launch_bounds__(256) k_norm_colsum(const float *__restrict__ p
 }
 
 // Stages of a ring: up to four, in what a CTA may have of an SM's 224 KB.
+constexpr size_t kRingMost = 224 * 1024;
 int ring_stages(int stage_bytes, int ctas_per_sm) { return std::max(1, std::min(4, 224 * 1024 / ctas_per_sm / stage_bytes)); }
-
-template <typename Kern>
-cudaError_t allow_smem(Kern *k, size_t bytes) {
-  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
 
 template <int X, bool VEC, int NT, int NV, bool WREG>
 cudaError_t launch_norm(NormParams p, cudaStream_t s) {
@@ -474,7 +470,8 @@ cudaError_t launch_norm(NormParams p, cudaStream_t s) {
     p.stage_bytes = NV * CT * per_pack;
     p.stages = std::min(ring_stages(p.stage_bytes, per_sm), (p.rows - 1) / (int)(grid * GROUPS) + 1);
     smem = (size_t)p.stages * p.stage_bytes;
-    const cudaError_t e = allow_smem(k_norm<X, VEC, NT, NV, WREG>, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = pi::allow_smem(k_norm<X, VEC, NT, NV, WREG>, smem, kRingMost, done);
     if (e != cudaSuccess) return e;
   }
   k_norm<X, VEC, NT, NV, WREG><<<grid, CT, smem, s>>>(p);
@@ -528,7 +525,8 @@ cudaError_t launch_grad(NormGradParams p, cudaStream_t s) {
     p.stages = ring_stages(p.stage_bytes, NT <= 512 ? 2 : 1);
   }
   const size_t smem = (size_t)p.stages * p.stage_bytes + (NT < 128 ? 2 * p.d * sizeof(float) : 0);
-  const cudaError_t e = allow_smem(k_norm_grad<X, VEC, NT, NV>, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = pi::allow_smem(k_norm_grad<X, VEC, NT, NV>, smem, kRingMost, done);
   if (e != cudaSuccess) return e;
   k_norm_grad<X, VEC, NT, NV><<<grid, CT, smem, s>>>(p);
   return cudaGetLastError();

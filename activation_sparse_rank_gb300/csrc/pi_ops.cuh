@@ -3,6 +3,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "pi_internal.cuh"
 
 namespace pi {
@@ -16,6 +18,22 @@ inline int dtype_size(int dt) { return dt == PI_DT_F32 ? 4 : 2; }
 
 // SMs of the current device (cached per device; 0 if the runtime has no device).
 int current_sms();
+
+// Let kernel k use `bytes` of dynamic shared memory, of which it never uses more
+// than `most`: asked of the runtime once per device and kernel (`done`: a bit a
+// device, each instantiation has its own).
+template <typename Kern>
+cudaError_t allow_smem(Kern *k, size_t bytes, size_t most, std::atomic<uint64_t> &done) {
+  if (bytes <= 40 * 1024) return cudaSuccess;        // with the static part still below the default limit
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 }  // namespace pi
 

@@ -641,7 +641,8 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   };
   if (pieces <= 64 * kRegVecs) return launch_row<DT, 64>(p, pieces, 1, s);
   if (p.rows >= 2 * pi::current_sms()) {
-    const cudaError_t e = cudaFuncSetAttribute(k_score_stream<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = pi::allow_smem(k_score_stream<DT>, kStreamSmem, kStreamSmem, done);
     if (e != cudaSuccess) return e;
     k_score_stream<DT><<<kStreamCtas * pi::current_sms(), kStreamThreads, kStreamSmem, s>>>(p);
     return cudaGetLastError();

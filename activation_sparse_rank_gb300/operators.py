@@ -40,9 +40,10 @@ def _dev(t: torch.Tensor, device: Optional[torch.device], name: str) -> torch.de
     """t is a CUDA tensor, on `device` if given."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-    return t.device
+    at = t.device
+    if device is not None and at != device:
+        raise ValueError(f"{name} is on {at}, not {device}")
+    return at
 
 
 def _whole(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
@@ -72,10 +73,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device   # a CUDA tensor exists: no set-up
+
+
 def _on(device: torch.device, stream, fn, *args):
     """fn(stream handle, *args) with `device` current and allocations on the call's stream."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
+        if _current_device() == device.index:
             return fn(_raw_stream(device.index), *args)
         with torch.cuda.device(device):
             return fn(_raw_stream(device.index), *args)
@@ -259,42 +263,45 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, y=None, sum=None, 
         if not _fits(weight, (d,), weight.dtype, dev):
             _whole(weight, (d,), weight.dtype, dev, "weight")
     if bias is not None:
+        if weight is not None and bias.dtype is not weight.dtype:
+            raise TypeError("weight and bias must have one type")
         w_dt = _dt(bias, "bias")
         if not _fits(bias, (d,), bias.dtype, dev):
             _whole(bias, (d,), bias.dtype, dev, "bias")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have one type")
     if add is not None:
         if not _fits(add, x.shape, add.dtype, dev):
             _whole(add, x.shape, add.dtype, dev, "add")
     elif sum is not None:
         raise ValueError("sum needs add")
-    return _on(dev, stream, _norm, x, rows, d, stride, dt, weight, bias, w_dt, eps, add, y, sum, mean, rstd, want_stats)
 
+    def run(handle):
+        nonlocal y, sum, mean, rstd
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        elif not _fits(y, x.shape, x.dtype, dev):
+            _whole(y, x.shape, x.dtype, dev, "y")
+        if add is not None:
+            if sum is None:
+                sum = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            elif not _fits(sum, x.shape, x.dtype, dev):
+                _whole(sum, x.shape, x.dtype, dev, "sum")
+        if mean is not None:
+            _whole(mean, (rows,), _f32, dev, "mean")
+        elif want_stats:
+            mean = torch.empty(rows, dtype=_f32, device=dev)
+        if rstd is not None:
+            _whole(rstd, (rows,), _f32, dev, "rstd")
+        elif want_stats:
+            rstd = torch.empty(rows, dtype=_f32, device=dev)
+        return lib.pi_layer_norm(
+            x.data_ptr(), stride, add.data_ptr() if add is not None else None, _DT[add.dtype] if add is not None else 0,
+            weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, w_dt, rows, d,
+            dt, eps, y.data_ptr(), sum.data_ptr() if sum is not None else None,
+            mean.data_ptr() if mean is not None else None, rstd.data_ptr() if rstd is not None else None, handle)
 
-def _norm(handle, x, rows, d, stride, dt, weight, bias, w_dt, eps, add, y, sum, mean, rstd, want_stats):
-    dev, shape = x.device, x.shape
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
-    elif not _fits(y, shape, x.dtype, dev):
-        _whole(y, shape, x.dtype, dev, "y")
-    if add is None:
-        pass
-    elif sum is None:
-        sum = torch.empty(shape, dtype=x.dtype, device=dev)
-    elif not _fits(sum, shape, x.dtype, dev):
-        _whole(sum, shape, x.dtype, dev, "sum")
-    if mean is not None:
-        _whole(mean, (rows,), _f32, dev, "mean")
-    elif want_stats:
-        mean = torch.empty(rows, dtype=_f32, device=dev)
-    if rstd is not None:
-        _whole(rstd, (rows,), _f32, dev, "rstd")
-    elif want_stats:
-        rstd = torch.empty(rows, dtype=_f32, device=dev)
-    _check(lib.pi_layer_norm(x.data_ptr(), stride, _ptr(add), 0 if add is None else _dt(add, "add"), _ptr(weight),
-                             _ptr(bias), w_dt, rows, d, dt, eps, y.data_ptr(), _ptr(sum), _ptr(mean), _ptr(rstd),
-                             handle), "pi_layer_norm")
+    if add is not None and add.dtype not in _DT:
+        raise TypeError(f"add must be float16, bfloat16 or float32, not {add.dtype}")
+    _check(_on(dev, stream, run), "pi_layer_norm")
     return y, sum, mean, rstd
 
 
@@ -363,14 +370,17 @@ def token_logprobs(logits, targets=None, top_k=0, stream=None) -> TokenScores:
 
 def _score(handle, logits, rows, vocab, dt, targets, top_k):
     dev = logits.device
+    index = value = logprob = None
     entropy = torch.empty(rows, dtype=_f32, device=dev)
     lse = torch.empty(rows, dtype=_f32, device=dev)
-    logprob = None if targets is None else torch.empty(rows, dtype=_f32, device=dev)
-    index = value = None
+    if targets is not None:
+        logprob = torch.empty(rows, dtype=_f32, device=dev)
     if top_k > 0:
         index = torch.empty((rows, top_k), dtype=_i32, device=dev)
         value = torch.empty((rows, top_k), dtype=_f32, device=dev)
-    _check(lib.pi_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
-                                 _ptr(targets), top_k, _ptr(logprob), entropy.data_ptr(), lse.data_ptr(), _ptr(index),
-                                 _ptr(value), handle), "pi_token_logprobs")
+    _check(lib.pi_token_logprobs(
+        logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
+        targets.data_ptr() if targets is not None else None, top_k, logprob.data_ptr() if targets is not None else None,
+        entropy.data_ptr(), lse.data_ptr(), index.data_ptr() if top_k > 0 else None,
+        value.data_ptr() if top_k > 0 else None, handle), "pi_token_logprobs")
     return TokenScores(logprob, entropy, lse, index, value)
