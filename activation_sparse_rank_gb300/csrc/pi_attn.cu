@@ -24,43 +24,13 @@
 // units form one line that is cut evenly over the CTAs, so a batch of very
 // different lengths keeps every SM busy to the end.  A unit cut between CTAs
 // leaves partial sums, which k_attn_combine adds in CTA order.
-#include "pi_kv.cuh"
-#include "pi_ops.cuh"
-#include "pi_ptx.cuh"
+#include "pi_attn.cuh"
 
-#include <algorithm>
-
-using namespace pidev;
+using namespace attn;
 
 namespace {
 
 constexpr int kTile = 64;                 // keys of a tile
-// The second product's weights 2^(x + ev - R) reach 2^(kBoost + kSlack), inside
-// fp16, and are subnormal only below 2^-(14 + kBoost) of the largest.  kSlack:
-// m and R follow a score only where it passes them by that much; the sums do
-// not depend on m and R, and most steps then leave the accumulators alone.
-constexpr float kBoost = 6.f, kSlack = 8.f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnParams {
-  pi_kv_cache c;
-  pi_kv_tokens tok;
-  const int32_t *length;
-  const void *q;
-  int64_t qt, qh;
-  void *out;
-  float *lse;
-  float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
-  float scale;             // sm_scale log2(e)
-  int q_heads, group, max_q, causal, row_tiles, grid;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void mma16816(float *c, const unsigned *a, unsigned b0, unsigned b1) {
   asm volatile(
@@ -68,84 +38,6 @@ __device__ __forceinline__ void mma16816(float *c, const unsigned *a, unsigned b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// Four codes as two fp16 pairs: one instruction each.
-__device__ __forceinline__ void widen4(unsigned w, unsigned &lo, unsigned &hi) {
-  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
-}
-__device__ __forceinline__ unsigned pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const unsigned *>(&h);
-}
-
-// Sequence s as the kernels see it: lengths made safe, faults flagged by flag_seq.
-struct Seq {
-  int row0, n, rows, len, first;    // packed row, query tokens used, query rows, keys, position of the first token
-};
-template <int ROWS>
-__device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
-  Seq q;
-  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1];
-  const int n = r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens ? 0 : r1 - r0;
-  const int64_t cap = min((int64_t)p.tok.table_stride * p.c.page_size, (int64_t)1 << 30);
-  const int len = p.length[s];
-  q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group;
-  q.len = len < 0 ? 0 : (int)min((int64_t)len, cap);
-  q.first = (len < 0 ? 0 : len) - n;
-  return q;
-}
-__device__ __forceinline__ void flag_seq(const AttnParams &p, int s) {
-  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1], len = p.length[s];
-  if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens || r1 - r0 > p.max_q) atomicOr(p.c.status, pi::kKvBadRows);
-  if (len < 0 || len > (int64_t)p.tok.table_stride * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
-}
-// Keys that any row of a row tile sees, and the tiles that hold them.
-template <int ROWS>
-__device__ __forceinline__ int unit_keys(const AttnParams &p, const Seq &q, int rt) {
-  if (rt * ROWS >= q.rows) return 0;
-  if (!p.causal) return q.len;
-  const int last = min(q.rows, (rt + 1) * ROWS) - 1;
-  return max(0, min(q.len, q.first + last / p.group + 1));
-}
-template <int ROWS>
-__device__ __forceinline__ int unit_tiles(const AttnParams &p, const Seq &q, int rt) {
-  return (unit_keys<ROWS>(p, q, rt) + kTile - 1) / kTile;
-}
-template <int ROWS>
-__device__ __forceinline__ int64_t seq_tiles(const AttnParams &p, int s) {
-  const Seq q = load_seq<ROWS>(p, s);
-  int64_t t = 0;
-  for (int rt = 0; rt < p.row_tiles && rt * ROWS < q.rows; ++rt) t += unit_tiles<ROWS>(p, q, rt);
-  return t * p.c.heads;
-}
-
-// Exclusive sum over the CTA's 128 threads; *total gets the whole sum.
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sm[w] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < w) before += sm[i];
-    all += sm[i];
-  }
-  *total = all;
-  return before + x - v;
-}
-
-__device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
-__device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
-
-struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 or 16 tokens and up to 128 bytes
-  CUtensorMap k, v;
-};
 
 // A tile (64 tokens) in shared memory, K then V, as the tile copies leave it:
 // boxes of min(D, 128) bytes by 64 rows, 16-byte chunks swizzled so that the
@@ -226,8 +118,7 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
   // stages; then, WARPS_M == 1, a unit's [4][ROWS][D] sums, [4][ROWS][3] (m, l, R)
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *sm = reinterpret_cast<float *>(ring);
-  __shared__ int64_t scan[4];
-  __shared__ int64_t found[2];
+  __shared__ ShareShared share_sm;
   __shared__ __align__(8) unsigned long long full[STAGES], empty[STAGES];   // a tile's copies have landed; all warps have read it
   __shared__ float scales[STAGES][2][4];           // K and V scale of its blocks; K below 0: no block
   __shared__ int failed;
@@ -243,45 +134,16 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
   }
   for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
 
-  // Where this CTA's share of the line of tiles begins.
-  const int per = (p.tok.n_seqs + 127) / 128;
-  int64_t mine = 0, total;
-  for (int i = 0; i < per; ++i) {
-    const int s = threadIdx.x * per + i;
-    if (s < p.tok.n_seqs) mine += seq_tiles<ROWS>(p, s);
-  }
-  int64_t at = cta_scan(mine, scan, &total);
-  if (total == 0) return;
-  const int shares = (int)min((int64_t)gridDim.x, total);    // every share has a tile, so every part between two of a unit is written
-  if (blockIdx.x >= shares) return;
-  const int64_t begin = cta_begin(blockIdx.x, total, shares), end = cta_begin(blockIdx.x + 1, total, shares);
-  if (at <= begin && begin < at + mine)
-    for (int i = 0; i < per; ++i) {
-      const int s = threadIdx.x * per + i;
-      const int64_t n = seq_tiles<ROWS>(p, s);
-      if (begin < at + n) {
-        found[0] = s, found[1] = at;
-        break;
-      }
-      at += n;
-    }
-  __syncthreads();
-  int s = (int)found[0], h = 0, rt = 0;
-  Seq sq = load_seq<ROWS>(p, s);
-  int64_t u0 = found[1];                           // line position of the current unit
-  {
-    const int64_t per_head = seq_tiles<ROWS>(p, s) / p.c.heads;
-    h = (int)((begin - u0) / per_head);
-    u0 += h * per_head;
-    for (int n; begin >= u0 + (n = unit_tiles<ROWS>(p, sq, rt)); ++rt) u0 += n;
-  }
-
+  Share at;
+  if (!find_share<ROWS, kTile>(p, share_sm, &at)) return;
   uint32_t full_ph = 0, empty_ph = 0, used = 0, pend = 0;    // a bit a stage: phases to wait for, filled ever, filled and not waited for
   bool dead = false;                               // a wait ran out: nothing more is copied or computed
   const bool by16 = p.c.page_size % kTile != 0;    // a tile may lie in several pages: blocks are copied one by one
-  for (int64_t pos = begin; pos < end;) {
+  for (int64_t pos = at.begin; pos < at.end;) {
+    const Seq &sq = at.sq;
+    const int s = at.s, h = at.h, rt = at.rt;
     const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
-    const int t0 = (int)(pos - u0), t1 = (int)min((int64_t)tiles, end - u0);
+    const int t0 = (int)(pos - at.u0), t1 = (int)min((int64_t)tiles, at.end - at.u0);
 
     // ---- the ring: the warps take turns to fill a stage; lane l looks after block l % 4 of the tile ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
@@ -662,105 +524,8 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
         }
     }
 
-    // ---- next unit ----
-    pos = u0 + t1;
-    if (pos >= end) break;
-    u0 += tiles;
-    do {                                           // units without keys take no place in the line
-      if (++rt >= p.row_tiles || rt * ROWS >= sq.rows) {
-        rt = 0;
-        if (++h >= p.c.heads) {
-          h = 0;
-          if (++s >= p.tok.n_seqs) return;
-          sq = load_seq<ROWS>(p, s);
-        }
-      }
-    } while (unit_tiles<ROWS>(p, sq, rt) == 0);
-  }
-}
-
-// Units cut between CTAs: their parts added in CTA order.  Units without keys:
-// 0 and -inf.  blockIdx.x: (sequence, head); a warp per row.
-template <int DT, int D, int ROWS>
-__global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
-  using E = Elem<DT>;
-  constexpr int LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
-  constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
-  __shared__ int64_t scan[4], start;
-  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads, lane = threadIdx.x & 31;
-  const int per = (p.tok.n_seqs + 127) / 128;
-  int64_t mine = 0, total;
-  for (int i = 0; i < per; ++i) {
-    const int t = threadIdx.x * per + i;
-    if (t < p.tok.n_seqs) mine += seq_tiles<ROWS>(p, t);
-  }
-  int64_t at = cta_scan(mine, scan, &total);
-  if (s / per == threadIdx.x) {
-    for (int t = threadIdx.x * per; t < s; ++t) at += seq_tiles<ROWS>(p, t);
-    start = at;
-  }
-  __syncthreads();
-  griddep_wait();
-  const int shares = (int)min((int64_t)p.grid, total);
-  const Seq sq = load_seq<ROWS>(p, s);
-  int64_t u0 = start + h * (seq_tiles<ROWS>(p, s) / p.c.heads);
-  for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows; ++rt) {
-    const int tiles = unit_tiles<ROWS>(p, sq, rt);
-    int64_t c0 = 0, c1 = -1;
-    if (tiles) {
-      c0 = cta_owner(u0, total, shares), c1 = cta_owner(u0 + tiles - 1, total, shares);
-      u0 += tiles;
-      if (c0 == c1) continue;
-    }
-    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
-      const int gr = rt * ROWS + row;
-      if (gr >= sq.rows) break;
-      float M = -INFINITY, L = 0.f;
-      auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
-      for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
-      M = warp_max(M);
-      const float ms = M == -INFINITY ? 0.f : M;
-      float4 o[VECS];
-#pragma unroll
-      for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
-        const int n = (int)min((int64_t)32, c1 - cb + 1);
-        float w = 0.f;
-        if (lane < n) {
-          const float *ml = part(cb + lane) + ROWS * D + 2 * row;
-          w = ex2(ml[0] - ms);
-          L += ml[1] * w;
-        }
-#pragma unroll 8
-        for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
-          const float *src = part(cb + min(i, n - 1)) + row * D;
-#pragma unroll
-          for (int k = 0; k < VECS; ++k) {
-            const int d = (lane % LANES + k * 32) * 4;
-            if (d >= D) continue;
-            const float4 x = *reinterpret_cast<const float4 *>(src + d);
-            if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
-          }
-        }
-      }
-      L = warp_sum(L);
-      if constexpr (LANES == 16) {
-        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
-        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
-      }
-      const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
-      const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-      for (int k = 0; k < VECS; ++k) {
-        const int d = (lane % LANES + k * 32) * 4;
-        if (d >= D || lane >= LANES) continue;
-        Pack<DT, 4> y;
-        y.v[0] = E::from(o[k].x * inv), y.v[1] = E::from(o[k].y * inv), y.v[2] = E::from(o[k].z * inv), y.v[3] = E::from(o[k].w * inv);
-        *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
-      }
-      if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
-    }
+    pos = at.u0 + t1;
+    if (pos >= at.end || !next_unit<ROWS, kTile>(p, &at)) break;
   }
 }
 
@@ -774,37 +539,6 @@ AttnShape attn_shape(int D, int64_t max_rows) {
   const int nb_max = D <= 128 ? 2 : 1;
   const int nb = max_rows <= 8 ? 1 : nb_max;
   return AttnShape{nb, max_rows <= 8 * nb ? 1 : 4};
-}
-
-// The driver's tensor-map encoder, looked up through the runtime so that the
-// library does not link libcuda.
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encoder() {
-  static EncodeFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
-// Codes as [n_pages heads][page_size][D]: a page of a head is one z, so every
-// coordinate stays small in a cache of any size.
-template <int D>
-bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
-  const EncodeFn enc = encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.heads};
-  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * c.page_size};
-  const cuuint32_t box[3] = {(cuuint32_t)Frag<D>::BOX, c.page_size % kTile ? 16u : (cuuint32_t)kTile, 1}, es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : D == 96 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current_sms()); }
@@ -824,7 +558,7 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, ROWS>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS < 16 ? ROWS / 4 : 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS < 16 ? ROWS / 4 : 4), dim3(128), 0, s, p);
 }
 
 template <int DT, int D>
@@ -837,6 +571,10 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
     return k.warps_m == 1 ? launch_attn<DT, D, 1, 1>(p, s) : launch_attn<DT, D, 1, 4>(p, s);
   }
 }
+
+// From how many query rows a head on the tcgen05 kernel (128 rows a unit, each
+// tile widened once for them) is taken.
+bool many_rows(int D, int64_t rows) { return (D == 64 || D == 128) && rows > 64; }
 
 template <int DT>
 cudaError_t attn_by_dim(const AttnParams &p, cudaStream_t s) {
@@ -868,7 +606,7 @@ size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, in
   pi::clear_error();
   if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
   const int D = c->head_dim;
-  const size_t rows = D <= 128 ? std::max((size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 64) : (size_t)attn_grid(D, 1) * 32;
+  const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 64, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
   return sizeof(float) * 2 * rows * (size_t)(D + 2);
 }
 
@@ -905,7 +643,10 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
                      sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
                      (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
+  if (many_rows(cache->head_dim, (int64_t)max_q * group))
+    PI_TRY_CUDA(run_tc(p, dtype, s));
+  else
+    PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
   return PI_OK;
 }
 

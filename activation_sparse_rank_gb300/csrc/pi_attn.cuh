@@ -1,0 +1,301 @@
+// What the attention kernels share (pi_attn.cu: few query rows a head;
+// pi_attn_tc.cu: many): parameters, the line of tiles that is cut over the CTAs,
+// the tensor maps of the codes and the sum of parts.
+#pragma once
+
+#include "pi_kv.cuh"
+#include "pi_ops.cuh"
+#include "pi_ptx.cuh"
+
+#include <algorithm>
+
+namespace attn {
+
+using namespace pidev;
+
+// The second product's weights 2^(x + ev - R) reach 2^(kBoost + kSlack), inside
+// fp16, and are subnormal only below 2^-(14 + kBoost) of the largest.  kSlack:
+// m and R follow a score only where it passes them by that much; the sums do
+// not depend on m and R, and most steps then leave the accumulators alone.
+constexpr float kBoost = 6.f, kSlack = 8.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  pi_kv_cache c;
+  pi_kv_tokens tok;
+  const int32_t *length;
+  const void *q;
+  int64_t qt, qh;
+  void *out;
+  float *lse;
+  float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
+  float scale;             // sm_scale log2(e)
+  int q_heads, group, max_q, causal, row_tiles, grid;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four codes as two fp16 pairs: one instruction each.
+__device__ __forceinline__ void widen4(unsigned w, unsigned &lo, unsigned &hi) {
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ unsigned pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const unsigned *>(&h);
+}
+
+// Sequence s as the kernels see it: lengths made safe, faults flagged by flag_seq.
+struct Seq {
+  int row0, n, rows, len, first;    // packed row, query tokens used, query rows, keys, position of the first token
+};
+__device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
+  Seq q;
+  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1];
+  const int n = r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens ? 0 : r1 - r0;
+  const int64_t cap = min((int64_t)p.tok.table_stride * p.c.page_size, (int64_t)1 << 30);
+  const int len = p.length[s];
+  q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group;
+  q.len = len < 0 ? 0 : (int)min((int64_t)len, cap);
+  q.first = (len < 0 ? 0 : len) - n;
+  return q;
+}
+__device__ __forceinline__ void flag_seq(const AttnParams &p, int s) {
+  const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1], len = p.length[s];
+  if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens || r1 - r0 > p.max_q) atomicOr(p.c.status, pi::kKvBadRows);
+  if (len < 0 || len > (int64_t)p.tok.table_stride * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
+}
+// Keys that any row of a row tile (ROWS rows) sees, and the tiles (TILE keys) that hold them.
+template <int ROWS>
+__device__ __forceinline__ int unit_keys(const AttnParams &p, const Seq &q, int rt) {
+  if (rt * ROWS >= q.rows) return 0;
+  if (!p.causal) return q.len;
+  const int last = min(q.rows, (rt + 1) * ROWS) - 1;
+  return max(0, min(q.len, q.first + last / p.group + 1));
+}
+template <int ROWS, int TILE>
+__device__ __forceinline__ int unit_tiles(const AttnParams &p, const Seq &q, int rt) {
+  return (unit_keys<ROWS>(p, q, rt) + TILE - 1) / TILE;
+}
+template <int ROWS, int TILE>
+__device__ __forceinline__ int64_t seq_tiles(const AttnParams &p, int s) {
+  const Seq q = load_seq(p, s);
+  int64_t t = 0;
+  for (int rt = 0; rt < p.row_tiles && rt * ROWS < q.rows; ++rt) t += unit_tiles<ROWS, TILE>(p, q, rt);
+  return t * p.c.heads;
+}
+
+// Exclusive sum over the CTA's first 128 threads (the others pass 0); *total gets the whole sum.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31 && w < 4) sm[w] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < w) before += sm[i];
+    all += sm[i];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ int64_t cta_begin(int64_t c, int64_t total, int shares) { return c * total / shares; }
+__device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int shares) { return ((tile + 1) * shares - 1) / total; }
+
+// One CTA's share of the line of tiles and its place in it.  A unit is a
+// (sequence, head, row tile); units without keys take no place.
+struct Share {
+  int64_t begin, end;      // tiles
+  int s, h, rt;            // the unit that `begin` lies in
+  int64_t u0;              // where that unit begins
+  Seq sq;
+};
+struct ShareShared {
+  int64_t scan[4], found[2];
+};
+// False if this CTA has none.  Every thread of the CTA calls it.
+template <int ROWS, int TILE>
+__device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm, Share *o) {
+  const int per = (p.tok.n_seqs + 127) / 128;
+  int64_t mine = 0, total;
+  if (threadIdx.x < 128)
+    for (int i = 0; i < per; ++i) {
+      const int s = threadIdx.x * per + i;
+      if (s < p.tok.n_seqs) mine += seq_tiles<ROWS, TILE>(p, s);
+    }
+  int64_t at = cta_scan(mine, sm.scan, &total);
+  const int shares = (int)min((int64_t)gridDim.x, total);    // every share has a tile, so every part between two of a unit is written
+  if (blockIdx.x >= shares) return false;
+  o->begin = cta_begin(blockIdx.x, total, shares), o->end = cta_begin(blockIdx.x + 1, total, shares);
+  if (at <= o->begin && o->begin < at + mine)
+    for (int i = 0; i < per; ++i) {
+      const int s = threadIdx.x * per + i;
+      const int64_t n = seq_tiles<ROWS, TILE>(p, s);
+      if (o->begin < at + n) {
+        sm.found[0] = s, sm.found[1] = at;
+        break;
+      }
+      at += n;
+    }
+  __syncthreads();
+  o->s = (int)sm.found[0], o->u0 = sm.found[1];
+  o->sq = load_seq(p, o->s);
+  const int64_t per_head = seq_tiles<ROWS, TILE>(p, o->s) / p.c.heads;
+  o->h = (int)((o->begin - o->u0) / per_head), o->rt = 0;
+  o->u0 += o->h * per_head;
+  for (int n; o->begin >= o->u0 + (n = unit_tiles<ROWS, TILE>(p, o->sq, o->rt)); ++o->rt) o->u0 += n;
+  return true;
+}
+// To the next unit with keys; false after the last.
+template <int ROWS, int TILE>
+__device__ __forceinline__ bool next_unit(const AttnParams &p, Share *o) {
+  o->u0 += unit_tiles<ROWS, TILE>(p, o->sq, o->rt);
+  do {
+    if (++o->rt >= p.row_tiles || o->rt * ROWS >= o->sq.rows) {
+      o->rt = 0;
+      if (++o->h >= p.c.heads) {
+        o->h = 0;
+        if (++o->s >= p.tok.n_seqs) return false;
+        o->sq = load_seq(p, o->s);
+      }
+    }
+  } while (unit_tiles<ROWS, TILE>(p, o->sq, o->rt) == 0);
+  return true;
+}
+
+struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 or 16 tokens and up to 128 bytes
+  CUtensorMap k, v;
+};
+
+// Units cut between CTAs: their parts added in CTA order.  Units without keys:
+// 0 and -inf.  blockIdx.x: (sequence, head); a warp per row.
+template <int DT, int D, int ROWS, int TILE>
+__global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
+  using E = Elem<DT>;
+  constexpr int LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
+  constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
+  __shared__ int64_t scan[4], start;
+  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads, lane = threadIdx.x & 31;
+  const int per = (p.tok.n_seqs + 127) / 128;
+  int64_t mine = 0, total;
+  for (int i = 0; i < per; ++i) {
+    const int t = threadIdx.x * per + i;
+    if (t < p.tok.n_seqs) mine += seq_tiles<ROWS, TILE>(p, t);
+  }
+  int64_t at = cta_scan(mine, scan, &total);
+  if (s / per == threadIdx.x) {
+    for (int t = threadIdx.x * per; t < s; ++t) at += seq_tiles<ROWS, TILE>(p, t);
+    start = at;
+  }
+  __syncthreads();
+  griddep_wait();
+  const int shares = (int)min((int64_t)p.grid, total);
+  const Seq sq = load_seq(p, s);
+  int64_t u0 = start + h * (seq_tiles<ROWS, TILE>(p, s) / p.c.heads);
+  for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows; ++rt) {
+    const int tiles = unit_tiles<ROWS, TILE>(p, sq, rt);
+    int64_t c0 = 0, c1 = -1;
+    if (tiles) {
+      c0 = cta_owner(u0, total, shares), c1 = cta_owner(u0 + tiles - 1, total, shares);
+      u0 += tiles;
+      if (c0 == c1) continue;
+    }
+    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
+      const int gr = rt * ROWS + row;
+      if (gr >= sq.rows) break;
+      float M = -INFINITY, L = 0.f;
+      auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
+      for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
+      M = warp_max(M);
+      const float ms = M == -INFINITY ? 0.f : M;
+      float4 o[VECS];
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
+        const int n = (int)min((int64_t)32, c1 - cb + 1);
+        float w = 0.f;
+        if (lane < n) {
+          const float *ml = part(cb + lane) + ROWS * D + 2 * row;
+          w = ex2(ml[0] - ms);
+          L += ml[1] * w;
+        }
+#pragma unroll 8
+        for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
+          const float *src = part(cb + min(i, n - 1)) + row * D;
+#pragma unroll
+          for (int k = 0; k < VECS; ++k) {
+            const int d = (lane % LANES + k * 32) * 4;
+            if (d >= D) continue;
+            const float4 x = *reinterpret_cast<const float4 *>(src + d);
+            if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
+          }
+        }
+      }
+      L = warp_sum(L);
+      if constexpr (LANES == 16) {
+        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
+        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
+      }
+      const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+      for (int k = 0; k < VECS; ++k) {
+        const int d = (lane % LANES + k * 32) * 4;
+        if (d >= D || lane >= LANES) continue;
+        Pack<DT, 4> y;
+        y.v[0] = E::from(o[k].x * inv), y.v[1] = E::from(o[k].y * inv), y.v[2] = E::from(o[k].z * inv), y.v[3] = E::from(o[k].w * inv);
+        *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
+      }
+      if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
+    }
+  }
+}
+
+// The driver's tensor-map encoder, looked up through the runtime so that the
+// library does not link libcuda.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Codes as [n_pages heads][page_size][D]: a page of a head is one z, so every
+// coordinate stays small in a cache of any size.
+template <int D>
+inline bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
+  const EncodeFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * c.page_size};
+  const cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), c.page_size % 64 ? 16u : 64u, 1}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : D == 96 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// pi_attn_tc.cu: head_dim 64 or 128, row_tiles and grid are its own.
+cudaError_t run_tc(const AttnParams &p, int dtype, cudaStream_t s);
+constexpr int kTcRows = 128;
+
+}  // namespace attn

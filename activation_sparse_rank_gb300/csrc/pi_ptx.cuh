@@ -7,7 +7,7 @@
 
 namespace pidev {
 
-constexpr unsigned kWaitTries = 1u << 22;   // a wait that runs this often without its phase gives up
+constexpr long long kWaitClocks = 4000000000ll;   // about 2 s: a wait that takes longer gives up
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -25,17 +25,21 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return done != 0;
+}
 // False if the phase did not complete within the limit.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  for (unsigned i = 0; i < kWaitTries; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+  if (bar_try(bar, parity)) return true;
+  const long long from = clock64();
+  do {
+    if (bar_try(bar, parity)) return true;
+  } while (clock64() - from < kWaitClocks);
   return false;
 }
 // Box at (x, y, z) of a three-dimensional tensor map; x is 0 or 128 bytes here.
