@@ -558,7 +558,7 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS < 16 ? ROWS / 4 : 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS / 4), dim3(128), 0, s, p);
 }
 
 template <int DT, int D>
@@ -572,7 +572,7 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
   }
 }
 
-// From how many query rows a head on the tcgen05 kernel (128 rows a unit, each
+// From how many query rows a head on the tcgen05 kernel (row tiles of 128, each
 // tile widened once for them) is taken.
 bool many_rows(int D, int64_t rows) { return (D == 64 || D == 128) && rows > 64; }
 

@@ -296,6 +296,6 @@ inline bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
 
 // pi_attn_tc.cu: head_dim 64 or 128, row_tiles and grid are its own.
 cudaError_t run_tc(const AttnParams &p, int dtype, cudaStream_t s);
-constexpr int kTcRows = 128;
+constexpr int kTcRows = 256;     // query rows of a unit there
 
 }  // namespace attn

@@ -1,11 +1,12 @@
 // Attention over the 8-bit cache for many query rows of a key/value head (a
 // prompt in chunks), on tcgen05.
 //
-// A unit is 128 query rows of a (sequence, head); a tile 128 keys.  Per tile
+// A unit is 256 query rows of a (sequence, head), two row tiles of 128; a tile of
+// keys has 128.  Per tile and row tile
 //   S = Q K^T       128 x 128, fp16 operands in shared memory, sums in TMEM
 //   P = 2^(S f - b) fp16, written over S
 //   O += P V        P from TMEM, V from shared memory ([token][dim], N-major)
-// E4M3 codes are exact in fp16: converter warps widen each tile once for the 128
+// E4M3 codes are exact in fp16: converter warps widen each tile once for the 256
 // rows.  The scales stay out of the operands: a block's K scale is part of the
 // factor f of its 16 columns, its V scale 2^ev of their exponent, so
 //   P_j = 2^(x_j + ev_j - R),  acc = sum P_j c_j = sum 2^(x_j - R) v_j,
@@ -13,12 +14,10 @@
 // with R + kBoost near the running maximum of x_j + ev_j (within kSlack): no
 // multiplication per element of K or V, and scales of any range.
 //
-// Bound by the tensor cores where the softmax keeps up: a tile is 4 x 128 x 128 x D
-// operations there, and 128 exponentials and about 450 instructions of each of
-// the 128 softmax threads.  Roles (12 warps, one CTA an SM): 0-3 softmax, a row a
-// thread; 4-7 converters, a token a thread; 8 tile copies and scales; 9 issues the
-// products.  K and V are double-buffered in fp16, S in TMEM, so the next S and the
-// conversion run under a tile's softmax.
+// Roles (16 warps, one CTA an SM): 0-3 and 4-7 softmax of the two row tiles, a row
+// a thread; 8-11 converters, a token a thread; 12 tile copies and scales; 13 issues
+// the products.  One row tile's products run under the other's softmax; K in fp16
+// is double-buffered, codes have three stages.
 //
 // The line of tiles is cut evenly over the CTAs as in pi_attn.cu.
 #include "pi_attn.cuh"
@@ -27,8 +26,9 @@ using namespace attn;
 
 namespace {
 
-constexpr int kRows = kTcRows, kKeys = 128, kBlocks = kKeys / PI_KV_BLOCK;
-constexpr int kThreads = 384;      // three warpgroups: register shares are set for each
+constexpr int kRows = kTcRows, kHalf = 128, kKeys = 128, kBlocks = kKeys / PI_KV_BLOCK;
+constexpr int kThreads = 512;      // four warpgroups: register shares are set for each
+constexpr int kStages = 3;         // of codes, K and V of a tile in turn
 constexpr int kScaleRing = 8;    // tiles whose scales are kept: copies run at most 5 tiles ahead of the softmax
 
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -43,7 +43,7 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
 }
 // kind::f16, fp16 operands, binary32 sums, M = 128
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
@@ -79,21 +79,27 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
       "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads above are complete; v's uses stay behind this.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < N; ++j) asm volatile("" : "+f"(v[j]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 template <int D>
 struct Smem {                       // byte offsets from a 1024-byte boundary
-  static constexpr int SLABS = D / 64, SLAB = 128 * 128;               // 64 fp16 dims of 128 rows
-  static constexpr int Q = 0, K = Q + SLABS * SLAB, V = K + 2 * SLABS * SLAB, CK = V + 2 * SLABS * SLAB, CV = CK + 128 * D;
-  static constexpr int BYTES = CV + 128 * D;
+  static constexpr int SLABS = D / 64, SLAB = 128 * 128, TILE = SLABS * SLAB;   // a slab: 64 fp16 dims of 128 rows
+  static constexpr int Q = 0, K = Q + 2 * TILE, V = K + 2 * TILE, C = V + TILE, BYTES = C + kStages * 128 * D;
 };
 struct Bars {
-  unsigned long long ck_full, ck_empty, cv_full, cv_empty;             // codes of a tile: copied, widened
-  unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2];     // fp16 tiles: written, used
-  unsigned long long s_full[2], p_full[2], o_done, q_full, drain;      // S ready, P ready, a tile's O done, Q of a unit written; after a failure
+  unsigned long long c_full[kStages], c_empty[kStages];                // codes: copied, widened
+  unsigned long long k_full[2], k_empty[2], v_full, v_empty;           // fp16 tiles: written, used
+  unsigned long long s_full[2], p_full[2], o_done[2], q_full[2];       // of a row tile: S ready, P ready, O of a tile done, Q of a unit written
+  unsigned long long drain;                                            // after a failure
 };
 
 // 16-byte chunk c of 128-byte row r in a 128-byte-swizzled slab.
@@ -114,41 +120,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
   __shared__ ShareShared share_sm;
   __shared__ float scales[kScaleRing][2][kBlocks];     // K and V scales of a tile's blocks; below 0: no block
   __shared__ int nan_at[kScaleRing][D];                // first position of a tile with a NaN among its values, by dim
-  __shared__ int nan_any[kScaleRing];
+  __shared__ int nan_any[kScaleRing], tile_bad[kScaleRing];   // a block is absent
   __shared__ uint32_t tmem_s;
   __shared__ volatile int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch();
   for (int s = blockIdx.x * kThreads + tid; s < p.tok.n_seqs; s += gridDim.x * kThreads) flag_seq(p, s);
   if (tid == 0) {
-    bar_init(smem_addr(&bars.ck_full), 33);            // the bytes' arrival, and each lane's scale copies
-    bar_init(smem_addr(&bars.ck_empty), 4);
-    bar_init(smem_addr(&bars.cv_full), 1);
-    bar_init(smem_addr(&bars.cv_empty), 4);
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(smem_addr(&bars.c_full[i]), 33);        // the bytes' arrival, and each lane's scale copies
+      bar_init(smem_addr(&bars.c_empty[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&bars.k_full[i]), 4);
       bar_init(smem_addr(&bars.k_empty[i]), 1);
-      bar_init(smem_addr(&bars.v_full[i]), 4);
-      bar_init(smem_addr(&bars.v_empty[i]), 1);
       bar_init(smem_addr(&bars.s_full[i]), 1);
       bar_init(smem_addr(&bars.p_full[i]), 4);
+      bar_init(smem_addr(&bars.o_done[i]), 1);
+      bar_init(smem_addr(&bars.q_full[i]), 4);
     }
-    bar_init(smem_addr(&bars.o_done), 1);
-    bar_init(smem_addr(&bars.q_full), 4);
+    bar_init(smem_addr(&bars.v_full), 4);
+    bar_init(smem_addr(&bars.v_empty), 1);
     bar_init(smem_addr(&bars.drain), 1);
     bar_init_fence();
     failed = 0;
   }
   Share at;
   if (!find_share<kRows, kKeys>(p, share_sm, &at)) return;
-  if (warp == 9) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_s, tmem_o = tmem + 256;
+  const uint32_t tmem = tmem_s;                        // S of the two row tiles, then O of the two
 
   // A wait that gives up makes every role leave its loop.
   auto wait = [&](unsigned long long *bar, uint32_t parity) {
@@ -165,41 +171,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
   // The CTA's units, for each role: work(unit) until it returns false.
   struct Unit {
     uint32_t g, index;       // tiles and units of this CTA before: buffers and phases follow from them
+    uint32_t g1, index1;     // of those, the ones with a second row tile
     int s, h, row0, keys, tiles, t0, t1;
+    bool two;                // the unit has a second row tile
     int least;               // keys that the unit's first row sees: below, no row masks anything
     Seq sq;
   };
   bool ok = true;
-  int ck_tile = -1, cv_tile = -1;                      // last tiles whose copies were issued (warp 8)
+  int copied = -1;                                     // the last stage use whose copies were issued (warp 12)
   auto units = [&](auto work) {
     Unit u;
-    u.g = u.index = 0;
+    u.g = u.index = u.g1 = u.index1 = 0;
     for (int64_t pos = at.begin; pos < at.end; ++u.index) {
       u.sq = at.sq;
       u.s = at.s, u.h = at.h, u.row0 = at.rt * kRows;
       u.keys = unit_keys<kRows>(p, u.sq, at.rt), u.tiles = (u.keys + kKeys - 1) / kKeys;
       u.t0 = (int)(pos - at.u0), u.t1 = (int)min((int64_t)u.tiles, at.end - at.u0);
       u.least = p.causal ? max(0, min(u.sq.len, u.sq.first + u.row0 / p.group + 1)) : u.sq.len;
+      u.two = u.row0 + kHalf < u.sq.rows;
       work(u);
       if (!ok) break;
       u.g += u.t1 - u.t0;
+      if (u.two) u.g1 += u.t1 - u.t0, ++u.index1;
       pos = at.u0 + u.t1;
       if (pos < at.end && !next_unit<kRows, kKeys>(p, &at)) break;
     }
   };
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    const int rt = warp >> 2, row = tid & 127;           // row tile, row of it
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + lanes + rt * 128, to = tmem + lanes + 256 + rt * 128;
     units([&](const Unit &u) {
-      // ================= softmax: row row0 + tid =================
+      // ================= softmax: row u.row0 + 128 rt + row =================
+      if (rt && !u.two) return;
       const Seq &sq = u.sq;
-      const uint32_t g = u.g;
       const int h = u.h, t0 = u.t0, t1 = u.t1;
-      const int row0 = u.row0, tiles = u.tiles, least = u.least;
-      const int r = row0 + tid;
+      const uint32_t first = rt ? u.g1 : u.g;            // phases of this row tile's barriers
+      const int r = u.row0 + kHalf * rt + row;
       const bool in = r < sq.rows;
       const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
       const int lim = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
+      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       float f = fabsf(p.scale);
       {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const typename E::T *>(p.q) +
@@ -211,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) raw[c] = src[c];
         }
-        float up = p.scale < 0.f ? -1.f : 1.f;         // the factor f is never negative
-        if constexpr (DT == PI_DT_BF16) {              // as in pi_attn.cu: the largest finite magnitude to [2^13, 2^14)
+        float up = p.scale < 0.f ? -1.f : 1.f;
+        if constexpr (DT == PI_DT_BF16) {                // as in pi_attn.cu: the largest finite magnitude to [2^13, 2^14)
           float mx = 0.f;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
@@ -229,176 +242,170 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           f2 v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_from16<DT>(raw[c], j), f2_of(up, up));
-          *reinterpret_cast<uint4 *>(sm + L::Q + c / 8 * L::SLAB + sw128(tid, c % 8)) = f2_to16<PI_DT_F16>(v);
+          *reinterpret_cast<uint4 *>(sm + L::Q + rt * L::TILE + c / 8 * L::SLAB + sw128(row, c % 8)) = f2_to16<PI_DT_F16>(v);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&bars.q_full));
+        if (lane == 0) bar_arrive(smem_addr(&bars.q_full[rt]));
       }
       float R = -INFINITY, sum = 0.f;
-      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-      uint32_t gt = g;
-      for (int t = t0; t < t1; ++t, ++gt) {
-        const uint32_t tb = tmem + lanes + (gt & 1) * 128;
-        if (!wait(&bars.s_full[gt & 1], gt >> 1)) {
+      for (int t = t0; t < t1; ++t) {
+        const uint32_t n = first + (t - t0), ring = (u.g + (t - t0)) % kScaleRing;
+        const int k0 = t * kKeys;
+        if (!wait(&bars.s_full[rt], n)) {
           ok = false;
-          break;
+          return;
         }
         fence_after();
-        float x[kKeys];
+        // Columns of half a tile as they are, masked ones -inf; absent blocks
+        // (a bad page, past the sequence) are masked too.
+        const float *ks = scales[ring][0], *vs = scales[ring][1];
+        const bool masked = k0 + kKeys > min_lim || tile_bad[ring];
+        auto load = [&](float *x, int half) {
+          tmem_ld32(ts + half * 64, x);
+          tmem_ld32(ts + half * 64 + 32, x + 32);
+          tmem_wait_ld<64>(x);
+          if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tb + c * 32, x + 32 * c);
-        tmem_wait_ld();
-        const float(*sc)[kBlocks] = scales[gt % kScaleRing];
-        const int k0 = t * kKeys;
-        float fb[kBlocks], ev[kBlocks];
-        float top = -INFINITY;                         // of x + ev
+            for (int b = 0; b < 4; ++b) {
+              const int cols = ks[half * 4 + b] < 0.f ? 0 : lim - k0 - half * 64 - 16 * b;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const float ks = sc[0][b];
-          // absent blocks (a bad page, past the sequence) are masked with the columns
-          const int cols = ks < 0.f ? 0 : lim - (k0 + 16 * b);
-          fb[b] = f * ks;
-          ev[b] = (float)((int)(__float_as_uint(sc[1][b]) >> 23 & 255) - 127);
-          float m = -INFINITY;
-          if (cols >= 16) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) m = fmaxf(m, x[16 * b + j]);
-            m = m * fb[b];
-          } else {
-            fb[b] = 1.f;                               // scaled here, so that a masked column is -inf whatever the factor
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              x[16 * b + j] = j < cols ? x[16 * b + j] * (f * ks) : -INFINITY;
-              m = fmaxf(m, x[16 * b + j]);
+              for (int j = 0; j < 16; ++j)
+                if (j >= cols) x[16 * b + j] = -INFINITY;
             }
-            if (cols <= 0) ev[b] = 0.f;
           }
-          top = fmaxf(top, m + ev[b]);
+        };
+        // not negative, and not 0, so that a masked column stays -inf
+        auto factor = [&](int b) { return fmaxf(f * fabsf(ks[b]), 1e-37f); };
+        auto exponent = [&](int b) { return (float)((int)(__float_as_uint(vs[b]) >> 23 & 255) - 127); };
+        float top = -INFINITY;                           // of x + ev
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float x[64];
+          load(x, half);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float m = x[16 * b];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) m = fmaxf(m, x[16 * b + j]);
+            top = fmaxf(top, fmaf(m, factor(half * 4 + b), exponent(half * 4 + b)));
+          }
         }
         const bool over = top - kBoost > R + kSlack;
         if (__any_sync(0xffffffffu, over)) {
           const float Rn = over ? fmaxf(R, top - kBoost) : R;
-          const float c = R == Rn || Rn == -INFINITY ? 1.f : ex2(R - Rn);
+          const float c = R == Rn ? 1.f : ex2(R - Rn);
           R = Rn;
           sum *= c;
-          if (t > t0) {                                // O is the products' until the tile before is done
-            if (!wait(&bars.o_done, gt - 1)) {
+          if (t > t0) {                                  // O is the products' until the tile before is done
+            if (!wait(&bars.o_done[rt], n - 1)) {
               ok = false;
-              break;
+              return;
             }
             fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[32];
-              tmem_ld32(tmem_o + lanes + q * 32, o);
-              tmem_wait_ld();
+              tmem_ld32(to + q * 32, o);
+              tmem_wait_ld<32>(o);
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] *= c;
-              tmem_st32(tmem_o + lanes + q * 32, reinterpret_cast<const uint32_t *>(o));
+              tmem_st32(to + q * 32, reinterpret_cast<const uint32_t *>(o));
             }
             tmem_wait_st();
           }
         }
         const float Rs = R == -INFINITY ? 0.f : R;
-#pragma unroll
+        // P takes the first 64 columns of S: its second half is written there only after S's is read
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+          float x[64];
+          load(x, half);
           uint32_t w[32];
 #pragma unroll
-          for (int bb = 0; bb < 4; ++bb) {
-            const int b = half * 4 + bb;
-            const float bias = ev[b] - Rs;
+          for (int b = 0; b < 4; ++b) {
+            const float fb = factor(half * 4 + b), ev = exponent(half * 4 + b), bias = ev - Rs;
             f2 part = f2_of(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const f2 z = f2_fma(f2_of(x[16 * b + 2 * j], x[16 * b + 2 * j + 1]), f2_of(fb[b], fb[b]), f2_of(bias, bias));
+              const f2 z = f2_fma(f2_of(x[16 * b + 2 * j], x[16 * b + 2 * j + 1]), f2_of(fb, fb), f2_of(bias, bias));
               const f2 e = f2_of(ex2(z.x), ex2(z.y));
               part = f2_add(part, e);
-              w[bb * 8 + j] = f2_narrow<PI_DT_F16>(e);
+              w[b * 8 + j] = f2_narrow<PI_DT_F16>(e);
             }
-            sum = fmaf(f2_sum(part), ex2(-ev[b]), sum);
+            sum = fmaf(f2_sum(part), ex2(-ev), sum);
           }
-          tmem_st32(tb + half * 32, w);
+          tmem_st32(ts + half * 32, w);
         }
         tmem_wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&bars.p_full[gt & 1]));
+        if (lane == 0) bar_arrive(smem_addr(&bars.p_full[rt]));
       }
       // ---- the unit's result, or this CTA's part of it ----
-      if (ok && !wait(&bars.o_done, gt - 1)) ok = false;
-      if (ok) {
-        fence_after();
-        const bool whole = t0 == 0 && t1 == tiles;
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        const int64_t orow = (int64_t)(sq.row0 + i) * p.q_heads + hq;
-        float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * kRows * (D + 2);
-        int first_nan = -1;                            // ring place of the first tile with a NaN that some rows do not see
-        for (int t = max(t0, least / kKeys); t < t1; ++t)
-          if (nan_any[(g + t - t0) % kScaleRing]) {
-            first_nan = t;
-            break;
-          }
+      if (!wait(&bars.o_done[rt], first + (t1 - t0) - 1)) {
+        ok = false;
+        return;
+      }
+      fence_after();
+      const bool whole = t0 == 0 && t1 == u.tiles;
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+      const int64_t orow = (int64_t)(sq.row0 + i) * p.q_heads + hq;
+      float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * kRows * (D + 2);
+      const int pr = kHalf * rt + row;
+      bool nan = false;                                  // some tile has NaN that some rows do not see
+      for (int t = max(t0, u.least / kKeys); t < t1; ++t) nan |= nan_any[(u.g + (t - t0)) % kScaleRing] != 0;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tmem_ld32(to + q * 32, o);
+        tmem_wait_ld<32>(o);
+        if (nan) {
+          for (int t = max(t0, u.least / kKeys); t < t1; ++t) {
+            const int ring = (u.g + (t - t0)) % kScaleRing;
+            if (!nan_any[ring]) continue;
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          tmem_ld32(tmem_o + lanes + q * 32, o);
-          tmem_wait_ld();
-          if (first_nan >= 0) {
-            for (int t = first_nan; t < t1; ++t) {
-              if (!nan_any[(g + t - t0) % kScaleRing]) continue;
-              const int *n = nan_at[(g + t - t0) % kScaleRing] + q * 32;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n[j] < lim) o[j] = __uint_as_float(0x7fffffffu);
-            }
-          }
-          if (whole) {
-            if (in) {
-              uint4 *dst = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(p.out) + orow * D + q * 32);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                f2 v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_of(o[8 * c + 2 * j], o[8 * c + 2 * j + 1]), f2_of(inv, inv));
-                dst[c] = f2_to16<DT>(v);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<float4 *>(part + tid * D + q * 32 + 4 * c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int j = 0; j < 32; ++j)
+              if (nan_at[ring][q * 32 + j] < lim) o[j] = __uint_as_float(0x7fffffffu);
           }
         }
-        fence_before();
-        if (!whole) {
-          part[kRows * D + 2 * tid] = R, part[kRows * D + 2 * tid + 1] = sum;
-        } else if (in && p.lse) {
-          p.lse[orow] = sum == 0.f ? -INFINITY : ((R == -INFINITY ? 0.f : R) + log2f(sum)) * kLn2;
+        if (whole) {
+          if (in) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(p.out) + orow * D + q * 32);
+            constexpr int W = 16 / sizeof(typename E::T);
+#pragma unroll
+            for (int c = 0; c < 32 / W; ++c) {
+              f2 v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_of(o[8 * c + 2 * j], o[8 * c + 2 * j + 1]), f2_of(inv, inv));
+              dst[c] = f2_to16<DT>(v);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4 *>(part + pr * D + q * 32 + 4 * c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
         }
       }
+      fence_before();
+      if (!whole) {
+        part[kRows * D + 2 * pr] = R, part[kRows * D + 2 * pr + 1] = sum;
+      } else if (in && p.lse) {
+        p.lse[orow] = sum == 0.f ? -INFINITY : ((R == -INFINITY ? 0.f : R) + log2f(sum)) * kLn2;
+      }
     });
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    const int r = tid - 256;
     units([&](const Unit &u) {
-      // ================= converters: token tid - 128 of each tile =================
+      // ================= converters: token r of each tile =================
       const Seq &sq = u.sq;
-      const uint32_t g = u.g;
-      const int t0 = u.t0, t1 = u.t1, least = u.least;
-      const int r = tid - 128;
-      uint32_t gt = g;
-      for (int t = t0; t < t1; ++t, ++gt) {
-        const int b = gt & 1, k0 = t * kKeys, ring = gt % kScaleRing;
-        // K
-        if (!wait(&bars.ck_full, gt) || (gt >= 2 && !wait(&bars.k_empty[b], (gt >> 1) - 1))) {
-          ok = false;
-          break;
-        }
-        const bool there = k0 + r < sq.len && scales[ring][0][r / PI_KV_BLOCK] >= 0.f;
+      for (int t = u.t0; t < u.t1; ++t) {
+        const uint32_t gt = u.g + (t - u.t0), b = gt & 1, ring = gt % kScaleRing;
+        const int k0 = t * kKeys;
         uint4 c[D / 16];
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) c[j] = *reinterpret_cast<const uint4 *>(sm + L::CK + code_at<D>(r, j));
-        auto store = [&](int base) {
+        bool there = false;
+        auto store = [&](char *tile) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             uint4 lo, hi;
@@ -406,27 +413,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             widen4(c[j].y, lo.z, lo.w);
             widen4(c[j].z, hi.x, hi.y);
             widen4(c[j].w, hi.z, hi.w);
-            char *slab = sm + base + (b * L::SLABS + j / 4) * L::SLAB;
-            *reinterpret_cast<uint4 *>(slab + sw128(r, j % 4 * 2)) = lo;
-            *reinterpret_cast<uint4 *>(slab + sw128(r, j % 4 * 2 + 1)) = hi;
+            *reinterpret_cast<uint4 *>(tile + j / 4 * L::SLAB + sw128(r, j % 4 * 2)) = lo;
+            *reinterpret_cast<uint4 *>(tile + j / 4 * L::SLAB + sw128(r, j % 4 * 2 + 1)) = hi;
           }
+          fence_async_smem();
+          __syncwarp();
         };
-        store(L::K);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&bars.ck_empty)), bar_arrive(smem_addr(&bars.k_full[b]));
-        // V
-        if (!wait(&bars.cv_full, gt) || (gt >= 2 && !wait(&bars.v_empty[b], (gt >> 1) - 1))) {
-          ok = false;
-          break;
-        }
+        auto codes = [&](uint32_t use) {                 // of stage use `use`; the stage is free again
+          const uint32_t st = use % kStages;
+          if (!wait(&bars.c_full[st], use / kStages)) return false;
+          const char *src = sm + L::C + st * 128 * D;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) c[j] = *reinterpret_cast<const uint4 *>(sm + L::CV + code_at<D>(r, j));
-        if (!there) {                                  // whatever the page held before, or nothing
+          for (int j = 0; j < D / 16; ++j) c[j] = *reinterpret_cast<const uint4 *>(src + code_at<D>(r, j));
+          there = k0 + r < sq.len && scales[ring][0][r / PI_KV_BLOCK] >= 0.f;
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(&bars.c_empty[st]));
+          return true;
+        };
+        // K
+        if (!codes(2 * gt) || (gt >= 2 && !wait(&bars.k_empty[b], (gt >> 1) - 1))) {
+          ok = false;
+          return;
+        }
+        store(sm + L::K + b * L::TILE);
+        if (lane == 0) bar_arrive(smem_addr(&bars.k_full[b]));
+        // V
+        if (!codes(2 * gt + 1)) {
+          ok = false;
+          return;
+        }
+        if (!there) {                                    // whatever the page held before, or nothing
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) c[j] = make_uint4(0, 0, 0, 0);
         }
-        if (k0 + kKeys > least) {
+        if (k0 + kKeys > u.least) {
           // A NaN among tokens that only some rows see would reach the others as
           // 0 * NaN: it is taken out, and each dim's first position with one noted.
           bool nan = false;
@@ -438,144 +458,142 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           }
           if (nan) {
             nan_any[ring] = 1;
-#pragma unroll 1
-            for (int d = 0; d < D; ++d) {
-              const int j = d / 16, e = d % 16 / 4, sh = d % 4 * 8;
-              unsigned v = 0;
-#pragma unroll
-              for (int jj = 0; jj < D / 16; ++jj)
-                if (jj == j) v = e == 0 ? c[jj].x : e == 1 ? c[jj].y : e == 2 ? c[jj].z : c[jj].w;
-              if ((v >> sh & 0x7f) == 0x7f) atomicMin(&nan_at[ring][d], k0 + r);
-            }
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-              c[j].x &= ~__vcmpeq4(c[j].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              c[j].y &= ~__vcmpeq4(c[j].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              c[j].z &= ~__vcmpeq4(c[j].z & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              c[j].w &= ~__vcmpeq4(c[j].w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              unsigned w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const unsigned is = __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll 1
+                for (unsigned left = is; left;) {
+                  const int k = (__ffs(left) - 1) / 8;
+                  left &= ~(255u << (8 * k));
+                  atomicMin(&nan_at[ring][16 * j + 4 * e + k], k0 + r);
+                }
+                w[e] &= ~is;
+              }
+              c[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+          __syncwarp();
         }
-        store(L::V);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&bars.cv_empty)), bar_arrive(smem_addr(&bars.v_full[b]));
+        if (gt >= 1 && !wait(&bars.v_empty, gt - 1)) {
+          ok = false;
+          return;
+        }
+        store(sm + L::V);
+        if (lane == 0) bar_arrive(smem_addr(&bars.v_full));
       }
     });
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (warp == 8) {
-    units([&](const Unit &u) {
-      // ================= tile copies; lane l looks after block l % 8 =================
-      const uint32_t g = u.g;
-      const int s = u.s, h = u.h, t0 = u.t0, t1 = u.t1, keys = u.keys, least = u.least;
-      const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
-      const int P = p.c.page_size, blocks = P / PI_KV_BLOCK, limit = min(keys, t1 * kKeys);
-      const bool by16 = P % 64 != 0;
-      uint32_t gt = g;
-      for (int t = t0; t < t1; ++t, ++gt) {
-        const int k = t * kKeys + (lane & 7) * 16, cp = k / P, co = k - cp * P;
-        const bool has = k < limit;
-        const int page = has ? table[cp] : -1;
-        const bool good = page >= 0 && page < p.c.n_pages;
-        if (has && !good && lane < 8) atomicOr(p.c.status, pi::kKvBadPage);
-        const unsigned mask = __ballot_sync(0xffffffffu, good) & 255u;
-        const int ring = gt % kScaleRing;
-        if (gt >= 1 && !wait(&bars.ck_empty, gt - 1)) {
-          ok = false;
-          break;
-        }
-        if (lane < 16) {
-          float *dst = &scales[ring][lane >> 3][lane & 7];
-          if (good)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)),
-                         "l"((lane >> 3 ? p.c.v_scales : p.c.k_scales) + ((int64_t)page * p.c.heads + h) * blocks + co / PI_KV_BLOCK)
-                         : "memory");
-          else
-            *dst = -1.f;
-        }
-        // boxes of 64 tokens where pages hold whole ones, else of 16
-        const int step = by16 ? 1 : 4;
-        int n_boxes = 0;
-        for (int b = 0; b < kBlocks; b += step) n_boxes += mask >> b & 1;
-        const uint32_t bytes = (uint32_t)n_boxes * step * 16 * D;
-        auto copy = [&](const CUtensorMap *map, int base, unsigned long long *bar) {
-          if (elect_one()) bar_expect(smem_addr(bar), bytes);
-          __syncwarp();
-#pragma unroll 1
-          for (int b = 0; b < kBlocks; b += step) {
-            const int z = __shfl_sync(0xffffffffu, page, b) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, b);
-            if ((mask >> b & 1) && elect_one()) tile_copy(smem_addr(sm + base + b * 16 * D), map, 0, y, z, smem_addr(bar));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12) {
+      units([&](const Unit &u) {
+        // ================= tile copies; lane l looks after block l % 8 =================
+        const int32_t *table = p.tok.page_table + (int64_t)u.s * p.tok.table_stride;
+        const int P = p.c.page_size, blocks = P / PI_KV_BLOCK, limit = min(u.keys, u.t1 * kKeys);
+        const int step = P % 64 ? 1 : 4;                 // boxes of 64 tokens where pages hold whole ones, else of 16
+        for (int t = u.t0; t < u.t1; ++t) {
+          const uint32_t gt = u.g + (t - u.t0), ring = gt % kScaleRing;
+          const int k = t * kKeys + (lane & 7) * 16, cp = k / P, co = k - cp * P;
+          const bool has = k < limit;
+          const int page = has ? table[cp] : -1;
+          const bool good = page >= 0 && page < p.c.n_pages;
+          if (has && !good && lane < 8) atomicOr(p.c.status, pi::kKvBadPage);
+          const unsigned mask = __ballot_sync(0xffffffffu, good) & 255u;
+          int n_boxes = 0;
+          for (int b = 0; b < kBlocks; b += step) n_boxes += mask >> b & 1;
+          auto copy = [&](const CUtensorMap *map, uint32_t use, bool with_scales) {
+            const uint32_t st = use % kStages, bar = smem_addr(&bars.c_full[st]);
+            if (use >= kStages && !wait(&bars.c_empty[st], use / kStages - 1)) return false;
+            if (with_scales) {
+              if (lane < 16) {
+                float *dst = &scales[ring][lane >> 3][lane & 7];
+                if (good)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)),
+                               "l"((lane >> 3 ? p.c.v_scales : p.c.k_scales) + ((int64_t)page * p.c.heads + u.h) * blocks + co / PI_KV_BLOCK)
+                               : "memory");
+                else
+                  *dst = -1.f;
+              }
+              if (lane == 0) tile_bad[ring] = mask != 255u;
+            } else if (t * kKeys + kKeys > u.least) {    // a tile whose NaN are noted
+              for (int d = lane; d < D; d += 32) nan_at[ring][d] = 0x7fffffff;
+              if (lane == 0) nan_any[ring] = 0;
+            }
             __syncwarp();
+            if (elect_one()) bar_expect(bar, (uint32_t)n_boxes * step * 16 * D);
+            __syncwarp();
+#pragma unroll 1
+            for (int b = 0; b < kBlocks; b += step) {
+              const int z = __shfl_sync(0xffffffffu, page, b) * p.c.heads + u.h, y = __shfl_sync(0xffffffffu, co, b);
+              if ((mask >> b & 1) && elect_one()) tile_copy(smem_addr(sm + L::C + st * 128 * D + b * 16 * D), map, 0, y, z, bar);
+              __syncwarp();
+            }
+            if (with_scales && lane < 16 && good) bar_arrive_copies(bar); else bar_arrive(bar);
+            copied = (int)use;
+            return true;
+          };
+          if (!copy(&maps.k, 2 * gt, true) || !copy(&maps.v, 2 * gt + 1, false)) {
+            ok = false;
+            return;
           }
-        };
-        copy(&maps.k, L::CK, &bars.ck_full);
-        ck_tile = gt;
-        if (lane < 16 && good) bar_arrive_copies(smem_addr(&bars.ck_full)); else bar_arrive(smem_addr(&bars.ck_full));
-        if (gt >= 1 && !wait(&bars.cv_empty, gt - 1)) {
-          ok = false;
-          break;
         }
-        if (t * kKeys + kKeys > least) {               // a tile whose NaN are noted
-          for (int d = lane; d < D; d += 32) nan_at[ring][d] = 0x7fffffff;
-          if (lane == 0) nan_any[ring] = 0;
-          __syncwarp();
-        }
-        copy(&maps.v, L::CV, &bars.cv_full);
-        cv_tile = gt;
-      }
-    });
-    } else if (warp == 9) {
-    units([&](const Unit &u) {
-      // ================= products =================
-      const uint32_t g = u.g;
-      const int t0 = u.t0, t1 = u.t1;
+      });
+    } else if (warp == 13) {
       const uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
-      auto issue_s = [&](uint32_t gt) {
-        if (!wait(&bars.k_full[gt & 1], gt >> 1)) return false;
-        fence_after();
-        if (elect_one()) {
-          const uint32_t q = smem_addr(sm + L::Q), k = smem_addr(sm + L::K + (gt & 1) * L::SLABS * L::SLAB);
+      units([&](const Unit &u) {
+        // ================= products =================
+        const int n_rt = u.two ? 2 : 1;
+        auto issue_s = [&](int rt, uint32_t gt) {        // S of a row tile; K's buffer is free after the last row tile's
+          if (rt == 0 && !wait(&bars.k_full[gt & 1], gt >> 1)) return false;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t q = smem_addr(sm + L::Q + rt * L::TILE), k = smem_addr(sm + L::K + (gt & 1) * L::TILE);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t o = e / 4 * L::SLAB + e % 4 * 32;
-            mma_ss(tmem + (gt & 1) * 128, sdesc(q + o, 16, 1024), sdesc(k + o, 16, 1024), id_s, e > 0);
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t o = e / 4 * L::SLAB + e % 4 * 32;
+              mma_ss(tmem + rt * 128, sdesc(q + o, 16, 1024), sdesc(k + o, 16, 1024), id_s, e > 0);
+            }
+            if (rt == n_rt - 1) mma_commit(smem_addr(&bars.k_empty[gt & 1]));
+            mma_commit(smem_addr(&bars.s_full[rt]));
           }
-          mma_commit(smem_addr(&bars.k_empty[gt & 1]));
-          mma_commit(smem_addr(&bars.s_full[gt & 1]));
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = wait(&bars.q_full, u.index) && issue_s(g);
-      uint32_t gt = g;
-      for (int t = t0; ok && t < t1; ++t, ++gt) {
-        if (t + 1 < t1) ok = issue_s(gt + 1);
-        ok = ok && wait(&bars.v_full[gt & 1], gt >> 1) && wait(&bars.p_full[gt & 1], gt >> 1);
-        if (!ok) break;
-        fence_after();
-        if (elect_one()) {
-          const uint32_t v = smem_addr(sm + L::V + (gt & 1) * L::SLABS * L::SLAB);
+          __syncwarp();
+          return true;
+        };
+        for (int rt = 0; ok && rt < n_rt; ++rt) ok = wait(&bars.q_full[rt], rt ? u.index1 : u.index) && issue_s(rt, u.g);
+        for (int t = u.t0; ok && t < u.t1; ++t) {
+          const uint32_t gt = u.g + (t - u.t0);
+          ok = wait(&bars.v_full, gt);
+          for (int rt = 0; ok && rt < n_rt; ++rt) {
+            if (!wait(&bars.p_full[rt], (rt ? u.g1 : u.g) + (t - u.t0))) {
+              ok = false;
+              break;
+            }
+            fence_after();
+            if (elect_one()) {
+              const uint32_t v = smem_addr(sm + L::V);
 #pragma unroll
-          for (int e = 0; e < kKeys / 16; ++e)
-            mma_ts(tmem_o, tmem + (gt & 1) * 128 + e * 8, sdesc(v + e * 2048, L::SLAB, 1024), id_o, t > t0 || e > 0);
-          mma_commit(smem_addr(&bars.v_empty[gt & 1]));
-          mma_commit(smem_addr(&bars.o_done));
+              for (int e = 0; e < kKeys / 16; ++e)
+                mma_ts(tmem + 256 + rt * 128, tmem + rt * 128 + e * 8, sdesc(v + e * 2048, L::SLAB, 1024), id_o, t > u.t0 || e > 0);
+              if (rt == n_rt - 1) mma_commit(smem_addr(&bars.v_empty));
+              mma_commit(smem_addr(&bars.o_done[rt]));
+            }
+            __syncwarp();
+            if (t + 1 < u.t1) ok = issue_s(rt, gt + 1);
+          }
         }
-        __syncwarp();
-      }
-    });
+      });
     }
   }
   // Copies and products on their way land before the CTA leaves (bounded).
   if (!ok) {
     failed = 1;
     if (lane == 0) atomicOr(p.c.status, pi::kKvTimeout);
-    if (warp == 8) {
-      if (ck_tile >= 0) bar_wait(smem_addr(&bars.ck_full), ck_tile & 1);
-      if (cv_tile >= 0) bar_wait(smem_addr(&bars.cv_full), cv_tile & 1);
-    }
-    if (warp == 9) {                                   // a commit follows every product before it
+    if (warp == 12 && copied >= 0)                       // stages fill in order, up to kStages of them on their way
+      for (int use = max(0, copied - kStages + 1); use <= copied; ++use)
+        bar_wait(smem_addr(&bars.c_full[use % kStages]), use / kStages & 1);
+    if (warp == 13) {                                  // a commit follows every product before it
       if (elect_one()) mma_commit(smem_addr(&bars.drain));
       __syncwarp();
       bar_wait(smem_addr(&bars.drain), 0);
@@ -584,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int DT, int D>
@@ -600,7 +618,7 @@ cudaError_t launch(AttnParams p, cudaStream_t s) {
   k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 32), dim3(128), 0, s, p);
 }
 
 }  // namespace
