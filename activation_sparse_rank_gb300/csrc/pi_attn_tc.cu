@@ -31,27 +31,23 @@ constexpr int kThreads = 512;      // four warpgroups: register shares are set f
 constexpr int kStages = 3;         // of codes, K and V of a tile in turn
 constexpr int kScaleRing = 8;    // tiles whose scales are kept: copies run at most 5 tiles ahead of the softmax
 
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  // shared-memory matrix descriptor, 128-byte swizzle
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
+// Shared-memory matrix descriptor, 128-byte swizzle: its low word holds the
+// address (and lbo), so a step of `bytes` adds bytes / 16 to it.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFF) >> 4 | ((lbo >> 4) & 0x3FFF) << 16; }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;        // groups of 8 rows 1024 bytes apart
 // kind::f16, fp16 operands, binary32 sums, M = 128
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-               "l"(a), "l"(b), "r"(id), "r"(acc));
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-               "r"(a), "l"(b), "r"(id), "r"(acc));
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi));
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -542,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
       });
     } else if (warp == 13) {
       const uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
+      const uint32_t q_lo = desc_lo(smem_addr(sm + L::Q), 16), k_lo = desc_lo(smem_addr(sm + L::K), 16), v_lo = desc_lo(smem_addr(sm + L::V), L::SLAB);
       units([&](const Unit &u) {
         // ================= products =================
         const int n_rt = u.two ? 2 : 1;
@@ -549,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           if (rt == 0 && !wait(&bars.k_full[gt & 1], gt >> 1)) return false;
           fence_after();
           if (elect_one()) {
-            const uint32_t q = smem_addr(sm + L::Q + rt * L::TILE), k = smem_addr(sm + L::K + (gt & 1) * L::TILE);
+            const uint32_t q = q_lo + rt * (L::TILE >> 4), k = k_lo + (gt & 1) * (L::TILE >> 4);
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
-              const uint32_t o = e / 4 * L::SLAB + e % 4 * 32;
-              mma_ss(tmem + rt * 128, sdesc(q + o, 16, 1024), sdesc(k + o, 16, 1024), id_s, e > 0);
+              const uint32_t o = (e / 4 * L::SLAB + e % 4 * 32) >> 4;
+              mma_ss(tmem + rt * 128, q + o, k + o, id_s, e > 0);
             }
             if (rt == n_rt - 1) mma_commit(smem_addr(&bars.k_empty[gt & 1]));
             mma_commit(smem_addr(&bars.s_full[rt]));
@@ -572,10 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             }
             fence_after();
             if (elect_one()) {
-              const uint32_t v = smem_addr(sm + L::V);
 #pragma unroll
               for (int e = 0; e < kKeys / 16; ++e)
-                mma_ts(tmem + 256 + rt * 128, tmem + rt * 128 + e * 8, sdesc(v + e * 2048, L::SLAB, 1024), id_o, t > u.t0 || e > 0);
+                mma_ts(tmem + 256 + rt * 128, tmem + rt * 128 + e * 8, v_lo + e * (2048 >> 4), id_o, t > u.t0 || e > 0);
               if (rt == n_rt - 1) mma_commit(smem_addr(&bars.v_empty));
               mma_commit(smem_addr(&bars.o_done[rt]));
             }
@@ -618,7 +614,7 @@ cudaError_t launch(AttnParams p, cudaStream_t s) {
   k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 32), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 64), dim3(128), 0, s, p);
 }
 
 }  // namespace

@@ -122,6 +122,19 @@ __device__ __forceinline__ uint4 f2_to16(const f2 *v) {
   }
 }
 
+template <int I>
+struct Int {
+  static constexpr int v = I;
+};
+// f(Int<0>) .. f(Int<N - 1>), written out: arrays that f indexes stay in registers.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Int<I>{});
+    each<N, I + 1>(f);
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

@@ -313,19 +313,6 @@ __device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, fl
   return found;
 }
 
-template <int I>
-struct Int {
-  static constexpr int v = I;
-};
-// f(Int<0>) .. f(Int<N - 1>), written out: the row's registers are never indexed at run time.
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void each(F f) {
-  if constexpr (I < N) {
-    f(Int<I>{});
-    each<N, I + 1>(f);
-  }
-}
-
 // One row for a cluster of CTAs; CTA r has the row's pieces [r share, (r + 1)
 // share), thread t of it pieces t, t + NT, ..., which it keeps in registers from
 // the maximum to the sums.
