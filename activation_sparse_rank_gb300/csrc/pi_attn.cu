@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
   for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
 
   Share at;
-  if (!find_share<ROWS, kTile>(p, share_sm, &at)) return;
+  if (!find_share<ROWS, kTile>(p, share_sm, blockIdx.x, &at)) return;
   uint32_t full_ph = 0, empty_ph = 0, used = 0, pend = 0;    // a bit a stage: phases to wait for, filled ever, filled and not waited for
   bool dead = false;                               // a wait ran out: nothing more is copied or computed
   const bool by16 = p.c.page_size % kTile != 0;    // a tile may lie in several pages: blocks are copied one by one
@@ -558,7 +558,7 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.tok.n_seqs * p.c.heads, ROWS / 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.grid, ROWS / 4), dim3(128), 0, s, p);
 }
 
 template <int DT, int D>

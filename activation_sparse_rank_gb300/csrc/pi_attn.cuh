@@ -81,14 +81,6 @@ template <int ROWS, int TILE>
 __device__ __forceinline__ int unit_tiles(const AttnParams &p, const Seq &q, int rt) {
   return (unit_keys<ROWS>(p, q, rt) + TILE - 1) / TILE;
 }
-template <int ROWS, int TILE>
-__device__ __forceinline__ int64_t seq_tiles(const AttnParams &p, int s) {
-  const Seq q = load_seq(p, s);
-  int64_t t = 0;
-  for (int rt = 0; rt < p.row_tiles && rt * ROWS < q.rows; ++rt) t += unit_tiles<ROWS, TILE>(p, q, rt);
-  return t * p.c.heads;
-}
-
 // Exclusive sum over the CTA's first 128 threads (the others pass 0); *total gets the whole sum.
 __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *sm, int64_t *total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -117,44 +109,77 @@ __device__ __forceinline__ int64_t cta_owner(int64_t tile, int64_t total, int sh
 // (sequence, head, row tile); units without keys take no place.
 struct Share {
   int64_t begin, end;      // tiles
+  int64_t total;           // of the line
+  int shares;              // that it is cut into
   int s, h, rt;            // the unit that `begin` lies in
   int64_t u0;              // where that unit begins
   Seq sq;
 };
 struct ShareShared {
-  int64_t scan[4], found[2];
+  int64_t scan[4], at;
+  int s, rt;
 };
-// False if this CTA has none.  Every thread of the CTA calls it.
+// Share `cta` of p.grid; false if there is none.  Every thread of the CTA calls it.
+// The line is ordered by sequence, head, row tile; a sequence's row tiles have
+// the same keys for every head, so the sums run over (sequence, row tile) pairs,
+// times the heads.
 template <int ROWS, int TILE>
-__device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm, Share *o) {
-  const int per = (p.tok.n_seqs + 127) / 128;
+__device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm, int cta, Share *o) {
+  const int64_t pairs = (int64_t)p.tok.n_seqs * p.row_tiles, per = (pairs + 127) / 128, k0 = threadIdx.x * per;
+  auto tiles_of = [&](int64_t k) {
+    const int s = (int)(k / p.row_tiles);
+    return unit_tiles<ROWS, TILE>(p, load_seq(p, s), (int)(k - (int64_t)s * p.row_tiles));
+  };
   int64_t mine = 0, total;
   if (threadIdx.x < 128)
-    for (int i = 0; i < per; ++i) {
-      const int s = threadIdx.x * per + i;
-      if (s < p.tok.n_seqs) mine += seq_tiles<ROWS, TILE>(p, s);
-    }
+    for (int64_t k = k0; k < k0 + per && k < pairs; ++k) mine += tiles_of(k);
   int64_t at = cta_scan(mine, sm.scan, &total);
-  const int shares = (int)min((int64_t)gridDim.x, total);    // every share has a tile, so every part between two of a unit is written
-  if (blockIdx.x >= shares) return false;
-  o->begin = cta_begin(blockIdx.x, total, shares), o->end = cta_begin(blockIdx.x + 1, total, shares);
-  if (at <= o->begin && o->begin < at + mine)
-    for (int i = 0; i < per; ++i) {
-      const int s = threadIdx.x * per + i;
-      const int64_t n = seq_tiles<ROWS, TILE>(p, s);
-      if (o->begin < at + n) {
-        sm.found[0] = s, sm.found[1] = at;
+  const int heads = p.c.heads;
+  total *= heads;
+  const int shares = (int)min((int64_t)p.grid, total);       // every share has a tile, so every part between two of a unit is written
+  o->total = total, o->shares = shares;
+  if (cta >= shares) return false;
+  o->begin = cta_begin(cta, total, shares), o->end = cta_begin(cta + 1, total, shares);
+  if (at * heads <= o->begin && o->begin < (at + mine) * heads)
+    for (int64_t k = k0;; ++k) {                     // the pair there is of the right sequence
+      const int n = tiles_of(k);
+      if (o->begin < (at + n) * heads) {
+        sm.s = (int)(k / p.row_tiles), sm.rt = (int)(k % p.row_tiles), sm.at = at;
         break;
       }
       at += n;
     }
   __syncthreads();
-  o->s = (int)sm.found[0], o->u0 = sm.found[1];
+  // in that sequence: its tiles of one head, then the head and the row tile
+  const int lane = threadIdx.x & 31;
+  o->s = sm.s;
   o->sq = load_seq(p, o->s);
-  const int64_t per_head = seq_tiles<ROWS, TILE>(p, o->s) / p.c.heads;
-  o->h = (int)((o->begin - o->u0) / per_head), o->rt = 0;
-  o->u0 += o->h * per_head;
-  for (int n; o->begin >= o->u0 + (n = unit_tiles<ROWS, TILE>(p, o->sq, o->rt)); ++o->rt) o->u0 += n;
+  int64_t before = 0, all = 0;
+  for (int r0 = 0; r0 < p.row_tiles; r0 += 32) {
+    const int n = r0 + lane < p.row_tiles ? unit_tiles<ROWS, TILE>(p, o->sq, r0 + lane) : 0;
+    all += __reduce_add_sync(0xffffffffu, n);
+    before += __reduce_add_sync(0xffffffffu, r0 + lane < sm.rt ? n : 0);
+  }
+  const int64_t start = (sm.at - before) * heads;
+  o->h = (int)((o->begin - start) / all);
+  int64_t u0 = start + o->h * all;
+  for (int r0 = 0; r0 < p.row_tiles; r0 += 32) {
+    const int n = r0 + lane < p.row_tiles ? unit_tiles<ROWS, TILE>(p, o->sq, r0 + lane) : 0;
+    int sum = n;                                     // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, u0 + sum > o->begin);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      o->rt = r0 + l;
+      o->u0 = u0 + __shfl_sync(0xffffffffu, sum - n, l);
+      break;
+    }
+    u0 += __shfl_sync(0xffffffffu, sum, 31);
+  }
   return true;
 }
 // To the next unit with keys; false after the last.
@@ -178,88 +203,86 @@ struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 o
   CUtensorMap k, v;
 };
 
-// Units cut between CTAs: their parts added in CTA order.  Units without keys:
-// 0 and -inf.  blockIdx.x: (sequence, head); a warp per row.
+// Units cut between CTAs: their parts added in CTA order.  blockIdx.x is a share;
+// the first whose begin lies inside a unit looks after that unit, a warp a row.
+// Rows of units without keys: 0 and -inf.
 template <int DT, int D, int ROWS, int TILE>
 __global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
   using E = Elem<DT>;
-  constexpr int LANES = D / 4 <= 16 ? 16 : 32;   // lanes across a row (D = 64: half a warp per part)
+  constexpr int LANES = D / 4 <= 16 ? 16 : 32;     // lanes across a row (D = 64: half a warp per part)
   constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
-  __shared__ int64_t scan[4], start;
-  const int s = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads, lane = threadIdx.x & 31;
-  const int per = (p.tok.n_seqs + 127) / 128;
-  int64_t mine = 0, total;
-  for (int i = 0; i < per; ++i) {
-    const int t = threadIdx.x * per + i;
-    if (t < p.tok.n_seqs) mine += seq_tiles<ROWS, TILE>(p, t);
-  }
-  int64_t at = cta_scan(mine, scan, &total);
-  if (s / per == threadIdx.x) {
-    for (int t = threadIdx.x * per; t < s; ++t) at += seq_tiles<ROWS, TILE>(p, t);
-    start = at;
-  }
-  __syncthreads();
-  griddep_wait();
-  const int shares = (int)min((int64_t)p.grid, total);
-  const Seq sq = load_seq(p, s);
-  int64_t u0 = start + h * (seq_tiles<ROWS, TILE>(p, s) / p.c.heads);
-  for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows; ++rt) {
-    const int tiles = unit_tiles<ROWS, TILE>(p, sq, rt);
-    int64_t c0 = 0, c1 = -1;
-    if (tiles) {
-      c0 = cta_owner(u0, total, shares), c1 = cta_owner(u0 + tiles - 1, total, shares);
-      u0 += tiles;
-      if (c0 == c1) continue;
+  __shared__ ShareShared share_sm;
+  const int lane = threadIdx.x & 31;
+  for (int s = blockIdx.x; s < p.tok.n_seqs; s += gridDim.x) {       // the leading row tiles of a sequence may see nothing
+    const Seq sq = load_seq(p, s);
+    int rows = 0;
+    for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows && unit_tiles<ROWS, TILE>(p, sq, rt) == 0; ++rt) rows = min(sq.rows, (rt + 1) * ROWS);
+    const int64_t first = (int64_t)sq.row0 * p.q_heads, n = (int64_t)(rows / p.group) * p.q_heads;
+    const int rest = rows % p.group;                 // a row tile may end inside a token's heads
+    for (int64_t i = blockIdx.y * 128 + threadIdx.x; i < (n + (rest ? p.q_heads : 0)) * (D / 8); i += gridDim.y * 128) {
+      const int64_t r = i / (D / 8);
+      if (r >= n && (r - n) % p.group >= rest) continue;
+      reinterpret_cast<uint4 *>(p.out)[(first + r) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
+      if (p.lse && i % (D / 8) == 0) p.lse[first + r] = -INFINITY;
     }
-    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
-      const int gr = rt * ROWS + row;
-      if (gr >= sq.rows) break;
-      float M = -INFINITY, L = 0.f;
-      auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
-      for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
-      M = warp_max(M);
-      const float ms = M == -INFINITY ? 0.f : M;
-      float4 o[VECS];
+  }
+  Share at;
+  const bool any = find_share<ROWS, TILE>(p, share_sm, blockIdx.x, &at);
+  griddep_wait();                                  // on every path: this grid does not end before the main kernel's
+  if (!any || at.begin == at.u0) return;
+  const int64_t c0 = cta_owner(at.u0, at.total, at.shares);
+  if (c0 != (int64_t)blockIdx.x - 1) return;
+  const int64_t c1 = cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares);
+  const Seq &sq = at.sq;
+  const int h = at.h, rt = at.rt;
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
+    const int gr = rt * ROWS + row;
+    if (gr >= sq.rows) break;
+    float M = -INFINITY, L = 0.f;
+    auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
+    for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
+    M = warp_max(M);
+    const float ms = M == -INFINITY ? 0.f : M;
+    float4 o[VECS];
 #pragma unroll
-      for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
-        const int n = (int)min((int64_t)32, c1 - cb + 1);
-        float w = 0.f;
-        if (lane < n) {
-          const float *ml = part(cb + lane) + ROWS * D + 2 * row;
-          w = ex2(ml[0] - ms);
-          L += ml[1] * w;
-        }
+    for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
+      const int n = (int)min((int64_t)32, c1 - cb + 1);
+      float w = 0.f;
+      if (lane < n) {
+        const float *ml = part(cb + lane) + ROWS * D + 2 * row;
+        w = ex2(ml[0] - ms);
+        L += ml[1] * w;
+      }
 #pragma unroll 8
-        for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
-          const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
-          const float *src = part(cb + min(i, n - 1)) + row * D;
+      for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
+        const float *src = part(cb + min(i, n - 1)) + row * D;
 #pragma unroll
-          for (int k = 0; k < VECS; ++k) {
-            const int d = (lane % LANES + k * 32) * 4;
-            if (d >= D) continue;
-            const float4 x = *reinterpret_cast<const float4 *>(src + d);
-            if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
-          }
+        for (int k = 0; k < VECS; ++k) {
+          const int d = (lane % LANES + k * 32) * 4;
+          if (d >= D) continue;
+          const float4 x = *reinterpret_cast<const float4 *>(src + d);
+          if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
         }
       }
-      L = warp_sum(L);
-      if constexpr (LANES == 16) {
-        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
-        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
-      }
-      const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
-      const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-      for (int k = 0; k < VECS; ++k) {
-        const int d = (lane % LANES + k * 32) * 4;
-        if (d >= D || lane >= LANES) continue;
-        Pack<DT, 4> y;
-        y.v[0] = E::from(o[k].x * inv), y.v[1] = E::from(o[k].y * inv), y.v[2] = E::from(o[k].z * inv), y.v[3] = E::from(o[k].w * inv);
-        *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
-      }
-      if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
     }
+    L = warp_sum(L);
+    if constexpr (LANES == 16) {
+      o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
+      o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
+    }
+    const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) {
+      const int d = (lane % LANES + k * 32) * 4;
+      if (d >= D || lane >= LANES) continue;
+      Pack<DT, 4> y;
+      y.v[0] = E::from(o[k].x * inv), y.v[1] = E::from(o[k].y * inv), y.v[2] = E::from(o[k].z * inv), y.v[3] = E::from(o[k].w * inv);
+      *reinterpret_cast<Pack<DT, 4> *>(static_cast<typename E::T *>(p.out) + orow * D + d) = y;
+    }
+    if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
   }
 }
 

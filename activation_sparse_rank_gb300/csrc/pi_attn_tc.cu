@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
     failed = 0;
   }
   Share at;
-  if (!find_share<kRows, kKeys>(p, share_sm, &at)) return;
+  if (!find_share<kRows, kKeys>(p, share_sm, blockIdx.x, &at)) return;
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -614,7 +614,7 @@ cudaError_t launch(AttnParams p, cudaStream_t s) {
   k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.tok.n_seqs * p.c.heads, 64), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.grid, 32), dim3(128), 0, s, p);
 }
 
 }  // namespace
