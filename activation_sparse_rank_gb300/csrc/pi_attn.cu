@@ -135,7 +135,9 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
   for (int s = blockIdx.x * 128 + threadIdx.x; s < p.tok.n_seqs; s += gridDim.x * 128) flag_seq(p, s);
 
   Share at;
-  if (!find_share<ROWS, kTile>(p, share_sm, blockIdx.x, &at)) return;
+  const bool any = find_share<ROWS, kTile>(p, share_sm, blockIdx.x, &at);
+  if (threadIdx.x == 0) write_plan<ROWS, kTile>(p, any, at);
+  if (!any) return;
   uint32_t full_ph = 0, empty_ph = 0, used = 0, pend = 0;    // a bit a stage: phases to wait for, filled ever, filled and not waited for
   bool dead = false;                               // a wait ran out: nothing more is copied or computed
   const bool by16 = p.c.page_size % kTile != 0;    // a tile may lie in several pages: blocks are copied one by one
@@ -558,7 +560,7 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.grid, ROWS / 4), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.grid, combine_y(ROWS)), dim3(kCombineThreads), 0, s, p);
 }
 
 template <int DT, int D>
@@ -574,7 +576,10 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
 
 // From how many query rows a head on the tcgen05 kernel (row tiles of 128, each
 // tile widened once for them) is taken.
-bool many_rows(int D, int64_t rows) { return (D == 64 || D == 128) && rows > 64; }
+#ifndef MR
+#define MR 64
+#endif
+bool many_rows(int D, int64_t rows) { return D <= 128 && rows > MR; }
 
 template <int DT>
 cudaError_t attn_by_dim(const AttnParams &p, cudaStream_t s) {
@@ -607,7 +612,7 @@ size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, in
   if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
   const int D = c->head_dim;
   const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 64, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
-  return sizeof(float) * 2 * rows * (size_t)(D + 2);
+  return sizeof(int4) * attn_grid(D, 1) + sizeof(float) * 2 * rows * (size_t)(D + 2);
 }
 
 pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
@@ -639,7 +644,8 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
   const int group = q_heads / cache->heads;
   const AttnShape shape = attn_shape(cache->head_dim, (int64_t)max_q * group);
   const int rows = 8 * shape.nb * shape.warps_m;
-  const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<float *>(ws),
+  const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<int4 *>(ws),
+                     reinterpret_cast<float *>(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1)),
                      sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
                      (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

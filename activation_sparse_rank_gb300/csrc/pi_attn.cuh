@@ -29,6 +29,7 @@ struct AttnParams {
   int64_t qt, qh;
   void *out;
   float *lse;
+  int4 *plan;              // [grid] for k_attn_combine: the unit that share i has to add up (sequence, head, row tile, parts; 0 parts: none)
   float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
   float scale;             // sm_scale log2(e)
   int q_heads, group, max_q, causal, row_tiles, grid;
@@ -199,79 +200,125 @@ __device__ __forceinline__ bool next_unit(const AttnParams &p, Share *o) {
   return true;
 }
 
+// Parts of a unit are added by the first share whose begin lies inside it (the
+// part before its begin is its neighbour's): thread 0 of that share's CTA says so.
+template <int ROWS, int TILE>
+__device__ __forceinline__ void write_plan(const AttnParams &p, bool any, const Share &at) {
+  int4 plan = make_int4(0, 0, 0, 0);
+  if (any && at.begin > at.u0) {
+    const int64_t c0 = cta_owner(at.u0, at.total, at.shares);
+    if (c0 == (int64_t)blockIdx.x - 1)
+      plan = make_int4(at.s, at.h, at.rt, (int)(cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares) - c0) + 1);
+  }
+  p.plan[blockIdx.x] = plan;
+}
+
 struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 or 16 tokens and up to 128 bytes
   CUtensorMap k, v;
 };
 
-// Units cut between CTAs: their parts added in CTA order.  blockIdx.x is a share;
-// the first whose begin lies inside a unit looks after that unit, a warp a row.
-// Rows of units without keys: 0 and -inf.
+// Units cut between CTAs: their parts added in CTA order, those of plan[blockIdx.x].
+// A row's parts come at the latency of L2, so of more than eight parts (a long
+// cache with few heads: up to one a CTA) four or sixteen warps take a row, a run
+// of parts each.  Rows of units without keys: 0 and -inf.
+constexpr int kCombineThreads = 512;
+constexpr int combine_y(int rows) { return rows <= 16 ? rows / 4 : rows <= 64 ? 4 : rows / 16; }
 template <int DT, int D, int ROWS, int TILE>
-__global__ void __launch_bounds__(128) k_attn_combine(const AttnParams p) {
+__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const AttnParams p) {
   using E = Elem<DT>;
   constexpr int LANES = D / 4 <= 16 ? 16 : 32;     // lanes across a row (D = 64: half a warp per part)
   constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
-  __shared__ ShareShared share_sm;
-  const int lane = threadIdx.x & 31;
+  constexpr int WARPS = kCombineThreads / 32;
+  __shared__ float4 sums[WARPS][D / 4];
+  __shared__ float2 stats[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int s = blockIdx.x; s < p.tok.n_seqs; s += gridDim.x) {       // the leading row tiles of a sequence may see nothing
     const Seq sq = load_seq(p, s);
     int rows = 0;
     for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows && unit_tiles<ROWS, TILE>(p, sq, rt) == 0; ++rt) rows = min(sq.rows, (rt + 1) * ROWS);
     const int64_t first = (int64_t)sq.row0 * p.q_heads, n = (int64_t)(rows / p.group) * p.q_heads;
     const int rest = rows % p.group;                 // a row tile may end inside a token's heads
-    for (int64_t i = blockIdx.y * 128 + threadIdx.x; i < (n + (rest ? p.q_heads : 0)) * (D / 8); i += gridDim.y * 128) {
+    for (int64_t i = blockIdx.y * kCombineThreads + threadIdx.x; i < (n + (rest ? p.q_heads : 0)) * (D / 8); i += gridDim.y * kCombineThreads) {
       const int64_t r = i / (D / 8);
       if (r >= n && (r - n) % p.group >= rest) continue;
       reinterpret_cast<uint4 *>(p.out)[(first + r) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
       if (p.lse && i % (D / 8) == 0) p.lse[first + r] = -INFINITY;
     }
   }
-  Share at;
-  const bool any = find_share<ROWS, TILE>(p, share_sm, blockIdx.x, &at);
   griddep_wait();                                  // on every path: this grid does not end before the main kernel's
-  if (!any || at.begin == at.u0) return;
-  const int64_t c0 = cta_owner(at.u0, at.total, at.shares);
-  if (c0 != (int64_t)blockIdx.x - 1) return;
-  const int64_t c1 = cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares);
-  const Seq &sq = at.sq;
-  const int h = at.h, rt = at.rt;
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 4) {
-    const int gr = rt * ROWS + row;
-    if (gr >= sq.rows) break;
+  const int4 plan = p.plan[blockIdx.x];
+  const int parts = plan.w, h = plan.y, rt = plan.z;
+  if (parts == 0) return;
+  const Seq sq = load_seq(p, plan.x);
+  const int64_t c0 = (int64_t)blockIdx.x - 1;
+  const int split = parts > 64 ? 16 : parts > 8 ? 4 : 1, sub = warp % split, rows = WARPS / split;
+  const int per = (parts + split - 1) / split, p0 = min(parts, sub * per), p1 = min(parts, p0 + per);
+  auto part = [&](int i) { return p.part + (2 * (c0 + i) + (i == 0)) * ROWS * (D + 2); };
+  for (int base = blockIdx.y * rows; base < min(ROWS, sq.rows - rt * ROWS); base += gridDim.y * rows) {
+    const int row = base + warp / split, gr = rt * ROWS + row;
+    const bool in = row < ROWS && gr < sq.rows;
     float M = -INFINITY, L = 0.f;
-    auto part = [&](int64_t c) { return p.part + (2 * c + (c == c0)) * ROWS * (D + 2); };
-    for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[ROWS * D + 2 * row]);
-    M = warp_max(M);
-    const float ms = M == -INFINITY ? 0.f : M;
     float4 o[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t cb = c0; cb <= c1; cb += 32) {  // 32 parts at a time: a lane per weight, then all lanes along the row
-      const int n = (int)min((int64_t)32, c1 - cb + 1);
-      float w = 0.f;
-      if (lane < n) {
-        const float *ml = part(cb + lane) + ROWS * D + 2 * row;
-        w = ex2(ml[0] - ms);
-        L += ml[1] * w;
-      }
+    if (in) {
+      for (int i = p0 + lane; i < p1; i += 32) M = fmaxf(M, part(i)[ROWS * D + 2 * row]);
+      M = warp_max(M);
+      const float ms = M == -INFINITY ? 0.f : M;
+      for (int b = p0; b < p1; b += 32) {          // 32 parts at a time: a lane per weight, then all lanes along the row
+        const int n = min(32, p1 - b);
+        float w = 0.f;
+        if (lane < n) {
+          const float *ml = part(b + lane) + ROWS * D + 2 * row;
+          w = ex2(ml[0] - ms);
+          L += ml[1] * w;
+        }
 #pragma unroll 8
-      for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);             // 0 past n
-        const float *src = part(cb + min(i, n - 1)) + row * D;
+        for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);           // 0 past n
+          const float *src = part(b + min(i, n - 1)) + row * D;
 #pragma unroll
-        for (int k = 0; k < VECS; ++k) {
-          const int d = (lane % LANES + k * 32) * 4;
-          if (d >= D) continue;
-          const float4 x = *reinterpret_cast<const float4 *>(src + d);
-          if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
+          for (int k = 0; k < VECS; ++k) {
+            const int d = (lane % LANES + k * 32) * 4;
+            if (d >= D) continue;
+            const float4 x = *reinterpret_cast<const float4 *>(src + d);
+            if (i < n) o[k].x = fmaf(x.x, wi, o[k].x), o[k].y = fmaf(x.y, wi, o[k].y), o[k].z = fmaf(x.z, wi, o[k].z), o[k].w = fmaf(x.w, wi, o[k].w);
+          }
         }
       }
+      L = warp_sum(L);
+      if constexpr (LANES == 16) {
+        o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
+        o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
+      }
     }
-    L = warp_sum(L);
-    if constexpr (LANES == 16) {
-      o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, 16), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, 16);
-      o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, 16), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, 16);
+    if (split > 1) {                               // uniform over the CTA
+      __syncthreads();                             // the quarters of the rows before have been read
+#pragma unroll
+      for (int k = 0; k < VECS; ++k)
+        if (lane < LANES && lane + k * 32 < D / 4) sums[warp][lane + k * 32] = o[k];
+      if (lane == 0) stats[warp] = make_float2(M, L);
+      __syncthreads();
+      if (sub) continue;
+      float ms = M;
+      for (int i = 1; i < split; ++i) ms = fmaxf(ms, stats[warp + i].x);
+      M = ms, ms = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+#pragma unroll
+      for (int k = 0; k < VECS; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < split; ++i) {
+        const float w = ex2(stats[warp + i].x - ms);
+        L += stats[warp + i].y * w;
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+          if (lane % LANES + k * 32 < D / 4) {
+            const float4 x = sums[warp + i][lane % LANES + k * 32];
+            o[k].x = fmaf(x.x, w, o[k].x), o[k].y = fmaf(x.y, w, o[k].y), o[k].z = fmaf(x.z, w, o[k].z), o[k].w = fmaf(x.w, w, o[k].w);
+          }
+      }
     }
+    if (!in) continue;
+    const float ms = M == -INFINITY ? 0.f : M;
     const int64_t orow = (int64_t)(sq.row0 + gr / p.group) * p.q_heads + h * p.group + gr % p.group;
     const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll
@@ -317,7 +364,7 @@ inline bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// pi_attn_tc.cu: head_dim 64 or 128, row_tiles and grid are its own.
+// pi_attn_tc.cu: head_dim up to 128, row_tiles and grid are its own.
 cudaError_t run_tc(const AttnParams &p, int dtype, cudaStream_t s);
 constexpr int kTcRows = 256;     // query rows of a unit there
 

@@ -88,7 +88,7 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 template <int D>
 struct Smem {                       // byte offsets from a 1024-byte boundary
-  static constexpr int SLABS = D / 64, SLAB = 128 * 128, TILE = SLABS * SLAB;   // a slab: 64 fp16 dims of 128 rows
+  static constexpr int SLABS = (D + 63) / 64, SLAB = 128 * 128, TILE = SLABS * SLAB;   // a slab: 64 fp16 dims of 128 rows
   static constexpr int Q = 0, K = Q + 2 * TILE, V = K + 2 * TILE, C = V + TILE, BYTES = C + kStages * 128 * D;
 };
 struct Bars {
@@ -100,10 +100,10 @@ struct Bars {
 
 // 16-byte chunk c of 128-byte row r in a 128-byte-swizzled slab.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-// Chunk c (16 codes) of row r of a tile of codes, as the tile copies swizzle it.
+// Chunk c (16 codes) of row r of a tile of codes, as the tile copies swizzle it (rows of 96 are not).
 template <int D>
 __device__ __forceinline__ uint32_t code_at(int r, int c) {
-  return D == 64 ? (uint32_t)(r * 64 + ((c ^ (r >> 1 & 3)) << 4)) : sw128(r, c);
+  return D == 64 ? (uint32_t)(r * 64 + ((c ^ (r >> 1 & 3)) << 4)) : D == 96 ? (uint32_t)(r * 96 + c * 16) : sw128(r, c);
 }
 
 template <int DT, int D>
@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
     failed = 0;
   }
   Share at;
-  if (!find_share<kRows, kKeys>(p, share_sm, blockIdx.x, &at)) return;
+  const bool any = find_share<kRows, kKeys>(p, share_sm, blockIdx.x, &at);
+  if (tid == 0) write_plan<kRows, kKeys>(p, any, at);
+  if (!any) return;
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -614,7 +616,7 @@ cudaError_t launch(AttnParams p, cudaStream_t s) {
   k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.grid, 32), dim3(128), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.grid, combine_y(kRows)), dim3(kCombineThreads), 0, s, p);
 }
 
 }  // namespace
@@ -623,6 +625,7 @@ namespace attn {
 
 cudaError_t run_tc(const AttnParams &p, int dtype, cudaStream_t s) {
   if (p.c.head_dim == 64) return dtype == PI_DT_F16 ? launch<PI_DT_F16, 64>(p, s) : launch<PI_DT_BF16, 64>(p, s);
+  if (p.c.head_dim == 96) return dtype == PI_DT_F16 ? launch<PI_DT_F16, 96>(p, s) : launch<PI_DT_BF16, 96>(p, s);
   return dtype == PI_DT_F16 ? launch<PI_DT_F16, 128>(p, s) : launch<PI_DT_BF16, 128>(p, s);
 }
 
