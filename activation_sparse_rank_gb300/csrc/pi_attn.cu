@@ -101,9 +101,8 @@ constexpr int attn_stages() {
   return n < 8 ? n : 8;
 }
 
-// NB: eights of query rows of a warp.  WARPS_M == 1: 8 NB rows, the four warps
-// take a tile's four blocks.  WARPS_M == 4: 32 NB rows, 8 NB a warp; every warp
-// goes over all four blocks.
+// NB: eights of query rows of a warp.  The four warps are WARPS_M groups of rows
+// by 4 / WARPS_M groups of a tile's blocks: a warp goes over WARPS_M of them.
 //
 // Both products have the codes as the 16-row operand and the query rows as the
 // 8 columns: S^T = K Q^T and O^T = V^T P^T.  Eight rows (or fewer) then cost
@@ -112,17 +111,17 @@ constexpr int attn_stages() {
 template <int DT, int D, int NB, int WARPS_M>
 __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using E = Elem<DT>;
-  constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
+  constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KW = 4 / WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
   using F = Frag<D>;
   extern __shared__ char smem_raw[];
-  // stages; then, WARPS_M == 1, a unit's [4][ROWS][D] sums, [4][ROWS][3] (m, l, R)
+  // stages; then, KW > 1, a unit's [KW][ROWS][D] sums, [KW][ROWS][3] (m, l, R)
   char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *sm = reinterpret_cast<float *>(ring);
   __shared__ ShareShared share_sm;
   __shared__ __align__(8) unsigned long long full[STAGES], empty[STAGES];   // a tile's copies have landed; all warps have read it
   __shared__ float scales[STAGES][2][4];           // K and V scale of its blocks; K below 0: no block
   __shared__ int failed;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp % WARPS_M, wk = warp / WARPS_M, g = lane >> 2, q4 = lane & 3;
   griddep_launch();                                // every CTA of this grid is resident: the next one may take what is left
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
     int stage = 0;
 
     // ---- the rows of this unit: Q^T in registers, row nb * 8 + g of the warp to this lane ----
-    const int base_row = rt * ROWS + (WARPS_M == 1 ? 0 : warp * WROWS);
+    const int base_row = rt * ROWS + wm * WROWS;
     unsigned bq[NB][KS][2];
     int lim[NB][2];                                // of the lane's columns: rows nb * 8 + 2 q4 + e
     float fac[NB][2];
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
       if (!dead) full_ph ^= 1u << st, pend &= ~(1u << st);
       const char *tile = ring + st * F::BYTES;
 #pragma unroll 1
-      for (int blk = WARPS_M == 1 ? warp : 0; blk < (WARPS_M == 1 ? warp + 1 : 4); ++blk) {
+      for (int blk = wk * WARPS_M; blk < (wk + 1) * WARPS_M; ++blk) {
         const int k0 = t * kTile + blk * 16;
         const char *src = tile + blk * 16 * F::BOX;
         if (k0 >= keys || dead) break;
@@ -447,16 +446,16 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
     }
     __syncthreads();                               // every warp is done with the ring
     if (failed) return;
-    if constexpr (WARPS_M == 1) {
-      float *st = sm + 4 * ROWS * D;
+    if constexpr (KW > 1) {
+      float *st = sm + KW * ROWS * D;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = nb * 8 + 2 * q4 + e;
-          float *o = st + (warp * ROWS + row) * 3;
+          const int row = wm * WROWS + nb * 8 + 2 * q4 + e;
+          float *o = st + (wk * ROWS + row) * 3;
           if (g == 0) o[0] = m[nb][e], o[1] = l[nb][e], o[2] = R[nb][e];
-          o = sm + (warp * ROWS + row) * D;
+          o = sm + (wk * ROWS + row) * D;
 #pragma unroll
           for (int i = 0; i < MT; i += 2)
             *reinterpret_cast<float4 *>(o + F::vdim(2 * i, g)) =
@@ -467,11 +466,11 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, st[(w * ROWS + row) * 3]);
+        for (int w = 0; w < KW; ++w) M = fmaxf(M, st[(w * ROWS + row) * 3]);
         const float ms = M == -INFINITY ? 0.f : M;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < KW; ++w) {
           const float *t = st + (w * ROWS + row) * 3;
           L += t[1] * ex2(t[0] - ms);
           const float c = t[2] == -INFINITY ? 0.f : ex2(t[2] - ms);
@@ -535,12 +534,13 @@ struct AttnShape {
   int nb, warps_m;
 };
 // Rows of a row tile: the fewest eights that hold all query rows of a head
-// while a warp's registers can (16 rows, 8 of 256 dims); above, four warps of
-// that share a tile of keys.
+// while a warp's registers can (16 rows, 8 of 256 dims); above, two warps of that
+// share a tile of keys (32 rows with two instead of four: 105 -> 73 us at 8 x 8192
+// keys x 8 heads of 128), of 256 dims up to four.
 AttnShape attn_shape(int D, int64_t max_rows) {
   const int nb_max = D <= 128 ? 2 : 1;
   const int nb = max_rows <= 8 ? 1 : nb_max;
-  return AttnShape{nb, max_rows <= 8 * nb ? 1 : 4};
+  return AttnShape{nb, max_rows <= 8 * nb ? 1 : max_rows <= 16 * nb ? 2 : 4};
 }
 
 int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current_sms()); }
@@ -548,7 +548,7 @@ int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current
 template <int DT, int D, int NB, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   constexpr int ROWS = 8 * NB * WARPS_M;
-  constexpr int kRing = attn_stages<D, NB>() * Frag<D>::BYTES, kSums = WARPS_M == 1 ? 4 * ROWS * (D + 3) * 4 : 0;
+  constexpr int kRing = attn_stages<D, NB>() * Frag<D>::BYTES, kSums = WARPS_M < 4 ? 4 / WARPS_M * ROWS * (D + 3) * 4 : 0;
   constexpr int smem = (kRing > kSums ? kRing : kSums) + 1024;
   static_assert(attn_stages<D, NB>() >= 2 && attn_stages<D, NB>() <= 8);
   AttnMaps maps;
@@ -568,18 +568,18 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
   const AttnShape k = attn_shape(D, (int64_t)p.max_q * p.group);
   if constexpr (D <= 128) {
     if (k.nb == 1) return launch_attn<DT, D, 1, 1>(p, s);
-    return k.warps_m == 1 ? launch_attn<DT, D, 2, 1>(p, s) : launch_attn<DT, D, 2, 4>(p, s);
+    return k.warps_m == 1 ? launch_attn<DT, D, 2, 1>(p, s) : launch_attn<DT, D, 2, 2>(p, s);
   } else {
-    return k.warps_m == 1 ? launch_attn<DT, D, 1, 1>(p, s) : launch_attn<DT, D, 1, 4>(p, s);
+    return k.warps_m == 1 ? launch_attn<DT, D, 1, 1>(p, s) : k.warps_m == 2 ? launch_attn<DT, D, 1, 2>(p, s) : launch_attn<DT, D, 1, 4>(p, s);
   }
 }
 
 // From how many query rows a head on the tcgen05 kernel (row tiles of 128, each
-// tile widened once for them) is taken.
-#ifndef MR
-#define MR 64
-#endif
-bool many_rows(int D, int64_t rows) { return D <= 128 && rows > MR; }
+// tile of keys widened once for them) is taken.  48 rows of 8 sequences x 8192 keys
+// x 8 heads of 128: 80 us there, 105 us with four warps of 16 rows here; of one
+// sequence of 3000 keys 24 and 32 us; of 64 sequences of 300 keys 70 and 58 us.
+// 32 rows with two warps of 16 rows here: 73, 24 and 49 us (there 79, 23 and 68).
+bool many_rows(int D, int64_t rows) { return D <= 128 && rows > 32; }
 
 template <int DT>
 cudaError_t attn_by_dim(const AttnParams &p, cudaStream_t s) {
@@ -611,7 +611,7 @@ size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, in
   pi::clear_error();
   if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
   const int D = c->head_dim;
-  const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 64, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
+  const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 32, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
   return sizeof(int4) * attn_grid(D, 1) + sizeof(float) * 2 * rows * (size_t)(D + 2);
 }
 
