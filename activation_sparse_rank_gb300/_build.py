@@ -21,8 +21,11 @@ OUT = Path(os.environ.get("PI_BUILD_DIR", str(PKG / "_lib")))
 LIB = OUT / "libpi.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--split-compile=0",
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "--expt-relaxed-constexpr", "-I", str(INCLUDE), "-I", str(CSRC)]
+# Compiled as one piece: the operators' kernels came out 5-15% slower in split
+# compilation (bf16 layer norm 16384 x 8192: 97 us, 84 us whole).
+WHOLE = {"pi_attn", "pi_attn_tc", "pi_kv", "pi_norm", "pi_score"}
 
 
 def nvcc() -> str:
@@ -41,7 +44,8 @@ def _compile(src: Path, extra) -> Path:
     obj = OUT / (src.stem + ".o")
     if obj.exists() and obj.stat().st_mtime >= max(src.stat().st_mtime, _headers_mtime()):
         return obj
-    cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", str(src), "-o", str(obj)]
+    split = [] if src.stem in WHOLE else ["--split-compile=0"]
+    cmd = [nvcc(), *ARCH, *FLAGS, *split, *extra, "-c", str(src), "-o", str(obj)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src.name}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -130,7 +130,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 // A warp's block: 16 rows of D elements as 16 D / 8 vectors of 8, vector
 // lane + 32 i to a lane.
 template <int DT, int D, bool VEC>
-__global__ void __launch_bounds__(256) k_kv_write(const KvCopyParams p) {
+__global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopyParams p) {
   using E = Elem<DT>;
   constexpr int VR = D / 8, NV = PI_KV_BLOCK * VR / 32, WPV = 8 * sizeof(typename E::T) / 16;
   kv_check_cu(p);

@@ -10,6 +10,7 @@
 #include "pi_ops.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 using namespace pidev;
 
@@ -57,10 +58,27 @@ __device__ __forceinline__ void load_cols(f2 *o, const void *p, int dt, int t, i
       if (p && t + i * NT < d / C::V) load_pack<C::V>(o + i * C::PP, p, dt, t + i * NT);
     }
   } else {
+    auto load = [&](auto type) {                     // all loads of one type, so that they are under way together
+      constexpr int Y = decltype(type)::value;
+      typename Elem<Y>::T raw[2 * C::NP];
 #pragma unroll
-    for (int j = 0; j < C::NP; ++j) {
-      const int c0 = t + 2 * j * NT, c1 = c0 + NT;
-      o[j] = f2_of(p && c0 < d ? load_any(p, dt, c0) : one, p && c1 < d ? load_any(p, dt, c1) : one);
+      for (int j = 0; j < 2 * C::NP; ++j)
+        if (t + j * NT < d) raw[j] = static_cast<const typename Elem<Y>::T *>(p)[t + j * NT];
+#pragma unroll
+      for (int j = 0; j < C::NP; ++j) {
+        const int c0 = t + 2 * j * NT;
+        o[j] = f2_of(c0 < d ? Elem<Y>::to(raw[2 * j]) : one, c0 + NT < d ? Elem<Y>::to(raw[2 * j + 1]) : one);
+      }
+    };
+    if (!p) {
+#pragma unroll
+      for (int j = 0; j < C::NP; ++j) o[j] = fill;
+    } else if (dt == PI_DT_F32) {
+      load(std::integral_constant<int, PI_DT_F32>());
+    } else if (dt == PI_DT_F16) {
+      load(std::integral_constant<int, PI_DT_F16>());
+    } else {
+      load(std::integral_constant<int, PI_DT_BF16>());
     }
   }
 }
@@ -132,12 +150,20 @@ struct NormParams {
   int stages, stage_bytes;   // ring of one CTA
 };
 
-// Group of NT threads (NT == 32: four a CTA, no CTA barrier) per row.
+// CTAs of NT threads (128 at least) that an SM holds.  Rows through the ring have
+// their loads in flight without a thread's registers: 512 threads, of 128
+// registers, do (16384 x 8192 bf16: 85 us, 155 us with 1024); plain loads need more.
+constexpr int norm_ctas(int NT, bool VEC) { return std::max(1, (VEC ? 512 : 1024) / std::max(NT, 128)); }
+// The same of the gradient kernel (256 threads at least), by columns of a thread.
+constexpr int grad_ctas_sm(int NT, int cols) { return NT > 256 ? 1 : cols <= 8 ? 3 : 2; }
+
+// Group of NT threads per row (a CTA has 128 at least: four groups of one warp,
+// two of two).
 // VEC: rows come through the ring, one after another to each group; otherwise
 // (odd widths, unaligned rows) plain loads, a group for each row.
 // WREG: weight and bias have x's type (or are absent) and stay in registers.
 template <int X, bool VEC, int NT, int NV, bool WREG>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p) {
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT, norm_ctas(NT, VEC)) k_norm(const NormParams p) {
   using E = Elem<X>;
   using T = typename E::T;
   using C = Cols<X, VEC, NT, NV>;
@@ -145,15 +171,16 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
   constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS;
   extern __shared__ __align__(16) char ring[];
   __shared__ float red[2][2][32];
-  const int t = threadIdx.x % NT;
+  const int t = threadIdx.x % NT, g = threadIdx.x / NT;
   const int nv = p.d / V;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
-  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT;
+  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + g;
 
+  // a stage: the groups' rows of x, then of what is added (its packs' halves apart)
   const int add_bytes = !VEC || !p.add ? 0 : V * (p.add_dt == PI_DT_F32 ? 4 : 2);   // per pack: 8, 16 or 32
-  auto x_slot = [&](int stage, int i) { return ring + (size_t)stage * p.stage_bytes + (i * CT + threadIdx.x) * 16; };
+  auto x_slot = [&](int stage, int i) { return ring + (size_t)stage * p.stage_bytes + (g * nv + t + i * NT) * 16; };
   auto a_slot = [&](int stage, int i, int half) {
-    return ring + (size_t)stage * p.stage_bytes + NV * CT * 16 + ((i * (add_bytes > 16 ? 2 : 1) + half) * CT + threadIdx.x) * 16;
+    return ring + (size_t)stage * p.stage_bytes + ((GROUPS * (1 + half) + g) * nv + t + i * NT) * 16;
   };
   auto fetch = [&](int64_t row, int stage) {
     if constexpr (VEC) {
@@ -189,6 +216,11 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
     }
   }
 
+  f2 ww[WREG ? 1 : NP], bb[WREG ? 1 : NP];           // plain loads: a row a group, so these come beside x's
+  if constexpr (!WREG && !VEC) {
+    load_cols<X, VEC, NT, NV>(ww, p.w, p.w_dt, t, p.d, 1.f);
+    load_cols<X, VEC, NT, NV>(bb, p.b, p.w_dt, t, p.d, 0.f);
+  }
   int turn = 0, at = 0, next = p.stages - 1;
   for (int64_t row = row0; row < p.rows; row += step, turn ^= 1) {
     f2 v[NP];
@@ -245,7 +277,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
     f2 s = f2_of(0.f, 0.f), q = s;
 #pragma unroll
     for (int j = 0; j < NP; ++j) s = f2_add(s, v[j]);
-    const float mean = cta_sum<NT>(f2_sum(s), red[turn][0]) / (float)p.d;
+    const float mean = group_sum<NT, CT>(f2_sum(s), red[turn][0], g) / (float)p.d;
     const f2 minus = f2_of(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -256,7 +288,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
         q = f2_fma(f2_mul(v[j], in_row<NT>(j, t, p.d)), v[j], q);
       }
     }
-    const float rstd = 1.0f / sqrtf(cta_sum<NT>(f2_sum(q), red[turn][1]) / (float)p.d + p.eps);
+    const float rstd = 1.0f / sqrtf(group_sum<NT, CT>(f2_sum(q), red[turn][1], g) / (float)p.d + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
@@ -268,11 +300,12 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm(const NormParams p
       for (int j = 0; j < NP; ++j)
         v[j] = f2_fma(f2_mul(v[j], scale), f2_from16<X>(rw[j / PP], j % PP), f2_from16<X>(rb[j / PP], j % PP));
     } else {
-      f2 w[NP], b[NP];
-      load_cols<X, VEC, NT, NV>(w, p.w, p.w_dt, t, p.d, 1.f);
-      load_cols<X, VEC, NT, NV>(b, p.b, p.w_dt, t, p.d, 0.f);
+      if constexpr (VEC) {
+        load_cols<X, VEC, NT, NV>(ww, p.w, p.w_dt, t, p.d, 1.f);
+        load_cols<X, VEC, NT, NV>(bb, p.b, p.w_dt, t, p.d, 0.f);
+      }
 #pragma unroll
-      for (int j = 0; j < NP; ++j) v[j] = f2_fma(f2_mul(v[j], scale), w[j], b[j]);
+      for (int j = 0; j < NP; ++j) v[j] = f2_fma(f2_mul(v[j], scale), ww[j], bb[j]);
     }
     store_cols<X, VEC, NT, NV>(y, v, t, p.d);
   }
@@ -293,12 +326,12 @@ struct NormGradParams {
 // HOLD: h and g of a row stay in registers between the passes; without it
 // (the widest rows, whose threads have 64 registers) they are formed again.
 template <int X, bool VEC, int NT, int NV>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGradParams p) {
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT, grad_ctas_sm(NT, 2 * Cols<X, VEC, NT, NV>::NP)) k_norm_grad(const NormGradParams p) {
   using E = Elem<X>;
   using T = typename E::T;
   using C = Cols<X, VEC, NT, NV>;
   constexpr int V = C::V, PP = C::PP, NP = C::NP;
-  constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS;
+  constexpr int GROUPS = NT < 256 ? 256 / NT : 1, CT = NT * GROUPS;
   constexpr bool HOLD = NT <= 512;
   extern __shared__ __align__(16) char ring[];       // stages, then (GROUPS > 1) [2, d] sums
   __shared__ float red[2][2][32];
@@ -309,7 +342,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGra
   const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *ds = static_cast<const T *>(p.dsum);
 
   auto slot = [&](int stage, int which, int i) {
-    return reinterpret_cast<uint4 *>(ring + (size_t)stage * p.stage_bytes + ((which * NV + i) * CT + threadIdx.x) * 16);
+    return reinterpret_cast<uint4 *>(ring + (size_t)stage * p.stage_bytes + ((which * GROUPS + g) * nv + t + i * NT) * 16);
   };
   auto fetch = [&](int64_t row, int stage) {
     if constexpr (VEC) {
@@ -372,10 +405,10 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) k_norm_grad(const NormGra
     float a = warp_sum(f2_sum(s1)), b = warp_sum(f2_sum(s2));
     if constexpr (NT > 32) {
       if ((threadIdx.x & 31) == 0) red[turn][0][threadIdx.x >> 5] = a, red[turn][1][threadIdx.x >> 5] = b;
-      __syncthreads();
+      group_sync<NT, CT>(g);
       const int l = threadIdx.x & 31;
-      a = warp_sum(l < NT / 32 ? red[turn][0][l] : 0.f);
-      b = warp_sum(l < NT / 32 ? red[turn][1][l] : 0.f);
+      a = warp_sum(l < NT / 32 ? red[turn][0][g * (NT / 32) + l] : 0.f);
+      b = warp_sum(l < NT / 32 ? red[turn][1][g * (NT / 32) + l] : 0.f);
     }
     const f2 m1 = f2_of(-a * inv, -a * inv), m2 = f2_of(-b * inv, -b * inv);
     if constexpr (!HOLD) form(h, gg, false);
@@ -460,14 +493,14 @@ int ring_stages(int stage_bytes, int ctas_per_sm) { return std::max(1, std::min(
 template <int X, bool VEC, int NT, int NV, bool WREG>
 cudaError_t launch_norm(NormParams p, cudaStream_t s) {
   constexpr int GROUPS = NT < 128 ? 128 / NT : 1, CT = NT * GROUPS, V = Cols<X, VEC, NT, NV>::V;
-  const int per_sm = std::max(1, 1024 / CT);
+  const int per_sm = norm_ctas(NT, VEC);
   unsigned grid = (unsigned)((p.rows + GROUPS - 1) / GROUPS);
   p.stages = 1, p.stage_bytes = 0;
   size_t smem = 0;
   if (VEC) {
     grid = std::min(grid, (unsigned)(per_sm * std::max(1, pi::current_sms())));
     const int per_pack = 16 * (1 + (!p.add ? 0 : V * pi::dtype_size(p.add_dt) > 16 ? 2 : 1));
-    p.stage_bytes = NV * CT * per_pack;
+    p.stage_bytes = GROUPS * (p.d / V) * per_pack;
     p.stages = std::min(ring_stages(p.stage_bytes, per_sm), (p.rows - 1) / (int)(grid * GROUPS) + 1);
     smem = (size_t)p.stages * p.stage_bytes;
     static std::atomic<uint64_t> done{0};
@@ -490,9 +523,10 @@ template <int X, bool VEC, int NV>
 cudaError_t norm_by_width(const NormParams &p, cudaStream_t s) {
   constexpr int C = 2 * Cols<X, VEC, 32, NV>::NP;    // columns of a thread
   if (p.d <= 32 * C) return norm_by_weight<X, VEC, 32, NV>(p, s);
+  if (p.d <= 64 * C) return norm_by_weight<X, VEC, 64, NV>(p, s);
   if (p.d <= 128 * C) return norm_by_weight<X, VEC, 128, NV>(p, s);
   if (p.d <= 256 * C) return norm_by_weight<X, VEC, 256, NV>(p, s);
-  if constexpr (512 * C < PI_MAX_D)
+  if constexpr (1024 * C <= PI_MAX_D)                // (the caller has chosen NV such that a row fits)
     if (p.d > 512 * C) return norm_by_weight<X, VEC, 1024, NV>(p, s);
   return norm_by_weight<X, VEC, 512, NV>(p, s);
 }
@@ -500,31 +534,33 @@ cudaError_t norm_by_width(const NormParams &p, cudaStream_t s) {
 template <int X>
 cudaError_t norm_by_type(const NormParams &p, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(typename Elem<X>::T);
-  if (!vec) return norm_by_width<X, false, 8>(p, s);
+  // plain loads: a warp a row while 16 columns a thread hold it (40000 x 301 bf16: 40 us,
+  // 57 with two warps and 8 columns); wider rows 8 columns (30000 x 805: 56 us, 89 with 16)
+  if (!vec) return p.d > 512 && p.d <= 4096 ? norm_by_width<X, false, 4>(p, s) : norm_by_width<X, false, 8>(p, s);
   // few rows: latency counts, one pack a thread; many: four, so that more bytes are on their way
   return p.rows <= 2 * pi::current_sms() && p.d <= 1024 * V ? norm_by_width<X, true, 1>(p, s) : norm_by_width<X, true, 4>(p, s);
 }
 
-// Columns of the gradient kernel up to which four warps of a CTA take a row each.
-constexpr int kGradWarpD = 256;
-// CTAs of the gradient kernel: a function of rows and d alone, because the
-// order in which dweight's rows are added follows from it.
-constexpr int kGradCtas = 304;
+// Columns of the gradient kernel up to which a warp takes a row, and up to which
+// half a CTA of 256 threads does, with 8 and with 16 columns a thread.
+constexpr int kGradWarpD = 256, kGradHalfD = 1024, kGradHalfD16 = 2048;
+// CTAs of the gradient kernel: a function of rows and d alone, because the order
+// in which dweight's rows are added follows from it; as many as the GPU's 152 SMs hold.
 int grad_ctas(int rows, int d) {
-  const int groups = d <= kGradWarpD ? 4 : 1;
-  return std::max(1, std::min((rows + groups - 1) / groups, kGradCtas));
+  const int groups = d <= kGradWarpD ? 8 : d <= kGradHalfD16 ? 2 : 1;
+  return std::max(1, std::min((rows + groups - 1) / groups, 152 * (d <= kGradHalfD ? 3 : d <= 256 * 16 ? 2 : 1)));
 }
 
 template <int X, bool VEC, int NT, int COLS>
 cudaError_t launch_grad(NormGradParams p, cudaStream_t s) {
-  constexpr int CT = NT < 128 ? 128 : NT, NV = VEC ? COLS * (int)sizeof(typename Elem<X>::T) / 16 : COLS / 2;
+  constexpr int CT = NT < 256 ? 256 : NT, GROUPS = CT / NT, V = 16 / (int)sizeof(typename Elem<X>::T), NV = VEC ? COLS * (int)sizeof(typename Elem<X>::T) / 16 : COLS / 2;
   const int grid = grad_ctas(p.rows, p.d);
   p.stages = 0, p.stage_bytes = 0;
   if (VEC) {
-    p.stage_bytes = (p.dsum ? 3 : 2) * NV * CT * 16;
-    p.stages = ring_stages(p.stage_bytes, NT <= 512 ? 2 : 1);
+    p.stage_bytes = (p.dsum ? 3 : 2) * GROUPS * (p.d / V) * 16;
+    p.stages = ring_stages(p.stage_bytes, grad_ctas_sm(NT, COLS));
   }
-  const size_t smem = (size_t)p.stages * p.stage_bytes + (NT < 128 ? 2 * p.d * sizeof(float) : 0);
+  const size_t smem = (size_t)p.stages * p.stage_bytes + (GROUPS > 1 ? 2 * p.d * sizeof(float) : 0);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = pi::allow_smem(k_norm_grad<X, VEC, NT, NV>, smem, kRingMost, done);
   if (e != cudaSuccess) return e;
@@ -536,8 +572,8 @@ template <int X, bool VEC>
 cudaError_t grad_by_width(const NormGradParams &p, cudaStream_t s) {
   // columns of a thread: 16 at most, two accumulators each
   if (p.d <= kGradWarpD) return launch_grad<X, VEC, 32, 8>(p, s);
-  if (p.d <= 128 * 8) return launch_grad<X, VEC, 128, 8>(p, s);
-  if (p.d <= 128 * 16) return launch_grad<X, VEC, 128, 16>(p, s);
+  if (p.d <= kGradHalfD) return launch_grad<X, VEC, 128, 8>(p, s);
+  if (p.d <= kGradHalfD16) return launch_grad<X, VEC, 128, 16>(p, s);
   if (p.d <= 256 * 16) return launch_grad<X, VEC, 256, 16>(p, s);
   if (p.d <= 512 * 16) return launch_grad<X, VEC, 512, 16>(p, s);
   return launch_grad<X, VEC, 1024, 16>(p, s);

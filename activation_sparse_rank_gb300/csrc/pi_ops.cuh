@@ -141,15 +141,21 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Sum over the CTA (every thread gets it); red: NT/32 floats of shared memory,
-// free for reuse after the next __syncthreads().
-template <int NT>
-__device__ __forceinline__ float cta_sum(float v, float *red) {
+// Barrier of group g of NT threads of a CTA of CT.
+template <int NT, int CT>
+__device__ __forceinline__ void group_sync(int g) {
+  if constexpr (NT == CT) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(NT) : "memory");
+}
+// Sum over group g (every thread gets it); red: CT/32 floats of shared memory,
+// free for reuse after the group's next barrier.
+template <int NT, int CT>
+__device__ __forceinline__ float group_sum(float v, float *red, int g) {
   v = warp_sum(v);
   if constexpr (NT == 32) return v;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = threadIdx.x % 32 < NT / 32 ? red[threadIdx.x % 32] : 0.f;
+  group_sync<NT, CT>(g);
+  float t = threadIdx.x % 32 < NT / 32 ? red[g * (NT / 32) + threadIdx.x % 32] : 0.f;
   return warp_sum(t);
 }
 
