@@ -137,87 +137,85 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
   const bool any = find_share<ROWS, kTile>(p, share_sm, blockIdx.x, &at);
   if (threadIdx.x == 0) write_plan<ROWS, kTile>(p, any, at);
   if (!any) return;
-  uint32_t full_ph = 0, empty_ph = 0, used = 0, pend = 0;    // a bit a stage: phases to wait for, filled ever, filled and not waited for
   bool dead = false;                               // a wait ran out: nothing more is copied or computed
   const bool by16 = p.c.page_size % kTile != 0;    // a tile may lie in several pages: blocks are copied one by one
+  const int page_size = p.c.page_size, blocks = page_size / PI_KV_BLOCK;
+  const int turn_pages = 4 * kTile / page_size, turn_rest = 4 * kTile - turn_pages * page_size;
+  // Tile n of this CTA uses stage n % STAGES for the n / STAGES-th time and is
+  // fetched by warp n % 4, STAGES - 1 tiles ahead: what a fetch needs is kept up
+  // by that warp alone, once in four tiles.
+  int done = 0, stage = 0, phase = 0;              // tiles read; the next one's stage and parity
+  int last_fetch = -1;                             // the last tile this warp fetched
   for (int64_t pos = at.begin; pos < at.end;) {
     const Seq &sq = at.sq;
     const int s = at.s, h = at.h, rt = at.rt;
     const int keys = unit_keys<ROWS>(p, sq, rt), tiles = (keys + kTile - 1) / kTile;
     const int t0 = (int)(pos - at.u0), t1 = (int)min((int64_t)tiles, at.end - at.u0);
 
-    // ---- the ring: the warps take turns to fill a stage; lane l looks after block l % 4 of the tile ----
+    // ---- fetches; lane l looks after block l % 4 of the tile ----
     const int32_t *table = p.tok.page_table + (int64_t)s * p.tok.table_stride;
-    const int copies = min(keys, t1 * kTile), blocks = p.c.page_size / PI_KV_BLOCK;
     const float *sc_head = ((lane & 4) ? p.c.v_scales : p.c.k_scales) + (int64_t)h * blocks;
-    // of the next tile: its first key, the page's place in the table and the offset in it of this lane's block
-    int ck = t0 * kTile, cp = (ck + (lane & 3) * 16) / p.c.page_size, co = ck + (lane & 3) * 16 - cp * p.c.page_size;
-    auto next_page = [&] { return ck + (lane & 3) * 16 < copies ? table[cp] : -1; };
-    auto fetch = [&](int st, int page, bool mine) {
-      if (ck < copies) {
-        if (used >> st & 1) {
-          if (mine && !dead && !bar_wait(smem_addr(&empty[st]), empty_ph >> st & 1)) dead = true;
-          dead = __any_sync(0xffffffffu, dead);
-          empty_ph ^= 1u << st;
+    const int copies = min(keys, t1 * kTile);
+    int next = done + ((warp - done) & 3);           // the tile this warp fetches next, and of this lane's block:
+    int ck = (t0 + next - done) * kTile + (lane & 3) * 16;       // the first key,
+    int cp = ck / page_size, co = ck - cp * page_size;           // the page's place in the table and the offset in it
+    int page = ck < copies ? table[cp] : -1;
+    auto fetch = [&] {                               // tile `next`
+      const int st = next % STAGES, use = next / STAGES;
+      if (use > 0 && !dead && !bar_wait(smem_addr(&empty[st]), (use - 1) & 1)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      if (!dead) {
+        const bool in = ck < copies, ok = in && page >= 0 && page < p.c.n_pages;
+        if (in && !ok && lane < 4) atomicOr(p.c.status, pi::kKvBadPage);
+        const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(ring + st * F::BYTES);
+        if (lane < 8) {
+          float *sc = &scales[st][lane >> 2][lane & 3];
+          if (ok)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(sc)),
+                         "l"(sc_head + (int64_t)page * p.c.heads * blocks + co / PI_KV_BLOCK) : "memory");
+          else
+            *sc = -1.f;
         }
-        used |= 1u << st;
-        if (mine && !dead) {
-          const bool in = ck + (lane & 3) * 16 < copies, ok = in && page >= 0 && page < p.c.n_pages;
-          if (in && !ok && lane < 4) atomicOr(p.c.status, pi::kKvBadPage);
-          const uint32_t bar = smem_addr(&full[st]), dst = smem_addr(ring + st * F::BYTES);
-          if (lane < 8) {
-            float *sc = &scales[st][lane >> 2][lane & 3];
-            if (ok)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(sc)),
-                           "l"(sc_head + (int64_t)page * p.c.heads * blocks + co / PI_KV_BLOCK) : "memory");
-            else
-              *sc = -1.f;
-          }
-          const unsigned good = __ballot_sync(0xffffffffu, ok) & 15u;
-          if (!by16) {
-            const int z = __shfl_sync(0xffffffffu, page, 0) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, 0);
-            if (elect_one()) {
-              if (good & 1) {
-                bar_expect(bar, F::BYTES);
+        const unsigned good = __ballot_sync(0xffffffffu, ok) & 15u;
+        if (!by16) {
+          const int z = __shfl_sync(0xffffffffu, page, 0) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, 0);
+          if (elect_one()) {
+            if (good & 1) {
+              bar_expect(bar, F::BYTES);
 #pragma unroll
-                for (int i = 0; i < F::BOXES; ++i) {
-                  tile_copy(dst + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
-                  tile_copy(dst + F::V_AT + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
-                }
-              } else {
-                bar_arrive(bar);
+              for (int i = 0; i < F::BOXES; ++i) {
+                tile_copy(dst + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
+                tile_copy(dst + F::V_AT + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
               }
+            } else {
+              bar_arrive(bar);
             }
-          } else {
-            if (elect_one()) bar_expect(bar, __popc(good) * (F::BYTES / 4));
+          }
+        } else {
+          if (elect_one()) bar_expect(bar, __popc(good) * (F::BYTES / 4));
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-              const int z = __shfl_sync(0xffffffffu, page, b) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, b);
-              if ((good >> b & 1) && elect_one()) {
+          for (int b = 0; b < 4; ++b) {
+            const int z = __shfl_sync(0xffffffffu, page, b) * p.c.heads + h, y = __shfl_sync(0xffffffffu, co, b);
+            if ((good >> b & 1) && elect_one()) {
 #pragma unroll
-                for (int i = 0; i < F::BOXES; ++i) {
-                  tile_copy(dst + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
-                  tile_copy(dst + F::V_AT + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
-                }
+              for (int i = 0; i < F::BOXES; ++i) {
+                tile_copy(dst + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.k, i * 128, y, z, bar);
+                tile_copy(dst + F::V_AT + b * 16 * F::BOX + i * F::BOX_BYTES, &maps.v, i * 128, y, z, bar);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
-          __syncwarp();
-          if (lane < 8 && ok) bar_arrive_copies(bar); else bar_arrive(bar);
         }
-        pend |= 1u << st;
+        __syncwarp();
+        if (lane < 8 && ok) bar_arrive_copies(bar); else bar_arrive(bar);
+        last_fetch = next;
       }
-      ck += kTile, co += kTile;
-      while (co >= p.c.page_size) co -= p.c.page_size, ++cp;
+      next += 4, ck += 4 * kTile, cp += turn_pages, co += turn_rest;
+      if (co >= page_size) co -= page_size, ++cp;
+      page = ck < copies ? table[cp] : -1;
     };
-    int page = next_page();
-#pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) {
-      fetch(i, page, warp == 0);
-      page = next_page();
-    }
-    int stage = 0;
+    const int unit_end = done + (t1 - t0);
+    while (next < min(unit_end, done + STAGES - 1)) fetch();
 
     // ---- the rows of this unit: Q^T in registers, row nb * 8 + g of the warp to this lane ----
     const int base_row = rt * ROWS + wm * WROWS;
@@ -283,10 +281,10 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
 
     for (int t = t0; t < t1; ++t) {
       const int st = stage;
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
-      if (!dead && !bar_wait(smem_addr(&full[st]), full_ph >> st & 1)) dead = true;
+      if (!dead && !bar_wait(smem_addr(&full[st]), phase)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
-      if (!dead) full_ph ^= 1u << st, pend &= ~(1u << st);
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      phase ^= stage == 0;
       const char *tile = ring + st * F::BYTES;
 #pragma unroll 1
       for (int blk = wk * WARPS_M; blk < (wk + 1) * WARPS_M; ++blk) {
@@ -424,8 +422,8 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&empty[st]));
       // one stage is kept behind: the tile before this one has been read, or nearly, by every warp
-      fetch(st == 0 ? STAGES - 1 : st - 1, page, (t & 3) == warp);
-      page = next_page();
+      if (next == done + STAGES - 1 && next < unit_end) fetch();
+      ++done;
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -439,8 +437,8 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
     const bool whole = t0 == 0 && t1 == tiles;
     float *part = p.part + (int64_t)(2 * blockIdx.x + (t0 == 0)) * ROWS * (D + 2);
     if (dead) {                                    // copies may still be on their way: give them time, then leave
-      for (int i = 0; i < STAGES; ++i)
-        if (pend >> i & 1) bar_wait(smem_addr(&full[i]), full_ph >> i & 1);
+      for (int n = max(0, last_fetch - STAGES); n <= last_fetch; ++n)
+        if ((n & 3) == warp) bar_wait(smem_addr(&full[n % STAGES]), n / STAGES & 1);
       if (lane == 0) atomicOr(p.c.status, pi::kKvTimeout);
       failed = 1;
     }
