@@ -270,13 +270,14 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
     min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
     min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
 
-    float acc[NB][MT][4], m[NB][2], l[NB][2], R[NB][2];
+    float acc[NB][MT][4], m[NB][2], l[NB][2], R[NB][2];      // m is 0 and R -inf while no key has been seen
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) acc[nb][i][0] = acc[nb][i][1] = acc[nb][i][2] = acc[nb][i][3] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nb][e] = R[nb][e] = -INFINITY, l[nb][e] = 0.f;
+      for (int e = 0; e < 2; ++e)
+        m[nb][e] = l[nb][e] = 0.f, R[nb][e] = -INFINITY;
     }
 
     for (int t = t0; t < t1; ++t) {
@@ -317,10 +318,14 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[nb][e] *= fac[nb][e & 1] * ks;
-            if (ragged && k0 + g + 8 * (e >> 1) >= lim[nb][e & 1]) x[nb][e] = -INFINITY;
-            over |= x[nb][e] > fminf(m[nb][e & 1], R[nb][e & 1] - ev + kBoost) + kSlack;
+          for (int e = 0; e < 2; ++e) {
+            const float fk = fac[nb][e] * ks, most = fminf(kSlack, R[nb][e] - m[nb][e] + (kBoost + kSlack - ev));
+#pragma unroll
+            for (int j = e; j < 4; j += 2) {
+              x[nb][j] = fmaf(x[nb][j], fk, -m[nb][e]);                // relative to m
+              if (ragged && k0 + g + 8 * (j >> 1) >= lim[nb][e]) x[nb][j] = -INFINITY;
+              over |= x[nb][j] > most;
+            }
           }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -330,9 +335,12 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
               float bm = fmaxf(x[nb][e], x[nb][2 + e]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-              const float mn = fmaxf(m[nb][e], bm), Rn = fmaxf(R[nb][e], bm + ev - kBoost);
-              if (mn != -INFINITY) l[nb][e] *= ex2(m[nb][e] - mn);
-              const float c = Rn == -INFINITY ? 1.f : ex2(R[nb][e] - Rn);
+              if (bm == -INFINITY) continue;           // every row of these keys is masked
+              const bool none = R[nb][e] == -INFINITY;
+              const float mn = none ? bm : m[nb][e] + fmaxf(bm, 0.f), Rn = fmaxf(R[nb][e], bm + m[nb][e] + ev - kBoost);
+              const float by = m[nb][e] - mn, c = ex2(R[nb][e] - Rn);
+              if (!none) l[nb][e] *= ex2(by);
+              x[nb][e] += by, x[nb][2 + e] += by;
               m[nb][e] = mn, R[nb][e] = Rn;
 #pragma unroll
               for (int i = 0; i < MT; ++i) acc[nb][i][e] *= c, acc[nb][i][2 + e] *= c;
@@ -345,9 +353,8 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
           float w[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float sub = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
-            const float f = R[nb][e] == -INFINITY ? 0.f : ex2(fminf(sub + ev - R[nb][e], 100.f));
-            const float u = ex2(x[nb][e] - sub), v = ex2(x[nb][2 + e] - sub);
+            const float f = ex2(fminf(m[nb][e] - R[nb][e] + ev, 100.f));
+            const float u = ex2(x[nb][e]), v = ex2(x[nb][2 + e]);
             l[nb][e] += u + v;
             w[e] = u * f, w[2 + e] = v * f;
           }
@@ -432,6 +439,11 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
 
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (R[nb][e] == -INFINITY) m[nb][e] = -INFINITY;
     // ---- the unit's result, or this CTA's part of it ----
     // Lane (g, q4) has, of rows 2 q4 + e of each eight, the dims vdim(j, g), j = 2 i + (k >> 1) of acc[i][k], k & 1 == e.
     const bool whole = t0 == 0 && t1 == tiles;
