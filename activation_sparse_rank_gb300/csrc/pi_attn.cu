@@ -553,7 +553,7 @@ AttnShape attn_shape(int D, int64_t max_rows) {
   return AttnShape{nb, max_rows <= 8 * nb ? 1 : max_rows <= 16 * nb ? 2 : 4};
 }
 
-int attn_grid(int D, int nb) { return attn_ctas(D, nb) * std::max(1, pi::current_sms()); }
+int attn_grid(int D, int nb) { return std::min(kMostShares, attn_ctas(D, nb) * std::max(1, pi::current_sms())); }
 
 template <int DT, int D, int NB, int WARPS_M>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
@@ -570,7 +570,7 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
-  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3((unsigned)p.grid, combine_y(ROWS)), dim3(kCombineThreads), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3(combine_grid(p, D, ROWS)), dim3(kCombineThreads), 0, s, p);
 }
 
 template <int DT, int D>

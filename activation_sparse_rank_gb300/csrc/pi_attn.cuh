@@ -29,7 +29,7 @@ struct AttnParams {
   int64_t qt, qh;
   void *out;
   float *lse;
-  int4 *plan;              // [grid] for k_attn_combine: the unit that share i has to add up (sequence, head, row tile, parts; 0 parts: none)
+  int4 *plan;              // [grid] the unit that share i has to add up: sequence, head, row tile, parts + (rows << 16); 0: none
   float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
   float scale;             // sm_scale log2(e)
   int q_heads, group, max_q, causal, row_tiles, grid;
@@ -207,8 +207,10 @@ __device__ __forceinline__ void write_plan(const AttnParams &p, bool any, const 
   int4 plan = make_int4(0, 0, 0, 0);
   if (any && at.begin > at.u0) {
     const int64_t c0 = cta_owner(at.u0, at.total, at.shares);
-    if (c0 == (int64_t)blockIdx.x - 1)
-      plan = make_int4(at.s, at.h, at.rt, (int)(cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares) - c0) + 1);
+    if (c0 == (int64_t)blockIdx.x - 1) {
+      const int parts = (int)(cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares) - c0) + 1;
+      plan = make_int4(at.s, at.h, at.rt, parts | min(ROWS, at.sq.rows - at.rt * ROWS) << 16);
+    }
   }
   p.plan[blockIdx.x] = plan;
 }
@@ -217,45 +219,79 @@ struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 o
   CUtensorMap k, v;
 };
 
-// Units cut between CTAs: their parts added in CTA order, those of plan[blockIdx.x].
-// A row's parts come at the latency of L2, so of more than eight parts (a long
-// cache with few heads: up to one a CTA) four or sixteen warps take a row, a run
-// of parts each.  Rows of units without keys: 0 and -inf.
-constexpr int kCombineThreads = 512;
-constexpr int combine_y(int rows) { return rows <= 16 ? rows / 4 : rows <= 64 ? 4 : rows / 16; }
+// Units cut between CTAs: their parts added in CTA order.  A row's parts come at
+// the latency of L2, so of more than eight parts (a long cache with few heads: up
+// to one a CTA) four or sixteen warps take a row, a run of parts each.  A pass of
+// 16 warps over rows of a unit is an item; a few CTAs an SM take all items, which
+// the plan's prefix sums find (a CTA for each share and four rows instead: 60 us
+// for attention of 128 query heads over 130001 keys, 48 so, as most had no work).
+// Rows of units without keys: 0 and -inf.
+constexpr int kCombineThreads = 512, kMostShares = 1024;
+constexpr int combine_ctas(int D) { return D <= 128 ? 3 : 2; }     // that an SM holds
+__host__ __device__ constexpr int combine_split(int parts) { return parts > 64 ? 16 : parts > 8 ? 4 : 1; }
 template <int DT, int D, int ROWS, int TILE>
-__global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const AttnParams p) {
+__global__ void __launch_bounds__(kCombineThreads, combine_ctas(D)) k_attn_combine(const AttnParams p) {
   using E = Elem<DT>;
   constexpr int LANES = D / 4 <= 16 ? 16 : 32;     // lanes across a row (D = 64: half a warp per part)
   constexpr int VECS = D / 4 <= 32 ? 1 : D / 4 / 32;
   constexpr int WARPS = kCombineThreads / 32;
   __shared__ float4 sums[WARPS][D / 4];
   __shared__ float2 stats[WARPS];
+  __shared__ int upto[kMostShares], warp_items[WARPS];       // items of the shares up to each
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int s = blockIdx.x; s < p.tok.n_seqs; s += gridDim.x) {       // the leading row tiles of a sequence may see nothing
-    const Seq sq = load_seq(p, s);
-    int rows = 0;
-    for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows && unit_tiles<ROWS, TILE>(p, sq, rt) == 0; ++rt) rows = min(sq.rows, (rt + 1) * ROWS);
-    const int64_t first = (int64_t)sq.row0 * p.q_heads, n = (int64_t)(rows / p.group) * p.q_heads;
-    const int rest = rows % p.group;                 // a row tile may end inside a token's heads
-    for (int64_t i = blockIdx.y * kCombineThreads + threadIdx.x; i < (n + (rest ? p.q_heads : 0)) * (D / 8); i += gridDim.y * kCombineThreads) {
-      const int64_t r = i / (D / 8);
-      if (r >= n && (r - n) % p.group >= rest) continue;
-      reinterpret_cast<uint4 *>(p.out)[(first + r) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
-      if (p.lse && i % (D / 8) == 0) p.lse[first + r] = -INFINITY;
+  for (int s0 = 0; s0 < p.tok.n_seqs; s0 += kCombineThreads) {       // the leading row tiles of a sequence may see nothing
+    auto blank = [&](const Seq &sq) {              // rows of them
+      int rows = 0;
+      for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows && unit_tiles<ROWS, TILE>(p, sq, rt) == 0; ++rt) rows = min(sq.rows, (rt + 1) * ROWS);
+      return rows;
+    };
+    if (!__syncthreads_or(s0 + (int)threadIdx.x < p.tok.n_seqs && blank(load_seq(p, s0 + threadIdx.x)))) continue;
+    for (int s = s0; s < min(p.tok.n_seqs, s0 + kCombineThreads); ++s) {
+      const Seq sq = load_seq(p, s);
+      const int rows = blank(sq);
+      const int64_t first = (int64_t)sq.row0 * p.q_heads, n = (int64_t)(rows / p.group) * p.q_heads;
+      const int rest = rows % p.group;             // a row tile may end inside a token's heads
+      for (int64_t i = blockIdx.x * kCombineThreads + threadIdx.x; i < (n + (rest ? p.q_heads : 0)) * (D / 8); i += gridDim.x * kCombineThreads) {
+        const int64_t r = i / (D / 8);
+        if (r >= n && (r - n) % p.group >= rest) continue;
+        reinterpret_cast<uint4 *>(p.out)[(first + r) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (p.lse && i % (D / 8) == 0) p.lse[first + r] = -INFINITY;
+      }
     }
   }
   griddep_wait();                                  // on every path: this grid does not end before the main kernel's
-  const int4 plan = p.plan[blockIdx.x];
-  const int parts = plan.w, h = plan.y, rt = plan.z;
-  if (parts == 0) return;
-  const Seq sq = load_seq(p, plan.x);
-  const int64_t c0 = (int64_t)blockIdx.x - 1;
-  const int split = parts > 64 ? 16 : parts > 8 ? 4 : 1, sub = warp % split, rows = WARPS / split;
-  const int per = (parts + split - 1) / split, p0 = min(parts, sub * per), p1 = min(parts, p0 + per);
-  auto part = [&](int i) { return p.part + (2 * (c0 + i) + (i == 0)) * ROWS * (D + 2); };
-  for (int base = blockIdx.y * rows; base < min(ROWS, sq.rows - rt * ROWS); base += gridDim.y * rows) {
-    const int row = base + warp / split, gr = rt * ROWS + row;
+  {
+    int n[2], at = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * threadIdx.x + k, w = i < p.grid ? p.plan[i].w : 0, per = WARPS / combine_split(w & 0xffff);
+      n[k] = w ? ((w >> 16) + per - 1) / per : 0;
+    }
+    int x = n[0] + n[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_items[warp] = x;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) at += warp_items[i];
+    upto[2 * threadIdx.x] = at + x - n[1], upto[2 * threadIdx.x + 1] = at + x;
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < upto[kMostShares - 1]; item += gridDim.x) {
+    int share = 0;                                   // the first with more items up to it
+#pragma unroll
+    for (int o = kMostShares / 2; o > 0; o >>= 1)
+      if (upto[share + o - 1] <= item) share += o;
+    const int4 plan = p.plan[share];
+    const int parts = plan.w & 0xffff, h = plan.y, rt = plan.z;
+    const Seq sq = load_seq(p, plan.x);
+    const int64_t c0 = (int64_t)share - 1;
+    const int split = combine_split(parts), sub = warp % split, rows = WARPS / split;
+    const int per = (parts + split - 1) / split, p0 = min(parts, sub * per), p1 = min(parts, p0 + per);
+    auto part = [&](int i) { return p.part + (2 * (c0 + i) + (i == 0)) * ROWS * (D + 2); };
+    const int row = (item - (share ? upto[share - 1] : 0)) * rows + warp / split, gr = rt * ROWS + row;
     const bool in = row < ROWS && gr < sq.rows;
     float M = -INFINITY, L = 0.f;
     float4 o[VECS];
@@ -331,6 +367,11 @@ __global__ void __launch_bounds__(kCombineThreads) k_attn_combine(const AttnPara
     }
     if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (ms + log2f(L)) * kLn2;
   }
+}
+
+// Its CTAs: no more than there can be items.
+inline unsigned combine_grid(const AttnParams &p, int D, int rows) {
+  return (unsigned)std::min<int64_t>((int64_t)p.tok.n_seqs * p.c.heads * p.row_tiles * rows, combine_ctas(D) * std::max(1, pi::current_sms()));
 }
 
 // The driver's tensor-map encoder, looked up through the runtime so that the

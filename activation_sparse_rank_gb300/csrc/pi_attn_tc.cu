@@ -612,11 +612,11 @@ cudaError_t launch(AttnParams p, cudaStream_t s) {
   cudaError_t e = pi::allow_smem(k_attn_tc<DT, D>, smem, smem, done);
   if (e != cudaSuccess) return e;
   p.row_tiles = (int)(((int64_t)p.max_q * p.group + kRows - 1) / kRows);
-  p.grid = pi::current_sms();
+  p.grid = std::min(kMostShares, std::max(1, pi::current_sms()));
   k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3((unsigned)p.grid, combine_y(kRows)), dim3(kCombineThreads), 0, s, p);
+  return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3(combine_grid(p, D, kRows)), dim3(kCombineThreads), 0, s, p);
 }
 
 }  // namespace
