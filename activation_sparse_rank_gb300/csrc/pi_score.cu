@@ -440,17 +440,20 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
 }
 
 // Many rows: a persistent CTA takes whole rows, one after another, in batches of
-// kBatch pieces a thread that come through a ring in shared memory: a thread
+// stream_batch pieces a thread that come through a ring in shared memory: a thread
 // copies its own pieces there (cp.async) and is the only one to read them, so a
 // batch needs no barrier, and what is on its way takes no registers.  Copies run
-// two batches ahead, into the next row too, so what is done at a row's end costs
-// little bandwidth.
-constexpr int kBatch = 4, kStages = 3, kStreamThreads = 256, kStreamCtas = 4;
-constexpr int kStreamSmem = kStages * kBatch * kStreamThreads * 16;
-template <int DT>
-__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) k_score_stream(const ScoreParams p) {
+// a batch ahead, into the next row too, so what is done at a row's end costs
+// little bandwidth; two batches ahead took 127 us for 2048 x 131072 (116 so), as
+// the ring then leaves L1 too little for the pieces that are read again.
+constexpr int kStages = 2;
+constexpr int stream_batch(int NT) { return NT == 64 ? 2 : 4; }
+constexpr int stream_smem(int NT) { return kStages * stream_batch(NT) * NT * 16; }
+constexpr int stream_ctas(int NT) { return 1024 / NT; }
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const ScoreParams p) {
   using E = Elem<DT>;
-  constexpr int NT = kStreamThreads, NW = NT / 32, PP = Row<DT>::V / 2, RB = kBatch;
+  constexpr int NW = NT / 32, PP = Row<DT>::V / 2, RB = stream_batch(NT);
   extern __shared__ __align__(16) uint4 ring[];      // [stage][piece][thread]
   __shared__ Stats red[NW];
   __shared__ TopShared<NW> sh;
@@ -610,6 +613,13 @@ cudaError_t launch_row(const ScoreParams &p, int pieces, int cluster, cudaStream
   return cudaLaunchKernelEx(&cfg, k_score_row<DT, NT>, p, (pieces + cluster - 1) / cluster);
 }
 
+template <int DT, int NT>
+cudaError_t launch_stream(const ScoreParams &p, cudaStream_t s) {
+  static_assert(stream_smem(NT) <= 40 * 1024);
+  k_score_stream<DT, NT><<<std::min(p.rows, stream_ctas(NT) * pi::current_sms()), NT, stream_smem(NT), s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int DT>
 cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(typename Elem<DT>::T);
@@ -626,14 +636,13 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
     while (c < kMaxCluster && (int64_t)threads * kRegVecs * c < pieces) c *= 2;
     return c;
   };
+  // rows enough for every SM: whole rows one after another (620 x 2000 bf16: 6.0 us, a
+  // CTA for each row 7.6; 5000 rows 17 and 29), by CTAs that suit their width
+  // (15630 x 2518 bf16: 50 us with 64 threads, 66 with 128; 2829 x 33510 fp16: 57 us with
+  // 128, 65 with 256; 2048 x 131072 bf16: 116 us with 256, 149 with 128)
+  if (p.rows >= 2 * pi::current_sms())
+    return pieces <= 640 ? launch_stream<DT, 64>(p, s) : pieces <= 6144 ? launch_stream<DT, 128>(p, s) : launch_stream<DT, 256>(p, s);
   if (pieces <= 64 * kRegVecs) return launch_row<DT, 64>(p, pieces, 1, s);
-  if (p.rows >= 2 * pi::current_sms()) {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = pi::allow_smem(k_score_stream<DT>, kStreamSmem, kStreamSmem, done);
-    if (e != cudaSuccess) return e;
-    k_score_stream<DT><<<kStreamCtas * pi::current_sms(), kStreamThreads, kStreamSmem, s>>>(p);
-    return cudaGetLastError();
-  }
   // 256 threads a CTA, so that several are at different stages on an SM; more
   // where a row needs them.  Few rows: as many CTAs as can share one.
   int cluster = fit(256);
