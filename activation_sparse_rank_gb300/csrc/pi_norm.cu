@@ -486,9 +486,11 @@ __global__ void __launch_bounds__(256) k_norm_colsum(const float *__restrict__ p
   }
 }
 
-// Stages of a ring: up to four, in what a CTA may have of an SM's 224 KB.
+// Stages of a ring in what a CTA may have of an SM's 224 KB: up to four forward.
+// The gradient has three rows to copy for one and two stages do (30000 x 760
+// binary32: 67 us, 95 with four, which leave L1 nothing).
 constexpr size_t kRingMost = 224 * 1024;
-int ring_stages(int stage_bytes, int ctas_per_sm) { return std::max(1, std::min(4, 224 * 1024 / ctas_per_sm / stage_bytes)); }
+int ring_stages(int stage_bytes, int ctas_per_sm, int most) { return std::max(1, std::min(most, 224 * 1024 / ctas_per_sm / stage_bytes)); }
 
 template <int X, bool VEC, int NT, int NV, bool WREG>
 cudaError_t launch_norm(NormParams p, cudaStream_t s) {
@@ -501,7 +503,7 @@ cudaError_t launch_norm(NormParams p, cudaStream_t s) {
     grid = std::min(grid, (unsigned)(per_sm * std::max(1, pi::current_sms())));
     const int per_pack = 16 * (1 + (!p.add ? 0 : V * pi::dtype_size(p.add_dt) > 16 ? 2 : 1));
     p.stage_bytes = GROUPS * (p.d / V) * per_pack;
-    p.stages = std::min(ring_stages(p.stage_bytes, per_sm), (p.rows - 1) / (int)(grid * GROUPS) + 1);
+    p.stages = std::min(ring_stages(p.stage_bytes, per_sm, 4), (p.rows - 1) / (int)(grid * GROUPS) + 1);
     smem = (size_t)p.stages * p.stage_bytes;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = pi::allow_smem(k_norm<X, VEC, NT, NV, WREG>, smem, kRingMost, done);
@@ -558,7 +560,7 @@ cudaError_t launch_grad(NormGradParams p, cudaStream_t s) {
   p.stages = 0, p.stage_bytes = 0;
   if (VEC) {
     p.stage_bytes = (p.dsum ? 3 : 2) * GROUPS * (p.d / V) * 16;
-    p.stages = ring_stages(p.stage_bytes, grad_ctas_sm(NT, COLS));
+    p.stages = ring_stages(p.stage_bytes, grad_ctas_sm(NT, COLS), 2);
   }
   const size_t smem = (size_t)p.stages * p.stage_bytes + (GROUPS > 1 ? 2 * p.d * sizeof(float) : 0);
   static std::atomic<uint64_t> done{0};
