@@ -20,6 +20,13 @@
 // is double-buffered, codes have three stages.
 //
 // The line of tiles is cut evenly over the CTAs as in pi_attn.cu.
+//
+// Measured: chunks of up to 512 tokens over caches of up to 8190, 64 bf16 heads of 128
+// on 8: 383 us (880 TFLOP/s, 45% of the dense bf16 rate).  A pair of row tiles takes
+// 4650 clocks a tile of keys, of which the products hold the tensor pipe for 3230; a
+// row tile's softmax, a row a thread, takes 2760.  Tried and slower: one pass of the
+// softmax over registers (538 us), both groups on one row tile's tiles of keys in turn
+// (435), K of the next tile widened before V of this one (470).
 #include "pi_attn.cuh"
 
 using namespace attn;

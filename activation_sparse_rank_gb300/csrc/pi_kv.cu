@@ -10,6 +10,11 @@
 // one load's latency for the single tokens of a decode step.  One warp per
 // (block, head, key or value): it alone reads and writes that block, so the
 // scale needs no atomics and no second pass.
+//
+// Measured: prompts of 30005 tokens in all x 8 heads x 128, bf16, 38 us (4.1 TB/s,
+// 61% of the copy rate: a warp's chain of place, rows, maximum, codes is longer
+// than 32 warps an SM hide); 60015 tokens x 8 x 64 read back 26 us (5.6 TB/s, 83%);
+// one token of 32 sequences x 32 heads 5.2 us.
 #include "pi_ops.cuh"
 #include "pi_kv.cuh"
 
@@ -129,6 +134,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 
 // A warp's block: 16 rows of D elements as 16 D / 8 vectors of 8, vector
 // lane + 32 i to a lane.
+// Registers for four CTAs an SM (write of the prompts above: 38 us; 57 with two, 50
+// with five, which spill); 256 dims hold twice as many rows a lane.
 template <int DT, int D, bool VEC>
 __global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopyParams p) {
   using E = Elem<DT>;
