@@ -63,6 +63,9 @@ def _fits(t, shape, dtype, device) -> bool:
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
 
 
+_Tensor, _empty = torch.Tensor, torch.empty
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -136,6 +139,7 @@ class KVCache:
             _whole(t, (pages, heads, page // PI_KV_BLOCK), _f32, device, n)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.device, self.n_pages, self.heads, self.page_size, self.head_dim = device, pages, heads, page, dim
+        self._index = device.index
         self._status = torch.zeros(1, dtype=_i32, device=device)
         self._c = pi_kv_cache(pages, page, heads, dim, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                               v_scales.data_ptr(), self._status.data_ptr())
@@ -147,21 +151,26 @@ class KVCache:
     def _tokens(self, page_table, cu, per_seq, name, n_tokens):
         dev = self.device
         _dev(page_table, dev, "page_table")
-        if page_table.dtype is not _i32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        if page_table.dtype is not _i32 or page_table.dim() != 2:
             raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
         n, pages = page_table.shape
+        stride, one = page_table.stride()
+        if one != 1:
+            raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
         if not _fits(cu, (n + 1,), _i32, dev):
             _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
         if not _fits(per_seq, (n,), _i32, dev):
             _whole(per_seq, (n,), _i32, dev, name)
         # a table of one row may carry any stride for it
-        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(), page_table.stride(0) if n > 1 else pages)
+        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(), stride if n > 1 else pages)
 
     def _rows(self, t, heads, name):
         """A [tokens, heads, head_dim] tensor with contiguous heads: its token and head strides."""
-        _dev(t, self.device, name)
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
-            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(t.shape)}")
+        if not isinstance(t, _Tensor) or t.get_device() != self._index:
+            _dev(t, self.device, name)
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim:
+            raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(shape)}")
         st, sh, sd = t.stride()
         if sd != 1:
             raise ValueError(f"{name}: the elements of a head must be contiguous")
@@ -174,7 +183,11 @@ class KVCache:
         if v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must have one shape and type")
         tok = self._tokens(page_table, cu_tokens, start, "start", k.shape[0])
-        _on(self.device, stream, self._write, tok, start, k, ks, v, vs, _dt(k, "k"))
+        dt = _dt(k, "k")
+        if stream is None and _current_device() == self._index:
+            self._write(_raw_stream(self._index), tok, start, k, ks, v, vs, dt)
+        else:
+            _on(self.device, stream, self._write, tok, start, k, ks, v, vs, dt)
 
     def _write(self, handle, tok, start, k, ks, v, vs, dt):
         _check(lib.pi_kv_write(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, dt,
@@ -214,18 +227,20 @@ class KVCache:
             raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
         tok = self._tokens(page_table, cu_tokens, length, "length", q.shape[0])
         scale = self._scale if sm_scale is None else sm_scale
+        if stream is None and _current_device() == self._index:
+            return self._attention(_raw_stream(self._index), tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
         return _on(self.device, stream, self._attention, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
 
     def _attention(self, handle, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws):
         dev, shape = self.device, q.shape
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            out = _empty(shape, dtype=q.dtype, device=dev)
         elif not _fits(out, shape, q.dtype, dev):
             _whole(out, shape, q.dtype, dev, "out")
         if lse is not None:
             _whole(lse, shape[:2], _f32, dev, "lse")
         elif want_lse:
-            lse = torch.empty(shape[:2], dtype=_f32, device=dev)
+            lse = _empty(shape[:2], dtype=_f32, device=dev)
         if ws is None:
             ws = self.attention_workspace(shape[1], tok.n_tokens, tok.n_seqs)
         _check(lib.pi_kv_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, q.data_ptr(), qs, shape[1],
@@ -257,51 +272,53 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, y=None, sum=None, 
     dev = _dev(x, None, "x")
     dt = _dt(x, "x")
     rows, d, stride = _rows2d(x, "x")
-    w_dt = 0
+    w_dt = add_dt = 0
+    w_ptr = b_ptr = add_ptr = None
     if weight is not None:
-        w_dt = _dt(weight, "weight")
+        w_dt, w_ptr = _dt(weight, "weight"), weight.data_ptr()
         if not _fits(weight, (d,), weight.dtype, dev):
             _whole(weight, (d,), weight.dtype, dev, "weight")
     if bias is not None:
-        if weight is not None and bias.dtype is not weight.dtype:
+        if weight is None:
+            w_dt = _dt(bias, "bias")
+        elif bias.dtype is not weight.dtype:
             raise TypeError("weight and bias must have one type")
-        w_dt = _dt(bias, "bias")
+        b_ptr = bias.data_ptr()
         if not _fits(bias, (d,), bias.dtype, dev):
             _whole(bias, (d,), bias.dtype, dev, "bias")
     if add is not None:
+        add_dt, add_ptr = _dt(add, "add"), add.data_ptr()
         if not _fits(add, x.shape, add.dtype, dev):
             _whole(add, x.shape, add.dtype, dev, "add")
     elif sum is not None:
         raise ValueError("sum needs add")
+    args = (x, stride, add_ptr, add_dt, w_ptr, b_ptr, w_dt, rows, d, dt, eps, y, sum, mean, rstd, want_stats, dev)
+    if stream is None and _current_device() == dev.index:
+        return _norm(_raw_stream(dev.index), *args)
+    return _on(dev, stream, _norm, *args)
 
-    def run(handle):
-        nonlocal y, sum, mean, rstd
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif not _fits(y, x.shape, x.dtype, dev):
-            _whole(y, x.shape, x.dtype, dev, "y")
-        if add is not None:
-            if sum is None:
-                sum = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            elif not _fits(sum, x.shape, x.dtype, dev):
-                _whole(sum, x.shape, x.dtype, dev, "sum")
-        if mean is not None:
-            _whole(mean, (rows,), _f32, dev, "mean")
-        elif want_stats:
-            mean = torch.empty(rows, dtype=_f32, device=dev)
-        if rstd is not None:
-            _whole(rstd, (rows,), _f32, dev, "rstd")
-        elif want_stats:
-            rstd = torch.empty(rows, dtype=_f32, device=dev)
-        return lib.pi_layer_norm(
-            x.data_ptr(), stride, add.data_ptr() if add is not None else None, _DT[add.dtype] if add is not None else 0,
-            weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, w_dt, rows, d,
-            dt, eps, y.data_ptr(), sum.data_ptr() if sum is not None else None,
-            mean.data_ptr() if mean is not None else None, rstd.data_ptr() if rstd is not None else None, handle)
 
-    if add is not None and add.dtype not in _DT:
-        raise TypeError(f"add must be float16, bfloat16 or float32, not {add.dtype}")
-    _check(_on(dev, stream, run), "pi_layer_norm")
+def _norm(handle, x, stride, add, add_dt, w, b, w_dt, rows, d, dt, eps, y, sum, mean, rstd, want_stats, dev):
+    shape, dtype = x.shape, x.dtype
+    if y is None:
+        y = _empty(shape, dtype=dtype, device=dev)
+    elif not _fits(y, shape, dtype, dev):
+        _whole(y, shape, dtype, dev, "y")
+    if add is not None or sum is not None:
+        if sum is None:
+            sum = _empty(shape, dtype=dtype, device=dev)
+        elif not _fits(sum, shape, dtype, dev):
+            _whole(sum, shape, dtype, dev, "sum")
+    if mean is not None:
+        _whole(mean, (rows,), _f32, dev, "mean")
+    elif want_stats:
+        mean = _empty(rows, dtype=_f32, device=dev)
+    if rstd is not None:
+        _whole(rstd, (rows,), _f32, dev, "rstd")
+    elif want_stats:
+        rstd = _empty(rows, dtype=_f32, device=dev)
+    _check(lib.pi_layer_norm(x.data_ptr(), stride, add, add_dt, w, b, w_dt, rows, d, dt, eps, y.data_ptr(), _ptr(sum),
+                             _ptr(mean), _ptr(rstd), handle), "pi_layer_norm")
     return y, sum, mean, rstd
 
 
@@ -365,19 +382,21 @@ def token_logprobs(logits, targets=None, top_k=0, stream=None) -> TokenScores:
     rows, vocab = logits.shape
     if targets is not None and not _fits(targets, (rows,), _i32, dev):
         _whole(targets, (rows,), _i32, dev, "targets")
+    if stream is None and _current_device() == dev.index:
+        return _score(_raw_stream(dev.index), logits, rows, vocab, dt, targets, top_k)
     return _on(dev, stream, _score, logits, rows, vocab, dt, targets, top_k)
 
 
 def _score(handle, logits, rows, vocab, dt, targets, top_k):
     dev = logits.device
     index = value = logprob = None
-    entropy = torch.empty(rows, dtype=_f32, device=dev)
-    lse = torch.empty(rows, dtype=_f32, device=dev)
+    entropy = _empty(rows, dtype=_f32, device=dev)
+    lse = _empty(rows, dtype=_f32, device=dev)
     if targets is not None:
-        logprob = torch.empty(rows, dtype=_f32, device=dev)
+        logprob = _empty(rows, dtype=_f32, device=dev)
     if top_k > 0:
-        index = torch.empty((rows, top_k), dtype=_i32, device=dev)
-        value = torch.empty((rows, top_k), dtype=_f32, device=dev)
+        index = _empty((rows, top_k), dtype=_i32, device=dev)
+        value = _empty((rows, top_k), dtype=_f32, device=dev)
     _check(lib.pi_token_logprobs(
         logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, dt, rows, vocab,
         targets.data_ptr() if targets is not None else None, top_k, logprob.data_ptr() if targets is not None else None,
