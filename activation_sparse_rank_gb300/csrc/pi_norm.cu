@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT, grad_ctas_sm(NT, 2 * Cols
     }
   };
   for (int s = 0; s < p.stages; ++s) fetch(row0 + s * step, s);
+  griddep_launch();                                  // the column sums' CTAs take the places that this grid leaves
 
   f2 dw[NP], db[NP], w[HOLD ? NP : 1];
 #pragma unroll
@@ -470,8 +471,9 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT, grad_ctas_sm(NT, 2 * Cols
 }
 
 // Column sums of part [n, 2 d]: 32 columns a CTA, 8 row classes added in order.
-__global__ void __launch_bounds__(256) k_norm_colsum(const float *__restrict__ part, int n, int d, float *dw, float *db) {
+__global__ void __launch_bounds__(256) k_norm_colsum(const float *part, int n, int d, float *dw, float *db) {
   __shared__ float red[8][32];
+  griddep_wait();
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
   float s = 0.f;
@@ -675,8 +677,7 @@ pi_status pi_layer_norm_backward(const void *dy, const void *x, int64_t x_stride
               : dtype == PI_DT_BF16 ? grad_by_type<PI_DT_BF16>(p, vec, s)
                                     : grad_by_type<PI_DT_F32>(p, vec, s));
   if (want) {
-    k_norm_colsum<<<(2 * d + 31) / 32, 256, 0, s>>>(part, grad_ctas(rows, d), d, dweight, dbias);
-    PI_TRY_CUDA(cudaGetLastError());
+    PI_TRY_CUDA(pi::launch_pdl(k_norm_colsum, dim3((unsigned)(2 * d + 31) / 32), dim3(256), 0, s, part, grad_ctas(rows, d), d, dweight, dbias));
   }
   return PI_OK;
 }

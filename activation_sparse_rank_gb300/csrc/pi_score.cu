@@ -244,9 +244,10 @@ __device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, fl
     __syncthreads();
     const int each = (last - first + NT - 1) / NT, n = sh.n_owners;
     if (n <= kSlots) {
+      const float by = 1.f / (float)each;            // i / each, exact: i + 0.5 is at least 0.5 / each from a whole quotient
 #pragma unroll 1
       for (int i = threadIdx.x; i < n * each; i += NT) {
-        const int c = first + i % each * NT + sh.owner[i / each];
+        const int o = (int)(((float)i + 0.5f) * by), c = first + (i - o * each) * NT + sh.owner[o];
         if (c >= last) continue;
         const uint4 r = w.inner(c) ? ld_stream(w.base() + c) : w.edge(c);
         if ((unsigned)(order_key(piece_max<DT>(r), 0) >> 32) < low) continue;
