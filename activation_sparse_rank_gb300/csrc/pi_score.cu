@@ -13,9 +13,9 @@
 // k-th largest of any selection of elements is at most the k-th largest of all.
 // Elements at or above that bound are few; they are ranked by counting.
 //
-// Measured: 2048 x 131072 bf16, 20 alternatives, 116 us (4.6 TB/s, 68% of the copy rate;
-// 608 CTAs take three or four rows each, and a row's end reads its likely pieces
-// again); 16 x 50007 binary32, 5 alternatives, 8 us.
+// Measured: 2048 x 131072 bf16, 20 alternatives, 105 us (5.1 TB/s, 76% of the copy rate;
+// 90 us without alternatives; 608 CTAs take three or four rows each); 16 x 50007
+// binary32, 5 alternatives, 6.9 us.
 #include "pi_ops.cuh"
 
 #include <algorithm>
@@ -110,7 +110,8 @@ __device__ __forceinline__ void store_leader(T *p, unsigned long long v) {
 }
 
 constexpr int kRegVecs = 16;         // 16-byte pieces of a row a thread holds
-constexpr int kSlots = 64;           // threads whose pieces are looked through for alternatives
+constexpr int kSlots = 128;          // runs of pieces that are looked through for alternatives
+constexpr int kRuns = 8;             // of a thread and row of k_score_stream, at most
 constexpr int kList = 512;           // alternatives ranked by counting
 constexpr int kMaxCluster = 8;
 
@@ -208,9 +209,13 @@ struct TopShared {
 //
 // The k-th largest of any of the elements is at most the k-th largest of all: the
 // thread maxima give a bound, and few threads have anything at or above it.
-// Their pieces are read again, from L2, by all threads.
+// Their pieces are read again, by all threads.  A row that has left L2 by then
+// costs HBM a sector for each piece, so where `runs` gives the maxima of a thread's
+// runs of `span` pieces ([run][thread]), only those at or above the bound are read
+// (2048 x 131072 bf16: 113 -> 105 us).
 template <int DT, int NT, typename F>
-__device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, float mt, int K, TopShared<NT / 32> &sh, F put) {
+__device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, float mt, int K, TopShared<NT / 32> &sh, F put,
+                                       const float *runs = nullptr, int span = 0) {
   using E = Elem<DT>;
   constexpr int NW = NT / 32, V = Row<DT>::V;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, M = min(32, max(4, (2 * K + NW - 1) / NW));
@@ -235,19 +240,24 @@ __device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, fl
   }
   __syncthreads();
   const unsigned tau = sh.tau;
-  // elements whose key is `low` or more, of the threads whose maximum is, into the list; false if they are too many
+  const int each = (last - first + NT - 1) / NT;     // pieces of a thread
+  // elements whose key is `low` or more, of the runs whose maximum is, into the list; false if they are too many
   auto collect = [&](unsigned low) {
     if (key && key >= low) {
-      const int n = atomicAdd(&sh.n_owners, 1);
-      if (n < kSlots) sh.owner[n] = threadIdx.x;
+      for (int k = 0; k < (runs ? (each + span - 1) / span : 1); ++k) {
+        if (runs && (unsigned)(order_key(runs[k * NT + threadIdx.x], 0) >> 32) < low) continue;
+        const int n = atomicAdd(&sh.n_owners, 1);
+        if (n < kSlots) sh.owner[n] = threadIdx.x | k << 16;
+      }
     }
     __syncthreads();
-    const int each = (last - first + NT - 1) / NT, n = sh.n_owners;
+    const int n = sh.n_owners, run = runs ? span : each;
     if (n <= kSlots) {
-      const float by = 1.f / (float)each;            // i / each, exact: i + 0.5 is at least 0.5 / each from a whole quotient
+      const float by = 1.f / (float)run;             // i / run, exact: i + 0.5 is at least 0.5 / run from a whole quotient
 #pragma unroll 1
-      for (int i = threadIdx.x; i < n * each; i += NT) {
-        const int o = (int)(((float)i + 0.5f) * by), c = first + (i - o * each) * NT + sh.owner[o];
+      for (int i = threadIdx.x; i < n * run; i += NT) {
+        const int o = (int)(((float)i + 0.5f) * by), at = sh.owner[o];
+        const int c = first + ((at >> 16) * run + i - o * run) * NT + (at & 0xffff);
         if (c >= last) continue;
         const uint4 r = w.inner(c) ? ld_stream(w.base() + c) : w.edge(c);
         if ((unsigned)(order_key(piece_max<DT>(r), 0) >> 32) < low) continue;
@@ -462,6 +472,7 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
   extern __shared__ __align__(16) uint4 ring[];      // [stage][piece][thread]
   __shared__ Stats red[NW];
   __shared__ TopShared<NW> sh;
+  __shared__ float runs[kRuns][NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = p.top_k;
 
   // the next batch to copy
@@ -502,6 +513,9 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const Row<DT> w(p, row);
     Stats st{-INFINITY, 0.f, 0.f};
+    const int per_run = ((w.pieces + RB * NT - 1) / (RB * NT) + kRuns - 1) / kRuns;    // batches of a run
+    float run_max = -INFINITY;
+    int run = 0, left = per_run;
 #pragma unroll 1
     for (int b = 0; b * RB * NT < w.pieces; ++b) {
       copy();                                        // into the stage that the last batch left
@@ -509,10 +523,10 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
       const uint4 *raw = ring + stage * RB * NT + threadIdx.x;
       stage = stage + 1 == kStages ? 0 : stage + 1;
       const int n = min(RB, (w.pieces - b * RB * NT + NT - 1) / NT);   // pieces of this batch that any thread has
-      float m = st.m;
 #pragma unroll
       for (int i = 0; i < RB; ++i)
-        if (i < n) m = max_nan(m, piece_max<DT>(raw[i * NT]));
+        if (i < n) run_max = max_nan(run_max, piece_max<DT>(raw[i * NT]));
+      const float m = max_nan(st.m, run_max);
       if (m > -INFINITY) {
         const float d = (st.m - m) * kLog2e, c = ex2(d);
         f2 Z = f2_of(c * st.Z, 0.f), S = f2_of(c == 0.f ? 0.f : c * fmaf(d, st.Z, st.S), 0.f);
@@ -534,6 +548,8 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
         st.Z = f2_sum(Z), st.S = f2_sum(S);
       }
       st.m = m;
+      runs[run][threadIdx.x] = run_max;              // the run so far
+      if (--left == 0) ++run, left = per_run, run_max = -INFINITY;
       __syncwarp();
     }
 
@@ -552,7 +568,7 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
       cta_top<DT, NT>(w, 0, w.pieces, mt, K, sh, [&](int k, unsigned long long key) {
         p.top_index[(int64_t)row * K + k] = (int)(0xffffffffu - (unsigned)key);
         p.top_logprob[(int64_t)row * K + k] = st.m == -INFINITY ? __uint_as_float(0x7fffffffu) : logit_of(key) - lse;
-      });
+      }, &runs[0][0], per_run * RB);
     __syncthreads();                                 // red and sh are free for the next row
   }
 }
@@ -620,7 +636,7 @@ cudaError_t launch_row(const ScoreParams &p, int pieces, int cluster, cudaStream
 
 template <int DT, int NT>
 cudaError_t launch_stream(const ScoreParams &p, cudaStream_t s) {
-  static_assert(stream_smem(NT) <= 40 * 1024);
+  static_assert(stream_smem(NT) + kRuns * NT * 4 + sizeof(TopShared<NT / 32>) + 512 <= 48 * 1024);
   k_score_stream<DT, NT><<<std::min(p.rows, stream_ctas(NT) * pi::current_sms()), NT, stream_smem(NT), s>>>(p);
   return cudaGetLastError();
 }
@@ -642,10 +658,11 @@ cudaError_t score_by_type(const ScoreParams &p, cudaStream_t s) {
     return c;
   };
   // rows enough for every SM: whole rows one after another (620 x 2000 bf16: 6.0 us, a
-  // CTA for each row 7.6; 5000 rows 17 and 29), by CTAs that suit their width
+  // CTA for each row 7.6; 5000 rows 17 and 29; 200 x 50007 binary32 14 us, a cluster for
+  // each 21, but 200 x 32000 bf16 10 and 8), by CTAs that suit their width
   // (15630 x 2518 bf16: 50 us with 64 threads, 66 with 128; 2829 x 33510 fp16: 57 us with
-  // 128, 65 with 256; 2048 x 131072 bf16: 116 us with 256, 149 with 128)
-  if (p.rows >= 2 * pi::current_sms())
+  // 128, 65 with 256; 2048 x 131072 bf16: 105 us with 256, 149 with 128)
+  if (p.rows >= (pieces > 6144 ? 1 : 2) * pi::current_sms())
     return pieces <= 640 ? launch_stream<DT, 64>(p, s) : pieces <= 6144 ? launch_stream<DT, 128>(p, s) : launch_stream<DT, 256>(p, s);
   // narrow rows: two warps; but the thread maxima of two bound many alternatives loosely
   // (16 x 5000 bf16, 20 of them: 9.3 us, 6.6 with 256 threads), unless most threads of
