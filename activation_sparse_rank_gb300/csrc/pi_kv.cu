@@ -11,9 +11,9 @@
 // (block, head, key or value): it alone reads and writes that block, so the
 // scale needs no atomics and no second pass.
 //
-// Measured: prompts of 30005 tokens in all x 8 heads x 128, bf16, 38 us (4.1 TB/s,
-// 61% of the copy rate: a warp's chain of place, rows, maximum, codes is longer
-// than 32 warps an SM hide); 60015 tokens x 8 x 64 read back 26 us (5.6 TB/s, 83%);
+// Measured: prompts of 30005 tokens in all x 8 heads x 128, bf16, 33 us (4.7 TB/s,
+// 69% of the copy rate: a warp's chain of place, rows, maximum, codes is longer
+// than 16 warps an SM with two blocks each hide); 60015 tokens x 8 x 64 read back 26 us (5.6 TB/s, 83%);
 // one token of 32 sequences x 32 heads 5.2 us.
 #include "pi_ops.cuh"
 #include "pi_kv.cuh"
@@ -134,10 +134,12 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 
 // A warp's block: 16 rows of D elements as 16 D / 8 vectors of 8, vector
 // lane + 32 i to a lane.
-// Registers for four CTAs an SM (write of the prompts above: 38 us; 57 with two, 50
-// with five, which spill); 256 dims hold twice as many rows a lane.
-template <int DT, int D, bool VEC>
-__global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopyParams p) {
+// AHEAD: a warp with several units loads the next one while it quantises one, at two
+// CTAs an SM (write of the prompts above: 34 us, 38 without it at four, 57 at two).
+// Otherwise registers for four CTAs (five spill: 50 us; 256 dims hold twice as many
+// rows a lane).
+template <int DT, int D, bool VEC, bool AHEAD>
+__global__ void __launch_bounds__(256, D <= 128 && !AHEAD ? 4 : 2) k_kv_write(const KvCopyParams p) {
   using E = Elem<DT>;
   constexpr int VR = D / 8, NV = PI_KV_BLOCK * VR / 32, WPV = 8 * sizeof(typename E::T) / 16;
   kv_check_cu(p);
@@ -145,11 +147,12 @@ __global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopy
   KvPlace at;
   bool ok;
   if (!kv_place(p, blockIdx.x / parts, &at, &ok) || !ok) return;
-  for (int i_unit = 0, unit = blockIdx.x % parts * 8 * p.per_warp + (threadIdx.x >> 5);
-       i_unit < p.per_warp && unit < 2 * p.c.heads; ++i_unit, unit += 8) {
+  int unit = blockIdx.x % parts * 8 * p.per_warp + (threadIdx.x >> 5);
+  const int units = min(2 * p.c.heads, unit + 8 * p.per_warp);
+  uint4 x[NV][WPV], next[AHEAD ? NV : 1][WPV];
+  auto load = [&](uint4 (*x)[WPV], int unit) {
     const int kv = unit >= p.c.heads, h = unit - kv * p.c.heads;
     const typename E::T *src = static_cast<const typename E::T *>(p.src[kv]) + (int64_t)at.row0 * p.st[kv] + h * p.sh[kv];
-    uint4 x[NV][WPV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -171,6 +174,14 @@ __global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopy
         }
       }
     }
+  };
+  if constexpr (AHEAD)
+    if (unit < units) load(x, unit);
+#pragma unroll 1
+  for (; unit < units; unit += 8) {
+    const int kv = unit >= p.c.heads, h = unit - kv * p.c.heads;
+    if constexpr (!AHEAD) load(x, unit);
+    else if (unit + 8 < units) load(next, unit + 8);
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -209,6 +220,12 @@ __global__ void __launch_bounds__(256, D <= 128 ? 4 : 2) k_kv_write(const KvCopy
       }
     }
     if (lane == 0) *scale = s;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < WPV; ++c) x[i][c] = next[i][c];
+    }
   }
 }
 
@@ -268,13 +285,17 @@ template <int DT, int D>
 cudaError_t launch_copy(KvCopyParams p, bool write, bool vec, cudaStream_t s) {
   const int units = 2 * p.c.heads;
   // finding a block's place takes three loads one after another: with enough
-  // blocks to fill the GPU a warp uses it for several heads
+  // blocks to fill the GPU a warp uses it for several heads (read of the prefixes above:
+  // 26 us, 29 with one)
   p.per_warp = std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)p.n_slots * units / (64 * std::max(1, pi::current_sms()))));
   const unsigned grid = (unsigned)((int64_t)std::max(1, p.n_slots) * ((units + 8 * p.per_warp - 1) / (8 * p.per_warp)));
-  if (write && vec)
-    k_kv_write<DT, D, true><<<grid, 256, 0, s>>>(p);
+  constexpr bool kAhead = D <= 128 && DT != PI_DT_F32;         // twice a unit's registers fit
+  if (write && vec && kAhead && p.per_warp > 1)
+    k_kv_write<DT, D, true, kAhead><<<grid, 256, 0, s>>>(p);
+  else if (write && vec)
+    k_kv_write<DT, D, true, false><<<grid, 256, 0, s>>>(p);
   else if (write)
-    k_kv_write<DT, D, false><<<grid, 256, 0, s>>>(p);
+    k_kv_write<DT, D, false, false><<<grid, 256, 0, s>>>(p);
   else
     k_kv_read<DT, D><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
