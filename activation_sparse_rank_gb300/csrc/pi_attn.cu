@@ -663,7 +663,10 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
   const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<int4 *>(ws),
                      reinterpret_cast<float *>(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1)),
                      sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
-                     (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb)};
+                     (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb),
+                     (pi::aligned_to(q, 32) && q_stride[0] % 16 == 0 && q_stride[1] % 16 == 0 ? 1 : 0) |
+                         (pi::aligned_to(out, 32) ? 2 : 0) |
+                         (pi::aligned_to(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1), 32) ? 4 : 0)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (many_rows(cache->head_dim, (int64_t)max_q * group))
     PI_TRY_CUDA(run_tc(p, dtype, s));

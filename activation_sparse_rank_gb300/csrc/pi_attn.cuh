@@ -33,7 +33,19 @@ struct AttnParams {
   float *part;             // [2 grid] partials of [ROWS, D] sums, then [ROWS, 2] (m, l)
   float scale;             // sm_scale log2(e)
   int q_heads, group, max_q, causal, row_tiles, grid;
+  int wide;                // q, out, part: bits 0, 1, 2 set where 32-byte accesses are aligned
 };
+
+// 32 bytes at once, for a row a thread: half the transactions of 16 bytes (prompts of
+// 85 tokens x 5 heads over 182 keys, 16 sequences x 22 heads: 111 -> 98 us).
+__device__ __forceinline__ void load32(const uint4 *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p));
+}
+__device__ __forceinline__ void store32(uint4 *p, const uint4 &a, const uint4 &b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+               "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

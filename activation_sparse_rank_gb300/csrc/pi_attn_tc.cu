@@ -22,7 +22,7 @@
 // The line of tiles is cut evenly over the CTAs as in pi_attn.cu.
 //
 // Measured: chunks of up to 512 tokens over caches of up to 8190, 64 bf16 heads of 128
-// on 8: 383 us (880 TFLOP/s, 45% of the dense bf16 rate).  A pair of row tiles takes
+// on 8: 374 us (900 TFLOP/s, 46% of the dense bf16 rate).  A pair of row tiles takes
 // 4650 clocks a tile of keys, of which the products hold the tensor pipe for 3230; a
 // row tile's softmax, a row a thread, takes 2760.  Tried and slower: one pass of the
 // softmax over registers (538 us), both groups on one row tile's tiles of keys in turn
@@ -226,8 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
         if (in) {
+          if (p.wide & 1) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) raw[c] = src[c];
+            for (int c = 0; c < D / 8; c += 2) load32(src + c, raw[c], raw[c + 1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) raw[c] = src[c];
+          }
         }
         float up = p.scale < 0.f ? -1.f : 1.f;
         if constexpr (DT == PI_DT_BF16) {                // as in pi_attn.cu: the largest finite magnitude to [2^13, 2^14)
@@ -377,19 +382,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         if (whole) {
           if (in) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<typename E::T *>(p.out) + orow * D + q * 32);
-            constexpr int W = 16 / sizeof(typename E::T);
+            uint4 y[4];
 #pragma unroll
-            for (int c = 0; c < 32 / W; ++c) {
+            for (int c = 0; c < 4; ++c) {
               f2 v[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_of(o[8 * c + 2 * j], o[8 * c + 2 * j + 1]), f2_of(inv, inv));
-              dst[c] = f2_to16<DT>(v);
+              y[c] = f2_to16<DT>(v);
+            }
+            if (p.wide & 2) {
+              store32(dst, y[0], y[1]), store32(dst + 2, y[2], y[3]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) dst[c] = y[c];
             }
           }
         } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(part + pr * D + q * 32);
+          const uint32_t *y = reinterpret_cast<const uint32_t *>(o);
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<float4 *>(part + pr * D + q * 32 + 4 * c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          for (int c = 0; c < 8; c += 2) {
+            const uint4 a = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+            const uint4 b = make_uint4(y[4 * c + 4], y[4 * c + 5], y[4 * c + 6], y[4 * c + 7]);
+            if (p.wide & 4) store32(dst + c, a, b);
+            else dst[c] = a, dst[c + 1] = b;
+          }
         }
       }
       fence_before();

@@ -124,3 +124,23 @@ def test_all_masked_blocks(pi):
         check(c, b, q, out, lse, length)
         empty = torch.from_numpy(np.repeat(np.array(length) == 0, new)).cuda()
         assert not out[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+@pytest.mark.parametrize("dim,group,new", [(64, 1, 5), (64, 4, 40), (96, 8, 20), (128, 8, 40), (256, 2, 20)])
+def test_sixteen_byte_alignment(pi, dim, group, new):
+    """Queries, output and workspace that start 16 bytes past a 32-byte boundary, queries with an odd stride of 16
+    bytes: the same bits as aligned ones."""
+    heads, length = 2, 700
+    b = batch([length - new], [new], 64)
+    c = random_cache(pi, b["pages"], heads, dim, 64)
+    n = heads * group
+    q = queries(new, n, dim, "bfloat16")
+    want, wlse = run(pi, c, b, q, [length])
+    d = b["dev"]
+    wide = torch.zeros(new * n * (dim + 8) + 8, dtype=torch.bfloat16, device="cuda")[8:].view(new, n, dim + 8)
+    wide[:, :, :dim] = q
+    out = torch.zeros(new * n * dim + 8, dtype=torch.bfloat16, device="cuda")[8:].view(new, n, dim)
+    ws = torch.empty(c.attention_workspace(n, new, 1).numel() + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert wide.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    got, lse = c.attention(wide[:, :, :dim], d["table"], d["cu"], d["length"], max_q=new, out=out, want_lse=True, ws=ws)
+    assert got is out and torch.equal(out, want) and torch.equal(lse, wlse)
