@@ -97,8 +97,8 @@ struct Frag {
   }
 };
 
-// CTAs of 128 threads that an SM holds, by the registers of the variant (80 for
-// 8 rows of 64, 128 for 8 of 128, 254 for 16 of 128); the grid is one wave of them.
+// CTAs of 128 threads that an SM holds, by the registers of the variant (96 for
+// 8 rows of 64, 128 for 8 of 128, 255 for 16 of 128); the grid is one wave of them.
 constexpr int attn_ctas(int D, int nb) { return nb == 1 ? (D == 64 ? 5 : D <= 128 ? 4 : 2) : D == 64 ? 4 : D == 96 ? 3 : 2; }
 // Ring stages of a CTA (a stage: a tile's four blocks) in its share of 224 KB.
 template <int D, int NB>

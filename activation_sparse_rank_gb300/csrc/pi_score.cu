@@ -7,11 +7,12 @@
 // with d = log2(e) (m - m'), c = 2^d.  Bound by HBM for many rows; by latency
 // for the few of a decode step.
 //
-// A row is read once and kept in registers (up to 128 bytes a thread; a cluster
-// of CTAs a row where one is too small or rows are few).  Each thread's maximum
-// gives its sums their reference and, together, the alternatives a bound: the
-// k-th largest of any selection of elements is at most the k-th largest of all.
-// Elements at or above that bound are few; they are ranked by counting.
+// Few rows: a row is read once and kept in registers (up to 256 bytes a thread; a
+// cluster of CTAs where one is too small).  Many rows stream through shared memory.
+// Each thread's maximum gives its sums their reference and, together, the
+// alternatives a bound: the k-th largest of any selection of elements is at most
+// the k-th largest of all.  Elements at or above that bound are few; they are
+// ranked by counting.
 //
 // Measured: 2048 x 131072 bf16, 20 alternatives, 105 us (5.1 TB/s, 76% of the copy rate;
 // 90 us without alternatives; 608 CTAs take three or four rows each); 16 x 50007
