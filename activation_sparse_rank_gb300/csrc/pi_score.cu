@@ -151,6 +151,31 @@ __device__ __forceinline__ uint4 clamp_piece(uint4 r, float least) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Whether what clamp_piece makes of 140 below m is at least 100 below m, so that its
+// weight is 0: not where m - 140 rounds to m, nor where it is past fp16's lowest value.
+template <int DT>
+__device__ __forceinline__ bool clamps_near(float m) {
+  return fabsf(m) < 0x1p24f && (DT != PI_DT_F16 || m > -65400.f);
+}
+// A piece's sums relative to m = -minus added to Z and S.  NEAR: what is further
+// below m than 140 has weight 0 either way, and is clamped before the subtraction,
+// in the element's type (one operation for two, and no 0 (-inf)).  Otherwise the
+// difference is clamped: then only what is -inf or far below has weight 0.
+template <int DT, bool NEAR>
+__device__ __forceinline__ void add_piece(const uint4 &raw, float least, f2 minus, f2 &Z, f2 &S) {
+  const f2 l2e = f2_of(kLog2e, kLog2e);
+  const uint4 r = NEAR ? clamp_piece<DT>(raw, least) : raw;
+#pragma unroll
+  for (int j = 0; j < 8 / (int)sizeof(typename Elem<DT>::T); ++j) {
+    f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
+    if constexpr (!NEAR) zz = f2_of(fmaxf(zz.x, -200.f), fmaxf(zz.y, -200.f));
+    const float2 z = f2_get(zz);
+    const f2 e = f2_of(ex2(z.x), ex2(z.y));
+    Z = f2_add(Z, e);
+    S = f2_fma(e, zz, S);
+  }
+}
+
 // keys[0, n) (distinct): the k largest in order, to put(rank, key).
 template <typename F>
 __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int k, F put) {
@@ -335,7 +360,7 @@ __device__ __forceinline__ int cta_top(const Row<DT> &w, int first, int last, fl
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p, int share) {
   using E = Elem<DT>;
-  constexpr int V = Row<DT>::V, PP = V / 2, NW = NT / 32;
+  constexpr int NW = NT / 32;
   __shared__ Stats red[NW];
   __shared__ TopShared<NW> sh;
   __shared__ unsigned long long in_keys[kMaxCluster][PI_MAX_TOP_K];
@@ -373,23 +398,14 @@ __global__ void __launch_bounds__(NT, 512 / NT) k_score_row(const ScoreParams p,
   });
   Stats st{mt, 0.f, 0.f};
   if (mt > -INFINITY) {                              // else nothing, or a NaN that m carries on
-    const f2 minus = f2_of(-mt, -mt), l2e = f2_of(kLog2e, kLog2e);
-    // what is further below the maximum has weight 0 either way, and this way no 0 (-inf)
-    const float least = mt - 140.f;
+    const f2 minus = f2_of(-mt, -mt);
     f2 Z = f2_of(0.f, 0.f), S = Z;
-    each<kRegVecs>([&](auto i) {
-      if (i.v == 0 || first + i.v * NT < last) {
-        const uint4 r = clamp_piece<DT>(raw[i.v], least);
-#pragma unroll
-        for (int j = 0; j < PP; ++j) {
-          const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
-          const float2 z = f2_get(zz);
-          const f2 e = f2_of(ex2(z.x), ex2(z.y));
-          Z = f2_add(Z, e);
-          S = f2_fma(e, zz, S);
-        }
-      }
-    });
+    auto add = [&](auto near) {
+      each<kRegVecs>([&](auto i) {
+        if (i.v == 0 || first + i.v * NT < last) add_piece<DT, decltype(near)::v>(raw[i.v], mt - 140.f, minus, Z, S);
+      });
+    };
+    if (clamps_near<DT>(mt)) add(Int<1>{}); else add(Int<0>{});
     st.Z = f2_sum(Z), st.S = f2_sum(S);
   }
   __syncwarp();
@@ -469,7 +485,7 @@ constexpr int stream_ctas(int NT) { return 1024 / NT; }
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const ScoreParams p) {
   using E = Elem<DT>;
-  constexpr int NW = NT / 32, PP = Row<DT>::V / 2, RB = stream_batch(NT);
+  constexpr int NW = NT / 32, RB = stream_batch(NT);
   extern __shared__ __align__(16) uint4 ring[];      // [stage][piece][thread]
   __shared__ Stats red[NW];
   __shared__ TopShared<NW> sh;
@@ -531,21 +547,13 @@ __global__ void __launch_bounds__(NT, stream_ctas(NT)) k_score_stream(const Scor
       if (m > -INFINITY) {
         const float d = (st.m - m) * kLog2e, c = ex2(d);
         f2 Z = f2_of(c * st.Z, 0.f), S = f2_of(c == 0.f ? 0.f : c * fmaf(d, st.Z, st.S), 0.f);
-        const f2 minus = f2_of(-m, -m), l2e = f2_of(kLog2e, kLog2e);
-        const float least = m - 140.f;               // as in k_score_row
+        const f2 minus = f2_of(-m, -m);
+        auto add = [&](auto near) {
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-          if (i < n) {
-            const uint4 r = clamp_piece<DT>(raw[i * NT], least);
-#pragma unroll
-            for (int j = 0; j < PP; ++j) {
-              const f2 zz = f2_mul(f2_add(f2_from16<DT>(r, j), minus), l2e);
-              const float2 z = f2_get(zz);
-              const f2 e = f2_of(ex2(z.x), ex2(z.y));
-              Z = f2_add(Z, e);
-              S = f2_fma(e, zz, S);
-            }
-          }
+          for (int i = 0; i < RB; ++i)
+            if (i < n) add_piece<DT, decltype(near)::v>(raw[i * NT], m - 140.f, minus, Z, S);
+        };
+        if (clamps_near<DT>(m)) add(Int<1>{}); else add(Int<0>{});
         st.Z = f2_sum(Z), st.S = f2_sum(S);
       }
       st.m = m;

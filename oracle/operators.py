@@ -201,3 +201,23 @@ def token_logprobs(x, targets, top_k):
                   np.abs(val[r][np.isfinite(val[r])]).max(initial=0.0))
         tol[r] = (1 + 2 * spread) * step + 4 * U32 * (far + abs(m))
     return logp, ent, lse, idx, val, tol
+
+
+def score_bounds(x, logp, ent, lse):
+    """Bounds on binary32's entropy, lse and logprob, each with its own terms (one
+    [rows] array each).  The entropy depends on differences of logits alone, so it
+    has no term in their size; lse is one sum m + ln Z, logprob one difference
+    more."""
+    x = np.asarray(x, dtype=np.float64)
+    step = 2.0 ** -21 + (x.shape[1] / 128 + 128) * U32
+    m = x.max(1, keepdims=True)
+    with np.errstate(invalid="ignore"):                      # rows without a distribution: NaN bounds, not used
+        z = x - m
+        p = np.exp(z)
+        total = p.sum(1)
+        spread = -np.where(p > 0, p * np.where(p > 0, z, 0.0), 0.0).sum(1) / total
+        log_z = np.log(total)
+        t_ent = (1 + 2 * spread) * step + 4 * U32 * (np.abs(log_z) + spread + np.abs(ent))
+        t_lse = step + 4 * U32 * log_z + 2 * U32 * np.abs(lse)
+        t_logp = t_lse + 2 * U32 * np.abs(logp)
+    return t_ent, t_lse, t_logp
