@@ -53,6 +53,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// sum + l 2^by, by <= 0 or not by much more: a part's l may be so large (its values
+// had the smallest scales) that it counts where 2^by alone would be 0.
+__device__ __forceinline__ float add_scaled(float sum, float l, float by) {
+  if (by < -120.f) {
+    const float h = ex2(0.5f * by);
+    return sum + l * h * h;
+  }
+  return fmaf(l, ex2(by), sum);
+}
+
 // Four codes as two fp16 pairs: one instruction each.
 __device__ __forceinline__ void widen4(unsigned w, unsigned &lo, unsigned &hi) {
   asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(kCombineThreads, combine_ctas(D)) k_attn_combi
         if (lane < n) {
           const float *ml = part(b + lane) + ROWS * D + 2 * row;
           w = ex2(ml[0] - ms);
-          L += ml[1] * w;
+          L = add_scaled(L, ml[1], ml[0] - ms);
         }
 #pragma unroll 8
         for (int i = lane / LANES; i < (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES); i += 32 / LANES) {
@@ -356,7 +366,7 @@ __global__ void __launch_bounds__(kCombineThreads, combine_ctas(D)) k_attn_combi
       for (int k = 0; k < VECS; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i = 0; i < split; ++i) {
         const float w = ex2(stats[warp + i].x - ms);
-        L += stats[warp + i].y * w;
+        L = add_scaled(L, stats[warp + i].y, stats[warp + i].x - ms);
 #pragma unroll
         for (int k = 0; k < VECS; ++k)
           if (lane % LANES + k * 32 < D / 4) {

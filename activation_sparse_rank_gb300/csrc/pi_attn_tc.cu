@@ -12,7 +12,9 @@
 //   P_j = 2^(x_j + ev_j - R),  acc = sum P_j c_j = sum 2^(x_j - R) v_j,
 //   L = sum 2^-ev_j P_j = sum 2^(x_j - R),  out = acc / L
 // with R + kBoost near the running maximum of x_j + ev_j (within kSlack): no
-// multiplication per element of K or V, and scales of any range.
+// multiplication per element of K or V.  L has the range for any two scales (2^-64
+// to 2^120): its terms lie between 2^-149 and 2^80.  P_j does not, so a block whose
+// scale is far below the largest so far (kFar) adds 2^100 P_j to L instead.
 //
 // Roles (16 warps, one CTA an SM): 0-3 and 4-7 softmax of the two row tiles, a row
 // a thread; 8-11 converters, a token a thread; 12 tile copies and scales; 13 issues
@@ -36,6 +38,9 @@ namespace {
 constexpr int kRows = kTcRows, kHalf = 128, kKeys = 128, kBlocks = kKeys / PI_KV_BLOCK;
 constexpr int kThreads = 512;      // four warpgroups: register shares are set for each
 constexpr int kStages = 3;         // of codes, K and V of a tile in turn
+// From P_j = 0, so x_j + ev_j < R - 126, and ev_j >= ev - kFar for every ev so far it
+// follows that x_j is 38 or more below the largest x: its weight is nothing.
+constexpr float kFar = 94.f;
 constexpr int kScaleRing = 8;    // tiles whose scales are kept: copies run at most 5 tiles ahead of the softmax
 
 // Shared-memory matrix descriptor, 128-byte swizzle: its low word holds the
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&bars.q_full[rt]));
       }
-      float R = -INFINITY, sum = 0.f;
+      float R = -INFINITY, sum = 0.f, largest = -200.f;   // largest: of the exponents so far
       for (int t = t0; t < t1; ++t) {
         const uint32_t n = first + (t - t0), ring = (u.g + (t - t0)) % kScaleRing;
         const int k0 = t * kKeys;
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         // not negative, and not 0, so that a masked column stays -inf
         auto factor = [&](int b) { return fmaxf(f * fabsf(ks[b]), 1e-37f); };
         auto exponent = [&](int b) { return (float)((int)(__float_as_uint(vs[b]) >> 23 & 255) - 127); };
-        float top = -INFINITY;                           // of x + ev
+        float top = -INFINITY, least = 200.f;            // of x + ev, of the tile's exponents
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float x[64];
@@ -299,14 +304,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
 #pragma unroll
             for (int j = 1; j < 16; ++j) m = fmaxf(m, x[16 * b + j]);
             top = fmaxf(top, fmaf(m, factor(half * 4 + b), exponent(half * 4 + b)));
+            largest = fmaxf(largest, exponent(half * 4 + b)), least = fminf(least, exponent(half * 4 + b));
           }
         }
         const bool over = top - kBoost > R + kSlack;
         if (__any_sync(0xffffffffu, over)) {
           const float Rn = over ? fmaxf(R, top - kBoost) : R;
-          const float c = R == Rn ? 1.f : ex2(R - Rn);
+          const float by = R == Rn ? 0.f : R - Rn, c = ex2(by);
           R = Rn;
-          sum *= c;
+          sum = add_scaled(0.f, sum, by);
           if (t > t0) {                                  // O is the products' until the tile before is done
             if (!wait(&bars.o_done[rt], n - 1)) {
               ok = false;
@@ -326,6 +332,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           }
         }
         const float Rs = R == -INFINITY ? 0.f : R;
+        if (least < largest - kFar) {                    // (the same for every row) rare: blocks far below
+#pragma unroll 1
+          for (int b = 0; b < kBlocks; b += 2) {
+            float x[32];
+            tmem_ld32(ts + b * 16, x);
+            tmem_wait_ld<32>(x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float fb = factor(b + e), ev = exponent(b + e);
+              const int cols = ks[b + e] < 0.f ? 0 : lim - k0 - 16 * (b + e);
+              float part = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) part += j < cols ? ex2(fmaf(x[16 * e + j], fb, ev - Rs + 100.f)) : 0.f;
+              if (ev < largest - kFar) sum = fmaf(part, ex2(-ev - 100.f), sum);
+            }
+          }
+        }
         // P takes the first 64 columns of S: its second half is written there only after S's is read
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -343,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
               part = f2_add(part, e);
               w[b * 8 + j] = f2_narrow<PI_DT_F16>(e);
             }
-            sum = fmaf(f2_sum(part), ex2(-ev), sum);
+            sum = fmaf(f2_sum(part), ev < largest - kFar ? 0.f : ex2(-ev), sum);
           }
           tmem_st32(ts + half * 32, w);
         }
