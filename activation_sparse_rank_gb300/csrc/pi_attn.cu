@@ -359,10 +359,11 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
           float w[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = ex2(fminf(m[nb][e] - R[nb][e] + ev, 100.f));
-            const float u = ex2(x[nb][e]), v = ex2(x[nb][2 + e]);
-            l[nb][e] += u + v;
-            w[e] = u * f, w[2 + e] = v * f;
+            // x <= 14 - shift, and shift <= 198 once a key has been seen (before that x is -inf and shift inf):
+            // of its own exponent, since 2^x is 0 where a weight of 2^(x + shift) still counts
+            const float shift = fminf(m[nb][e] - R[nb][e] + ev, 200.f);
+            l[nb][e] += ex2(x[nb][e]) + ex2(x[nb][2 + e]);
+            w[e] = ex2(x[nb][e] + shift), w[2 + e] = ex2(x[nb][2 + e] + shift);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j)

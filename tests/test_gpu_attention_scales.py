@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 # head dim and query rows a head of each kernel and row tile
 ROWS = [(64, 1), (64, 16), (128, 30), (256, 30), (64, 33), (96, 70), (128, 300)]
-ONE = 0x38                                           # a code
+ONE, MINUS_72 = 0x38, 0xe9                           # codes
 
 
 def check(c, b, q, out, lse, length, causal=False, scale=None):
@@ -77,3 +77,27 @@ def test_scales_over_their_whole_range(pi, dim, rows, length):
     q = queries(rows, 2, dim, "bfloat16", seed=2)
     out, lse = run(pi, c, b, q, [length])
     check(c, b, q, out, lse, length, causal=True)
+
+
+@pytest.mark.parametrize("dim,rows", ROWS)
+@pytest.mark.parametrize("length", [64, 2000])
+@pytest.mark.parametrize("order", ["large first", "large last"])
+def test_small_weights_of_large_values(pi, dim, rows, order, length):
+    """Weights of e^-72 on values of 2^104 beside weights of 1 on values of 1: both are of the result."""
+    length = max(length, rows)
+    b = batch([length - rows], [rows], 64)
+    c = random_cache(pi, b["pages"], 1, dim, 64)
+    n = -(-length // 16)
+    large = [(i < n // 2) == (order == "large first") for i in range(n)]
+    value_blocks(c, b, length, [ONE] * n, [104 if x else 0 for x in large])
+    c.k_codes.zero_()
+    c.k_scales.fill_(1.0)
+    for i in range(n):
+        if large[i]:
+            page, at = int(b["table"][0, i * 16 // 64]), i * 16 % 64
+            c.k_codes[page, :, at:at + 16, 0] = MINUS_72
+    q = torch.zeros(rows, 1, dim, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1
+    out, lse = run(pi, c, b, q, [length], causal=False, sm_scale=1.0)
+    check(c, b, q, out, lse, length, scale=1.0)
+    assert ((out > 1.5) & (out < 4)).all()
