@@ -59,7 +59,8 @@ class pi_kv_cache(C.Structure):
 
 
 class pi_kv_tokens(C.Structure):
-    _fields_ = [("n_seqs", _i32), ("n_tokens", _i32), ("cu", _p), ("page_table", _p), ("table_stride", _i32)]
+    _fields_ = [("n_seqs", _i32), ("n_tokens", _i32), ("cu", _p), ("page_table", _p), ("table_stride", _i32),
+                ("table_pages", _i32)]
 
 
 _SIG = {

@@ -661,7 +661,7 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
   const int group = q_heads / cache->heads;
   const AttnShape shape = attn_shape(cache->head_dim, (int64_t)max_q * group);
   const int rows = 8 * shape.nb * shape.warps_m;
-  const AttnParams p{*cache, *tokens, length, q, q_stride[0], q_stride[1], out, lse, static_cast<int4 *>(ws),
+  const AttnParams p{*cache, pi::with_pages(*tokens), length, q, q_stride[0], q_stride[1], out, lse, static_cast<int4 *>(ws),
                      reinterpret_cast<float *>(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1)),
                      sm_scale * kLog2e, q_heads, group, max_q, causal != 0,
                      (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb),

@@ -80,7 +80,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
   Seq q;
   const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1];
   const int n = r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens ? 0 : r1 - r0;
-  const int64_t cap = min((int64_t)p.tok.table_stride * p.c.page_size, (int64_t)1 << 30);
+  const int64_t cap = min((int64_t)p.tok.table_pages * p.c.page_size, (int64_t)1 << 30);
   const int len = p.length[s];
   q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group;
   q.len = len < 0 ? 0 : (int)min((int64_t)len, cap);
@@ -90,7 +90,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
 __device__ __forceinline__ void flag_seq(const AttnParams &p, int s) {
   const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1], len = p.length[s];
   if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens || r1 - r0 > p.max_q) atomicOr(p.c.status, pi::kKvBadRows);
-  if (len < 0 || len > (int64_t)p.tok.table_stride * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
+  if (len < 0 || len > (int64_t)p.tok.table_pages * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
 }
 // Keys that any row of a row tile (ROWS rows) sees, and the tiles (TILE keys) that hold them.
 template <int ROWS>

@@ -73,7 +73,7 @@ __device__ __forceinline__ bool kv_place(const KvCopyParams &p, int slot, KvPlac
   const int per = p.c.page_size / PI_KV_BLOCK;
   const int64_t pg = b / per;
   o->blk = (int)(b - pg * per);
-  *readable = pg < p.tok.table_stride;
+  *readable = pg < p.tok.table_pages;
   o->page = *readable ? p.tok.page_table[(int64_t)s * p.tok.table_stride + pg] : 0;
   if (*readable && (o->page < 0 || o->page >= p.c.n_pages)) {
     if ((threadIdx.x & 31) == 0) atomicOr(p.c.status, pi::kKvBadPage);
@@ -343,7 +343,8 @@ pi_status check_tokens(const pi_kv_tokens *t) {
     return fail(PI_ERR_INVALID_ARG, "n_seqs=%d or n_tokens=%d out of range", t->n_seqs, t->n_tokens);
   if (t->n_seqs && (!t->cu || !t->page_table || !aligned_to(t->cu, 4) || !aligned_to(t->page_table, 4)))
     return fail(PI_ERR_INVALID_ARG, "cu and page_table must be non-NULL and 4-byte aligned");
-  if (t->n_seqs && t->table_stride < 1) return fail(PI_ERR_INVALID_ARG, "table_stride=%d", t->table_stride);
+  if (t->n_seqs && (t->table_stride < 1 || t->table_pages < 0))
+    return fail(PI_ERR_INVALID_ARG, "table_stride=%d, table_pages=%d", t->table_stride, t->table_pages);
   return PI_OK;
 }
 
@@ -359,7 +360,7 @@ pi_status check_copy(const pi_kv_cache *c, const pi_kv_tokens *t, const int32_t 
   if (!pi::dtype_ok(dtype)) return pi::fail(PI_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   if (t->n_seqs && (!start || !pi::aligned_to(start, 4)))
     return pi::fail(PI_ERR_INVALID_ARG, "start must be non-NULL and 4-byte aligned");
-  *p = KvCopyParams{*c, *t, start, {}, {}, {}, {}, t->n_tokens / PI_KV_BLOCK + 2 * t->n_seqs, 1};
+  *p = KvCopyParams{*c, pi::with_pages(*t), start, {}, {}, {}, {}, t->n_tokens / PI_KV_BLOCK + 2 * t->n_seqs, 1};
   if ((int64_t)(p->n_slots + 1) * (2 * c->heads / 8 + 1) >= (int64_t)1 << 31)
     return pi::fail(PI_ERR_UNSUPPORTED, "n_tokens=%d with heads=%d is too large for one call", t->n_tokens, c->heads);
   return PI_OK;

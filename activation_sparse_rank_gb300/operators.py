@@ -161,8 +161,10 @@ class KVCache:
             _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
         if not _fits(per_seq, (n,), _i32, dev):
             _whole(per_seq, (n,), _i32, dev, name)
+        if pages == 0 and n:
+            raise ValueError("page_table must have a page for each sequence at least")
         # a table of one row may carry any stride for it
-        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(), stride if n > 1 else pages)
+        return pi_kv_tokens(n, n_tokens, cu.data_ptr(), page_table.data_ptr(), stride if n > 1 else pages, pages)
 
     def _rows(self, t, heads, name):
         """A [tokens, heads, head_dim] tensor with contiguous heads: its token and head strides."""

@@ -389,14 +389,16 @@ typedef struct {
  * call's packed token arrays.  Its position p lies in page
  * page_table[s * table_stride + p / page_size].  All device int32; entries of
  * a table row past the sequence's last page are not read.  A page outside
- * [0, n_pages), a position past table_stride pages, a negative position or a
+ * [0, n_pages), a position past table_pages pages, a negative position or a
  * cu that is not ascending within [0, n_tokens] is skipped and flagged in the
- * cache's status; the accesses stay in bounds. */
+ * cache's status; the accesses stay in bounds.  table_pages counts the entries
+ * of a row that are the table's (a table may be some columns of a wider one);
+ * 0 stands for table_stride. */
 typedef struct {
   int32_t n_seqs, n_tokens;
   const int32_t *cu;           /* [n_seqs + 1] */
-  const int32_t *page_table;   /* [n_seqs, table_stride] */
-  int32_t table_stride;
+  const int32_t *page_table;   /* [n_seqs, table_pages], rows table_stride entries apart */
+  int32_t table_stride, table_pages;
 } pi_kv_tokens;
 
 /* Quantise new keys and values into the cache.  Row cu[s] + i of k and v goes
