@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(256, D <= 128 && !AHEAD ? 4 : 2) k_kv_write(co
         codes[v] = encode8(f, f2_of(inv, inv));
       }
     }
+    __syncwarp();                                    // every lane has read the old scale
     if (lane == 0) *scale = s;
     if constexpr (AHEAD) {
 #pragma unroll
