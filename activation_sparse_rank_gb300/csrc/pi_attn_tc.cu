@@ -41,7 +41,10 @@ constexpr int kStages = 3;         // of codes, K and V of a tile in turn
 // From P_j = 0, so x_j + ev_j < R - 126, and ev_j >= ev - kFar for every ev so far it
 // follows that x_j is 38 or more below the largest x: its weight is nothing.
 constexpr float kFar = 94.f;
-constexpr int kScaleRing = 8;    // tiles whose scales are kept: copies run at most 5 tiles ahead of the softmax
+// Tiles whose scales and NaN are kept.  Copies run at most 5 tiles ahead of the first
+// softmax group, which every unit waits for; the second has no part in units of one
+// row tile, so the copies wait until it has read what it needs of a unit's last three.
+constexpr int kScaleRing = 8;
 
 // Shared-memory matrix descriptor, 128-byte swizzle: its low word holds the
 // address (and lbo), so a step of `bytes` adds bytes / 16 to it.
@@ -107,6 +110,7 @@ struct Bars {
   unsigned long long c_full[kStages], c_empty[kStages];                // codes: copied, widened
   unsigned long long k_full[2], k_empty[2], v_full, v_empty;           // fp16 tiles: written, used
   unsigned long long s_full[2], p_full[2], o_done[2], q_full[2];       // of a row tile: S ready, P ready, O of a tile done, Q of a unit written
+  unsigned long long read[2];                                          // the second row tile's group is done with a unit (in turn)
   unsigned long long drain;                                            // after a failure
 };
 
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
       bar_init(smem_addr(&bars.p_full[i]), 4);
       bar_init(smem_addr(&bars.o_done[i]), 1);
       bar_init(smem_addr(&bars.q_full[i]), 4);
+      bar_init(smem_addr(&bars.read[i]), 4);
     }
     bar_init(smem_addr(&bars.v_full), 4);
     bar_init(smem_addr(&bars.v_empty), 1);
@@ -438,6 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
       } else if (in && p.lse) {
         p.lse[orow] = sum == 0.f ? -INFINITY : ((R == -INFINITY ? 0.f : R) + log2f(sum)) * kLn2;
       }
+      if (rt) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&bars.read[u.index1 & 1]));
+      }
     });
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -533,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 12) {
+      uint32_t end1 = 0;                                 // tiles up to the end of the last unit with two row tiles
       units([&](const Unit &u) {
         // ================= tile copies; lane l looks after block l % 8 =================
         const int32_t *table = p.tok.page_table + (int64_t)u.s * p.tok.table_stride;
@@ -540,6 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         const int step = P % 64 ? 1 : 4;                 // boxes of 64 tokens where pages hold whole ones, else of 16
         for (int t = u.t0; t < u.t1; ++t) {
           const uint32_t gt = u.g + (t - u.t0), ring = gt % kScaleRing;
+          // Of the units with two row tiles before this one, all but the last are done with their tiles
+          // (a barrier for every other one, so that none is a phase ahead); the last with its last three
+          // where this tile takes their places.
+          if ((t == u.t0 && u.index1 >= 2 && !wait(&bars.read[u.index1 & 1], (u.index1 >> 1) - 1)) ||
+              (u.index1 >= 1 && gt == end1 + kScaleRing - 3 && !wait(&bars.read[(u.index1 - 1) & 1], (u.index1 - 1) >> 1))) {
+            ok = false;
+            return;
+          }
           const int k = t * kKeys + (lane & 7) * 16, cp = k / P, co = k - cp * P;
           const bool has = k < limit;
           const int page = has ? table[cp] : -1;
@@ -584,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             return;
           }
         }
+        if (u.two) end1 = u.g + (u.t1 - u.t0);
       });
     } else if (warp == 13) {
       const uint32_t id_s = idesc(kKeys, false), id_o = idesc(D, true);
