@@ -13,8 +13,9 @@
 //   L = sum 2^-ev_j P_j = sum 2^(x_j - R),  out = acc / L
 // with R + kBoost near the running maximum of x_j + ev_j (within kSlack): no
 // multiplication per element of K or V.  L has the range for any two scales (2^-64
-// to 2^120): its terms lie between 2^-149 and 2^80.  P_j does not, so a block whose
-// scale is far below the largest so far (kFar) adds 2^100 P_j to L instead.
+// to 2^120): its terms lie between 2^-149 and 2^80.  P_j does not: where a block's
+// scale is far below the largest so far (kFar), a pass of its own adds to L the terms
+// of those P_j that are 0.
 //
 // Roles (16 warps, one CTA an SM): 0-3 and 4-7 softmax of the two row tiles, a row
 // a thread; 8-11 converters, a token a thread; 12 tile copies and scales; 13 issues
@@ -40,7 +41,7 @@ constexpr int kThreads = 512;      // four warpgroups: register shares are set f
 constexpr int kStages = 3;         // of codes, K and V of a tile in turn
 // From P_j = 0, so x_j + ev_j < R - 126, and ev_j >= ev - kFar for every ev so far it
 // follows that x_j is 38 or more below the largest x: its weight is nothing.
-constexpr float kFar = 94.f;
+constexpr int kFar = 94;
 // Tiles whose scales and NaN are kept.  Copies run at most 5 tiles ahead of the first
 // softmax group, which every unit waits for; the second has no part in units of one
 // row tile, so the copies wait until it has read what it needs of a unit's last three.
@@ -268,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&bars.q_full[rt]));
       }
-      float R = -INFINITY, sum = 0.f, largest = -200.f;   // largest: of the exponents so far
+      float R = -INFINITY, sum = 0.f;
+      int largest = 0;                                   // exponent of the V scales so far (biased)
       for (int t = t0; t < t1; ++t) {
         const uint32_t n = first + (t - t0), ring = (u.g + (t - t0)) % kScaleRing;
         const int k0 = t * kKeys;
@@ -281,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         // (a bad page, past the sequence) are masked too.
         const float *ks = scales[ring][0], *vs = scales[ring][1];
         const bool masked = k0 + kKeys > min_lim || tile_bad[ring];
+        const int own = (int)(__float_as_uint(vs[lane & 7]) >> 23 & 255);
+        largest = max(largest, __reduce_max_sync(0xffffffffu, own));
+        const bool far = __any_sync(0xffffffffu, own < largest - kFar);      // rare
         auto load = [&](float *x, int half) {
           tmem_ld32(ts + half * 64, x);
           tmem_ld32(ts + half * 64 + 32, x + 32);
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         // not negative, and not 0, so that a masked column stays -inf
         auto factor = [&](int b) { return fmaxf(f * fabsf(ks[b]), 1e-37f); };
         auto exponent = [&](int b) { return (float)((int)(__float_as_uint(vs[b]) >> 23 & 255) - 127); };
-        float top = -INFINITY, least = 200.f;            // of x + ev, of the tile's exponents
+        float top = -INFINITY;                           // of x + ev
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float x[64];
@@ -309,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
 #pragma unroll
             for (int j = 1; j < 16; ++j) m = fmaxf(m, x[16 * b + j]);
             top = fmaxf(top, fmaf(m, factor(half * 4 + b), exponent(half * 4 + b)));
-            largest = fmaxf(largest, exponent(half * 4 + b)), least = fminf(least, exponent(half * 4 + b));
           }
         }
         const bool over = top - kBoost > R + kSlack;
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           }
         }
         const float Rs = R == -INFINITY ? 0.f : R;
-        if (least < largest - kFar) {                    // (the same for every row) rare: blocks far below
+        if (far) {
 #pragma unroll 1
           for (int b = 0; b < kBlocks; b += 2) {
             float x[32];
@@ -345,12 +349,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             tmem_wait_ld<32>(x);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float fb = factor(b + e), ev = exponent(b + e);
+              const float fb = factor(b + e), ev = exponent(b + e), bias = ev - Rs;
               const int cols = ks[b + e] < 0.f ? 0 : lim - k0 - 16 * (b + e);
               float part = 0.f;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) part += j < cols ? ex2(fmaf(x[16 * e + j], fb, ev - Rs + 100.f)) : 0.f;
-              if (ev < largest - kFar) sum = fmaf(part, ex2(-ev - 100.f), sum);
+              for (int j = 0; j < 16; ++j) {
+                const float z = fmaf(x[16 * e + j], fb, bias);       // as below, where 2^z is 0 from -126 down
+                part += j < cols && z < -126.f ? ex2(z + 100.f) : 0.f;
+              }
+              if (ev < (float)(largest - 127 - kFar)) sum = fmaf(part, ex2(-ev - 100.f), sum);
             }
           }
         }
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
               part = f2_add(part, e);
               w[b * 8 + j] = f2_narrow<PI_DT_F16>(e);
             }
-            sum = fmaf(f2_sum(part), ev < largest - kFar ? 0.f : ex2(-ev), sum);
+            sum = fmaf(f2_sum(part), ex2(-ev), sum);
           }
           tmem_st32(ts + half * 32, w);
         }
