@@ -235,9 +235,19 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvCopyParams p) {
   using E = Elem<DT>;
   constexpr int VR = D / 8, NV = PI_KV_BLOCK * VR / 32, W = 16 / sizeof(typename E::T);
   kv_check_cu(p);
-  // rows of no sequence
-  const int r0 = max(0, min(p.tok.n_tokens, p.tok.n_seqs ? p.tok.cu[0] : p.tok.n_tokens));
-  const int r1 = max(r0, min(p.tok.n_tokens, p.tok.n_seqs ? p.tok.cu[p.tok.n_seqs] : p.tok.n_tokens));
+  // rows of no sequence: below every entry of cu, and from the largest on
+  int r0 = p.tok.n_seqs ? p.tok.cu[0] : p.tok.n_tokens, r1 = p.tok.n_seqs ? p.tok.cu[p.tok.n_seqs] : p.tok.n_tokens;
+  if (p.tok.n_seqs && (r0 > 0 || r1 < p.tok.n_tokens)) {             // the ends alone do not say so where cu does not ascend
+    __shared__ int least, most;
+    if (threadIdx.x == 0) least = r0, most = r1;
+    __syncthreads();
+    for (int s = threadIdx.x; s <= p.tok.n_seqs; s += blockDim.x) r0 = min(r0, p.tok.cu[s]), r1 = max(r1, p.tok.cu[s]);
+    r0 = __reduce_min_sync(0xffffffffu, r0), r1 = __reduce_max_sync(0xffffffffu, r1);
+    if ((threadIdx.x & 31) == 0) atomicMin(&least, r0), atomicMax(&most, r1);
+    __syncthreads();
+    r0 = least, r1 = most;
+  }
+  r0 = max(0, min(p.tok.n_tokens, r0)), r1 = max(r0, min(p.tok.n_tokens, r1));
   const int64_t per_row = (int64_t)p.c.heads * D / W;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (r0 + (p.tok.n_tokens - r1)) * per_row;
        i += (int64_t)gridDim.x * blockDim.x) {

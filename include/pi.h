@@ -391,7 +391,8 @@ typedef struct {
  * a table row past the sequence's last page are not read.  A page outside
  * [0, n_pages), a position past table_pages pages, a negative position or a
  * cu that is not ascending within [0, n_tokens] is skipped and flagged in the
- * cache's status; the accesses stay in bounds.  table_pages counts the entries
+ * cache's status; the accesses stay in bounds.  (Where cu does not ascend,
+ * writing and reading may skip other sequences of the call too.)  table_pages counts the entries
  * of a row that are the table's (a table may be some columns of a wider one);
  * 0 stands for table_stride. */
 typedef struct {
@@ -420,7 +421,8 @@ pi_status pi_kv_write(const pi_kv_cache *cache, const pi_kv_tokens *tokens, cons
 /* Read positions start[s] .. start[s] + (cu[s+1] - cu[s]) of each sequence back
  * as k, v [n_tokens, heads, head_dim] of `dtype`, contiguous, 16-byte aligned
  * (either may be NULL).  Rows that cannot be read (a bad page or position) and
- * rows of no sequence are zero; rows of a bad cu range are left as they were. */
+ * rows of no sequence (below every entry of cu, or from the largest on) are
+ * zero; rows of a bad cu range are left as they were. */
 pi_status pi_kv_read(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
                      void *k, void *v, int32_t dtype, void *stream);
 
