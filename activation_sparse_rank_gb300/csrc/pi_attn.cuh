@@ -75,6 +75,7 @@ __device__ __forceinline__ unsigned pack_half2(float lo, float hi) {
 // Sequence s as the kernels see it: lengths made safe, faults flagged by flag_seq.
 struct Seq {
   int row0, n, rows, len, first;    // packed row, query tokens used, query rows, keys, position of the first token
+  int left;                         // tokens past max_q
 };
 __device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
   Seq q;
@@ -82,7 +83,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams &p, int s) {
   const int n = r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens ? 0 : r1 - r0;
   const int64_t cap = min((int64_t)p.tok.table_pages * p.c.page_size, (int64_t)1 << 30);
   const int len = p.length[s];
-  q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group;
+  q.row0 = r0, q.n = min(n, p.max_q), q.rows = q.n * p.group, q.left = n - q.n;
   q.len = len < 0 ? 0 : (int)min((int64_t)len, cap);
   q.first = (len < 0 ? 0 : len) - n;
   return q;
@@ -247,7 +248,7 @@ struct AttnMaps {          // [n_pages heads][page_size][D] codes, boxes of 64 o
 // 16 warps over rows of a unit is an item; a few CTAs an SM take all items, which
 // the plan's prefix sums find (a CTA for each share and four rows instead: 60 us
 // for attention of 128 query heads over 130001 keys, 48 so, as most had no work).
-// Rows of units without keys: 0 and -inf.
+// Rows of units without keys, and of tokens past max_q: 0 and -inf.
 constexpr int kCombineThreads = 512, kMostShares = 1024;
 constexpr int combine_ctas(int D) { return D <= 128 ? 3 : 2; }     // that an SM holds
 __host__ __device__ constexpr int combine_split(int parts) { return parts > 64 ? 16 : parts > 8 ? 4 : 1; }
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(kCombineThreads, combine_ctas(D)) k_attn_combi
       for (int rt = 0; rt < p.row_tiles && rt * ROWS < sq.rows && unit_tiles<ROWS, TILE>(p, sq, rt) == 0; ++rt) rows = min(sq.rows, (rt + 1) * ROWS);
       return rows;
     };
-    if (!__syncthreads_or(s0 + (int)threadIdx.x < p.tok.n_seqs && blank(load_seq(p, s0 + threadIdx.x)))) continue;
+    auto any = [&](const Seq &sq) { return sq.left > 0 || blank(sq) > 0; };
+    if (!__syncthreads_or(s0 + (int)threadIdx.x < p.tok.n_seqs && any(load_seq(p, s0 + threadIdx.x)))) continue;
     for (int s = s0; s < min(p.tok.n_seqs, s0 + kCombineThreads); ++s) {
       const Seq sq = load_seq(p, s);
       const int rows = blank(sq);
@@ -278,6 +280,11 @@ __global__ void __launch_bounds__(kCombineThreads, combine_ctas(D)) k_attn_combi
         if (r >= n && (r - n) % p.group >= rest) continue;
         reinterpret_cast<uint4 *>(p.out)[(first + r) * (D / 8) + i % (D / 8)] = make_uint4(0, 0, 0, 0);
         if (p.lse && i % (D / 8) == 0) p.lse[first + r] = -INFINITY;
+      }
+      const int64_t past = first + (int64_t)sq.n * p.q_heads;
+      for (int64_t i = blockIdx.x * kCombineThreads + threadIdx.x; i < (int64_t)sq.left * p.q_heads * (D / 8); i += gridDim.x * kCombineThreads) {
+        reinterpret_cast<uint4 *>(p.out)[past * (D / 8) + i] = make_uint4(0, 0, 0, 0);
+        if (p.lse && i % (D / 8) == 0) p.lse[past + i / (D / 8)] = -INFINITY;
       }
     }
   }

@@ -217,18 +217,27 @@ class KVCache:
             raise PiError(1, "pi_kv_attention_workspace_bytes")
         return torch.empty(n, dtype=_u8, device=self.device)
 
-    def attention(self, q, page_table, cu_tokens, length, max_q=1, sm_scale=None, causal=True, out=None, lse=None,
+    def attention(self, q, page_table, cu_tokens, length, max_q=None, sm_scale=None, causal=True, out=None, lse=None,
                   want_lse=False, ws=None, stream=None):
         """Attention of each sequence's newest tokens q [tokens, q_heads, head_dim]
         (float16 or bfloat16) over its cache.  length[s] counts the tokens in the
-        cache, the new ones among them; max_q bounds the new tokens of any
-        sequence.  Returns out, or (out, lse) with want_lse or an lse tensor."""
+        cache, the new ones among them.  max_q bounds the new tokens of any
+        sequence and is best given: by default it is 1 where q has no more rows
+        than there are sequences, else all of q's rows, and the kernels are
+        chosen by it.  Rows past max_q get 0 (lse -inf) and show in
+        ``device_status``; rows of no sequence are left as they were (unset in
+        an ``out`` made here).  Returns out, or (out, lse) with want_lse or an
+        lse tensor."""
         heads = q.shape[1] if q.dim() == 3 else 0
         qs = self._rows(q, heads, "q")
         if q.dtype is not torch.float16 and q.dtype is not torch.bfloat16:
             raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
         tok = self._tokens(page_table, cu_tokens, length, "length", q.shape[0])
         scale = self._scale if sm_scale is None else sm_scale
+        if max_q is None:
+            max_q = 1 if tok.n_tokens <= tok.n_seqs else tok.n_tokens
+        elif max_q == 0:
+            max_q = 1                                # the library would leave every row as it is, unlooked at
         if stream is None and _current_device() == self._index:
             return self._attention(_raw_stream(self._index), tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
         return _on(self.device, stream, self._attention, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)

@@ -437,7 +437,8 @@ pi_status pi_kv_read(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const
  *           (strides multiples of 8 elements, base 16-byte aligned)
  *   length  device int32 [n_seqs], tokens of the sequence in the cache, the new
  *           ones among them
- *   max_q   host: at least the largest n_s (rows past it are left out and flagged)
+ *   max_q   host: at least the largest n_s (rows past it get out 0 and lse -inf,
+ *           and are flagged)
  *   out     [n_tokens, q_heads, head_dim] of q's type, contiguous, 16-byte aligned
  *   lse     fp32 [n_tokens, q_heads] or NULL
  *   ws      pi_kv_attention_workspace_bytes(...) bytes, 16-byte aligned scratch
