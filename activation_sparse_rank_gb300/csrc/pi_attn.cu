@@ -651,13 +651,13 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
     return pi::fail(PI_ERR_INVALID_ARG, "q's strides must be multiples of 8 elements");
   if (!pi::aligned_to(length, 4) || !pi::aligned_to(lse, 4))
     return pi::fail(PI_ERR_INVALID_ARG, "length and lse must be 4-byte aligned");
+  max_q = std::min(max_q, tokens->n_tokens);
   if ((int64_t)cache->n_pages * cache->heads >= (int64_t)1 << 31 ||
       (int64_t)tokens->n_seqs * cache->heads >= (int64_t)1 << 31 || (int64_t)max_q * (q_heads / cache->heads) >= 1 << 30)
     return pi::fail(PI_ERR_UNSUPPORTED, "n_pages x heads, n_seqs x heads or max_q x q_heads / heads is too large");
   const size_t need = pi_kv_attention_workspace_bytes(cache, q_heads, tokens->n_tokens, tokens->n_seqs);
   if (!ws || !pi::aligned_to(ws, 16) || ws_bytes < need)
     return pi::fail(PI_ERR_INVALID_ARG, "ws must be 16-byte aligned and hold %zu bytes, has %zu", need, ws_bytes);
-  max_q = std::min(max_q, tokens->n_tokens);
   const int group = q_heads / cache->heads;
   const AttnShape shape = attn_shape(cache->head_dim, (int64_t)max_q * group);
   const int rows = 8 * shape.nb * shape.warps_m;
