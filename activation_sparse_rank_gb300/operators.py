@@ -176,6 +176,10 @@ class KVCache:
         st, sh, sd = t.stride()
         if sd != 1:
             raise ValueError(f"{name}: the elements of a head must be contiguous")
+        if shape[0] <= 1:                            # the stride of a single row may be anything, and no copy changes it
+            st = heads * self.head_dim
+        if heads == 1:
+            sh = self.head_dim
         return _Stride2(st, sh)
 
     def write(self, k, v, page_table, cu_tokens, start, stream=None):
