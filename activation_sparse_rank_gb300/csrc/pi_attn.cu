@@ -27,8 +27,9 @@
 //
 // Measured: 64 sequences of up to 8191 tokens, 64 bf16 heads of 128 on 8: 113 us (4.9
 // TB/s, 73% of the copy rate; 100 us of it are left without any arithmetic: launch,
-// units' beginnings and ends); 128 fp16 heads of 64 on 8 over 130001 tokens: 47 us (42%;
-// 380 instructions for 16 tokens x 16 rows, issue slots half full); 16 heads of 64 over
+// units' beginnings and ends); 128 fp16 heads of 64 on 8 over 130001 tokens: 48 us (41%;
+// 380 instructions for 16 tokens x 16 rows, issue slots half full; the variant of 16 rows
+// of 64 dims spills 48 bytes at four CTAs an SM, that of 8 rows of 128 dims 36); 16 heads of 64 over
 // 513 tokens: 11 us, the latency of two launches and one pass.
 #include "pi_attn.cuh"
 
@@ -552,7 +553,7 @@ struct AttnShape {
 };
 // Rows of a row tile: the fewest eights that hold all query rows of a head
 // while a warp's registers can (16 rows, 8 of 256 dims); above, two warps of that
-// share a tile of keys (32 rows with two instead of four: 105 -> 73 us at 8 x 8192
+// share a tile of keys (32 rows with two instead of four: 105 -> 66 us at 8 x 8192
 // keys x 8 heads of 128), of 256 dims up to four.
 AttnShape attn_shape(int D, int64_t max_rows) {
   const int nb_max = D <= 128 ? 2 : 1;
@@ -593,9 +594,9 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
 
 // From how many query rows a head on the tcgen05 kernel (row tiles of 128, each
 // tile of keys widened once for them) is taken.  48 rows of 8 sequences x 8192 keys
-// x 8 heads of 128: 80 us there, 105 us with four warps of 16 rows here; of one
-// sequence of 3000 keys 24 and 32 us; of 64 sequences of 300 keys 70 and 58 us.
-// 32 rows with two warps of 16 rows here: 73, 24 and 49 us (there 79, 23 and 68).
+// x 8 heads of 128: 79 us there, 105 us with four warps of 16 rows here; of one
+// sequence of 3000 keys 24 and 32 us; of 64 sequences of 300 keys 68 and 58 us.
+// 32 rows with two warps of 16 rows here: 66, 21 and 48 us (there 79, 23 and 68).
 bool many_rows(int D, int64_t rows) { return D <= 128 && rows > 32; }
 
 template <int DT>

@@ -25,7 +25,8 @@
 // The line of tiles is cut evenly over the CTAs as in pi_attn.cu.
 //
 // Measured: chunks of up to 512 tokens over caches of up to 8190, 64 bf16 heads of 128
-// on 8: 374 us (900 TFLOP/s, 46% of the dense bf16 rate).  A pair of row tiles takes
+// on 8: 377 us (895 TFLOP/s, 45% of the dense bf16 rate; 128 dims of bf16 spill 162 bytes
+// a thread, fp16 132).  A pair of row tiles takes
 // 4650 clocks a tile of keys, of which the products hold the tensor pipe for 3230; a
 // row tile's softmax, a row a thread, takes 2760.  Tried and slower: one pass of the
 // softmax over registers (538 us), both groups on one row tile's tiles of keys in turn

@@ -11,7 +11,7 @@
 // (block, head, key or value): it alone reads and writes that block, so the
 // scale needs no atomics and no second pass.
 //
-// Measured: prompts of 30005 tokens in all x 8 heads x 128, bf16, 33 us (4.7 TB/s,
+// Measured: prompts of 30005 tokens in all x 8 heads x 128, bf16, 34 us (4.6 TB/s,
 // 69% of the copy rate: a warp's chain of place, rows, maximum, codes is longer
 // than 16 warps an SM with two blocks each hide); 60015 tokens x 8 x 64 read back 26 us (5.6 TB/s, 83%);
 // one token of 32 sequences x 32 heads 5.2 us.
@@ -136,8 +136,9 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 // lane + 32 i to a lane.
 // AHEAD: a warp with several units loads the next one while it quantises one, at two
 // CTAs an SM (write of the prompts above: 34 us, 38 without it at four, 57 at two).
-// Otherwise registers for four CTAs (five spill: 50 us; 256 dims hold twice as many
-// rows a lane).
+// Otherwise registers for four CTAs (five: 50 us; 256 dims hold twice as many rows a
+// lane).  Those of 64 dims do not spill; of more dims 16-bit rows spill up to 152 bytes
+// a thread, binary32 rows up to 540.
 template <int DT, int D, bool VEC, bool AHEAD>
 __global__ void __launch_bounds__(256, D <= 128 && !AHEAD ? 4 : 2) k_kv_write(const KvCopyParams p) {
   using E = Elem<DT>;

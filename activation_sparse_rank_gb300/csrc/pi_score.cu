@@ -14,9 +14,9 @@
 // the k-th largest of all.  Elements at or above that bound are few; they are
 // ranked by counting.
 //
-// Measured: 2048 x 131072 bf16, 20 alternatives, 105 us (5.1 TB/s, 76% of the copy rate;
+// Measured: 2048 x 131072 bf16, 20 alternatives, 107 us (5.0 TB/s, 75% of the copy rate;
 // 90 us without alternatives; 608 CTAs take three or four rows each); 16 x 50007
-// binary32, 5 alternatives, 6.9 us.
+// binary32, 5 alternatives, 7.2 us.
 #include "pi_ops.cuh"
 
 #include <algorithm>

@@ -9,6 +9,9 @@ each operator's formula, limits and treatment of special values.
 that the caller does not supply are allocated on the stream the call runs on;
 inputs made on another stream have to be ordered before it by the caller, and
 must not be freed before it has passed, as with every torch operator.
+
+The calls are not known to autograd: an output never requires grad, whatever
+the inputs do.  ``layer_norm_backward`` is called by hand.
 """
 from __future__ import annotations
 
@@ -228,7 +231,7 @@ class KVCache:
         cache, the new ones among them.  max_q bounds the new tokens of any
         sequence and is best given: by default it is 1 where q has no more rows
         than there are sequences, else all of q's rows, and the kernels are
-        chosen by it.  Rows past max_q get 0 (lse -inf) and show in
+        chosen by it (single tokens and a long prompt: two calls).  Rows past max_q get 0 (lse -inf) and show in
         ``device_status``; rows of no sequence are left as they were (unset in
         an ``out`` made here).  Returns out, or (out, lse) with want_lse or an
         lse tensor."""
