@@ -23,11 +23,15 @@ from .binding import (  # noqa: F401
 from .operators import (  # noqa: F401
     PI_KV_BLOCK,
     PI_KV_MAX_PAGE,
+    PI_MAX_ROTARY,
     PI_MAX_TOP_K,
     KVCache,
+    Rotary,
     TokenScores,
     layer_norm,
     layer_norm_backward,
+    rotary,
+    rotary_backward,
     token_logprobs,
 )
 
@@ -35,6 +39,7 @@ __all__ = [
     "KVCache",
     "Layer",
     "PiError",
+    "Rotary",
     "TokenScores",
     "PI_ACT_RELU",
     "PI_ACT_REGLU",
@@ -42,6 +47,7 @@ __all__ = [
     "PI_KV_BLOCK",
     "PI_KV_MAX_PAGE",
     "PI_MAX_BATCH",
+    "PI_MAX_ROTARY",
     "PI_MAX_TOP_K",
     "PI_STACK_LAYERS_PER_LAUNCH",
     "hot_first_perm",
@@ -50,6 +56,8 @@ __all__ = [
     "lib",
     "lib_path",
     "profile_activations",
+    "rotary",
+    "rotary_backward",
     "stack_forward",
     "stack_forward_host",
     "token_logprobs",

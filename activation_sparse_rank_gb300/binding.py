@@ -41,6 +41,7 @@ PI_DT_F32 = 2
 PI_KV_BLOCK = 16
 PI_KV_MAX_PAGE = 256
 PI_MAX_TOP_K = 64
+PI_MAX_ROTARY = 512
 
 _p = C.c_void_p
 _i32 = C.c_int32
@@ -51,6 +52,10 @@ class pi_layer_desc(C.Structure):
     _fields_ = [("d", _i32), ("ffn", _i32), ("rank", _i32), ("act", _i32),
                 ("W_up", _p), ("W_gate", _p), ("b", _p), ("W_down", _p),
                 ("W_p1", _p), ("W_p2", _p), ("c_p", _p), ("row_format", _i32)]
+
+
+class pi_rotary(C.Structure):
+    _fields_ = [("dim", _i32), ("interleaved", _i32), ("magnitude", C.c_float), ("turns", _p)]
 
 
 class pi_kv_cache(C.Structure):
@@ -87,6 +92,8 @@ _SIG = {
     "pi_forward_launches": (C.c_int32, [_p, _i32]),
     "pi_layer_set_hot_count": (C.c_int, [_p, _i32]),
     "pi_kv_write": (C.c_int, [_p, _p, _p, _p, _p, _p, _p, _i32, _p]),
+    "pi_rotary_apply": (C.c_int, [_p, _p, _i32, _i32, _i32, _p, _p, _p, _p, _i32, _i32, _p]),
+    "pi_kv_append": (C.c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i32, _p, _i32, _p]),
     "pi_kv_read": (C.c_int, [_p, _p, _p, _p, _p, _i32, _p]),
     "pi_kv_attention_workspace_bytes": (C.c_size_t, [_p, _i32, _i32, _i32]),
     "pi_kv_attention": (C.c_int, [_p, _p, _p, _i32, _p, _p, _i32, _i32, C.c_float, _i32, _p, _p, _p, C.c_size_t, _p]),

@@ -1,7 +1,8 @@
 """The operators around the FFN block, as Python calls on torch tensors.
 
-``KVCache`` (a paged key/value cache in E4M3 codes: ``write``, ``read``,
-``attention``), ``layer_norm`` with ``layer_norm_backward``, and
+``KVCache`` (a paged key/value cache in E4M3 codes: ``write``, ``append``,
+``read``, ``attention``), ``rotary`` with ``rotary_backward`` (positions by a
+``Rotary``), ``layer_norm`` with ``layer_norm_backward``, and
 ``token_logprobs``.  Argument checks and marshalling only; include/pi.h states
 each operator's formula, limits and treatment of special values.
 
@@ -11,21 +12,22 @@ inputs made on another stream have to be ordered before it by the caller, and
 must not be freed before it has passed, as with every torch operator.
 
 The calls are not known to autograd: an output never requires grad, whatever
-the inputs do.  ``layer_norm_backward`` is called by hand.
+the inputs do.  ``layer_norm_backward`` and ``rotary_backward`` are called by hand.
 """
 from __future__ import annotations
 
 import ctypes as C
 import math
+from fractions import Fraction
 from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import (PI_DT_BF16, PI_DT_F16, PI_DT_F32, PI_KV_BLOCK, PI_KV_MAX_PAGE, PI_MAX_TOP_K, PiError, _check,
-                      lib, pi_kv_cache, pi_kv_tokens)
+from .binding import (PI_DT_BF16, PI_DT_F16, PI_DT_F32, PI_KV_BLOCK, PI_KV_MAX_PAGE, PI_MAX_ROTARY, PI_MAX_TOP_K, PiError,
+                      _check, lib, pi_kv_cache, pi_kv_tokens, pi_rotary)
 
-__all__ = ["KVCache", "TokenScores", "layer_norm", "layer_norm_backward", "token_logprobs", "PI_KV_BLOCK",
-           "PI_KV_MAX_PAGE", "PI_MAX_TOP_K"]
+__all__ = ["KVCache", "Rotary", "TokenScores", "layer_norm", "layer_norm_backward", "rotary", "rotary_backward",
+           "token_logprobs", "PI_KV_BLOCK", "PI_KV_MAX_PAGE", "PI_MAX_ROTARY", "PI_MAX_TOP_K"]
 
 _DT = {torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16, torch.float32: PI_DT_F32}
 _Stride2 = C.c_int64 * 2
@@ -100,6 +102,137 @@ def _ws(ws: torch.Tensor, device) -> int:
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
     return ws.numel() * ws.element_size()
+
+
+# 1 / (2 pi): frequencies as fractions of a turn are right to their last bit
+_TURNS_PER_RADIAN = Fraction("0.1591549430918953357688837633725143620344596457404564487476673440588967976342")
+
+
+def _frequencies(dim, base, scaling, factor, original_length, beta_fast, beta_slow, magnitude, inv_freq):
+    """Radians a position of each pair, and the magnitude (see ``Rotary``)."""
+    if dim < 2 or dim % 2 or dim > PI_MAX_ROTARY:
+        raise ValueError(f"dim must be an even number up to {PI_MAX_ROTARY}, not {dim}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', not {scaling!r}")
+    if not (1.0 < base < math.inf and 0.0 < factor < math.inf):
+        raise ValueError(f"base must be above 1 and factor above 0, both finite, not {base} and {factor}")
+    if inv_freq is not None:
+        if scaling is not None:
+            raise ValueError("inv_freq and scaling exclude each other")
+        freq = [float(f) for f in inv_freq]
+        if len(freq) != dim // 2 or not all(math.isfinite(f) for f in freq):
+            raise ValueError(f"inv_freq must be {dim // 2} finite numbers")
+    else:
+        if scaling == "ntk" and dim > 2:
+            base = base * factor ** (dim / (dim - 2))
+        freq = [base ** (-2 * i / dim) for i in range(dim // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    if scaling == "yarn":
+        if original_length is None or original_length < 1 or not 0 < beta_slow <= beta_fast:
+            raise ValueError("'yarn' needs original_length of at least 1 and 0 < beta_slow <= beta_fast")
+
+        def pair_of(turns):                      # the pair that makes so many turns over original_length
+            return dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+        lo, hi = max(0, math.floor(pair_of(beta_fast))), min(dim - 1, math.ceil(pair_of(beta_slow)))
+        ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(dim // 2)]
+        freq = [f * (1 - r) + f / factor * r for f, r in zip(freq, ramp)]
+        if magnitude is None and factor > 1:
+            magnitude = 0.1 * math.log(factor) + 1.0
+    magnitude = 1.0 if magnitude is None else float(magnitude)
+    if not math.isfinite(magnitude):
+        raise ValueError("magnitude must be finite")
+    return freq, magnitude
+
+
+class Rotary:
+    """Rotary positions: frequencies of the dim / 2 pairs of a head's first
+    ``dim`` elements, kept on the device as exact fractions of a turn.
+
+    Pair i is the elements (2i, 2i + 1) where ``interleaved``, else (i, i + dim / 2);
+    it turns by base^(-2i / dim) radians a position.  ``scaling`` stretches the
+    frequencies for contexts ``factor`` times longer:
+      "linear"  every frequency divided by factor
+      "ntk"     base raised by factor^(dim / (dim - 2)): the slowest pair is divided by factor, the fastest keeps its own
+      "yarn"    pairs that make fewer than beta_slow turns over original_length positions are divided by factor, those of
+                more than beta_fast keep their own, a ramp between; results times magnitude, by default 0.1 ln(factor) + 1
+    ``inv_freq`` (dim / 2 numbers, radians a position) replaces all of these.
+    ``magnitude`` multiplies the turned elements (default 1, but for "yarn").
+    """
+
+    def __init__(self, dim, base=10000.0, interleaved=False, scaling=None, factor=1.0, original_length=None, beta_fast=32.0,
+                 beta_slow=1.0, magnitude=None, inv_freq=None, device="cuda"):
+        freq, magnitude = _frequencies(dim, base, scaling, factor, original_length, beta_fast, beta_slow, magnitude, inv_freq)
+        turns = [round(Fraction(f) * _TURNS_PER_RADIAN * (1 << 64)) % (1 << 64) for f in freq]
+        self.dim, self.interleaved, self.magnitude, self.inv_freq = dim, bool(interleaved), magnitude, freq
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.device = _dev(self.turns, None, "device")
+        self._c = pi_rotary(dim, int(self.interleaved), magnitude, self.turns.data_ptr())
+        self._ref = C.addressof(self._c)
+
+
+def _heads3(t, device, name):
+    """Strides of a [tokens, heads, head_dim] tensor with contiguous heads; those of single tokens and heads may be anything."""
+    if not isinstance(t, _Tensor) or t.device != device:
+        _dev(t, device, name)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return _Stride2(st if n > 1 else h * d, sh if h > 1 else d)
+
+
+def _places(positions, n, device):
+    if not _fits(positions, (n,), _i32, device):
+        _whole(positions, (n,), _i32, device, "positions")
+
+
+def _turn(x, positions, rope, out, inverse, stream, name):
+    dev = rope.device
+    xs = _heads3(x, dev, name)
+    dt = _dt(x, name)
+    n = x.shape[0]
+    _places(positions, n, dev)
+    if out is not None:
+        if not isinstance(out, _Tensor) or out.shape != x.shape or out.dtype is not x.dtype:
+            raise ValueError(f"the output must be {tuple(x.shape)} {x.dtype}")
+        if out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
+            os = _heads3(out, dev, "the output")     # rows may lie apart, but not in one another
+            d, (t, h) = x.shape[2], sorted(((os[0], n), (os[1], x.shape[1])))
+            if x.numel() and (t[0] < d and t[1] > 1 or h[0] < (t[1] - 1) * t[0] + d and h[1] > 1):
+                raise ValueError("the output's elements share memory")
+    if stream is None and _current_device() == dev.index:
+        return _rotary(_raw_stream(dev.index), x, xs, positions, rope, out, inverse, dt)
+    return _on(dev, stream, _rotary, x, xs, positions, rope, out, inverse, dt)
+
+
+def _rotary(handle, x, xs, positions, rope, out, inverse, dt):
+    n, h, d = x.shape
+    if out is None:
+        out = _empty((n, h, d), dtype=x.dtype, device=rope.device)
+        ys = _Stride2(h * d, d)
+    else:
+        ys = _heads3(out, rope.device, "the output")
+    if h:
+        _check(lib.pi_rotary_apply(rope._ref, positions.data_ptr(), n, h, d, x.data_ptr(), xs, out.data_ptr(), ys, dt, inverse,
+                                   handle), "pi_rotary_apply")
+    return out
+
+
+def rotary(x, positions, rope, out=None, stream=None):
+    """x [tokens, heads, head_dim] with the pairs of ``rope`` turned by positions
+    (int32 [tokens]); elements past rope.dim as they are.  Queries and keys that lie
+    side by side are one call.  ``out`` may be x (in place), or any tensor of x's shape
+    and type with contiguous heads that shares no memory with x."""
+    return _turn(x, positions, rope, out, 0, stream, "x")
+
+
+def rotary_backward(dy, positions, rope, dx=None, stream=None):
+    """Gradient of ``rotary`` with respect to x: dy turned the other way (times the
+    magnitude as well).  ``dx`` may be dy."""
+    return _turn(dy, positions, rope, dx, 1, stream, "dy")
 
 
 class KVCache:
@@ -201,6 +334,50 @@ class KVCache:
     def _write(self, handle, tok, start, k, ks, v, vs, dt):
         _check(lib.pi_kv_write(self._ref, C.addressof(tok), start.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, dt,
                                handle), "pi_kv_write")
+
+    def append(self, k, v, page_table, cu_tokens, start, rope, positions=None, q=None, q_out=None, stream=None):
+        """``write`` with the keys turned by ``rope`` (rope.dim a multiple of 16) on the
+        way, from binary32, and the same tokens' queries q [tokens, q_heads, head_dim]
+        turned in the same launch.  Row cu_tokens[s] + i is turned by
+        positions[cu_tokens[s] + i] (int32 [tokens]), by default start[s] + i; its place
+        in the cache is start[s] + i either way.  Returns the turned queries, or None
+        without q; q_out may be q itself (contiguous).  Rows of no sequence are left as
+        they were (unset in a q_out made here)."""
+        ks, vs = self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v")
+        if v.shape != k.shape or v.dtype is not k.dtype:
+            raise ValueError("k and v must have one shape and type")
+        if not isinstance(rope, Rotary):
+            raise TypeError("rope must be a Rotary")
+        if rope.device != self.device:
+            raise ValueError(f"rope is on {rope.device}, not {self.device}")
+        tok = self._tokens(page_table, cu_tokens, start, "start", k.shape[0])
+        dt = _dt(k, "k")
+        qs = None
+        if q is not None:
+            qs = self._rows(q, q.shape[1] if q.dim() == 3 else 0, "q")
+            if q.shape[0] != k.shape[0] or q.dtype is not k.dtype:
+                raise ValueError("q must have k's tokens and type")
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        if positions is not None:
+            _places(positions, k.shape[0], self.device)
+        if stream is None and _current_device() == self._index:
+            return self._append(_raw_stream(self._index), tok, start, k, ks, v, vs, dt, rope, positions, q, qs, q_out)
+        return _on(self.device, stream, self._append, tok, start, k, ks, v, vs, dt, rope, positions, q, qs, q_out)
+
+    def _append(self, handle, tok, start, k, ks, v, vs, dt, rope, positions, q, qs, q_out):
+        heads = 0
+        if q is not None:
+            heads = q.shape[1]
+            if q_out is None:
+                q_out = _empty(q.shape, dtype=q.dtype, device=self.device)
+            elif not _fits(q_out, q.shape, q.dtype, self.device):
+                _whole(q_out, q.shape, q.dtype, self.device, "q_out")
+        turns = heads and tok.n_tokens
+        _check(lib.pi_kv_append(self._ref, C.addressof(tok), start.data_ptr(), rope._ref, _ptr(positions), k.data_ptr(), ks,
+                                v.data_ptr(), vs, q.data_ptr() if turns else None, qs, heads if turns else 0,
+                                q_out.data_ptr() if turns else None, dt, handle), "pi_kv_append")
+        return q_out
 
     def read(self, page_table, cu_tokens, start, n_tokens, dtype=torch.float16, k=None, v=None, stream=None):
         """Positions start[s] .. of each sequence as (k, v) [n_tokens, heads, head_dim] of `dtype`."""

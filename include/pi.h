@@ -427,6 +427,49 @@ pi_status pi_kv_write(const pi_kv_cache *cache, const pi_kv_tokens *tokens, cons
 pi_status pi_kv_read(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
                      void *k, void *v, int32_t dtype, void *stream);
 
+/* Rotary positions.  The first `dim` elements of a head make dim / 2 pairs: of
+ * neighbours (2i, 2i + 1) where interleaved, else (i, i + dim / 2).  Pair i of a
+ * token at position n is turned by the angle t = 2 pi n turns[i] / 2^64:
+ *   a' = magnitude (a cos t - b sin t),  b' = magnitude (a sin t + b cos t)
+ * dim even, 2 to PI_MAX_ROTARY.  turns: device uint64 [dim / 2], 8-byte aligned, a
+ * frequency in turns a position modulo 1, as a fraction of 2^64: an angle is exact
+ * modulo a turn at any position.  Cosines and sines are binary32 (off by 2^-22 at
+ * most, relative to magnitude), results are rounded once, to their type. */
+#define PI_MAX_ROTARY 512
+typedef struct {
+  int32_t dim, interleaved;
+  float magnitude;
+  const uint64_t *turns;
+} pi_rotary;
+
+/* x turned by its tokens' positions (inverse != 0: by the negative angles, times
+ * magnitude as well, which is the gradient's way back).
+ *   positions  device int32 [n_tokens] (below 0: turned the other way)
+ *   x, y       [n_tokens, heads, head_dim] of `dtype`, elements of a head contiguous;
+ *              stride[0] / stride[1] elements between tokens / heads (host int64[2]).
+ *              y may be x with x's strides; otherwise the two share no element, and
+ *              no two elements of y one place
+ * Elements from `dim` on are copied.  head_dim up to PI_MAX_D, heads up to 65535. */
+pi_status pi_rotary_apply(const pi_rotary *rotary, const int32_t *positions, int32_t n_tokens, int32_t heads,
+                          int32_t head_dim, const void *x, const int64_t *x_stride, void *y,
+                          const int64_t *y_stride, int32_t dtype, int32_t inverse, void *stream);
+
+/* pi_kv_write of keys that are turned on the way, and the same tokens' queries
+ * turned, in one launch.  Row cu[s] + i of k, v and q is at position start[s] + i
+ * of sequence s in the cache and is turned by positions[cu[s] + i] (device int32
+ * [n_tokens]), or by start[s] + i where positions is NULL.
+ *   q      [n_tokens, q_heads, head_dim] of `dtype`, strides as k; or NULL with q_heads 0
+ *   q_out  [n_tokens, q_heads, head_dim] of `dtype`, contiguous, 16-byte aligned; may
+ *          be q itself (contiguous)
+ * Turned keys are quantised from binary32 (as pi_rotary_apply to binary32 and
+ * pi_kv_write of that).  rotary->dim a multiple of 16.  Rows that cannot be written
+ * (a bad page or position) still have their queries turned; rows of no sequence and
+ * of a bad cu range are left as they were. */
+pi_status pi_kv_append(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
+                       const pi_rotary *rotary, const int32_t *positions, const void *k, const int64_t *k_stride,
+                       const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,
+                       int32_t q_heads, void *q_out, int32_t dtype, void *stream);
+
 /* Attention of each sequence's newest tokens over its cached keys and values.
  * Row cu[s] + i of q is the token at position length[s] - n_s + i, with
  * n_s = cu[s+1] - cu[s], and sees positions 0 .. its own (causal != 0) or

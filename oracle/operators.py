@@ -93,6 +93,27 @@ class CacheOracle:
         return np.array(out).reshape(last - first, *self.value[which].shape[1::2])
 
 
+# ---- rotary positions ---------------------------------------------------------------
+
+def rotary(x, positions, freq, magnitude, interleaved, inverse=False):
+    """x [tokens, heads, dim] with its first 2 len(freq) elements turned, and a bound
+    on each element in binary32 before it is rounded to its type: a cosine or sine
+    is off by 2^-22 (angle 2^-25 of an eighth turn, 2^-23 of the function, 2^-24 of
+    the magnitude), products and sum by half a step each."""
+    x = np.asarray(x, dtype=np.float64)
+    r = 2 * len(freq)
+    pi = np.longdouble("3.14159265358979323846264338327950288")              # far positions: more bits than float64's
+    t = np.fmod(np.asarray(positions, dtype=np.longdouble)[:, None] * np.asarray(freq, dtype=np.longdouble), 2 * pi)
+    t = t.astype(np.float64)
+    c, s = magnitude * np.cos(t)[:, None], magnitude * np.sin(t)[:, None] * (-1 if inverse else 1)
+    first, second = (slice(0, r, 2), slice(1, r, 2)) if interleaved else (slice(0, r // 2), slice(r // 2, r))
+    a, b = x[..., first], x[..., second]
+    y, tol = x.copy(), np.zeros_like(x)
+    y[..., first], y[..., second] = a * c - b * s, a * s + b * c
+    tol[..., first] = tol[..., second] = (np.abs(a) + np.abs(b)) * abs(magnitude) * (2.0 ** -22 + 2 * U32)
+    return y, tol
+
+
 # ---- attention ----------------------------------------------------------------------
 
 def attention(q, k, v, first, scale, causal=True):
