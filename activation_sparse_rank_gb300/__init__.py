@@ -25,17 +25,22 @@ from .operators import (  # noqa: F401
     PI_KV_MAX_PAGE,
     PI_MAX_ROTARY,
     PI_MAX_TOP_K,
+    PI_MAX_TREE,
+    DraftVerdict,
     KVCache,
     Rotary,
     TokenScores,
+    draft_tree,
     layer_norm,
     layer_norm_backward,
     rotary,
     rotary_backward,
     token_logprobs,
+    verify_draft,
 )
 
 __all__ = [
+    "DraftVerdict",
     "KVCache",
     "Layer",
     "PiError",
@@ -49,7 +54,9 @@ __all__ = [
     "PI_MAX_BATCH",
     "PI_MAX_ROTARY",
     "PI_MAX_TOP_K",
+    "PI_MAX_TREE",
     "PI_STACK_LAYERS_PER_LAUNCH",
+    "draft_tree",
     "hot_first_perm",
     "layer_norm",
     "layer_norm_backward",
@@ -61,4 +68,5 @@ __all__ = [
     "stack_forward",
     "stack_forward_host",
     "token_logprobs",
+    "verify_draft",
 ]

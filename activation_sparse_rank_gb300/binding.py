@@ -42,6 +42,7 @@ PI_KV_BLOCK = 16
 PI_KV_MAX_PAGE = 256
 PI_MAX_TOP_K = 64
 PI_MAX_ROTARY = 512
+PI_MAX_TREE = 256
 
 _p = C.c_void_p
 _i32 = C.c_int32
@@ -98,6 +99,8 @@ _SIG = {
     "pi_kv_attention_workspace_bytes": (C.c_size_t, [_p, _i32, _i32, _i32]),
     "pi_kv_attention": (C.c_int, [_p, _p, _p, _i32, _p, _p, _i32, _i32, C.c_float, _i32, _p, _p, _p, C.c_size_t, _p]),
     "pi_kv_status": (C.c_int, [_p, _p]),
+    "pi_draft_tree": (C.c_int, [_p, _p, _i32, _i32, _i32, _p, _p, _p]),
+    "pi_verify_draft": (C.c_int, [_p, _i64, _p, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p]),
     "pi_layer_norm": (C.c_int, [_p, _i64, _p, _i32, _p, _p, _i32, _i32, _i32, _i32, C.c_float, _p, _p, _p, _p, _p]),
     "pi_layer_norm_backward_workspace_bytes": (C.c_size_t, [_i32, _i32]),
     "pi_layer_norm_backward": (C.c_int, [_p, _p, _i64, _p, _i32, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p, _p,

@@ -1,0 +1,401 @@
+// Drafted tokens: the tree they make, and which of them the target accepts.
+//
+// The tree.  A node's way to its root by doubling: in each round a node takes the
+// bits of the node that it points to and then points where that one does, so a
+// chain of n takes log2 n rounds.  Bound by latency: a CTA a sequence.
+//
+// Verification (speculative sampling with several drafts a node).  At a node with
+// target p and draft q the children are gone through in turn, with w = p and W = 1:
+//   accept child x if u q(x) W < w(x);  else w = max(w - W q, 0), W = sum w
+// and the token after the last accepted node is the first i with sum_{j<=i} w_j > u W.
+//
+// Sums are whole numbers of 2^-60: adding them is associative, so the result does
+// not depend on how a row is split, and a probability's 24 bits are kept down to
+// 2^-37.  A row is read only where a sum is needed: for a chain once for the whole
+// sequence (at the rejection, or after the last token), and there its sums also say
+// which warp has the sampled token.  What is needed of the other rows is the drafted
+// token's two elements, all fetched at once at the start.
+//
+// A cluster of CTAs a sequence; they exchange one number each a pass, through
+// distributed shared memory.
+#include "pi_ops.cuh"
+
+#include <algorithm>
+
+using namespace pidev;
+
+namespace {
+
+constexpr int kNodes = PI_MAX_TREE;
+
+struct TreeParams {
+  const int32_t *parent, *cu;
+  int n_seqs, n_tokens, max_q, words;
+  int32_t *mask, *depth;
+};
+
+__global__ void __launch_bounds__(kNodes) k_draft_tree(const TreeParams p) {
+  __shared__ int to[2][kNodes];
+  __shared__ unsigned bits[2][kNodes / 32][kNodes];
+  const int s = blockIdx.x, i = threadIdx.x, r0 = p.cu[s], r1 = p.cu[s + 1];
+  if (r0 < 0 || r1 < r0 || r1 > p.n_tokens) return;
+  const int n = min(r1 - r0, p.max_q);
+  int at = -1, now = 0;
+  unsigned own[kNodes / 32];
+  if (i < n) {
+    at = p.parent[r0 + i];
+    if (at < 0 || at >= i) at = -1;
+  }
+  to[0][i] = at;
+#pragma unroll
+  for (int w = 0; w < kNodes / 32; ++w) {
+    own[w] = i < n && i / 32 == w ? 1u << i % 32 : 0u;
+    if (w < p.words) bits[0][w][i] = own[w];
+  }
+  while (__syncthreads_or(at >= 0)) {                // the rows of this round are written
+    if (at >= 0) {
+#pragma unroll
+      for (int w = 0; w < kNodes / 32; ++w)
+        if (w < p.words) own[w] |= bits[now][w][at];
+      at = to[now][at];
+    }
+    now ^= 1;
+    to[now][i] = at;
+#pragma unroll
+    for (int w = 0; w < kNodes / 32; ++w)
+      if (w < p.words) bits[now][w][i] = own[w];
+  }
+  if (i < n) {
+    int d = -1;
+#pragma unroll
+    for (int w = 0; w < kNodes / 32; ++w)
+      if (w < p.words) d += __popc(own[w]);
+    if (p.depth) p.depth[r0 + i] = d;
+  }
+  if (p.mask)
+    for (int k = i; k < n * p.words; k += blockDim.x) p.mask[(int64_t)r0 * p.words + k] = bits[now][k % p.words][k / p.words];
+  for (int64_t k = (int64_t)n * p.words + i; k < (int64_t)(r1 - r0) * p.words; k += blockDim.x)       // rows past max_q
+    if (p.mask) p.mask[(int64_t)r0 * p.words + k] = 0;
+  for (int k = n + i; k < r1 - r0; k += blockDim.x)
+    if (p.depth) p.depth[r0 + k] = -1;
+}
+
+// ---- verification -----------------------------------------------------------------
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostCluster = 8;
+constexpr int kMostVocab = 1 << 21;
+constexpr int kMostChunks = kMostVocab / 4 / 32 / kWarps + 1;        // pieces of 32 vectors that a warp's share of a row has
+
+struct VerifyParams {
+  const void *target, *draft;
+  int64_t t_stride, q_stride;
+  int vocab, n_seqs, n_tokens, max_q;
+  const int32_t *drawn, *parent, *cu;
+  const float *accept, *sample;
+  int32_t *accepted, *path, *token;
+};
+
+using u64 = unsigned long long;
+
+// A probability: NaN and what is below 0 count as 0, what is above 1 as 1.
+__device__ __forceinline__ float unit(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+// p in [0, 1] in whole 2^-60, 1 at least where it is not 0.
+__device__ __forceinline__ u64 whole(float p) {
+  const unsigned b = __float_as_uint(p);
+  const int e = (int)(b >> 23) - 90;                 // p = m 2^(e - 60)
+  const unsigned m = (b & 0x7fffffu) | 0x800000u;
+  const u64 v = e >= 0 ? (u64)m << e : (u64)(m >> min(-e, 31));
+  return b == 0 ? 0 : v == 0 ? 1 : v;
+}
+// a b 2^-60, rounded down
+__device__ __forceinline__ u64 times(u64 a, u64 b) { return __umul64hi(a, b) << 4 | a * b >> 60; }
+
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// A value into the same shared variable of the cluster's CTA `rank`.
+__device__ __forceinline__ void store_in(u64 *at, int rank, u64 v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, const int size) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int V = 16 / sizeof(T);
+  __shared__ int s_parent[kNodes], s_drawn[kNodes], s_path[kNodes];
+  __shared__ float s_u[kNodes], s_p[kNodes], s_q[kNodes];
+  __shared__ u64 mass[kNodes + 1];                   // W after so many rejections at this node
+  __shared__ int gone[kNodes];                       // drafted tokens rejected there (no draft)
+  __shared__ u64 warp_total[2][kWarps], cta_total[2][kMostCluster], chunk[kMostChunks];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % size, s = blockIdx.x / size;
+  if (size > 1) cluster_arrive();                    // waited for before another CTA's memory is written
+  const int r0 = p.cu[s], r1 = p.cu[s + 1];
+  const int n = r0 < 0 || r1 < r0 || r1 > p.n_tokens ? 0 : min(r1 - r0, p.max_q);
+  const T *target = static_cast<const T *>(p.target), *draft = static_cast<const T *>(p.draft);
+  if (tid < n) {
+    const int up = p.parent[r0 + tid], x = p.drawn[r0 + tid];
+    const bool hangs = tid > 0 && up >= 0 && up < tid, in = hangs && x >= 0 && x < p.vocab;
+    s_parent[tid] = hangs ? up : -1, s_drawn[tid] = x;
+    s_u[tid] = p.accept[r0 + tid];
+    s_p[tid] = in ? unit(E::to(target[(r0 + up) * p.t_stride + x])) : 0.f;
+    s_q[tid] = !in ? 0.f : draft ? unit(E::to(draft[(r0 + up) * p.q_stride + x])) : 1.f;
+  }
+  if (rank == 0)
+    for (int i = tid; i < p.max_q; i += kThreads) p.path[(int64_t)s * p.max_q + i] = i || n == 0 ? -1 : 0;
+  __syncthreads();
+  if (size > 1) cluster_wait();
+  if (n == 0) {
+    if (rank == 0 && tid == 0) p.accepted[s] = 0, p.token[s] = -1;
+    return;
+  }
+
+  int cur = 0, count = 0, j = 0, passes = 0;
+  int no = 0;                                        // rejections at this node
+  const T *prow = target + (int64_t)r0 * p.t_stride, *qrow = draft ? draft + (int64_t)r0 * p.q_stride : nullptr;
+  // What the target has left of element i after `no` rejections.
+  auto left = [&](float pi, float qi, int i) {
+    u64 w = whole(pi);
+    if (no == 0) return w;
+    if (draft) {
+      const u64 q = whole(qi);
+      w = pi > qi ? (w > q ? w - q : 1) : 0;
+      for (int k = 1; k < no; ++k) {
+        const u64 less = times(mass[k], q);
+        w = w > less ? w - less : 0;
+      }
+    } else {
+      for (int k = 0; k < no; ++k)
+        if (gone[k] == i) w = 0;
+    }
+    return w;
+  };
+  // Element i of the row is element i + shift of a line whose vectors of V are aligned.
+  int shift = 0, per_warp = 0;
+  bool both = true;                                  // the two rows are aligned alike
+  auto load = [&](const T *row, int i, bool vec, float *x) {         // V elements from i on, 0 where there are none
+    if (vec && i >= 0 && i + V <= p.vocab) {
+      const Pack<DT, V> v = *reinterpret_cast<const Pack<DT, V> *>(row + i);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = unit(E::to(v.v[e]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = i + e >= 0 && i + e < p.vocab ? unit(E::to(row[i + e])) : 0.f;
+    }
+  };
+  auto line = [&] {
+    shift = (int)(reinterpret_cast<uintptr_t>(prow) / sizeof(T) % V);
+    both = !qrow || (reinterpret_cast<uintptr_t>(prow) - reinterpret_cast<uintptr_t>(qrow)) % 16 == 0;
+    const int chunks = ((p.vocab + shift + V - 1) / V + 31) / 32;
+    per_warp = (chunks + size * kWarps - 1) / (size * kWarps);
+  };
+  // Sum of what is left over this lane's part of chunk c.
+  auto sum_of = [&](int c) {
+    const int i = (c * 32 + lane) * V - shift;
+    if (i >= p.vocab) return (u64)0;
+    float x[V], y[V];
+    load(prow, i, true, x);
+    if (no && draft) load(qrow, i, both, y);
+    u64 t = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) t += left(x[e], no && draft ? y[e] : 0.f, i + e);
+    return t;
+  };
+  // A pass over the row: every CTA gets the whole sum.
+  auto pass = [&] {
+    line();
+    const int b = passes++ & 1, c0 = (rank * kWarps + warp) * per_warp;
+    u64 t = 0;
+#pragma unroll 4
+    for (int c = c0; c < c0 + per_warp; ++c) t += sum_of(c);
+    t = warp_sum64(t);
+    if (lane == 0) warp_total[b][warp] = t;
+    __syncthreads();
+    if (warp == 0) {
+      const u64 mine = warp_sum64(lane < kWarps ? warp_total[b][lane] : 0);
+      if (lane < size) store_in(&cta_total[b][rank], lane, mine);
+      __syncwarp();
+    }
+    if (size > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    u64 all = 0;
+    for (int k = 0; k < size; ++k) all += cta_total[b][k];
+    return all;
+  };
+  auto next_child = [&] {                            // of cur, after j; n if there is none
+    for (int k = (j + 1) & ~31; k < n; k += 32) {
+      const unsigned is = __ballot_sync(0xffffffffu, k + lane > j && k + lane < n && s_parent[k + lane] == cur);
+      if (is) return k + __ffs(is) - 1;
+    }
+    return n;
+  };
+
+  u64 all = 0;                                       // sum of what is left, where `no` > 0
+  bool behind = false;                               // the last pass's parts are not those of `all`
+  while ((j = next_child()) < n) {
+    // u q W < w, in 64 bits; W = 1 and w = p exactly before the first rejection
+    bool yes;
+    const double uq = (double)s_u[j] * (double)s_q[j];
+    if (no == 0) yes = uq < (double)s_p[j];
+    else yes = uq * ((double)all * 0x1p-60) < (double)left(s_p[j], s_q[j], s_drawn[j]) * 0x1p-60;
+    if (yes) {
+      cur = j, ++count, no = 0, behind = false;
+      if (tid == 0) s_path[count] = j;
+      prow = target + (int64_t)(r0 + cur) * p.t_stride;
+      if (draft) qrow = draft + (int64_t)(r0 + cur) * p.q_stride;
+      continue;
+    }
+    const u64 was = no ? left(s_p[j], s_q[j], s_drawn[j]) : 0;
+    __syncthreads();                                 // the lists of the node before have been read
+    if (tid == 0) gone[no] = s_drawn[j], mass[no] = all;
+    __syncthreads();
+    if (no++ == 0 || draft) all = pass();
+    else all -= was, behind = true;                  // a given token takes its own share along
+  }
+  if (no == 0 || behind) all = pass();
+  if (all == 0 && no) {                              // nothing is left: the target itself
+    no = 0;
+    all = pass();
+  }
+  if (rank == 0) {
+    if (tid == 0) p.accepted[s] = count;
+    for (int i = 1 + tid; i <= count; i += kThreads) p.path[(int64_t)s * p.max_q + i] = s_path[i];
+  }
+  if (all == 0) {
+    if (rank == 0 && tid == 0) p.token[s] = -1;
+    return;
+  }
+  // ---- the first element whose sum up to it is above u times the whole ----
+  const float u = p.sample[s];
+  const u64 part = !(u > 0.f) ? 0 : u >= 1.f ? ~0ull : (u64)((double)u * 0x1p64);
+  u64 rest = __umul64hi(part, all);                  // below `all`
+  const int b = (passes - 1) & 1;
+  for (int k = 0; k < rank; ++k) {
+    const u64 t = cta_total[b][k];
+    if (rest < t) return;                            // in a CTA before this one
+    rest -= t;
+  }
+  if (rest >= cta_total[b][rank]) return;
+  int w = 0;
+  while (w < kWarps - 1 && rest >= warp_total[b][w]) rest -= warp_total[b][w++];
+  const int c0 = (rank * kWarps + w) * per_warp;
+  for (int k = warp; k < per_warp; k += kWarps) {
+    const u64 t = warp_sum64(sum_of(c0 + k));
+    if (lane == 0) chunk[k] = t;
+  }
+  __syncthreads();
+  if (warp) return;
+  int k = 0;
+  while (k < per_warp - 1 && rest >= chunk[k]) rest -= chunk[k++];
+  const u64 own = sum_of(c0 + k);
+  u64 upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += t;
+  }
+  const int first = __ffs(__ballot_sync(0xffffffffu, upto > rest)) - 1;
+  if (lane == first) {
+    rest -= upto - own;
+    const int i = ((c0 + k) * 32 + lane) * V - shift;
+    float x[V], y[V];
+    load(prow, i, true, x);
+    if (no && draft) load(qrow, i, both, y);
+    int e = 0;
+#pragma unroll
+    for (int m = 0; m < V; ++m) {
+      const u64 t = left(x[m], no && draft ? y[m] : 0.f, i + m);
+      if (e == m && rest >= t) rest -= t, ++e;
+    }
+    p.token[s] = min(i + e, p.vocab - 1);
+  }
+}
+
+template <int DT>
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t s) {
+  const int sms = std::max(1, pi::current_sms());
+  const int64_t row = ((int64_t)p.vocab * (int)sizeof(typename Elem<DT>::T) + 511) / 512;      // chunks of a row
+  int size = 1;
+  while (size < kMostCluster && (int64_t)p.n_seqs * size * 2 <= 2 * sms && row >= 2 * size * kWarps) size *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.n_seqs * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_verify<DT>, p, size);
+}
+
+pi_status check_nodes(int n_seqs, int n_tokens, int max_q, const int32_t *parent, const int32_t *cu) {
+  if (n_seqs < 0 || n_tokens < 0 || n_seqs > (1 << 20) || n_tokens > (1 << 28))
+    return pi::fail(PI_ERR_INVALID_ARG, "n_seqs=%d or n_tokens=%d out of range", n_seqs, n_tokens);
+  if (max_q < 1 || max_q > PI_MAX_TREE) return pi::fail(PI_ERR_UNSUPPORTED, "max_q=%d: 1 to %d", max_q, PI_MAX_TREE);
+  if (n_seqs && (!cu || !pi::aligned_to(cu, 4))) return pi::fail(PI_ERR_INVALID_ARG, "cu must be non-NULL and 4-byte aligned");
+  if (n_seqs && n_tokens && (!parent || !pi::aligned_to(parent, 4)))
+    return pi::fail(PI_ERR_INVALID_ARG, "parent must be non-NULL and 4-byte aligned");
+  return PI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pi_status pi_draft_tree(const int32_t *parent, const int32_t *cu, int32_t n_seqs, int32_t n_tokens, int32_t max_q,
+                        int32_t *mask, int32_t *depth, void *stream) {
+  pi::clear_error();
+  const pi_status st = check_nodes(n_seqs, n_tokens, max_q, parent, cu);
+  if (st != PI_OK) return st;
+  if (!pi::aligned_to(mask, 4) || !pi::aligned_to(depth, 4))
+    return pi::fail(PI_ERR_INVALID_ARG, "mask and depth must be 4-byte aligned");
+  if (n_seqs == 0 || n_tokens == 0 || (!mask && !depth)) return PI_OK;
+  const TreeParams p{parent, cu, n_seqs, n_tokens, max_q, (max_q + 31) / 32, mask, depth};
+  k_draft_tree<<<n_seqs, p.words * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  PI_TRY_CUDA(cudaGetLastError());
+  return PI_OK;
+}
+
+pi_status pi_verify_draft(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride, int32_t dtype,
+                          int32_t vocab, const int32_t *drawn, const int32_t *parent, const int32_t *cu, int32_t n_seqs,
+                          int32_t n_tokens, int32_t max_q, const float *accept, const float *sample, int32_t *accepted,
+                          int32_t *path, int32_t *token, void *stream) {
+  pi::clear_error();
+  const pi_status st = check_nodes(n_seqs, n_tokens, max_q, parent, cu);
+  if (st != PI_OK) return st;
+  if (!pi::dtype_ok(dtype)) return pi::fail(PI_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (vocab < 1) return pi::fail(PI_ERR_INVALID_ARG, "vocab=%d: at least 1", vocab);
+  if (vocab > kMostVocab) return pi::fail(PI_ERR_UNSUPPORTED, "vocab=%d: up to %d", vocab, kMostVocab);
+  if (n_seqs == 0) return PI_OK;
+  const int e = pi::dtype_size(dtype);
+  if (!accepted || !path || !token || !sample || !pi::aligned_to(accepted, 4) || !pi::aligned_to(path, 4) ||
+      !pi::aligned_to(token, 4) || !pi::aligned_to(sample, 4))
+    return pi::fail(PI_ERR_INVALID_ARG, "accepted, path, token and sample must be non-NULL and 4-byte aligned");
+  if (n_tokens && (!target || !drawn || !accept || !pi::aligned_to(target, e) || !pi::aligned_to(draft, e) ||
+                   !pi::aligned_to(drawn, 4) || !pi::aligned_to(accept, 4)))
+    return pi::fail(PI_ERR_INVALID_ARG, "target, drawn and accept must be non-NULL, arrays aligned to their type");
+  if (target_stride < vocab || (draft && draft_stride < vocab))
+    return pi::fail(PI_ERR_INVALID_ARG, "rows lie in one another: strides %lld and %lld, vocab %d", (long long)target_stride,
+                    (long long)draft_stride, vocab);
+  const VerifyParams p{target, draft, target_stride, draft_stride, vocab, n_seqs, n_tokens, max_q, drawn, parent, cu, accept, sample,
+                       accepted, path, token};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PI_TRY_CUDA(dtype == PI_DT_F16    ? launch_verify<PI_DT_F16>(p, s)
+              : dtype == PI_DT_BF16 ? launch_verify<PI_DT_BF16>(p, s)
+                                    : launch_verify<PI_DT_F32>(p, s));
+  return PI_OK;
+}
+
+}  // extern "C"

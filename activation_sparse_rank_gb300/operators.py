@@ -2,8 +2,8 @@
 
 ``KVCache`` (a paged key/value cache in E4M3 codes: ``write``, ``append``,
 ``read``, ``attention``), ``rotary`` with ``rotary_backward`` (positions by a
-``Rotary``), ``layer_norm`` with ``layer_norm_backward``, and
-``token_logprobs``.  Argument checks and marshalling only; include/pi.h states
+``Rotary``), ``draft_tree`` and ``verify_draft`` for drafted tokens,
+``layer_norm`` with ``layer_norm_backward``, and ``token_logprobs``.  Argument checks and marshalling only; include/pi.h states
 each operator's formula, limits and treatment of special values.
 
 ``stream`` is a torch stream (default: the current one).  Outputs and scratch
@@ -23,11 +23,12 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import (PI_DT_BF16, PI_DT_F16, PI_DT_F32, PI_KV_BLOCK, PI_KV_MAX_PAGE, PI_MAX_ROTARY, PI_MAX_TOP_K, PiError,
-                      _check, lib, pi_kv_cache, pi_kv_tokens, pi_rotary)
+from .binding import (PI_DT_BF16, PI_DT_F16, PI_DT_F32, PI_KV_BLOCK, PI_KV_MAX_PAGE, PI_MAX_ROTARY, PI_MAX_TOP_K, PI_MAX_TREE,
+                      PiError, _check, lib, pi_kv_cache, pi_kv_tokens, pi_rotary)
 
-__all__ = ["KVCache", "Rotary", "TokenScores", "layer_norm", "layer_norm_backward", "rotary", "rotary_backward",
-           "token_logprobs", "PI_KV_BLOCK", "PI_KV_MAX_PAGE", "PI_MAX_ROTARY", "PI_MAX_TOP_K"]
+__all__ = ["DraftVerdict", "KVCache", "Rotary", "TokenScores", "draft_tree", "layer_norm", "layer_norm_backward", "rotary",
+           "rotary_backward", "token_logprobs", "verify_draft", "PI_KV_BLOCK", "PI_KV_MAX_PAGE", "PI_MAX_ROTARY",
+           "PI_MAX_TOP_K", "PI_MAX_TREE"]
 
 _DT = {torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16, torch.float32: PI_DT_F32}
 _Stride2 = C.c_int64 * 2
@@ -598,3 +599,103 @@ def _score(handle, logits, rows, vocab, dt, targets, top_k):
         entropy.data_ptr(), lse.data_ptr(), index.data_ptr() if top_k > 0 else None,
         value.data_ptr() if top_k > 0 else None, handle), "pi_token_logprobs")
     return TokenScores(logprob, entropy, lse, index, value)
+
+
+def _most_nodes(max_q, n):
+    """max_q as given, or as few as there can be."""
+    if max_q is None:
+        if n > PI_MAX_TREE:
+            raise ValueError(f"max_q must be given for more than {PI_MAX_TREE} nodes")
+        return max(1, n)
+    if not 1 <= max_q <= PI_MAX_TREE:
+        raise ValueError(f"max_q must be 1 to {PI_MAX_TREE}, not {max_q}")
+    return max_q
+
+
+def _nodes(parent, cu_tokens, device):
+    if parent.dim() != 1 or not _fits(parent, parent.shape, _i32, device):
+        _whole(parent, (parent.numel(),), _i32, device, "parent")
+    if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1:
+        raise ValueError("cu_tokens must be int32 [sequences + 1]")
+    if not _fits(cu_tokens, cu_tokens.shape, _i32, device):
+        _whole(cu_tokens, cu_tokens.shape, _i32, device, "cu_tokens")
+    return cu_tokens.shape[0] - 1, parent.shape[0]
+
+
+def draft_tree(parent, cu_tokens, max_q=None, stream=None):
+    """Trees of drafted tokens, packed by sequence: parent (int32 [tokens]) is the
+    index in its sequence of the node that a node hangs on, or -1.  Returns (mask, depth): int32
+    [tokens, ceil(max_q / 32)], bit j set for the nodes j of the sequence on a node's
+    way from its root (itself among them), as ``KVCache.attention`` takes it, and int32
+    [tokens], the nodes above it.  max_q bounds the nodes of any sequence, by default all nodes."""
+    dev = _dev(parent, None, "parent")
+    seqs, n = _nodes(parent, cu_tokens, dev)
+    max_q = _most_nodes(max_q, n)
+    if stream is None and _current_device() == dev.index:
+        return _draft_tree(_raw_stream(dev.index), parent, cu_tokens, seqs, n, max_q, dev)
+    return _on(dev, stream, _draft_tree, parent, cu_tokens, seqs, n, max_q, dev)
+
+
+def _draft_tree(handle, parent, cu_tokens, seqs, n, max_q, dev):
+    mask = _empty((n, (max_q + 31) // 32), dtype=_i32, device=dev)
+    depth = _empty(n, dtype=_i32, device=dev)
+    _check(lib.pi_draft_tree(parent.data_ptr(), cu_tokens.data_ptr(), seqs, n, max_q, mask.data_ptr(), depth.data_ptr(),
+                             handle), "pi_draft_tree")
+    return mask, depth
+
+
+class DraftVerdict(NamedTuple):
+    """What ``verify_draft`` returns; int32 [sequences], path [sequences, max_q]."""
+    accepted: torch.Tensor
+    path: torch.Tensor
+    token: torch.Tensor
+
+
+def _probs(t, shape, dtype, device, name):
+    _dev(t, device, name)
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be [tokens, vocab]" + ("" if shape is None else f" as the target, {tuple(shape)}")
+                         + f", got {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must have the target's type, {dtype}")
+    if t.stride(1) != 1 and t.shape[1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def verify_draft(target, draft, tokens, parent, cu_tokens, accept_u, sample_u, max_q=None, stream=None) -> DraftVerdict:
+    """Which drafted tokens the target accepts, and the token that follows them.
+
+    Nodes as in ``draft_tree``, each sequence's first node its last known token, with
+    ``tokens`` (int32 [tokens]; that of the first node is not used).  Row r of target and draft
+    (probabilities [tokens, vocab] of one type) says what follows node r; draft is None
+    where the drafted tokens were chosen, not drawn.  accept_u (float32 [tokens]) and
+    sample_u (float32 [sequences]) are uniform numbers in [0, 1).  Returns (accepted,
+    path, token): how many drafted tokens were accepted, the nodes (0, the accepted
+    ones, -1 behind them) and the next token.  max_q as in ``draft_tree``."""
+    dev = _dev(target, None, "target")
+    dt = _dt(target, "target")
+    ts = _probs(target, None, None, dev, "target")
+    qs = 0 if draft is None else _probs(draft, target.shape, target.dtype, dev, "draft")
+    seqs, n = _nodes(parent, cu_tokens, dev)
+    if target.shape[0] != n:
+        raise ValueError(f"target has {target.shape[0]} rows for {n} nodes")
+    for t, shape, dtype, name in ((tokens, (n,), _i32, "tokens"), (accept_u, (n,), _f32, "accept_u"),
+                                  (sample_u, (seqs,), _f32, "sample_u")):
+        if not _fits(t, shape, dtype, dev):
+            _whole(t, shape, dtype, dev, name)
+    max_q = _most_nodes(max_q, n)
+    args = (target, ts, draft, qs, dt, tokens, parent, cu_tokens, seqs, n, max_q, accept_u, sample_u, dev)
+    if stream is None and _current_device() == dev.index:
+        return _verify(_raw_stream(dev.index), *args)
+    return _on(dev, stream, _verify, *args)
+
+
+def _verify(handle, target, ts, draft, qs, dt, tokens, parent, cu_tokens, seqs, n, max_q, accept_u, sample_u, dev):
+    accepted = _empty(seqs, dtype=_i32, device=dev)
+    path = _empty((seqs, max_q), dtype=_i32, device=dev)
+    token = _empty(seqs, dtype=_i32, device=dev)
+    _check(lib.pi_verify_draft(target.data_ptr(), ts, _ptr(draft), qs, dt, target.shape[1], tokens.data_ptr(), parent.data_ptr(),
+                               cu_tokens.data_ptr(), seqs, n, max_q, accept_u.data_ptr(), sample_u.data_ptr(),
+                               accepted.data_ptr(), path.data_ptr(), token.data_ptr(), handle), "pi_verify_draft")
+    return DraftVerdict(accepted, path, token)

@@ -557,6 +557,45 @@ pi_status pi_token_logprobs(const void *logits, int64_t row_stride, int32_t dtyp
                             const int32_t *target, int32_t top_k, float *logprob, float *entropy, float *lse,
                             int32_t *top_index, float *top_logprob, void *stream);
 
+/* Drafted tokens as trees.  Sequence s has nodes cu[s] .. cu[s+1]-1 of the packed
+ * arrays, at most max_q (1 to PI_MAX_TREE); parent[r] is the index in the sequence of
+ * the node that node r hangs on, below r's own, or -1 (what is not below its own
+ * counts as -1).  A chain is parent = -1, 0, 1, 2, ...
+ *   mask   int32 [n_tokens, (max_q + 31) / 32]: bit j of a node's row (bit j % 32 of word
+ *          j / 32) is set for the nodes j on its way from the root, itself among them
+ *   depth  int32 [n_tokens]: nodes above it
+ * (either may be NULL).  Rows past max_q of a sequence get no bits and depth -1; rows
+ * of no sequence and of a bad cu range are left as they were. */
+#define PI_MAX_TREE 256
+pi_status pi_draft_tree(const int32_t *parent, const int32_t *cu, int32_t n_seqs, int32_t n_tokens,
+                        int32_t max_q, int32_t *mask, int32_t *depth, void *stream);
+
+/* Which drafted tokens the target accepts, and the token after them.  A sequence's
+ * first node is its last known token; the others hang on it (nodes that do not are
+ * not reached).  From that node on, with w = p (the target's probabilities after the
+ * node), q the draft's and W = 1, its children j are taken in order of index:
+ *   accepted where accept[j] q(x_j) W < w(x_j), x_j = drawn[j]: the walk goes on there
+ *   else w = max(w - W q, 0), W = sum w
+ * and the next token is the first i with w_0 + .. + w_i > sample[s] sum w (of p where
+ * w has no mass; -1 where p has none either, or a sequence no node).  Without a draft
+ * (NULL) children are given tokens, not drawn ones: q(x_j) = 1, and w(x_j) = 0 after a
+ * rejection.  Tokens so chosen are distributed as the target's own, where siblings
+ * are drawn independently from q.
+ *   target, draft  [n_tokens, vocab] of `dtype`, row r the probabilities after node r,
+ *                  rows stride elements apart; each row sums to about 1 (up to 8), NaN
+ *                  and negative numbers count as 0
+ *   drawn          int32 [n_tokens]; a token outside the vocabulary is never accepted
+ *   accept, sample fp32 [n_tokens], [n_seqs], uniform numbers in [0, 1)
+ *   accepted       int32 [n_seqs]: drafted tokens accepted
+ *   path           int32 [n_seqs, max_q]: 0, then the accepted nodes, then -1
+ *   token          int32 [n_seqs]
+ * Comparisons are in 64 bits, sums in whole 2^-60: exact, and the same however a row
+ * is split.  vocab up to 2^21.  Nodes past max_q of a sequence are not looked at. */
+pi_status pi_verify_draft(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                          int32_t dtype, int32_t vocab, const int32_t *drawn, const int32_t *parent,
+                          const int32_t *cu, int32_t n_seqs, int32_t n_tokens, int32_t max_q, const float *accept,
+                          const float *sample, int32_t *accepted, int32_t *path, int32_t *token, void *stream);
+
 /* Thread-local text of the last error ("" if none). */
 const char *pi_last_error(void);
 

@@ -242,3 +242,54 @@ def score_bounds(x, logp, ent, lse):
         t_lse = step + 4 * U32 * log_z + 2 * U32 * np.abs(lse)
         t_logp = t_lse + 2 * U32 * np.abs(logp)
     return t_ent, t_lse, t_logp
+
+
+# ---- drafted tokens -------------------------------------------------------------------
+
+def draft_tree(parent, cu, max_q):
+    """Bits of the nodes on each node's way (bool [tokens, words * 32]) and its depth."""
+    words = (max_q + 31) // 32
+    mask, depth = np.zeros((len(parent), 32 * words), bool), np.full(len(parent), -1)
+    for s in range(len(cu) - 1):
+        for i in range(min(int(cu[s + 1] - cu[s]), max_q)):
+            r, up = cu[s] + i, parent[cu[s] + i]
+            if 0 <= up < i:
+                mask[r], depth[r] = mask[cu[s] + up], depth[cu[s] + up]
+            mask[r, i] = True
+            depth[r] += 1
+    return mask, depth
+
+
+def verify_draft(target, draft, drawn, parent, cu, accept, sample, max_q):
+    """accepted, path and token of each sequence, one at a time, in float64."""
+    target = np.nan_to_num(np.clip(np.asarray(target, np.float64), 0, 1), nan=0.0)
+    draft = None if draft is None else np.nan_to_num(np.clip(np.asarray(draft, np.float64), 0, 1), nan=0.0)
+    vocab = target.shape[1]
+    accepted, paths, token = [], [], []
+    for s in range(len(cu) - 1):
+        n, path = min(int(cu[s + 1] - cu[s]), max_q), [0]
+        if n == 0:
+            accepted.append(0), paths.append([-1] * max_q), token.append(-1)
+            continue
+        w, mass = target[cu[s]].copy(), 1.0
+        for j in range(1, n):
+            if parent[cu[s] + j] != path[-1]:
+                continue
+            row, x = cu[s] + path[-1], drawn[cu[s] + j]
+            there = 0 <= x < vocab
+            if there and accept[cu[s] + j] * (1.0 if draft is None else draft[row, x]) * mass < w[x]:
+                path.append(j)
+                w, mass = target[cu[s] + j].copy(), 1.0
+                continue
+            if draft is not None:
+                w = np.maximum(w - mass * draft[row], 0)
+            elif there:
+                w[x] = 0
+            mass = w.sum()
+        if not w.any():
+            w = target[cu[s] + path[-1]]
+        upto = np.cumsum(w)
+        token.append(int(np.argmax(upto > sample[s] * upto[-1])) if upto[-1] > 0 else -1)
+        accepted.append(len(path) - 1)
+        paths.append(path + [-1] * (max_q - len(path)))
+    return np.array(accepted), np.array(paths).reshape(-1, max_q), np.array(token)
