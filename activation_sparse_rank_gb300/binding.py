@@ -98,6 +98,7 @@ _SIG = {
     "pi_kv_read": (C.c_int, [_p, _p, _p, _p, _p, _i32, _p]),
     "pi_kv_attention_workspace_bytes": (C.c_size_t, [_p, _i32, _i32, _i32]),
     "pi_kv_attention": (C.c_int, [_p, _p, _p, _i32, _p, _p, _i32, _i32, C.c_float, _i32, _p, _p, _p, C.c_size_t, _p]),
+    "pi_kv_tree_attention": (C.c_int, [_p, _p, _p, _i32, _p, _i32, _p, _p, _i32, _i32, C.c_float, _p, _p, _p, C.c_size_t, _p]),
     "pi_kv_status": (C.c_int, [_p, _p]),
     "pi_draft_tree": (C.c_int, [_p, _p, _i32, _i32, _i32, _p, _p, _p]),
     "pi_verify_draft": (C.c_int, [_p, _i64, _p, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p]),

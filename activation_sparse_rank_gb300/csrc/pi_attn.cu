@@ -115,7 +115,10 @@ constexpr int attn_stages() {
 // 8 columns: S^T = K Q^T and O^T = V^T P^T.  Eight rows (or fewer) then cost
 // half the products and registers of a 16-row tile of queries; P^T comes from
 // S^T's registers by one 8 x 8 transposition (movmatrix) of each half.
-template <int DT, int D, int NB, int WARPS_M>
+//
+// TREE: the new tokens are nodes of trees, of which a row sees what its bits say.
+// Only blocks from the first new token on look at them.
+template <int DT, int D, int NB, int WARPS_M, bool TREE>
 __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using E = Elem<DT>;
   constexpr int WROWS = 8 * NB, ROWS = WROWS * WARPS_M, KW = 4 / WARPS_M, KS = D / 16, MT = D / 16, STAGES = attn_stages<D, NB>();
@@ -276,6 +279,17 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
     for (int nb = 0; nb < NB; ++nb) min_lim = min(min_lim, min(lim[nb][0], lim[nb][1]));
     min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 1));
     min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 2));
+    const int32_t *tree[NB][2];                    // the columns' bits
+    if constexpr (TREE) {
+      min_lim = min(min_lim, max(0, sq.first));
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = base_row + nb * 8 + 2 * q4 + e;
+          tree[nb][e] = r < sq.rows ? p.tree + (int64_t)(sq.row0 + r / p.group) * p.words : nullptr;
+        }
+    }
 
     float acc[NB][MT][4], m[NB][2], l[NB][2], R[NB][2];      // m is 0 and R -inf while no key has been seen
 #pragma unroll
@@ -320,6 +334,13 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
         }
         // ---- running maximum, taken up only where a score passes it by kSlack ----
         const bool ragged = k0 + 16 > min_lim;
+        unsigned sees[NB][2];                      // TREE: the block's tokens, bit by bit
+        if constexpr (TREE) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sees[nb][e] = ragged ? tree_sees(tree[nb][e], p.words, k0 - sq.first) : 0xffffu;
+        }
         const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
         bool over = false;
 #pragma unroll
@@ -331,6 +352,7 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
             for (int j = e; j < 4; j += 2) {
               x[nb][j] = fmaf(x[nb][j], fk, -m[nb][e]);                // relative to m
               if (ragged && k0 + g + 8 * (j >> 1) >= lim[nb][e]) x[nb][j] = -INFINITY;
+              if (TREE && !(sees[nb][e] >> (g + 8 * (j >> 1)) & 1)) x[nb][j] = -INFINITY;
               over |= x[nb][j] > most;
             }
           }
@@ -396,7 +418,8 @@ __global__ void __launch_bounds__(128, attn_ctas(D, NB)) k_attn(const AttnParams
               for (int j = 0; j < 2; ++j)
                 asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
                              : "=r"(see[nb][j])
-                             : "r"(pack_half2(k0 + 8 * j + g < lim[nb][0], k0 + 8 * j + g < lim[nb][1])));
+                             : "r"(pack_half2(k0 + 8 * j + g < lim[nb][0] && (!TREE || (sees[nb][0] >> (8 * j + g) & 1)),
+                                              k0 + 8 * j + g < lim[nb][1] && (!TREE || (sees[nb][1] >> (8 * j + g) & 1)))));
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               unsigned n[4];
@@ -563,7 +586,7 @@ AttnShape attn_shape(int D, int64_t max_rows) {
 
 int attn_grid(int D, int nb) { return std::min(kMostShares, attn_ctas(D, nb) * std::max(1, pi::current_sms())); }
 
-template <int DT, int D, int NB, int WARPS_M>
+template <int DT, int D, int NB, int WARPS_M, bool TREE>
 cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   constexpr int ROWS = 8 * NB * WARPS_M;
   constexpr int kRing = attn_stages<D, NB>() * Frag<D>::BYTES, kSums = WARPS_M < 4 ? 4 / WARPS_M * ROWS * (D + 3) * 4 : 0;
@@ -572,13 +595,18 @@ cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
   AttnMaps maps;
   if (!encode_codes<D>(&maps.k, p.c, p.c.k_codes) || !encode_codes<D>(&maps.v, p.c, p.c.v_codes)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = pi::allow_smem(k_attn<DT, D, NB, WARPS_M>, smem, smem, done);
+  cudaError_t e = pi::allow_smem(k_attn<DT, D, NB, WARPS_M, TREE>, smem, smem, done);
   if (e != cudaSuccess) return e;
-  k_attn<DT, D, NB, WARPS_M><<<p.grid, 128, smem, s>>>(p, maps);
+  k_attn<DT, D, NB, WARPS_M, TREE><<<p.grid, 128, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // its prefix sums overlap the main kernel's end
   return pi::launch_pdl(k_attn_combine<DT, D, ROWS, kTile>, dim3(combine_grid(p, D, ROWS)), dim3(kCombineThreads), 0, s, p);
+}
+
+template <int DT, int D, int NB, int WARPS_M>
+cudaError_t launch_attn(const AttnParams &p, cudaStream_t s) {
+  return p.tree ? launch_attn<DT, D, NB, WARPS_M, true>(p, s) : launch_attn<DT, D, NB, WARPS_M, false>(p, s);
 }
 
 template <int DT, int D>
@@ -623,19 +651,11 @@ int current_sms() {
 
 }  // namespace pi
 
-extern "C" {
+namespace {
 
-size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, int32_t n_tokens, int32_t n_seqs) {
-  pi::clear_error();
-  if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
-  const int D = c->head_dim;
-  const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 32, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
-  return sizeof(int4) * attn_grid(D, 1) + sizeof(float) * 2 * rows * (size_t)(D + 2);
-}
-
-pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
-                          const void *q, const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
-                          int32_t causal, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+pi_status attend(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q, const int32_t *mask,
+                 int32_t words, const void *q, const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
+                 int32_t causal, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
   pi::clear_error();
   pi_status st = pi::check_cache(cache);
   if (st == PI_OK) st = pi::check_tokens(tokens);
@@ -653,6 +673,9 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
   if (!pi::aligned_to(length, 4) || !pi::aligned_to(lse, 4))
     return pi::fail(PI_ERR_INVALID_ARG, "length and lse must be 4-byte aligned");
   max_q = std::min(max_q, tokens->n_tokens);
+  if (mask && max_q > PI_MAX_TREE) return pi::fail(PI_ERR_UNSUPPORTED, "max_q=%d: up to %d with a mask", max_q, PI_MAX_TREE);
+  if (mask && (int64_t)words * 32 < max_q)
+    return pi::fail(PI_ERR_INVALID_ARG, "mask_words=%d hold no bits for max_q=%d", words, max_q);
   if ((int64_t)cache->n_pages * cache->heads >= (int64_t)1 << 31 ||
       (int64_t)tokens->n_seqs * cache->heads >= (int64_t)1 << 31 || (int64_t)max_q * (q_heads / cache->heads) >= 1 << 30)
     return pi::fail(PI_ERR_UNSUPPORTED, "n_pages x heads, n_seqs x heads or max_q x q_heads / heads is too large");
@@ -668,13 +691,41 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
                      (int)(((int64_t)max_q * group + rows - 1) / rows), attn_grid(cache->head_dim, shape.nb),
                      (pi::aligned_to(q, 32) && q_stride[0] % 16 == 0 && q_stride[1] % 16 == 0 ? 1 : 0) |
                          (pi::aligned_to(out, 32) ? 2 : 0) |
-                         (pi::aligned_to(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1), 32) ? 4 : 0)};
+                         (pi::aligned_to(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1), 32) ? 4 : 0),
+                     mask, words};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (many_rows(cache->head_dim, (int64_t)max_q * group))
     PI_TRY_CUDA(run_tc(p, dtype, s));
   else
     PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
   return PI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pi_kv_attention_workspace_bytes(const pi_kv_cache *c, int32_t q_heads, int32_t n_tokens, int32_t n_seqs) {
+  pi::clear_error();
+  if (pi::check_cache(c) != PI_OK || q_heads < 1 || n_tokens < 0 || n_seqs < 0) return 0;
+  const int D = c->head_dim;
+  const size_t rows = D <= 128 ? std::max({(size_t)attn_grid(D, 1) * 8, (size_t)attn_grid(D, 2) * 32, (size_t)std::max(1, pi::current_sms()) * kTcRows}) : (size_t)attn_grid(D, 1) * 32;
+  return sizeof(int4) * attn_grid(D, 1) + sizeof(float) * 2 * rows * (size_t)(D + 2);
+}
+
+pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
+                          const void *q, const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
+                          int32_t causal, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  return attend(cache, tokens, length, max_q, nullptr, 0, q, q_stride, q_heads, dtype, sm_scale, causal, out, lse, ws, ws_bytes, stream);
+}
+
+pi_status pi_kv_tree_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length, int32_t max_q,
+                               const int32_t *mask, int32_t mask_words, const void *q, const int64_t *q_stride, int32_t q_heads,
+                               int32_t dtype, float sm_scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  pi::clear_error();
+  if (!mask || !pi::aligned_to(mask, 4) || mask_words < 1)
+    return pi::fail(PI_ERR_INVALID_ARG, "mask must be non-NULL and 4-byte aligned, mask_words=%d at least 1", mask_words);
+  return attend(cache, tokens, length, max_q, mask, mask_words, q, q_stride, q_heads, dtype, sm_scale, 1, out, lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -34,6 +34,8 @@ struct AttnParams {
   float scale;             // sm_scale log2(e)
   int q_heads, group, max_q, causal, row_tiles, grid;
   int wide;                // q, out, part: bits 0, 1, 2 set where 32-byte accesses are aligned
+  const int32_t *tree;     // or NULL: bits of the new tokens that each of them sees, words a row
+  int words;
 };
 
 // 32 bytes at once, for a row a thread: half the transactions of 16 bytes (prompts of
@@ -92,6 +94,14 @@ __device__ __forceinline__ void flag_seq(const AttnParams &p, int s) {
   const int r0 = p.tok.cu[s], r1 = p.tok.cu[s + 1], len = p.length[s];
   if (r0 < 0 || r1 < r0 || r1 > p.tok.n_tokens || r1 - r0 > p.max_q) atomicOr(p.c.status, pi::kKvBadRows);
   if (len < 0 || len > (int64_t)p.tok.table_pages * p.c.page_size || len > 1 << 30) atomicOr(p.c.status, pi::kKvBadRange);
+}
+// Whether a token sees the 16 keys from new token j0 on (bit by bit; below 0: the
+// cache before the new ones, seen by all).  row: its bits, NULL for a padding row.
+__device__ __forceinline__ unsigned tree_sees(const int32_t *row, int words, int j0) {
+  if (!row || j0 <= -16) return 0xffffu;
+  const int w = j0 >> 5;
+  const unsigned lo = w < 0 ? ~0u : w < words ? (unsigned)row[w] : 0u, hi = w + 1 < words ? (unsigned)row[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, j0 & 31) & 0xffffu;
 }
 // Keys that any row of a row tile (ROWS rows) sees, and the tiles (TILE keys) that hold them.
 template <int ROWS>

@@ -403,7 +403,7 @@ class KVCache:
         return torch.empty(n, dtype=_u8, device=self.device)
 
     def attention(self, q, page_table, cu_tokens, length, max_q=None, sm_scale=None, causal=True, out=None, lse=None,
-                  want_lse=False, ws=None, stream=None):
+                  want_lse=False, ws=None, stream=None, tree=None):
         """Attention of each sequence's newest tokens q [tokens, q_heads, head_dim]
         (float16 or bfloat16) over its cache.  length[s] counts the tokens in the
         cache, the new ones among them.  max_q bounds the new tokens of any
@@ -412,22 +412,36 @@ class KVCache:
         chosen by it (single tokens and a long prompt: two calls).  Rows past max_q get 0 (lse -inf) and show in
         ``device_status``; rows of no sequence are left as they were (unset in
         an ``out`` made here).  Returns out, or (out, lse) with want_lse or an
-        lse tensor."""
+        lse tensor.
+
+        tree (``draft_tree``'s mask, int32 [tokens, words]): the new tokens are drafted
+        ones, and one sees of them those whose bits its row has (up to itself), beside the
+        cache before them.  max_q is then at most 32 words and PI_MAX_TREE, the default included."""
         heads = q.shape[1] if q.dim() == 3 else 0
         qs = self._rows(q, heads, "q")
         if q.dtype is not torch.float16 and q.dtype is not torch.bfloat16:
             raise TypeError(f"q must be float16 or bfloat16, not {q.dtype}")
         tok = self._tokens(page_table, cu_tokens, length, "length", q.shape[0])
         scale = self._scale if sm_scale is None else sm_scale
+        if tree is not None:
+            words = tree.shape[1] if tree.dim() == 2 else 0
+            if not _fits(tree, (tok.n_tokens, words), _i32, self.device):
+                _whole(tree, (tok.n_tokens, words), _i32, self.device, "tree")
+            if not causal:
+                raise ValueError("tree is causal: a token sees none behind it")
+            if max_q is None:
+                max_q = min(tok.n_tokens, 32 * words, PI_MAX_TREE)
+            if max_q > min(32 * words, PI_MAX_TREE) and tok.n_tokens:
+                raise ValueError(f"max_q={max_q}: tree has bits for {32 * words}, {PI_MAX_TREE} at most")
         if max_q is None:
             max_q = 1 if tok.n_tokens <= tok.n_seqs else tok.n_tokens
         elif max_q == 0:
             max_q = 1                                # the library would leave every row as it is, unlooked at
         if stream is None and _current_device() == self._index:
-            return self._attention(_raw_stream(self._index), tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
-        return _on(self.device, stream, self._attention, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws)
+            return self._attention(_raw_stream(self._index), tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws, tree)
+        return _on(self.device, stream, self._attention, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws, tree)
 
-    def _attention(self, handle, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws):
+    def _attention(self, handle, tok, length, max_q, q, qs, scale, causal, out, lse, want_lse, ws, tree):
         dev, shape = self.device, q.shape
         if out is None:
             out = _empty(shape, dtype=q.dtype, device=dev)
@@ -439,6 +453,11 @@ class KVCache:
             lse = _empty(shape[:2], dtype=_f32, device=dev)
         if ws is None:
             ws = self.attention_workspace(shape[1], tok.n_tokens, tok.n_seqs)
+        if tree is not None and tok.n_tokens:
+            _check(lib.pi_kv_tree_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, tree.data_ptr(), tree.shape[1],
+                                            q.data_ptr(), qs, shape[1], _DT[q.dtype], scale, out.data_ptr(), _ptr(lse),
+                                            ws.data_ptr(), _ws(ws, dev), handle), "pi_kv_tree_attention")
+            return out if lse is None else (out, lse)
         _check(lib.pi_kv_attention(self._ref, C.addressof(tok), length.data_ptr(), max_q, q.data_ptr(), qs, shape[1],
                                    _DT[q.dtype], scale, 1 if causal else 0, out.data_ptr(), _ptr(lse), ws.data_ptr(),
                                    _ws(ws, dev), handle), "pi_kv_attention")

@@ -492,6 +492,8 @@ pi_status pi_kv_append(const pi_kv_cache *cache, const pi_kv_tokens *tokens, con
  * each; below 2^-20 of the largest, to 2^-31 of it), for the sum with the codes
  * only, not for the weights' own sum; and a bf16 query row, scaled by a power of
  * two, to fp16 (elements below 2^-30 of its largest lose bits).
+ * With more than 32 query rows a head (max_q x q_heads / heads; head_dim up to 128)
+ * scores of 2^24 and more in size may give NaN (pi_kv_tree_attention takes any).
  * max_q chooses the kernels and row tiles for all sequences of a call: many
  * single tokens and a long prompt are better two calls (256 single tokens over
  * 2000 keys, 64 heads on 8 of 128: 193 us; with a prompt of 512 tokens in the
@@ -502,6 +504,17 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
                           int32_t max_q, const void *q, const int64_t *q_stride, int32_t q_heads,
                           int32_t dtype, float sm_scale, int32_t causal, void *out, float *lse,
                           void *ws, size_t ws_bytes, void *stream);
+
+/* pi_kv_attention for drafted tokens that make trees: row cu[s] + i of q sees the
+ * positions 0 .. length[s]-n_s-1, and position length[s]-n_s + j for those j <= i whose
+ * bit is set in its row of mask (pi_draft_tree's, or any bits).
+ *   mask  device int32 [n_tokens, mask_words], bit j in word j / 32; mask_words * 32 at
+ *         least max_q, which is at most PI_MAX_TREE
+ * The nodes' keys and values are in the cache, in the order of q's rows. */
+pi_status pi_kv_tree_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length,
+                               int32_t max_q, const int32_t *mask, int32_t mask_words, const void *q,
+                               const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
+                               void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronize `stream`; PI_ERR_DEVICE_CHECK if a kernel flagged a page, position
  * or token range of this cache since the last query (and clear the flag). */

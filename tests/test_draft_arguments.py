@@ -81,3 +81,19 @@ def test_oracle_of_the_verification():
     same = O.verify_draft(p, p, [0, 0], [-1, 0], [0, 2, 2], [0, 1.0], [0.8, 0.8], 2)
     assert [v.tolist() for v in same] == [[0, 0], [[0, -1], [-1, -1]], [2, -1]]
     assert O.verify_draft(0 * p, None, [0], [-1], [0, 1], [0], [0.5], 1)[2].tolist() == [-1]
+
+
+def test_tree_attention_abi_refusals(pi):
+    lib, fake = pi.lib, C.c_void_p(1 << 20)
+    c = pi.binding.pi_kv_cache(4, 32, 2, 64, 1 << 20, 1 << 20, 1 << 20, 1 << 20, 1 << 20)
+    tok = pi.binding.pi_kv_tokens(1, 300, 1 << 20, 1 << 20, 20)
+    need = lib.pi_kv_attention_workspace_bytes(C.byref(c), 4, 300, 1)
+
+    def attend(mask=fake, words=8, q=fake, st=(C.c_int64 * 2)(256, 64), heads=4, dt=0, max_q=3, n=need):
+        return lib.pi_kv_tree_attention(C.byref(c), C.byref(tok), fake, max_q, mask, words, q, st, heads, dt, 0.125, fake, None,
+                                        fake, n, None)
+
+    for bad in (dict(mask=None), dict(mask=C.c_void_p((1 << 20) + 2)), dict(words=0), dict(q=None), dict(heads=3), dict(dt=2),
+                dict(max_q=-1), dict(n=need - 1), dict(words=1, max_q=33)):
+        assert attend(**bad) == 1, bad
+    assert attend(max_q=257, words=9) == 2 and attend(max_q=0) == 0
