@@ -11,7 +11,8 @@
 //
 // Sums are whole numbers of 2^-60: adding them is associative, so the result does
 // not depend on how a row is split, and a probability's 24 bits are kept down to
-// 2^-37.  A row is read only where a sum is needed: for a chain once for the whole
+// 2^-37; what is left after a rejection has 48 bits (binary32 pairs: GB300's 64-bit
+// floating point is 64 times slower).  A row is read only where a sum is needed: for a chain once for the whole
 // sequence (at the rejection, or after the last token), and there its sums also say
 // which warp has the sampled token.  What is needed of the other rows is the drafted
 // token's two elements, all fetched at once at the start.
@@ -82,10 +83,9 @@ __global__ void __launch_bounds__(kNodes) k_draft_tree(const TreeParams p) {
 
 // ---- verification -----------------------------------------------------------------
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMostCluster = 8;
 constexpr int kMostVocab = 1 << 21;
-constexpr int kMostChunks = kMostVocab / 4 / 32 / kWarps + 1;        // pieces of 32 vectors that a warp's share of a row has
+constexpr int kAtOnce = 4;                           // pieces of a row that a warp loads together
 
 struct VerifyParams {
   const void *target, *draft;
@@ -99,17 +99,63 @@ struct VerifyParams {
 using u64 = unsigned long long;
 
 // A probability: NaN and what is below 0 count as 0, what is above 1 as 1.
-__device__ __forceinline__ float unit(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
-// p in [0, 1] in whole 2^-60, 1 at least where it is not 0.
-__device__ __forceinline__ u64 whole(float p) {
-  const unsigned b = __float_as_uint(p);
-  const int e = (int)(b >> 23) - 90;                 // p = m 2^(e - 60)
-  const unsigned m = (b & 0x7fffffu) | 0x800000u;
-  const u64 v = e >= 0 ? (u64)m << e : (u64)(m >> min(-e, 31));
-  return b == 0 ? 0 : v == 0 ? 1 : v;
+__device__ __forceinline__ float unit(float p) { return __saturatef(p); }
+
+// What is left of a probability, h + l in binary32 with |l| at most half a last place of h
+// (48 bits; for whole steps of 2^-24 and the like exact).
+struct Left {
+  f2 h, l;                                           // of two elements
+};
+__device__ __forceinline__ f2 minus(f2 a, f2 b) { return f2_fma(b, f2_of(-1.f, -1.f), a); }
+// max(p - q, 0)
+__device__ __forceinline__ Left first_left(f2 p, f2 q) {
+  const f2 m = f2_of(fminf(p.x, q.x), fminf(p.y, q.y)), d = minus(p, m);
+  return Left{d, minus(minus(p, d), m)};             // p >= m: what d lost
 }
-// a b 2^-60, rounded down
-__device__ __forceinline__ u64 times(u64 a, u64 b) { return __umul64hi(a, b) << 4 | a * b >> 60; }
+// max(w - W q, 0), W = mass.x + mass.y
+__device__ __forceinline__ Left next_left(const Left &w, f2 q, float2 mass) {
+  const f2 big = f2_of(-mass.x, -mass.x), n = f2_mul(q, big);
+  const f2 nl = f2_fma(q, f2_of(-mass.y, -mass.y), f2_fma(q, big, f2_mul(q, f2_of(mass.x, mass.x))));
+  const f2 s = f2_add(w.h, n), t = minus(s, w.h);    // s + what it lost = w.h + n
+  const f2 lost = f2_add(minus(w.h, minus(s, t)), minus(n, t)), tail = f2_add(lost, f2_add(w.l, nl));
+  const f2 h = f2_add(s, tail), l = minus(tail, minus(h, s));
+  return Left{f2_of(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)), f2_of(h.x > 0.f ? l.x : 0.f, h.y > 0.f ? l.y : 0.f)};
+}
+
+// Sums of what is left in whole 2^-60: each is cut into three numbers of 22 bits or less,
+// read off the last bits of a sum with a constant whose last place is 2^-22, 2^-44 and
+// 2^-60; what such a sum rounds away is exact and goes on to the next (l with it, to 2^-48).
+constexpr float kTo22 = 2.f, kTo44 = 0x1.8p-21f, kTo60 = 0x1.8p-37f;
+constexpr float kTiny = 0x1p-61f;                    // below, what is not 0 counts as 1 more
+struct Parts {
+  unsigned a, b, c;
+};
+__device__ __forceinline__ void add_left(Parts &s, const Left &w) {
+  const f2 t = f2_add(w.h, f2_of(kTo22, kTo22)), r = f2_add(minus(w.h, f2_add(t, f2_of(-kTo22, -kTo22))), w.l);
+  const f2 u = f2_add(r, f2_of(kTo44, kTo44)), q = minus(r, f2_add(u, f2_of(-kTo44, -kTo44)));
+  const f2 v = f2_add(q, f2_of(kTo60, kTo60));
+  s.a += __float_as_uint(t.x) + __float_as_uint(t.y);
+  s.b += __float_as_uint(u.x) + __float_as_uint(u.y);
+  s.c += __float_as_uint(v.x) + __float_as_uint(v.y);
+  s.c += (w.h.x > 0.f && w.h.x < kTiny) + (w.h.y > 0.f && w.h.y < kTiny);
+}
+// The sum of n elements, less the constants' bits.
+__device__ __forceinline__ u64 joined(const Parts &s, unsigned n) {
+  return ((u64)(s.a - n * __float_as_uint(kTo22)) << 38) + (u64)((int64_t)(int)(s.b - n * __float_as_uint(kTo44)) << 16) +
+         (u64)(int64_t)(int)(s.c - n * __float_as_uint(kTo60));
+}
+
+// A sum of whole 2^-60 in two parts.
+__device__ __forceinline__ float2 in_two(u64 s) {
+  const float h = __ull2float_rz(s);
+  return make_float2(h * 0x1p-60f, (float)(s - __float2ull_rz(h)) * 0x1p-60f);
+}
+// a b in two parts
+__device__ __forceinline__ float2 product(float a, float b) {
+  const float h = a * b;
+  return make_float2(h, fmaf(a, b, -h));
+}
+constexpr float kUp = 0x1p60f;                       // keeps the parts of small products above binary32's least
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
@@ -125,14 +171,16 @@ __device__ __forceinline__ void store_in(u64 *at, int rank, u64 v) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, const int size) {
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, const int size) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), kWarps = NT / 32;
+  constexpr int kMostChunks = kMostVocab / 4 / 32 / kWarps + 1;      // pieces of 32 vectors that a warp's share of a row has
+  constexpr int kRun = 512 / V;                      // pieces whose parts, added, stay within 32 bits
   __shared__ int s_parent[kNodes], s_drawn[kNodes], s_path[kNodes];
   __shared__ float s_u[kNodes], s_p[kNodes], s_q[kNodes];
-  __shared__ u64 mass[kNodes + 1];                   // W after so many rejections at this node
+  __shared__ float2 mass[kNodes];                    // W after so many rejections at this node, in two parts
   __shared__ int gone[kNodes];                       // drafted tokens rejected there (no draft)
   __shared__ u64 warp_total[2][kWarps], cta_total[2][kMostCluster], chunk[kMostChunks];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -150,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
     s_q[tid] = !in ? 0.f : draft ? unit(E::to(draft[(r0 + up) * p.q_stride + x])) : 1.f;
   }
   if (rank == 0)
-    for (int i = tid; i < p.max_q; i += kThreads) p.path[(int64_t)s * p.max_q + i] = i || n == 0 ? -1 : 0;
+    for (int i = tid; i < p.max_q; i += NT) p.path[(int64_t)s * p.max_q + i] = i || n == 0 ? -1 : 0;
   __syncthreads();
   if (size > 1) cluster_wait();
   if (n == 0) {
@@ -161,22 +209,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
   int cur = 0, count = 0, j = 0, passes = 0;
   int no = 0;                                        // rejections at this node
   const T *prow = target + (int64_t)r0 * p.t_stride, *qrow = draft ? draft + (int64_t)r0 * p.q_stride : nullptr;
-  // What the target has left of element i after `no` rejections.
-  auto left = [&](float pi, float qi, int i) {
-    u64 w = whole(pi);
+  // What the target has left of elements i and i + 1 after `no` rejections.
+  auto left = [&](f2 pi, f2 qi, int i) {
+    Left w{pi, f2_of(0.f, 0.f)};
     if (no == 0) return w;
     if (draft) {
-      const u64 q = whole(qi);
-      w = pi > qi ? (w > q ? w - q : 1) : 0;
-      for (int k = 1; k < no; ++k) {
-        const u64 less = times(mass[k], q);
-        w = w > less ? w - less : 0;
-      }
+      w = first_left(pi, qi);
+      for (int k = 1; k < no; ++k) w = next_left(w, qi, mass[k]);
     } else {
-      for (int k = 0; k < no; ++k)
-        if (gone[k] == i) w = 0;
+      for (int k = 0; k < no; ++k) {
+        if (gone[k] == i) w.h.x = 0.f;
+        if (gone[k] == i + 1) w.h.y = 0.f;
+      }
     }
     return w;
+  };
+  auto left_of = [&](float pi, float qi, int i) {    // one element, in whole 2^-60
+    Parts s = {0, 0, 0};
+    add_left(s, left(f2_of(pi, 0.f), f2_of(qi, 0.f), i));
+    return joined(s, 2);
   };
   // Element i of the row is element i + shift of a line whose vectors of V are aligned.
   int shift = 0, per_warp = 0;
@@ -197,25 +248,85 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
     const int chunks = ((p.vocab + shift + V - 1) / V + 31) / 32;
     per_warp = (chunks + size * kWarps - 1) / (size * kWarps);
   };
-  // Sum of what is left over this lane's part of chunk c.
+  // Sum of what is left over this lane's part of piece c.
   auto sum_of = [&](int c) {
     const int i = (c * 32 + lane) * V - shift;
-    if (i >= p.vocab) return (u64)0;
     float x[V], y[V];
     load(prow, i, true, x);
     if (no && draft) load(qrow, i, both, y);
-    u64 t = 0;
+    Parts s = {0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < V; ++e) t += left(x[e], no && draft ? y[e] : 0.f, i + e);
-    return t;
+    for (int e = 0; e < V; e += 2) add_left(s, left(f2_of(x[e], x[e + 1]), no && draft ? f2_of(y[e], y[e + 1]) : f2_of(0.f, 0.f), i + e));
+    return joined(s, V);
+  };
+  // The same over pieces c0 .. c1 - 1.  What is drawn: with a draft and a rejection.
+  auto sum_run = [&](int c0, int c1, auto drawn) {
+    constexpr bool DRAWN = decltype(drawn)::v;
+    // pieces of whole vectors: their loads go out together, without a look at the row's ends
+    const int i0 = both ? min(c1, max(c0, shift ? 1 : 0)) : c1, i1 = max(i0, min(c1, (p.vocab + shift) / (32 * V)));
+    u64 all = 0;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      if (c == i0) c = i1;
+      if (c < c1) all += sum_of(c);
+    }
+    const Pack<DT, V> *pv = reinterpret_cast<const Pack<DT, V> *>(prow - shift) + lane;
+    const Pack<DT, V> *qv = DRAWN ? reinterpret_cast<const Pack<DT, V> *>(qrow - shift) + lane : nullptr;
+#pragma unroll 1
+    for (int from = i0; from < i1; from += kRun) {
+      const int to = min(i1, from + kRun);
+      Parts s = {0, 0, 0};
+      auto add = [&](int c, const Pack<DT, V> &x, const Pack<DT, V> &y) {
+        Left w[V / 2];
+        f2 qi[V / 2];
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const f2 pi = f2_of(unit(E::to(x.v[e])), unit(E::to(x.v[e + 1])));
+          if constexpr (DRAWN) {
+            qi[e / 2] = f2_of(unit(E::to(y.v[e])), unit(E::to(y.v[e + 1])));
+            w[e / 2] = first_left(pi, qi[e / 2]);
+          } else {
+            w[e / 2] = left(pi, f2_of(0.f, 0.f), (c * 32 + lane) * V - shift + e);
+          }
+        }
+        if constexpr (DRAWN) {
+#pragma unroll 1
+          for (int k = 1; k < no; ++k) {
+            const float2 m = mass[k];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) w[e] = next_left(w[e], qi[e], m);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) add_left(s, w[e]);
+      };
+      int c = from;
+#pragma unroll 1
+      for (; c + kAtOnce <= to; c += kAtOnce) {
+        Pack<DT, V> x[kAtOnce], y[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          x[k] = pv[(c + k) * 32];
+          if constexpr (DRAWN) y[k] = qv[(c + k) * 32];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) add(c + k, x[k], y[k]);
+      }
+#pragma unroll 1
+      for (; c < to; ++c) {
+        Pack<DT, V> x = pv[c * 32], y;
+        if constexpr (DRAWN) y = qv[c * 32];
+        add(c, x, y);
+      }
+      all += joined(s, (unsigned)(to - from) * V);
+    }
+    return all;
   };
   // A pass over the row: every CTA gets the whole sum.
   auto pass = [&] {
     line();
     const int b = passes++ & 1, c0 = (rank * kWarps + warp) * per_warp;
-    u64 t = 0;
-#pragma unroll 4
-    for (int c = c0; c < c0 + per_warp; ++c) t += sum_of(c);
+    u64 t = no && draft ? sum_run(c0, c0 + per_warp, Int<1>{}) : sum_run(c0, c0 + per_warp, Int<0>{});
     t = warp_sum64(t);
     if (lane == 0) warp_total[b][warp] = t;
     __syncthreads();
@@ -243,26 +354,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
   };
 
   u64 all = 0;                                       // sum of what is left, where `no` > 0
+  float2 whole_mass = make_float2(1.f, 0.f);         // the same, in two parts
   bool behind = false;                               // the last pass's parts are not those of `all`
   while ((j = next_child()) < n) {
-    // u q W < w, in 64 bits; W = 1 and w = p exactly before the first rejection
-    bool yes;
-    const double uq = (double)s_u[j] * (double)s_q[j];
-    if (no == 0) yes = uq < (double)s_p[j];
-    else yes = uq * ((double)all * 0x1p-60) < (double)left(s_p[j], s_q[j], s_drawn[j]) * 0x1p-60;
-    if (yes) {
+    // u q W < w; both sides in two parts, exact before the first rejection (W = 1 and w = p)
+    const float2 uq = product(s_u[j], s_q[j] * kUp);
+    float2 need = uq, has = make_float2(s_p[j] * kUp, 0.f);
+    if (no) {
+      const Left w = left(f2_of(s_p[j], 0.f), f2_of(s_q[j], 0.f), s_drawn[j]);
+      has = make_float2(w.h.x * kUp, w.l.x * kUp);
+      need = product(uq.x, whole_mass.x);
+      need.y += uq.x * whole_mass.y + uq.y * whole_mass.x;
+      const float up = need.x + need.y;
+      need = make_float2(up, need.y - (up - need.x));
+    }
+    if (need.x < has.x || (need.x == has.x && need.y < has.y)) {
       cur = j, ++count, no = 0, behind = false;
       if (tid == 0) s_path[count] = j;
       prow = target + (int64_t)(r0 + cur) * p.t_stride;
       if (draft) qrow = draft + (int64_t)(r0 + cur) * p.q_stride;
       continue;
     }
-    const u64 was = no ? left(s_p[j], s_q[j], s_drawn[j]) : 0;
+    const u64 was = no && !draft ? left_of(s_p[j], s_q[j], s_drawn[j]) : 0;
     __syncthreads();                                 // the lists of the node before have been read
-    if (tid == 0) gone[no] = s_drawn[j], mass[no] = all;
+    if (tid == 0) {
+      gone[no] = s_drawn[j], mass[no] = whole_mass;
+    }
     __syncthreads();
     if (no++ == 0 || draft) all = pass();
     else all -= was, behind = true;                  // a given token takes its own share along
+    whole_mass = in_two(all);
   }
   if (no == 0 || behind) all = pass();
   if (all == 0 && no) {                              // nothing is left: the target itself
@@ -271,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
   }
   if (rank == 0) {
     if (tid == 0) p.accepted[s] = count;
-    for (int i = 1 + tid; i <= count; i += kThreads) p.path[(int64_t)s * p.max_q + i] = s_path[i];
+    for (int i = 1 + tid; i <= count; i += NT) p.path[(int64_t)s * p.max_q + i] = s_path[i];
   }
   if (all == 0) {
     if (rank == 0 && tid == 0) p.token[s] = -1;
@@ -279,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
   }
   // ---- the first element whose sum up to it is above u times the whole ----
   const float u = p.sample[s];
-  const u64 part = !(u > 0.f) ? 0 : u >= 1.f ? ~0ull : (u64)((double)u * 0x1p64);
+  const u64 part = !(u > 0.f) ? 0 : u >= 1.f ? ~0ull : __float2ull_rz(u * 0x1p64f);
   u64 rest = __umul64hi(part, all);                  // below `all`
   const int b = (passes - 1) & 1;
   for (int k = 0; k < rank; ++k) {
@@ -316,28 +437,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const VerifyParams p, co
     int e = 0;
 #pragma unroll
     for (int m = 0; m < V; ++m) {
-      const u64 t = left(x[m], no && draft ? y[m] : 0.f, i + m);
+      const u64 t = left_of(x[m], no && draft ? y[m] : 0.f, i + m);
       if (e == m && rest >= t) rest -= t, ++e;
     }
     p.token[s] = min(i + e, p.vocab - 1);
   }
 }
 
-template <int DT>
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t s) {
-  const int sms = std::max(1, pi::current_sms());
-  const int64_t row = ((int64_t)p.vocab * (int)sizeof(typename Elem<DT>::T) + 511) / 512;      // chunks of a row
-  int size = 1;
-  while (size < kMostCluster && (int64_t)p.n_seqs * size * 2 <= 2 * sms && row >= 2 * size * kWarps) size *= 2;
+template <int DT, int NT>
+cudaError_t launch_verify(const VerifyParams &p, int size, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.n_seqs * size));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_verify<DT>, p, size);
+  return cudaLaunchKernelEx(&cfg, k_verify<DT, NT>, p, size);
+}
+
+// CTAs of a sequence: while all are on the SMs at once and a warp has two pieces of a row.
+// 512 threads where that leaves SMs free, else 256, of which an SM holds four.
+template <int DT>
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t s) {
+  const int sms = std::max(1, pi::current_sms());
+  const int64_t pieces = ((int64_t)p.vocab * (int)sizeof(typename Elem<DT>::T) + 511) / 512;
+  int size = 1;
+  while (size < kMostCluster && (int64_t)p.n_seqs * size * 2 <= 4 * sms && pieces >= 4 * size * 8) size *= 2;
+  return (int64_t)p.n_seqs * size <= sms && pieces >= 2 * size * 16 ? launch_verify<DT, 512>(p, size, s) : launch_verify<DT, 256>(p, size, s);
 }
 
 pi_status check_nodes(int n_seqs, int n_tokens, int max_q, const int32_t *parent, const int32_t *cu) {

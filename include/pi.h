@@ -602,8 +602,8 @@ pi_status pi_draft_tree(const int32_t *parent, const int32_t *cu, int32_t n_seqs
  *   accepted       int32 [n_seqs]: drafted tokens accepted
  *   path           int32 [n_seqs, max_q]: 0, then the accepted nodes, then -1
  *   token          int32 [n_seqs]
- * Comparisons are in 64 bits, sums in whole 2^-60: exact, and the same however a row
- * is split.  vocab up to 2^21.  Nodes past max_q of a sequence are not looked at. */
+ * Comparisons are in 64 bits, w after a rejection in 48 or more, sums in whole 2^-60
+ * and the same however a row is split.  vocab up to 2^21.  Nodes past max_q of a sequence are not looked at. */
 pi_status pi_verify_draft(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
                           int32_t dtype, int32_t vocab, const int32_t *drawn, const int32_t *parent,
                           const int32_t *cu, int32_t n_seqs, int32_t n_tokens, int32_t max_q, const float *accept,
