@@ -449,7 +449,7 @@ typedef struct {
  *              stride[0] / stride[1] elements between tokens / heads (host int64[2]).
  *              y may be x with x's strides; otherwise the two share no element, and
  *              no two elements of y one place
- * Elements from `dim` on are copied.  head_dim up to PI_MAX_D, heads up to 65535. */
+ * Elements from `dim` on are copied.  head_dim up to 1024, heads up to 65535. */
 pi_status pi_rotary_apply(const pi_rotary *rotary, const int32_t *positions, int32_t n_tokens, int32_t heads,
                           int32_t head_dim, const void *x, const int64_t *x_stride, void *y,
                           const int64_t *y_stride, int32_t dtype, int32_t inverse, void *stream);
