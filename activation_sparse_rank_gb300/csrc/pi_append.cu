@@ -27,7 +27,7 @@ struct AppendParams {
   int q_heads;
 };
 
-template <int DT, int D, bool VEC, bool HALF>
+template <int DT, int D, bool VEC, bool HALF, bool AHEAD>
 __global__ void __launch_bounds__(256, 2) k_kv_append(const AppendParams a) {
   using E = Elem<DT>;
   using T = typename E::T;
@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(const AppendParams a) {
   auto col = [&](int t, bool turned, int second) {
     return HALF && turned && t < rp ? t + second * rp : 2 * t + second;
   };
-  uint4 x[NP][2][W];
-  auto load = [&](int unit) {
+  uint4 x[NP][2][W], next[AHEAD ? NP : 1][2][W];
+  auto load = [&](uint4 (*x)[2][W], int unit) {
     const int kind = unit < p.c.heads ? 0 : unit < 2 * p.c.heads ? 1 : 2;
     const int h = unit - kind * p.c.heads;
     const int64_t st = kind == 2 ? a.qt : p.st[kind], sh = kind == 2 ? a.qh : p.sh[kind];
@@ -86,15 +86,29 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(const AppendParams a) {
     if (turned && t < rp && row >= 0 && row < at.n) rope_turn<8, HALF>(v, table + row * 4 * rp + t, rp);
   };
 
-  if (unit < units) load(unit);
+  if (unit < units) load(x, unit);
   const int freqs = a.r.dim / 2;
   for (int i = threadIdx.x; i < at.n * freqs; i += 256) {
     const int r = i / freqs, f = i % freqs;
     rope_put<8>(table + r * 4 * rp, rp, f, rope_angle(a.r.turns[f], a.pos ? a.pos[at.row0 + r] : at.pos + r, a.r.magnitude));
   }
   __syncthreads();
+  auto advance = [&] {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int c = 0; c < W; ++c) x[i][s][c] = next[i][s][c];
+    } else if (unit + 8 < units) {
+      load(x, unit + 8);
+    }
+  };
 #pragma unroll 1
-  for (; unit < units; unit += 8, unit < units ? load(unit) : void()) {
+  for (; unit < units; advance(), unit += 8) {
+    if constexpr (AHEAD)
+      if (unit + 8 < units) load(next, unit + 8);
     if (unit >= 2 * p.c.heads) {
       const int h = unit - 2 * p.c.heads;
 #pragma unroll
@@ -163,10 +177,11 @@ cudaError_t launch(AppendParams a, bool vec, cudaStream_t s) {
   // as in the cache write: with enough blocks to fill the GPU a warp does several heads of one
   a.kv.per_warp = std::max<int64_t>(1, std::min<int64_t>((units + 7) / 8, (int64_t)a.kv.n_slots * units / (64 * std::max(1, pi::current_sms()))));
   const unsigned grid = (unsigned)((int64_t)std::max(1, a.kv.n_slots) * ((units + 8 * a.kv.per_warp - 1) / (8 * a.kv.per_warp)));
+  constexpr bool kAhead = D <= 128 && DT != PI_DT_F32;             // twice a unit's registers fit
   if (a.r.interleaved)
-    vec ? k_kv_append<DT, D, true, false><<<grid, 256, 0, s>>>(a) : k_kv_append<DT, D, false, false><<<grid, 256, 0, s>>>(a);
+    vec ? k_kv_append<DT, D, true, false, kAhead><<<grid, 256, 0, s>>>(a) : k_kv_append<DT, D, false, false, false><<<grid, 256, 0, s>>>(a);
   else
-    vec ? k_kv_append<DT, D, true, true><<<grid, 256, 0, s>>>(a) : k_kv_append<DT, D, false, true><<<grid, 256, 0, s>>>(a);
+    vec ? k_kv_append<DT, D, true, true, kAhead><<<grid, 256, 0, s>>>(a) : k_kv_append<DT, D, false, true, false><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -4,7 +4,12 @@
 // single tokens of a decode step.  The angles of a token are the same for all of
 // its heads, so a CTA takes whole tokens (or many heads of one), computes their
 // cosines and sines once, into shared memory, while its first rows are on their
-// way, and every thread then turns units of two vectors, one access each.
+// way, and every thread then turns units of two vectors, one access each, at one place
+// of several heads.
+//
+// Measured: 16001 tokens x 72 heads of 128 bf16 out of a packed projection 88 us (6.7 TB/s,
+// 99% of the copy rate); 40 heads of 32 tokens 2.5 us; 100000 tokens of one head 37 us: there
+// the angles, one for two elements, take the time.
 #include "pi_rope.cuh"
 
 #include <algorithm>
@@ -126,12 +131,13 @@ __global__ void __launch_bounds__(kMostThreads, 3) k_rotary(const RotaryParams p
 
 template <int DT, int V>
 cudaError_t launch(RotaryParams p, cudaStream_t s) {
-  // Two units a thread, loaded before the angles are computed: of one token's heads, of small
-  // tokens several, of more heads than 512 threads take several CTAs.  Little work in all: one
-  // unit a thread, in small CTAs.
+  // About three units a thread, of which two are loaded before the angles are computed, in CTAs of
+  // about 128 threads: of one token's heads, of small tokens several, more heads take several CTAs
+  // (8190 tokens x 71 heads of 64, 16 turned: 26 us; with 512 threads and two units 33.  16001 x 72 x
+  // 128: 89 and 86).  Little work in all: one unit a thread, in small CTAs.
   const int64_t units = ((p.copy ? p.dim : p.r.dim) + 2 * V - 1) / (2 * V), all = (int64_t)p.heads * units * p.tokens;
-  const bool few = all < (int64_t)2 * kMostThreads * std::max(1, pi::current_sms());
-  const int64_t most = std::max<int64_t>(1, (few ? 64 : kMostThreads) / units), each = few ? 1 : 2;    // rows at once, in turn
+  const bool few = all < (int64_t)1024 * std::max(1, pi::current_sms());
+  const int64_t most = std::max<int64_t>(1, (few ? 64 : 128) / units), each = few ? 1 : 3;     // rows at once, in turn
   p.per_tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kMostTokens, most * each / p.heads));
   const int64_t parts = std::min<int64_t>(p.heads, (p.heads + most * each - 1) / (most * each));
   p.per_heads = (int)((p.heads + parts - 1) / parts);
