@@ -25,7 +25,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "--expt-relaxed-constexpr", "-I", str(INCLUDE), "-I", str(CSRC)]
 # Compiled as one piece: the operators' kernels came out 5-15% slower in split
 # compilation (bf16 layer norm 16384 x 8192: 97 us, 84 us whole).
-WHOLE = {"pi_append", "pi_attn", "pi_attn_tc", "pi_draft", "pi_kv", "pi_norm", "pi_rope", "pi_score"}
+WHOLE = {"pi_append", "pi_attn", "pi_attn_tc", "pi_attn_tree", "pi_draft", "pi_kv", "pi_norm", "pi_rope", "pi_score"}
 
 
 def nvcc() -> str:

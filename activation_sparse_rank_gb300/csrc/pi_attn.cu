@@ -695,7 +695,7 @@ pi_status attend(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int
                      mask, words};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (many_rows(cache->head_dim, (int64_t)max_q * group))
-    PI_TRY_CUDA(run_tc(p, dtype, s));
+    PI_TRY_CUDA(mask ? run_tree(p, dtype, s) : run_tc(p, dtype, s));
   else
     PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));
   return PI_OK;

@@ -153,16 +153,23 @@ struct ShareShared {
   int64_t scan[4], at;
   int s, rt;
 };
+// EXTRA: tiles' worth of time that a unit's beginning and end take.  They come first in
+// its place in the line, so the CTAs that have many short units get fewer tiles.
 // Share `cta` of p.grid; false if there is none.  Every thread of the CTA calls it.
 // The line is ordered by sequence, head, row tile; a sequence's row tiles have
 // the same keys for every head, so the sums run over (sequence, row tile) pairs,
 // times the heads.
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int EXTRA = 0>
+__device__ __forceinline__ int unit_place(const AttnParams &p, const Seq &q, int rt) {
+  const int n = unit_tiles<ROWS, TILE>(p, q, rt);
+  return EXTRA && n ? n + EXTRA : n;
+}
+template <int ROWS, int TILE, int EXTRA = 0>
 __device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm, int cta, Share *o) {
   const int64_t pairs = (int64_t)p.tok.n_seqs * p.row_tiles, per = (pairs + 127) / 128, k0 = threadIdx.x * per;
   auto tiles_of = [&](int64_t k) {
     const int s = (int)(k / p.row_tiles);
-    return unit_tiles<ROWS, TILE>(p, load_seq(p, s), (int)(k - (int64_t)s * p.row_tiles));
+    return unit_place<ROWS, TILE, EXTRA>(p, load_seq(p, s), (int)(k - (int64_t)s * p.row_tiles));
   };
   int64_t mine = 0, total;
   if (threadIdx.x < 128)
@@ -190,7 +197,7 @@ __device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm,
   o->sq = load_seq(p, o->s);
   int64_t before = 0, all = 0;
   for (int r0 = 0; r0 < p.row_tiles; r0 += 32) {
-    const int n = r0 + lane < p.row_tiles ? unit_tiles<ROWS, TILE>(p, o->sq, r0 + lane) : 0;
+    const int n = r0 + lane < p.row_tiles ? unit_place<ROWS, TILE, EXTRA>(p, o->sq, r0 + lane) : 0;
     all += __reduce_add_sync(0xffffffffu, n);
     before += __reduce_add_sync(0xffffffffu, r0 + lane < sm.rt ? n : 0);
   }
@@ -198,7 +205,7 @@ __device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm,
   o->h = (int)((o->begin - start) / all);
   int64_t u0 = start + o->h * all;
   for (int r0 = 0; r0 < p.row_tiles; r0 += 32) {
-    const int n = r0 + lane < p.row_tiles ? unit_tiles<ROWS, TILE>(p, o->sq, r0 + lane) : 0;
+    const int n = r0 + lane < p.row_tiles ? unit_place<ROWS, TILE, EXTRA>(p, o->sq, r0 + lane) : 0;
     int sum = n;                                     // inclusive
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -217,9 +224,9 @@ __device__ __forceinline__ bool find_share(const AttnParams &p, ShareShared &sm,
   return true;
 }
 // To the next unit with keys; false after the last.
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int EXTRA = 0>
 __device__ __forceinline__ bool next_unit(const AttnParams &p, Share *o) {
-  o->u0 += unit_tiles<ROWS, TILE>(p, o->sq, o->rt);
+  o->u0 += unit_place<ROWS, TILE, EXTRA>(p, o->sq, o->rt);
   do {
     if (++o->rt >= p.row_tiles || o->rt * ROWS >= o->sq.rows) {
       o->rt = 0;
@@ -235,13 +242,14 @@ __device__ __forceinline__ bool next_unit(const AttnParams &p, Share *o) {
 
 // Parts of a unit are added by the first share whose begin lies inside it (the
 // part before its begin is its neighbour's): thread 0 of that share's CTA says so.
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int EXTRA = 0>
 __device__ __forceinline__ void write_plan(const AttnParams &p, bool any, const Share &at) {
   int4 plan = make_int4(0, 0, 0, 0);
-  if (any && at.begin > at.u0) {
-    const int64_t c0 = cta_owner(at.u0, at.total, at.shares);
+  const int64_t first = at.u0 + EXTRA;                 // its first tile
+  if (any && at.begin > first) {
+    const int64_t c0 = cta_owner(first, at.total, at.shares);
     if (c0 == (int64_t)blockIdx.x - 1) {
-      const int parts = (int)(cta_owner(at.u0 + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares) - c0) + 1;
+      const int parts = (int)(cta_owner(first + unit_tiles<ROWS, TILE>(p, at.sq, at.rt) - 1, at.total, at.shares) - c0) + 1;
       plan = make_int4(at.s, at.h, at.rt, parts | min(ROWS, at.sq.rows - at.rt * ROWS) << 16);
     }
   }
@@ -444,8 +452,9 @@ inline bool encode_codes(CUtensorMap *m, const pi_kv_cache &c, uint8_t *base) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// pi_attn_tc.cu: head_dim up to 128, row_tiles and grid are its own.
+// pi_attn_tc.cu, and pi_attn_tree.cu where there is a tree: head_dim up to 128, row_tiles and grid are their own.
 cudaError_t run_tc(const AttnParams &p, int dtype, cudaStream_t s);
+cudaError_t run_tree(const AttnParams &p, int dtype, cudaStream_t s);
 constexpr int kTcRows = 256;     // query rows of a unit there
 
 }  // namespace attn

@@ -31,90 +31,12 @@
 // row tile's softmax, a row a thread, takes 2760.  Tried and slower: one pass of the
 // softmax over registers (538 us), both groups on one row tile's tiles of keys in turn
 // (435), K of the next tile widened before V of this one (470).
-#include "pi_attn.cuh"
+#include "pi_attn_tc.cuh"
 
 using namespace attn;
 
 namespace {
 
-constexpr int kRows = kTcRows, kHalf = 128, kKeys = 128, kBlocks = kKeys / PI_KV_BLOCK;
-constexpr int kThreads = 512;      // four warpgroups: register shares are set for each
-constexpr int kStages = 3;         // of codes, K and V of a tile in turn
-// From P_j = 0, so x_j + ev_j < R - 126, and ev_j >= ev - kFar for every ev so far it
-// follows that x_j is 38 or more below the largest x: its weight is nothing.
-constexpr int kFar = 94;
-constexpr float kHuge = 0x1p22f;
-// Tiles whose scales and NaN are kept.  Copies run at most 5 tiles ahead of the first
-// softmax group, which every unit waits for; the second has no part in units of one
-// row tile, so the copies wait until it has read what it needs of a unit's last three.
-constexpr int kScaleRing = 8;
-
-// Shared-memory matrix descriptor, 128-byte swizzle: its low word holds the
-// address (and lbo), so a step of `bytes` adds bytes / 16 to it.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr & 0x3FFFF) >> 4 | ((lbo >> 4) & 0x3FFF) << 16; }
-constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;        // groups of 8 rows 1024 bytes apart
-// kind::f16, fp16 operands, binary32 sums, M = 128
-__device__ __forceinline__ uint32_t idesc(int n, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi));
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi));
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-               : "memory");
-}
-// The loads above are complete; v's uses stay behind this.
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld(float *v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < N; ++j) asm volatile("" : "+f"(v[j]));
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-template <int D>
-struct Smem {                       // byte offsets from a 1024-byte boundary
-  static constexpr int SLABS = (D + 63) / 64, SLAB = 128 * 128, TILE = SLABS * SLAB;   // a slab: 64 fp16 dims of 128 rows
-  static constexpr int Q = 0, K = Q + 2 * TILE, V = K + 2 * TILE, C = V + TILE, BYTES = C + kStages * 128 * D;
-};
 struct Bars {
   unsigned long long c_full[kStages], c_empty[kStages];                // codes: copied, widened
   unsigned long long k_full[2], k_empty[2], v_full, v_empty;           // fp16 tiles: written, used
@@ -123,33 +45,7 @@ struct Bars {
   unsigned long long drain;                                            // after a failure
 };
 
-// 16-byte chunk c of 128-byte row r in a 128-byte-swizzled slab.
-__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-// Chunk c (16 codes) of row r of a tile of codes, as the tile copies swizzle it (rows of 96 are not).
-template <int D>
-__device__ __forceinline__ uint32_t code_at(int r, int c) {
-  return D == 64 ? (uint32_t)(r * 64 + ((c ^ (r >> 1 & 3)) << 4)) : D == 96 ? (uint32_t)(r * 96 + c * 16) : sw128(r, c);
-}
-
-// Which of the dims d .. d + 31 are NaN in a value at positions k0 .. k1 - 1 that a row of a tree sees.
-template <int D>
-__device__ __noinline__ unsigned nan_of_seen(const AttnParams &p, int s, int h, int k0, int k1, int first, const int32_t *tree, int d) {
-  unsigned is = 0;
-  for (int k = k0; k < k1; ++k) {
-    const int j = k - first;
-    if (j >= 0 && !(tree[j >> 5] >> (j & 31) & 1)) continue;           // j is at most the row's own place: inside its words
-    const int page = p.tok.page_table[(int64_t)s * p.tok.table_stride + k / p.c.page_size];
-    if (page < 0 || page >= p.c.n_pages) continue;
-    const uint8_t *c = p.c.v_codes + (((int64_t)page * p.c.heads + h) * p.c.page_size + k % p.c.page_size) * D + d;
-    for (int e = 0; e < 32; ++e) is |= ((c[e] & 0x7f) == 0x7f ? 1u : 0u) << e;
-  }
-  return is;
-}
-
-// TREE: as in pi_attn.cu.  A tree's tokens are at most 256, so the tiles that hold
-// some of them are three, as those of a unit's own tokens.
-static_assert(PI_MAX_TREE <= 2 * kKeys);
-template <int DT, int D, bool TREE>
+template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, const __grid_constant__ AttnMaps maps) {
   using E = Elem<DT>;
   using L = Smem<D>;
@@ -229,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
       u.s = at.s, u.h = at.h, u.row0 = at.rt * kRows;
       u.keys = unit_keys<kRows>(p, u.sq, at.rt), u.tiles = (u.keys + kKeys - 1) / kKeys;
       u.t0 = (int)(pos - at.u0), u.t1 = (int)min((int64_t)u.tiles, at.end - at.u0);
-      u.least = p.causal ? max(0, min(u.sq.len, u.sq.first + (TREE ? 0 : u.row0 / p.group + 1))) : u.sq.len;
+      u.least = p.causal ? max(0, min(u.sq.len, u.sq.first + u.row0 / p.group + 1)) : u.sq.len;
       u.two = u.row0 + kHalf < u.sq.rows;
       work(u);
       if (!ok) break;
@@ -254,12 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
       const bool in = r < sq.rows;
       const int i = in ? r / p.group : 0, hq = h * p.group + (in ? r % p.group : 0);
       const int lim = in && p.causal ? max(0, min(sq.len, sq.first + i + 1)) : sq.len;
-      int min_lim = __reduce_min_sync(0xffffffffu, lim);
-      const int32_t *tree = nullptr;                     // the row's bits
-      if constexpr (TREE) {
-        min_lim = min(min_lim, max(0, sq.first));
-        if (in) tree = p.tree + (int64_t)(sq.row0 + i) * p.words;
-      }
+      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       float f = fabsf(p.scale);
       {
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const typename E::T *>(p.q) +
@@ -317,11 +208,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
         const int own = (int)(__float_as_uint(vs[lane & 7]) >> 23 & 255);
         largest = max(largest, __reduce_max_sync(0xffffffffu, own));
         const bool far = __any_sync(0xffffffffu, own < largest - kFar);      // rare
-        auto seen = [&](int b) {                         // TREE: columns of block b that the row sees, bit by bit
-          const int cols = ks[b] < 0.f ? 0 : lim - k0 - 16 * b;
-          const unsigned m = cols <= 0 ? 0u : cols >= 16 ? 0xffffu : (1u << cols) - 1;
-          return m & tree_sees(tree, p.words, k0 + 16 * b - sq.first);
-        };
         auto load = [&](float *x, int half) {
           tmem_ld32(ts + half * 64, x);
           tmem_ld32(ts + half * 64 + 32, x + 32);
@@ -329,17 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           if (masked) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              if constexpr (TREE) {
-                const unsigned m = seen(half * 4 + b);
+              const int cols = ks[half * 4 + b] < 0.f ? 0 : lim - k0 - half * 64 - 16 * b;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (!(m >> j & 1)) x[16 * b + j] = -INFINITY;
-              } else {
-                const int cols = ks[half * 4 + b] < 0.f ? 0 : lim - k0 - half * 64 - 16 * b;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (j >= cols) x[16 * b + j] = -INFINITY;
-              }
+              for (int j = 0; j < 16; ++j)
+                if (j >= cols) x[16 * b + j] = -INFINITY;
             }
           }
         };
@@ -358,36 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             for (int j = 1; j < 16; ++j) m = fmaxf(m, x[16 * b + j]);
             top = fmaxf(top, fmaf(m, factor(half * 4 + b), exponent(half * 4 + b)));
           }
-        }
-        // Scores so large that their last place counts (rare): a fused difference from R would be off
-        // by as much, and 2^z not finite.  Rounded as the largest was, its own difference is exact.
-        // Not without TREE: the branch costs registers there (chunks of a prompt 377 -> 430 us).
-        const float most = fmaxf(fabsf(top), R == -INFINITY ? 0.f : fabsf(R));
-        const bool mine = TREE && most > kHuge && most < INFINITY, huge = TREE && __any_sync(0xffffffffu, mine);
-        auto two_steps = [&](float x, int b) { return __fadd_rn(__fmul_rn(x, factor(b)), exponent(b)); };
-        auto two_blocks = [&](float *x, int b) {         // columns of blocks b and b + 1, as `load`
-          tmem_ld32(ts + b * 16, x);
-          tmem_wait_ld<32>(x);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int cols = ks[b + e] < 0.f ? 0 : lim - k0 - 16 * (b + e);
-            unsigned m = cols <= 0 ? 0u : cols >= 16 ? 0xffffu : (1u << cols) - 1;
-            if (TREE) m &= tree_sees(tree, p.words, k0 + 16 * (b + e) - sq.first);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (!(m >> j & 1)) x[16 * e + j] = -INFINITY;
-          }
-        };
-        if (huge) {
-          float rough = -INFINITY;
-#pragma unroll 1
-          for (int b = 0; b < kBlocks; b += 2) {
-            float x[32];
-            two_blocks(x, b);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) rough = fmaxf(rough, two_steps(x[j], b + j / 16));
-          }
-          if (mine) top = rough;
         }
         const bool over = top - kBoost > R + kSlack;
         if (__any_sync(0xffffffffu, over)) {
@@ -424,45 +273,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
             for (int e = 0; e < 2; ++e) {
               const float fb = factor(b + e), ev = exponent(b + e), bias = ev - Rs;
               const int cols = ks[b + e] < 0.f ? 0 : lim - k0 - 16 * (b + e);
-              unsigned m = 0;
-              if constexpr (TREE) m = seen(b + e);
               float part = 0.f;
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const float z = fmaf(x[16 * e + j], fb, bias);       // as below, where 2^z is 0 from -126 down
-                part += (TREE ? (m >> j & 1) != 0 : j < cols) && z < -126.f ? ex2(z + 100.f) : 0.f;
+                part += j < cols && z < -126.f ? ex2(z + 100.f) : 0.f;
               }
               if (ev < (float)(largest - 127 - kFar)) sum = fmaf(part, ex2(-ev - 100.f), sum);
             }
           }
         }
-        if (huge) {
-#pragma unroll 1
-          for (int b = 0; b < kBlocks; b += 2) {         // P of two blocks takes columns of S that have been read
-            float x[32];
-            uint32_t w[16];
-            two_blocks(x, b);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float fb = factor(b + e), ev = exponent(b + e);
-              float part[2] = {0.f, 0.f};
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float y = x[16 * e + 2 * j + i];
-                  v[i] = ex2(mine ? two_steps(y, b + e) - Rs : fmaf(y, fb, ev - Rs));
-                  part[i] += v[i];
-                }
-                w[8 * e + j] = f2_narrow<PI_DT_F16>(f2_of(v[0], v[1]));
-              }
-              sum = fmaf(part[0] + part[1], ex2(-ev), sum);
-            }
-            tmem_st16(ts + b * 8, w);
-            tmem_wait_st();
-          }
-        } else
         // P takes the first 64 columns of S: its second half is written there only after S's is read
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -511,17 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
           for (int t = max(t0, u.least / kKeys); t < t1; ++t) {
             const int ring = (u.g + (t - t0)) % kScaleRing;
             if (!nan_any[ring]) continue;
-            if constexpr (TREE) {
-              // which of the tokens it is says the cache itself (rare)
-              const unsigned is = in ? nan_of_seen<D>(p, u.s, h, t * kKeys, min(lim, (t + 1) * kKeys), sq.first, tree, q * 32) : 0;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (is >> j & 1) o[j] = __uint_as_float(0x7fffffffu);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (nan_at[ring][q * 32 + j] < lim) o[j] = __uint_as_float(0x7fffffffu);
-            }
+            for (int j = 0; j < 32; ++j)
+              if (nan_at[ring][q * 32 + j] < lim) o[j] = __uint_as_float(0x7fffffffu);
           }
         }
         if (whole) {
@@ -786,25 +598,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tc(const AttnParams p, con
   if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int DT, int D, bool TREE>
+template <int DT, int D>
 cudaError_t launch(AttnParams p, cudaStream_t s) {
   constexpr int smem = Smem<D>::BYTES + 1024;
   AttnMaps maps;
   if (!encode_codes<D>(&maps.k, p.c, p.c.k_codes) || !encode_codes<D>(&maps.v, p.c, p.c.v_codes)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = pi::allow_smem(k_attn_tc<DT, D, TREE>, smem, smem, done);
+  cudaError_t e = pi::allow_smem(k_attn_tc<DT, D>, smem, smem, done);
   if (e != cudaSuccess) return e;
   p.row_tiles = (int)(((int64_t)p.max_q * p.group + kRows - 1) / kRows);
   p.grid = std::min(kMostShares, std::max(1, pi::current_sms()));
-  k_attn_tc<DT, D, TREE><<<p.grid, kThreads, smem, s>>>(p, maps);
+  k_attn_tc<DT, D><<<p.grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return pi::launch_pdl(k_attn_combine<DT, D, kRows, kKeys>, dim3(combine_grid(p, D, kRows)), dim3(kCombineThreads), 0, s, p);
-}
-
-template <int DT, int D>
-cudaError_t launch(const AttnParams &p, cudaStream_t s) {
-  return p.tree ? launch<DT, D, true>(p, s) : launch<DT, D, false>(p, s);
 }
 
 }  // namespace
