@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 from fractions import Fraction
+from functools import lru_cache
 from typing import NamedTuple, Optional
 
 import torch
@@ -31,7 +32,7 @@ __all__ = ["DraftVerdict", "KVCache", "Rotary", "TokenScores", "draft_tree", "la
            "PI_MAX_TOP_K", "PI_MAX_TREE"]
 
 _DT = {torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16, torch.float32: PI_DT_F32}
-_Stride2 = C.c_int64 * 2
+_Stride2 = lru_cache(maxsize=256)(C.c_int64 * 2)     # the library only reads them, so calls may share one
 _f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
 
 
@@ -174,11 +175,12 @@ class Rotary:
 
 def _heads3(t, device, name):
     """Strides of a [tokens, heads, head_dim] tensor with contiguous heads; those of single tokens and heads may be anything."""
-    if not isinstance(t, _Tensor) or t.device != device:
+    if not isinstance(t, _Tensor) or t.get_device() != device.index:
         _dev(t, device, name)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
+    n, h, d = shape
     st, sh, sd = t.stride()
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
