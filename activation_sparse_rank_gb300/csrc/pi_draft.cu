@@ -8,6 +8,8 @@
 // target p and draft q the children are gone through in turn, with w = p and W = 1:
 //   accept child x if u q(x) W < w(x);  else w = max(w - W q, 0), W = sum w
 // and the token after the last accepted node is the first i with sum_{j<=i} w_j > u W.
+// Nothing that is left was 0 before, so after k rejections w = max(p - A q, 0), A the sum
+// of the W before each (1 for the first): one step however many there were.
 //
 // Sums are whole numbers of 2^-60: adding them is associative, so the result does
 // not depend on how a row is split, and a probability's 24 bits are kept down to
@@ -112,12 +114,12 @@ __device__ __forceinline__ Left first_left(f2 p, f2 q) {
   const f2 m = f2_of(fminf(p.x, q.x), fminf(p.y, q.y)), d = minus(p, m);
   return Left{d, minus(minus(p, d), m)};             // p >= m: what d lost
 }
-// max(w - W q, 0), W = mass.x + mass.y
-__device__ __forceinline__ Left next_left(const Left &w, f2 q, float2 mass) {
-  const f2 big = f2_of(-mass.x, -mass.x), n = f2_mul(q, big);
-  const f2 nl = f2_fma(q, f2_of(-mass.y, -mass.y), f2_fma(q, big, f2_mul(q, f2_of(mass.x, mass.x))));
-  const f2 s = f2_add(w.h, n), t = minus(s, w.h);    // s + what it lost = w.h + n
-  const f2 lost = f2_add(minus(w.h, minus(s, t)), minus(n, t)), tail = f2_add(lost, f2_add(w.l, nl));
+// max(p - A q, 0), A = a.x + a.y
+__device__ __forceinline__ Left later_left(f2 p, f2 q, float2 a) {
+  const f2 big = f2_of(-a.x, -a.x), n = f2_mul(q, big);
+  const f2 nl = f2_fma(q, f2_of(-a.y, -a.y), f2_fma(q, big, f2_mul(q, f2_of(a.x, a.x))));
+  const f2 s = f2_add(p, n), t = minus(s, p);        // s + what it lost = p + n
+  const f2 tail = f2_add(f2_add(minus(p, minus(s, t)), minus(n, t)), nl);
   const f2 h = f2_add(s, tail), l = minus(tail, minus(h, s));
   return Left{f2_of(fmaxf(h.x, 0.f), fmaxf(h.y, 0.f)), f2_of(h.x > 0.f ? l.x : 0.f, h.y > 0.f ? l.y : 0.f)};
 }
@@ -180,7 +182,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
   constexpr int kRun = 512 / V;                      // pieces whose parts, added, stay within 32 bits
   __shared__ int s_parent[kNodes], s_drawn[kNodes], s_path[kNodes];
   __shared__ float s_u[kNodes], s_p[kNodes], s_q[kNodes];
-  __shared__ float2 mass[kNodes];                    // W after so many rejections at this node, in two parts
   __shared__ int gone[kNodes];                       // drafted tokens rejected there (no draft)
   __shared__ u64 warp_total[2][kWarps], cta_total[2][kMostCluster], chunk[kMostChunks];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -208,14 +209,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
 
   int cur = 0, count = 0, j = 0, passes = 0;
   int no = 0;                                        // rejections at this node
+  float2 taken = make_float2(0.f, 0.f);              // the W before each of them, added up, in two parts
   const T *prow = target + (int64_t)r0 * p.t_stride, *qrow = draft ? draft + (int64_t)r0 * p.q_stride : nullptr;
   // What the target has left of elements i and i + 1 after `no` rejections.
   auto left = [&](f2 pi, f2 qi, int i) {
     Left w{pi, f2_of(0.f, 0.f)};
     if (no == 0) return w;
     if (draft) {
-      w = first_left(pi, qi);
-      for (int k = 1; k < no; ++k) w = next_left(w, qi, mass[k]);
+      w = no == 1 ? first_left(pi, qi) : later_left(pi, qi, taken);
     } else {
       for (int k = 0; k < no; ++k) {
         if (gone[k] == i) w.h.x = 0.f;
@@ -259,9 +260,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
     for (int e = 0; e < V; e += 2) add_left(s, left(f2_of(x[e], x[e + 1]), no && draft ? f2_of(y[e], y[e + 1]) : f2_of(0.f, 0.f), i + e));
     return joined(s, V);
   };
-  // The same over pieces c0 .. c1 - 1.  What is drawn: with a draft and a rejection.
+  // The same over pieces c0 .. c1 - 1.  drawn: 1 with a draft and one rejection, 2 with more.
   auto sum_run = [&](int c0, int c1, auto drawn) {
-    constexpr bool DRAWN = decltype(drawn)::v;
+    constexpr bool DRAWN = decltype(drawn)::v > 0, MANY = decltype(drawn)::v > 1;
     // pieces of whole vectors: their loads go out together, without a look at the row's ends
     const int i0 = both ? min(c1, max(c0, shift ? 1 : 0)) : c1, i1 = max(i0, min(c1, (p.vocab + shift) / (32 * V)));
     u64 all = 0;
@@ -277,28 +278,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
       const int to = min(i1, from + kRun);
       Parts s = {0, 0, 0};
       auto add = [&](int c, const Pack<DT, V> &x, const Pack<DT, V> &y) {
-        Left w[V / 2];
-        f2 qi[V / 2];
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           const f2 pi = f2_of(unit(E::to(x.v[e])), unit(E::to(x.v[e + 1])));
           if constexpr (DRAWN) {
-            qi[e / 2] = f2_of(unit(E::to(y.v[e])), unit(E::to(y.v[e + 1])));
-            w[e / 2] = first_left(pi, qi[e / 2]);
+            const f2 qi = f2_of(unit(E::to(y.v[e])), unit(E::to(y.v[e + 1])));
+            add_left(s, MANY ? later_left(pi, qi, taken) : first_left(pi, qi));
           } else {
-            w[e / 2] = left(pi, f2_of(0.f, 0.f), (c * 32 + lane) * V - shift + e);
+            add_left(s, left(pi, f2_of(0.f, 0.f), (c * 32 + lane) * V - shift + e));
           }
         }
-        if constexpr (DRAWN) {
-#pragma unroll 1
-          for (int k = 1; k < no; ++k) {
-            const float2 m = mass[k];
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) w[e] = next_left(w[e], qi[e], m);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) add_left(s, w[e]);
       };
       int c = from;
 #pragma unroll 1
@@ -326,7 +315,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
   auto pass = [&] {
     line();
     const int b = passes++ & 1, c0 = (rank * kWarps + warp) * per_warp;
-    u64 t = no && draft ? sum_run(c0, c0 + per_warp, Int<1>{}) : sum_run(c0, c0 + per_warp, Int<0>{});
+    u64 t = !no || !draft ? sum_run(c0, c0 + per_warp, Int<0>{}) : no == 1 ? sum_run(c0, c0 + per_warp, Int<1>{}) : sum_run(c0, c0 + per_warp, Int<2>{});
     t = warp_sum64(t);
     if (lane == 0) warp_total[b][warp] = t;
     __syncthreads();
@@ -369,18 +358,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyParams p, 
       need = make_float2(up, need.y - (up - need.x));
     }
     if (need.x < has.x || (need.x == has.x && need.y < has.y)) {
-      cur = j, ++count, no = 0, behind = false;
+      cur = j, ++count, no = 0, behind = false, whole_mass = make_float2(1.f, 0.f), taken = make_float2(0.f, 0.f);
       if (tid == 0) s_path[count] = j;
       prow = target + (int64_t)(r0 + cur) * p.t_stride;
       if (draft) qrow = draft + (int64_t)(r0 + cur) * p.q_stride;
       continue;
     }
     const u64 was = no && !draft ? left_of(s_p[j], s_q[j], s_drawn[j]) : 0;
-    __syncthreads();                                 // the lists of the node before have been read
-    if (tid == 0) {
-      gone[no] = s_drawn[j], mass[no] = whole_mass;
+    if (draft) {
+      const float h = taken.x + whole_mass.x, z = h - taken.x;       // two parts added, then put in order
+      const float l = (taken.x - (h - z)) + (whole_mass.x - z) + (taken.y + whole_mass.y);
+      taken = make_float2(h + l, l - ((h + l) - h));
+    } else {
+      __syncthreads();                               // the list of the node before has been read
+      if (tid == 0) gone[no] = s_drawn[j];
+      __syncthreads();
     }
-    __syncthreads();
     if (no++ == 0 || draft) all = pass();
     else all -= was, behind = true;                  // a given token takes its own share along
     whole_mass = in_two(all);
