@@ -25,7 +25,8 @@
 // bounds it, of 3700 clocks a tile of keys at 64 dims, 4900 at 128: 2500 in the softmax, the rest the issue of
 // its 16 products and their latency; the tensor pipe is busy for a third, the exponentials' for a fifth.
 // Tried and slower: half tiles of keys as items with S of 64 columns (two row tiles 207 us), weights
-// relative to the last maximum in one pass (225), a warp for each group's products (202).
+// relative to the last maximum in one pass (225), a warp for each group's products (202); 64 dims with P beside
+// S in TMEM and the next S issued before P V (213).
 #include "pi_attn_tc.cuh"
 
 using namespace attn;

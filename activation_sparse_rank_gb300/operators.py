@@ -201,11 +201,12 @@ def _turn(x, positions, rope, out, inverse, stream, name):
     if out is not None:
         if not isinstance(out, _Tensor) or out.shape != x.shape or out.dtype is not x.dtype:
             raise ValueError(f"the output must be {tuple(x.shape)} {x.dtype}")
-        if out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
-            os = _heads3(out, dev, "the output")     # rows may lie apart, but not in one another
-            d, (t, h) = x.shape[2], sorted(((os[0], n), (os[1], x.shape[1])))
-            if x.numel() and (t[0] < d and t[1] > 1 or h[0] < (t[1] - 1) * t[0] + d and h[1] > 1):
-                raise ValueError("the output's elements share memory")
+        os = _heads3(out, dev, "the output")         # rows may lie apart, but not in one another
+        d, (t, h) = x.shape[2], sorted(((os[0], n), (os[1], x.shape[1])))
+        if x.numel() and (t[0] < d and t[1] > 1 or h[0] < (t[1] - 1) * t[0] + d and h[1] > 1):
+            raise ValueError("the output's elements share memory")
+        if out.data_ptr() == x.data_ptr() and (os[0], os[1]) != (xs[0], xs[1]):
+            raise ValueError("the output begins where " + name + " does, with other strides")
     if stream is None and _current_device() == dev.index:
         return _rotary(_raw_stream(dev.index), x, xs, positions, rope, out, inverse, dt)
     return _on(dev, stream, _rotary, x, xs, positions, rope, out, inverse, dt)

@@ -169,6 +169,34 @@ def test_what_is_no_distribution(pi):
         assert run(pi, c).accepted.tolist() == [0] * 5
 
 
+@pytest.mark.parametrize("vocab", [1, 2, 31, 127, 128, 129, 4095, 4097, 300001])
+def test_vocabularies(pi, vocab):
+    """Rows around the pieces that warps share, and wider than usual."""
+    rng = np.random.default_rng(vocab)
+    for dtype in ("float32", "bfloat16"):
+        c = case(rng, [3, 2], vocab, 2, dtype)
+        same(run(pi, c), oracle(c))
+
+
+def test_two_calls_at_once_and_another_stream(pi):
+    """Calls on two streams that overlap: no state is shared."""
+    rng = np.random.default_rng(8)
+    cases = [case(rng, [5] * 30, 30011, 2, "float32") for _ in range(2)]
+    tensors = [(c["target"].cuda(), c["draft"].cuda(), ints(c["drawn"]), ints(c["parent"]), ints(c["cu"]), floats(c["accept"]),
+                floats(c["sample"])) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            got[i].append(pi.verify_draft(*tensors[i], 5, stream=s))
+    torch.cuda.synchronize()
+    for c, results in zip(cases, got):
+        want = oracle(c)
+        for r in results:
+            same(r, want)
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3])
 def test_strides(pi, offset):
     """Rows that begin anywhere, target and draft not alike."""

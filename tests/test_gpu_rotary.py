@@ -84,8 +84,12 @@ def test_strides_and_in_place(pi, dtype, offset):
     assert torch.equal(to, apart)
     one = normal(1, 4, 64, dtype=dtype).expand(9, 4, 64)                               # a broadcast row
     close(pi.rotary(one, ints(pos), rope), one, pos, rope, dtype)
-    with pytest.raises(ValueError):
-        pi.rotary(qk, ints(pos), rope, out=one)
+    for out, x in ((one, qk), (one, one)):
+        with pytest.raises(ValueError):
+            pi.rotary(x, ints(pos), rope, out=out)
+    square = normal(4, 4, 64, dtype=dtype)
+    with pytest.raises(ValueError):                   # the same memory in another order
+        pi.rotary(square, ints(pos[:4]), rope, out=square.transpose(0, 1))
 
 
 def test_gradient(pi):
