@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(const AttnParams p, c
   char *sm = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ Bars bars;
   __shared__ ShareShared share_sm;
-  __shared__ float scales[kRing][2][kBlocks];     // K and V scales of a tile's blocks; below 0: no block
-  __shared__ int nan_any[kRing], tile_bad[kRing];   // a tile's values have NaN that not all rows see; a block is absent
+  __shared__ float scales[kRing][2][kBlocks];          // K and V scales of a tile's blocks; below 0: no block
+  __shared__ int nan_any[kRing], tile_bad[kRing];      // a tile's values have NaN that not all rows see; a block is absent
   __shared__ float2 sums[2][kHalf];                    // one row tile: R and the sum of each group's rows
   __shared__ uint32_t tmem_s;
   __shared__ volatile int failed;
@@ -339,14 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(const AttnParams p, c
           const int ex = max((int)(__float_as_uint(mx) >> 23), 27) - 127 - 13;
           if (mx > 0.f) up *= __uint_as_float((unsigned)(127 - ex) << 23), f *= __uint_as_float((unsigned)(127 + ex) << 23);
         }
-        if (u.two || grp == 0) {
+        if (u.two || grp == 0) {                         // one row tile: the second group has only looked for its factors
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          f2 v[4];
+          for (int c = 0; c < D / 8; ++c) {
+            f2 v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_from16<DT>(raw[c], j), f2_of(up, up));
-          *reinterpret_cast<uint4 *>(sm + L::Q + rt * L::TILE + c / 8 * L::SLAB + sw128(row, c % 8)) = f2_to16<PI_DT_F16>(v);
-        }
+            for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_from16<DT>(raw[c], j), f2_of(up, up));
+            *reinterpret_cast<uint4 *>(sm + L::Q + rt * L::TILE + c / 8 * L::SLAB + sw128(row, c % 8)) = f2_to16<PI_DT_F16>(v);
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(smem_addr(&bars.q_full[rt]));
