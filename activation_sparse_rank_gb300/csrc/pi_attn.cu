@@ -626,6 +626,11 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
 // sequence of 3000 keys 24 and 32 us; of 64 sequences of 300 keys 68 and 58 us.
 // 32 rows with two warps of 16 rows here: 66, 21 and 48 us (there 79, 23 and 68).
 bool many_rows(int D, int64_t rows) { return D <= 128 && rows > 32; }
+// A tree's kernel of many rows (pi_attn_tree.cu) is ahead from 17 rows on where caches are long: 24 to 32 rows, 8 heads of
+// 128, 16 sequences of 20 to 8191 keys 73 us there, 93 to 98 here; 8 of 8192 65 and 70; one of 30000 39 and 40; of 64
+// dims 51 and 63, 47 and 55, 32 and 33.  One of 3000: 24 and 21; 64 of 300: 60 and 43 to 47.  Lengths are known on the
+// device alone; the page table says how long a cache may be.
+bool many_nodes(int D, int64_t rows, int64_t most_keys) { return D <= 128 && rows > 16 && most_keys >= 4096; }
 
 template <int DT>
 cudaError_t attn_by_dim(const AttnParams &p, cudaStream_t s) {
@@ -694,7 +699,8 @@ pi_status attend(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int
                          (pi::aligned_to(static_cast<int4 *>(ws) + attn_grid(cache->head_dim, 1), 32) ? 4 : 0),
                      mask, words};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (many_rows(cache->head_dim, (int64_t)max_q * group))
+  const int64_t q_rows = (int64_t)max_q * group;
+  if (many_rows(cache->head_dim, q_rows) || (mask && many_nodes(cache->head_dim, q_rows, (int64_t)p.tok.table_pages * cache->page_size)))
     PI_TRY_CUDA(mask ? run_tree(p, dtype, s) : run_tc(p, dtype, s));
   else
     PI_TRY_CUDA(dtype == PI_DT_F16 ? attn_by_dim<PI_DT_F16>(p, s) : attn_by_dim<PI_DT_BF16>(p, s));

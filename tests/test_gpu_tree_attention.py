@@ -172,9 +172,11 @@ def test_a_chain_is_causal_attention(pi, heads, group, dim, page, dtype):
 
 
 def test_cut_units_and_many_sequences(pi):
-    """A long cache under one tree (its units cut over many CTAs), and more sequences than SMs."""
+    """A long cache under one tree (its units cut over many CTAs), with few and with many rows, and more
+    sequences than SMs."""
     rng = np.random.default_rng(0)
-    for new, length, heads, group in ([21], [20000], 1, 8), ([3] * 200, list(range(3, 203)), 1, 2):
+    for new, length, heads, group in (([21], [20000], 1, 8), ([3, 2], [5000, 2], 2, 8), ([20], [4100], 3, 1),
+                                      ([3] * 200, list(range(3, 203)), 1, 2)):
         b = batch([n - m for n, m in zip(length, new)], new, 64)
         c = random_cache(pi, b["pages"], heads, 64, 64)
         q = queries(b["n"], heads * group, 64, "float16")
