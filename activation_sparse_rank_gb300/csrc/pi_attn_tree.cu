@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tree(const AttnParams p, c
         const float2 other = sums[grp ^ 1][row];
         const float Rn = fmaxf(R, other.x), by = R - Rn, to_it = other.x - Rn;
         mine = R == -INFINITY ? 0.f : ex2(by), theirs = other.x == -INFINITY ? 0.f : ex2(to_it);
-        const float a = R == -INFINITY ? 0.f : add_scaled(0.f, sum, by), b = other.x == -INFINITY ? 0.f : add_scaled(0.f, other.y, to_it);
+        // without a maximum a group's sum is 0, or NaN of NaN scores, which counts
+        const float a = R == -INFINITY ? sum : add_scaled(0.f, sum, by), b = other.x == -INFINITY ? other.y : add_scaled(0.f, other.y, to_it);
         sum = grp ? b + a : a + b, R = Rn;
       }
       fence_after();
