@@ -132,7 +132,7 @@ __device__ __forceinline__ Left later_left(f2 p, f2 q, float2 a) {
 // read off the last bits of a sum with a constant whose last place is 2^-22, 2^-44 and
 // 2^-60; what such a sum rounds away is exact and goes on to the next (l with it, to 2^-48).
 constexpr float kTo22 = 2.f, kTo44 = 0x1.8p-21f, kTo60 = 0x1.8p-37f;
-constexpr float kTiny = 0x1p-61f;                    // below, what is not 0 counts as 1 more
+constexpr float kTiny = 0x1p-61f;                    // up to here, what is not 0 would round to 0 (a tie, to even): 1 more
 struct Parts {
   unsigned a, b, c;
 };
@@ -143,7 +143,7 @@ __device__ __forceinline__ void add_left(Parts &s, const Left &w) {
   s.a += __float_as_uint(t.x) + __float_as_uint(t.y);
   s.b += __float_as_uint(u.x) + __float_as_uint(u.y);
   s.c += __float_as_uint(v.x) + __float_as_uint(v.y);
-  s.c += (w.h.x > 0.f && w.h.x < kTiny) + (w.h.y > 0.f && w.h.y < kTiny);
+  s.c += (w.h.x > 0.f && w.h.x <= kTiny) + (w.h.y > 0.f && w.h.y <= kTiny);
 }
 // The sum of n elements, less the constants' bits.
 __device__ __forceinline__ u64 joined(const Parts &s, unsigned n) {
