@@ -182,7 +182,7 @@ def _heads3(t, device, name):
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
     n, h, d = shape
     st, sh, sd = t.stride()
-    if sd != 1 and d > 1:
+    if sd != 1 and d > 1 and n and h:                # without elements the strides may be anything
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     return _Stride2(st if n > 1 else h * d, sh if h > 1 else d)
 
@@ -295,7 +295,7 @@ class KVCache:
             raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
         n, pages = page_table.shape
         stride, one = page_table.stride()
-        if one != 1:
+        if one != 1 and n and pages > 1:             # the stride of a single page, or of no row, may be anything
             raise ValueError("page_table must be an int32 [sequences, pages] tensor with contiguous rows")
         if not _fits(cu, (n + 1,), _i32, dev):
             _whole(cu, (n + 1,), _i32, dev, "cu_tokens")
@@ -314,7 +314,7 @@ class KVCache:
         if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim:
             raise ValueError(f"{name} must be [tokens, {heads}, {self.head_dim}], got {tuple(shape)}")
         st, sh, sd = t.stride()
-        if sd != 1:
+        if sd != 1 and shape[0] and heads:           # without elements the strides may be anything
             raise ValueError(f"{name}: the elements of a head must be contiguous")
         if shape[0] <= 1:                            # the stride of a single row may be anything, and no copy changes it
             st = heads * self.head_dim
@@ -595,7 +595,7 @@ def token_logprobs(logits, targets=None, top_k=0, stream=None) -> TokenScores:
     tokens (int32 indices, log-probabilities), equal logits by lower index."""
     dev = _dev(logits, None, "logits")
     dt = _dt(logits, "logits")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1 and logits.shape[0]):
         raise ValueError("logits must be [rows, vocab] with contiguous rows")
     rows, vocab = logits.shape
     if targets is not None and not _fits(targets, (rows,), _i32, dev):
@@ -680,7 +680,7 @@ def _probs(t, shape, dtype, device, name):
                          + f", got {tuple(t.shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must have the target's type, {dtype}")
-    if t.stride(1) != 1 and t.shape[1] != 1:
+    if t.stride(1) != 1 and t.shape[1] != 1 and t.shape[0]:
         raise ValueError(f"{name}: rows must be contiguous")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
