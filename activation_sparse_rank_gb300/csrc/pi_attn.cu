@@ -628,8 +628,9 @@ cudaError_t attn_by_rows(const AttnParams &p, cudaStream_t s) {
 bool many_rows(int D, int64_t rows) { return D <= 128 && rows > 32; }
 // A tree's kernel of many rows (pi_attn_tree.cu) is ahead from 17 rows on where caches are long: 24 to 32 rows, 8 heads of
 // 128, 16 sequences of 20 to 8191 keys 73 us there, 93 to 98 here; 8 of 8192 65 and 70; one of 30000 39 and 40; of 64
-// dims 51 and 63, 47 and 55, 32 and 33.  One of 3000: 24 and 21; 64 of 300: 60 and 43 to 47.  Lengths are known on the
-// device alone; the page table says how long a cache may be.
+// dims 51 and 63, 47 and 55, 32 and 33.  8 of 4000: 45 either way.  One of 3000: 24 and 21; 64 of 300: 61 and 45 to 47.
+// Lengths are known on the device alone; the page table says how long a cache may be, so short caches under a wide
+// one pay those differences (the header says so).
 bool many_nodes(int D, int64_t rows, int64_t most_keys) { return D <= 128 && rows > 16 && most_keys >= 4096; }
 
 template <int DT>

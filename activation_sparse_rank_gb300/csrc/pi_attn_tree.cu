@@ -24,6 +24,7 @@
 // (134); 60011 tokens under a tree of 64, 128 fp16 heads of 64 on 8: 201 us (625 TFLOP/s).  A row tile's chain
 // bounds it, of 3700 clocks a tile of keys at 64 dims, 4900 at 128: 2500 in the softmax, the rest the issue of
 // its 16 products and their latency; the tensor pipe is busy for a third, the exponentials' for a fifth.
+// Of 128 dims 164 to 206 bytes a thread are spilled, of 64 and 96 dims 16.
 // Tried and slower: half tiles of keys as items with S of 64 columns (two row tiles 207 us), weights
 // relative to the last maximum in one pass (225), a warp for each group's products (202); 64 dims with P beside
 // S in TMEM and the next S issued before P V (213).

@@ -9,12 +9,13 @@
 //   accept child x if u q(x) W < w(x);  else w = max(w - W q, 0), W = sum w
 // and the token after the last accepted node is the first i with sum_{j<=i} w_j > u W.
 // Nothing that is left was 0 before, so after k rejections w = max(p - A q, 0), A the sum
-// of the W before each (1 for the first): one step however many there were.
+// of the W before each (1 for the first): one step however many there were.  Without a
+// draft w is p without the refused tokens: a pass compares each element with each of them.
 //
 // Sums are whole numbers of 2^-60: adding them is associative, so the result does
 // not depend on how a row is split, and a probability's 24 bits are kept down to
-// 2^-37; what is left after a rejection has 48 bits (binary32 pairs: GB300's 64-bit
-// floating point is 64 times slower).  A row is read only where a sum is needed: for a chain once for the whole
+// 2^-37; what is left after a rejection, its sum and both sides of a comparison have 48 bits
+// (binary32 pairs: GB300's 64-bit floating point is 64 times slower).  A row is read only where a sum is needed: for a chain once for the whole
 // sequence (at the rejection, or after the last token), and there its sums also say
 // which warp has the sampled token.  What is needed of the other rows is the drafted
 // token's two elements, all fetched at once at the start.
@@ -23,9 +24,12 @@
 // distributed shared memory.
 //
 // Measured: 64 sequences with 8 nodes against 131072 tokens, binary32: 28 us; a pass of all of them
-// takes 12 us for the target alone (5.4 TB/s: HBM), 16 with the draft, and a second refusal at a node 5 us
+// takes 12 us for the target alone (2.7 TB/s), 16 with the draft (4.2), and a second refusal at a node 4 to 5 us
 // more for its sequence alone (12 if all have one): latency and the fetch of instructions, 23 of them an element for the
-// first refusal, 31 for the later ones.  One sequence, a chain of four against 50007: 8.2 us.
+// target alone and the first refusal, 31 for the later ones.  HBM does not bound a pass (18% of it from cold caches): 0.84
+// waves of CTAs issue in a third of the cycles, and 40% of the warps' waiting is for instructions, 21% for loads.
+// One sequence, a chain of four against 50007: 8.4 us.  Given tokens, all refused, 64 sequences against 131072: 18 us for
+// one at a node, 31 for two, 44 for seven (two passes from two on; binary32; bf16 7 to 11% more).
 #include "pi_ops.cuh"
 
 #include <algorithm>

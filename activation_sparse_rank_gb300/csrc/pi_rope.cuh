@@ -5,8 +5,9 @@
 //
 // Angles.  A frequency is kept as a whole number of 2^-64 turns a position, so the
 // product with a position modulo 2^64 is the angle modulo a turn, exactly, however
-// far the position; what is left of it beside the nearest quarter turn is below
-// 1/8 and is rounded to binary32 (2^-25 of it: 2.4e-8 of an angle).
+// far the position; what is left of it beside the nearest quarter turn, 1/4 of a half turn at
+// most, is cut to whole 2^-31 half turns (1.5e-9 of an angle, however small) and rounded to
+// binary32 (2^-27 half turns at most: 2.4e-8).
 #pragma once
 
 #include "pi_ops.cuh"

@@ -345,8 +345,10 @@ class KVCache:
         turned in the same launch.  Row cu_tokens[s] + i is turned by
         positions[cu_tokens[s] + i] (int32 [tokens]), by default start[s] + i; its place
         in the cache is start[s] + i either way.  Returns the turned queries, or None
-        without q; q_out may be q itself (contiguous).  Rows of no sequence are left as
-        they were (unset in a q_out made here)."""
+        without q; q_out may be q itself (contiguous), and shares no other memory with q, k
+        or v.  Rows of no sequence are left as they were (unset in a q_out made here).
+        Drafted tokens that are refused and appended over leave the scale that they
+        raised in a block begun before them."""
         ks, vs = self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v")
         if v.shape != k.shape or v.dtype is not k.dtype:
             raise ValueError("k and v must have one shape and type")
@@ -419,7 +421,9 @@ class KVCache:
 
         tree (``draft_tree``'s mask, int32 [tokens, words]): the new tokens are drafted
         ones, and one sees of them those whose bits its row has (up to itself), beside the
-        cache before them.  max_q is then at most 32 words and PI_MAX_TREE, the default included."""
+        cache before them.  max_q is then at most 32 words and PI_MAX_TREE, the default included.
+        From 17 to 32 query rows a head the page table's width chooses the kernel: short
+        sequences are faster under the columns that they use (page_table[:, :n])."""
         heads = q.shape[1] if q.dim() == 3 else 0
         qs = self._rows(q, heads, "q")
         if q.dtype is not torch.float16 and q.dtype is not torch.bfloat16:

@@ -464,7 +464,11 @@ pi_status pi_rotary_apply(const pi_rotary *rotary, const int32_t *positions, int
  * Turned keys are quantised from binary32 (as pi_rotary_apply to binary32 and
  * pi_kv_write of that).  rotary->dim a multiple of 16.  Rows that cannot be written
  * (a bad page or position) still have their queries turned; rows of no sequence and
- * of a bad cu range are left as they were. */
+ * of a bad cu range are left as they were.  q_out shares no memory with k and v, and none
+ * with a q that it is not.
+ * Drafted tokens that are refused and written over leave their scale: they raise the scale of
+ * a block that had been begun, as any write does, the block's earlier tokens are rounded to it,
+ * and the tokens that take their place start from it. */
 pi_status pi_kv_append(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *start,
                        const pi_rotary *rotary, const int32_t *positions, const void *k, const int64_t *k_stride,
                        const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,
@@ -476,7 +480,8 @@ pi_status pi_kv_append(const pi_kv_cache *cache, const pi_kv_tokens *tokens, con
  * 0 .. length[s]-1 (causal == 0).  Query head h reads key/value head
  * h / (q_heads / heads).
  *   out = sum_j softmax_j(sm_scale q.k_j) v_j,  lse = log sum_j exp(sm_scale q.k_j)
- * A row that sees nothing has out 0 and lse -inf.
+ * A row that sees nothing has out 0 and lse -inf, as has one whose scores are all -inf;
+ * a score that is NaN or +inf makes its row's out and lse NaN.
  *   q       [n_tokens, q_heads, head_dim], fp16 or bf16, q_stride as k_stride
  *           (strides multiples of 8 elements, base 16-byte aligned)
  *   length  device int32 [n_seqs], tokens of the sequence in the cache, the new
@@ -510,7 +515,12 @@ pi_status pi_kv_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, 
  * bit is set in its row of mask (pi_draft_tree's, or any bits).
  *   mask  device int32 [n_tokens, mask_words], bit j in word j / 32; mask_words * 32 at
  *         least max_q, which is at most PI_MAX_TREE
- * The nodes' keys and values are in the cache, in the order of q's rows. */
+ * The nodes' keys and values are in the cache, in the order of q's rows.
+ * With 17 to 32 query rows a head (head_dim up to 128) the width of the page table chooses the
+ * kernel, since lengths are on the device: from table_pages x page_size = 4096 on it is the one for
+ * many rows.  The same data under a wider table may then differ in its last bits, and short
+ * sequences take longer there (64 of 300 tokens, 24 rows a head, 8 heads of 128: 61 us, 45 under a
+ * narrow table); a view of the table's first columns is as good as a narrow one. */
 pi_status pi_kv_tree_attention(const pi_kv_cache *cache, const pi_kv_tokens *tokens, const int32_t *length,
                                int32_t max_q, const int32_t *mask, int32_t mask_words, const void *q,
                                const int64_t *q_stride, int32_t q_heads, int32_t dtype, float sm_scale,
@@ -602,8 +612,9 @@ pi_status pi_draft_tree(const int32_t *parent, const int32_t *cu, int32_t n_seqs
  *   accepted       int32 [n_seqs]: drafted tokens accepted
  *   path           int32 [n_seqs, max_q]: 0, then the accepted nodes, then -1
  *   token          int32 [n_seqs]
- * Comparisons are in 64 bits, w after a rejection in 48 or more, sums in whole 2^-60
- * and the same however a row is split.  vocab up to 2^21.  Nodes past max_q of a sequence are not looked at. */
+ * Comparisons are exact before the first rejection at a node; after it w, W and both sides
+ * are pairs of binary32 (48 bits).  Sums are in whole 2^-60, where anything above 0 is 1 at
+ * least, and the same however a row is split.  vocab up to 2^21.  Nodes past max_q of a sequence are not looked at. */
 pi_status pi_verify_draft(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
                           int32_t dtype, int32_t vocab, const int32_t *drawn, const int32_t *parent,
                           const int32_t *cu, int32_t n_seqs, int32_t n_tokens, int32_t max_q, const float *accept,
